@@ -10,6 +10,12 @@
  *   bn_fwd_infer  BatchNorm2d inference forward (running statistics)
  *   bn_bwd        BatchNorm2d training backward (dx, dgamma, dbeta)
  *   softmax_fwd   row softmax over a [rows, N] tensor
+ *   dropout_fwd   dropout from a counter-based generator (also its backward)
+ *   dropout_add_rms_fwd, dropout_add_rms_bwd
+ *                 dropout + residual add + RMSNorm, and its backward
+ *   logprob_fwd, logprob_bwd
+ *                 log-softmax of one target per row of logits, and its gradient
+ *   policy_loss   clipped policy loss with a KL term, with its gradient
  *   bn_fwd_partial_stats / bn_fwd_apply_stats, bn_bwd_partial_sums /
  *   bn_bwd_apply_sums   the local halves of synchronized BatchNorm
  *
@@ -36,7 +42,8 @@
  *   and N is a multiple of 16/sizeof(element); otherwise a scalar kernel runs.
  * Aliasing.  Outputs may not overlap inputs or each other, with one
  *   exception: add_rms_fwd accepts residual_out == residual (the residual
- *   stream updated in place).  Any other overlap returns NRM_ERR_ALIAS.
+ *   stream updated in place); the training operators name the tensors that
+ *   may be replaced in place.  Any other overlap returns NRM_ERR_ALIAS.
  * Errors.  Arguments are validated before anything is launched; an invalid
  *   call returns a non-zero nrm_status and launches nothing.  After the
  *   launch, cudaGetLastError is checked (NRM_ERR_LAUNCH).  Errors raised
@@ -71,11 +78,13 @@ typedef enum {
     NRM_ERR_SHAPE = 2,         /* negative extent, N < 1, size overflow, BN count < 2 */
     NRM_ERR_DTYPE = 3,         /* dtype is not an nrm_dtype */
     NRM_ERR_ALIAS = 4,         /* an output overlaps an input or another output */
-    NRM_ERR_VALUE = 5,         /* eps < 0 or not finite; momentum outside [0, 1];
-                                  a pointer not aligned to its element size */
+    NRM_ERR_VALUE = 5,         /* eps < 0 or not finite; momentum or p outside
+                                  [0, 1]; an inverse temperature, clip bound or
+                                  KL coefficient out of range; a pointer not
+                                  aligned to its element size */
     NRM_ERR_UNSUPPORTED = 6,   /* valid but not provided (e.g. a forced plan that
                                   cannot run this shape) */
-    NRM_ERR_WORKSPACE = 7,     /* BatchNorm workspace NULL, too small or misaligned */
+    NRM_ERR_WORKSPACE = 7,     /* workspace NULL, too small or misaligned */
     NRM_ERR_DEVICE = 8,        /* no current CUDA device or attribute query failed */
     NRM_ERR_LAUNCH = 9,        /* cudaGetLastError reported a launch failure */
     NRM_ERR_POINTER = 10,      /* pointer checks on, and a pointer is not device
@@ -353,6 +362,156 @@ int bn_bwd_apply_sums(const void *dy, const void *x, const void *gamma, const fl
                       int64_t count, void *dx, float *dgamma, float *dbeta, int64_t batch,
                       int64_t C, int64_t HW, int dtype, cudaStream_t stream);
 
+/*
+ * Dropout whose mask is never stored: y = d(x), element by element,
+ *   d(v) = kept ? v * scale : +0      (a dropped infinity or NaN gives +0)
+ * The mask is a function of (seed, offset, row, column) alone -- not of the
+ * type, the strides or the kernel -- so the same call on another tensor drops
+ * the same places: the BACKWARD is this operator on dy (dx = dropout_fwd(dy)
+ * with the same p, seed and offset).
+ * Generator: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) with the 64-bit seed as key and the
+ * counter (column / 8, row, offset low word, offset high word); its four
+ * words are eight 16-bit numbers, low half first, for the columns of the
+ * block.  An element is kept when its number is >= T = floor(65536 p + 0.5);
+ * scale = 65536 / (65536 - T), the reciprocal of the exact probability of
+ * keeping, so the expectation is x.  p is thus held to 2^-17; T = 0 drops
+ * nothing, T = 65536 everything.  Calls that should be independent need
+ * different seeds or offsets.
+ *   x           [rows, N] dtype, read only;  y [rows, N] dtype, may be x
+ *   p           0 <= p <= 1
+ *   offset_dev  device int64 [1] added to offset (modulo 2^64) when the kernel
+ *               runs, or NULL: what a replayed graph advances to draw anew
+ *   rows <= 2^32, N <= 2^35 (32-bit counter words), else NRM_ERR_SHAPE
+ */
+int dropout_fwd(const void *x, void *y, int64_t rows, int64_t N, double p, uint64_t seed,
+                uint64_t offset, const int64_t *offset_dev, int dtype, cudaStream_t stream);
+int dropout_fwd_ld(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t rows, int64_t N,
+                   double p, uint64_t seed, uint64_t offset, const int64_t *offset_dev, int dtype,
+                   cudaStream_t stream);
+
+/*
+ * The pre-norm residual path in training:
+ *   residual_out = round_to_dtype(binary32(residual) + d(x))
+ *   y            = RMSNorm(residual_out, w)
+ * with dropout_fwd's d (mask by row and column).  With p = 0 this is
+ * add_rms_fwd.  Arguments, in-place residual and errors as add_rms_fwd;
+ * rstd [rows] binary32 is what the backward needs.
+ */
+int dropout_add_rms_fwd(const void *x, const void *residual, const void *w, void *residual_out,
+                        void *y, float *rstd, int64_t rows, int64_t N, double p, uint64_t seed,
+                        uint64_t offset, const int64_t *offset_dev, float eps, int dtype,
+                        cudaStream_t stream);
+int dropout_add_rms_fwd_ld(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                           const void *w, void *residual_out, int64_t ldro, void *y, int64_t ldy,
+                           float *rstd, int64_t rows, int64_t N, double p, uint64_t seed,
+                           uint64_t offset, const int64_t *offset_dev, float eps, int dtype,
+                           cudaStream_t stream);
+
+/*
+ * Its backward.  With h = residual_out and rstd as the forward wrote them,
+ * xhat = h * rstd, g = dy * w and c = (1/N) sum_j g_j xhat_j per row:
+ *   dh        = rstd * (g - xhat * c) + dresidual_out
+ *   dresidual = dh,   dx = d(dh),   dw = sum over rows of dy * xhat
+ * The mask is made again from p, seed and offset (the forward's).  With p = 0
+ * this is the backward of add_rms_fwd (dx == dresidual) and of rms_fwd
+ * (h = x).  Sums are binary32 in an order that depends on the shape alone:
+ * the same call gives the same bits.
+ *   dy, residual_out   [rows, N] dtype, read only
+ *   rstd               [rows] binary32
+ *   w                  [N] dtype or NULL (= 1)
+ *   dresidual_out      [rows, N] dtype, the gradient of residual_out, or NULL (= 0)
+ *   dx                 [rows, N] dtype or NULL (not written); may be dy
+ *   dresidual          [rows, N] dtype or NULL (not written); may be dresidual_out
+ *   dw                 [N] binary32 or NULL (not written); rows == 0 writes zeros
+ *   (at least one of dx, dresidual, dw; an in-place pair has one row stride)
+ *   workspace          device memory, 16-byte aligned, at least
+ *                      dropout_add_rms_bwd_workspace_size(rows, N, dtype)
+ *                      bytes, scratch; calls sharing one must be ordered on
+ *                      the GPU
+ */
+size_t dropout_add_rms_bwd_workspace_size(int64_t rows, int64_t N, int dtype);
+int dropout_add_rms_bwd(const void *dy, const void *residual_out, const float *rstd, const void *w,
+                        const void *dresidual_out, void *dx, void *dresidual, float *dw,
+                        int64_t rows, int64_t N, double p, uint64_t seed, uint64_t offset,
+                        const int64_t *offset_dev, int dtype, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_out, int64_t ldro,
+                           const float *rstd, const void *w, const void *dresidual_out,
+                           int64_t lddro, void *dx, int64_t lddx, void *dresidual, int64_t lddr,
+                           float *dw, int64_t rows, int64_t N, double p, uint64_t seed,
+                           uint64_t offset, const int64_t *offset_dev, int dtype, void *workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Log-probability of one target per row of logits z[rows, V], s = inv_temp:
+ *   lse = log sum_j exp(s z_j),   logp = s z_target - lse
+ *   logits   [rows, V] dtype, read only; -inf entries (masked) have probability 0
+ *   targets  [rows] int64.  A row whose target is outside [0, V) (padding,
+ *            conventionally -100) takes no part: its logits are not read, logp = lse = 0
+ *   logp, lse  [rows] binary32, written; one of them may be NULL
+ *   V < 2^31 (NRM_ERR_SHAPE); inv_temp > 0, finite
+ * A row whose entries are all -inf gives logp = lse = -inf.
+ */
+int logprob_fwd(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
+                int64_t V, float inv_temp, int dtype, cudaStream_t stream);
+int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
+                   int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream);
+
+/*
+ * Gradient of the logits for a gradient dlogp [rows] (binary32) of the
+ * log-probabilities -- of any loss on them -- and the forward's lse:
+ *   dlogits_j = dlogp * s * ((j == target) - exp(s z_j - lse))
+ * Rows without a target in [0, V), rows with dlogp = 0 and rows without a
+ * finite logit (lse = -inf) get zeros, their logits are not read.
+ *   dlogits  [rows, V] dtype, written; may be logits (same row stride)
+ */
+int logprob_bwd(const float *dlogp, const void *logits, const int64_t *targets, const float *lse,
+                void *dlogits, int64_t rows, int64_t V, float inv_temp, int dtype,
+                cudaStream_t stream);
+int logprob_bwd_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
+                   const float *lse, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
+                   float inv_temp, int dtype, cudaStream_t stream);
+
+/*
+ * Clipped policy loss with a KL term over token rows, and its gradient, in
+ * one launch over the logits (plus one that adds the rows' terms).  With logp
+ * as logprob_fwd, per row r that takes part:
+ *   ratio = exp(logp - old_logp)
+ *   l     = max(-A ratio, -A clip(ratio, 1 - clip_low, 1 + clip_high))
+ *           + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1)
+ *   loss  = sum_r weight_r l_r
+ *   dlogits_j = grad_scale * dloss/dlogp * s * ((j == target) - softmax_j)
+ * dloss/dlogp of the first term is -A ratio where the unclipped branch is the
+ * larger (or equal), else 0.
+ *   targets     [rows] int64, as logprob_fwd
+ *   old_logp, advantages (A)   [rows] binary32
+ *   weights     [rows] binary32 or NULL (= 1): mask and averaging
+ *   ref_logp    [rows] binary32; NULL only with kl_coef = 0
+ *   grad_scale  device binary32 [1] or NULL (= 1): the gradient of the loss
+ *   loss        [1] binary32, written (0 when no row takes part)
+ *   logp        [rows] binary32 or NULL
+ *   dlogits     [rows, V] dtype or NULL (loss only); may be logits (same row stride)
+ *   0 <= clip_low <= 1, clip_high >= 0 and finite, kl_coef >= 0 and finite
+ *   workspace   device memory, 16-byte aligned, policy_loss_workspace_size(rows)
+ *               bytes, scratch; calls sharing one must be ordered on the GPU
+ * A row with a target outside [0, V) or weight 0 takes no part: its logits,
+ * old_logp, advantage and ref_logp are not read, logp = 0, dlogits = 0.  A row
+ * without a finite logit adds nothing either: logp = -inf, dlogits = 0.
+ */
+size_t policy_loss_workspace_size(int64_t rows);
+int policy_loss(const void *logits, const int64_t *targets, const float *old_logp,
+                const float *advantages, const float *weights, const float *ref_logp,
+                double clip_low, double clip_high, float kl_coef, float inv_temp,
+                const float *grad_scale, float *loss, float *logp, void *dlogits, int64_t rows,
+                int64_t V, int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, const float *old_logp,
+                   const float *advantages, const float *weights, const float *ref_logp,
+                   double clip_low, double clip_high, float kl_coef, float inv_temp,
+                   const float *grad_scale, float *loss, float *logp, void *dlogits, int64_t lddl,
+                   int64_t rows, int64_t V, int dtype, void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char *nrm_status_string(int status);
 
@@ -405,7 +564,10 @@ typedef enum {
  * next plan that runs; bn_bwd takes NRM_PLAN_GENERIC as its scalar plan,
  * NRM_PLAN_PERSIST as its one-pass plan (dy and x read once) and anything
  * else as its streaming plan where the layout allows it;
- * bn_fwd_infer takes NRM_PLAN_GENERIC as its scalar element-wise kernel.
+ * bn_fwd_infer takes NRM_PLAN_GENERIC as its scalar element-wise kernel;
+ * dropout_add_rms_fwd and dropout_add_rms_bwd take NRM_PLAN_GENERIC as the
+ * plan of rows that outgrow the registers (any length), and the training
+ * operators follow no other forced plan.
  * Returns NRM_OK or NRM_ERR_UNSUPPORTED for
  * an unknown plan.  Process-wide; not meant to change while calls run.
  */

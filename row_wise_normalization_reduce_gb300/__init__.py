@@ -2,8 +2,10 @@
 
 LayerNorm, RMSNorm, fused residual-add + RMSNorm, BatchNorm2d training
 forward, inference forward, training backward and their synchronized
-(multi-process) form, and row softmax, computed by the
-hand-written CUDA kernels of libnrm.so (C ABI in include/nrm.h).  This
+(multi-process) form, row softmax, and the training operators around them
+(dropout from a counter-based generator, alone and fused with the residual
+add and RMSNorm, forward and backward; target log-probabilities of logits and
+the clipped policy loss, with their gradients), computed by the hand-written CUDA kernels of libnrm.so (C ABI in include/nrm.h).  This
 package is the thin Python binding over that library.
 """
 from ._binding import (  # noqa: F401
@@ -13,7 +15,10 @@ from ._binding import (  # noqa: F401
     bn_fwd_train_workspace_size, device_fault, force_plan, last_plan, lib, ln_fwd, rms_fwd,
     set_bn_group_bytes, set_pointer_checks, set_wait_limit, softmax_fwd, status_string,
     bn_fwd_partial_stats, bn_fwd_apply_stats, bn_bwd_partial_sums, bn_bwd_apply_sums,
-    add_rms_fwd_host, add_rms_fwd_host_workspace)
+    add_rms_fwd_host, add_rms_fwd_host_workspace,
+    dropout_fwd, dropout_bwd, dropout_add_rms_fwd, dropout_add_rms_bwd,
+    dropout_add_rms_bwd_workspace_size, logprob_fwd, logprob_bwd, policy_loss,
+    policy_loss_workspace_size)
 from .sync import exchange_parts, global_count, sync_bn_bwd, sync_bn_fwd_train  # noqa: F401
 
 

@@ -7,6 +7,7 @@ library is missing the first call raises; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -27,7 +28,10 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_U64 = ctypes.c_uint64
 _F = ctypes.c_float
+_D = ctypes.c_double
+_SZ = ctypes.c_size_t
 _INT = ctypes.c_int
 
 
@@ -81,6 +85,29 @@ def _declare(lib):
     lib.add_rms_fwd_host.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _INT, _P,
                                      ctypes.c_size_t, _P]
     lib.add_rms_fwd_host.restype = _INT
+    drop = [_D, _U64, _U64, _P]  # p, seed, offset, offset_dev
+    lib.dropout_fwd.argtypes = [_P, _P, _I64, _I64, *drop, _INT, _P]
+    lib.dropout_fwd_ld.argtypes = [_P, _I64, _P, _I64, _I64, _I64, *drop, _INT, _P]
+    lib.dropout_add_rms_fwd.argtypes = [_P] * 6 + [_I64, _I64, *drop, _F, _INT, _P]
+    lib.dropout_add_rms_fwd_ld.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
+                                           _I64, *drop, _F, _INT, _P]
+    lib.dropout_add_rms_bwd_workspace_size.argtypes = [_I64, _I64, _INT]
+    lib.dropout_add_rms_bwd_workspace_size.restype = _SZ
+    lib.dropout_add_rms_bwd.argtypes = [_P] * 8 + [_I64, _I64, *drop, _INT, _P, _SZ, _P]
+    lib.dropout_add_rms_bwd_ld.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P,
+                                           _I64, _P, _I64, _I64, *drop, _INT, _P, _SZ, _P]
+    lib.logprob_fwd.argtypes = [_P] * 4 + [_I64, _I64, _F, _INT, _P]
+    lib.logprob_fwd_ld.argtypes = [_P, _I64, _P, _P, _P, _I64, _I64, _F, _INT, _P]
+    lib.logprob_bwd.argtypes = [_P] * 5 + [_I64, _I64, _F, _INT, _P]
+    lib.logprob_bwd_ld.argtypes = [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P]
+    lib.policy_loss_workspace_size.argtypes = [_I64]
+    lib.policy_loss_workspace_size.restype = _SZ
+    lib.policy_loss.argtypes = [_P] * 6 + [_D, _D, _F, _F] + [_P] * 4 + [_I64, _I64, _INT, _P, _SZ, _P]
+    lib.policy_loss_ld.argtypes = [_P, _I64] + [_P] * 5 + [_D, _D, _F, _F] + [_P] * 4 + [
+        _I64, _I64, _I64, _INT, _P, _SZ, _P]
+    for f in ("dropout_fwd", "dropout_add_rms_fwd", "dropout_add_rms_bwd", "logprob_fwd",
+              "logprob_bwd", "policy_loss"):
+        getattr(lib, f).restype = getattr(lib, f + "_ld").restype = _INT
     lib.nrm_status_string.argtypes = [_INT]
     lib.nrm_status_string.restype = ctypes.c_char_p
     lib.nrm_force_plan.argtypes = [_INT, _INT, _INT, _INT, _INT]
@@ -508,6 +535,223 @@ def bn_bwd_apply_sums(dy, x, save_mean, save_rstd, parts, count, gamma=None, *, 
                                      stream if stream is not None else _stream(x.device))
     _check(st, "bn_bwd_apply_sums")
     return dx, dgamma, dbeta
+
+
+# ---------------------------------------------------------------------------
+# Training operators.
+# ---------------------------------------------------------------------------
+def _on_stream(f):
+    """Keyword `stream` (a raw stream handle or a torch stream): everything the
+    call allocates and launches belongs to that stream."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        t = args[0] if args else next(v for v in kw.values() if isinstance(v, torch.Tensor))
+        if not t.is_cuda:
+            raise ValueError(f"{f.__name__}: the tensors must be CUDA tensors")
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+def _launch(name, device, *args):
+    """One C call on `device`'s current stream."""
+    f = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, torch.cuda.current_stream().cuda_stream)
+    _check(st, name)
+
+
+def _like(t, x, name):
+    """`t`, or a new contiguous tensor like x; and its row stride."""
+    if t is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[-1]
+    return t, _same_rows(t, x, name)
+
+
+def _row_values(t, x, name, dtype=torch.float32):
+    """One value per row of x."""
+    if t.dtype != dtype or t.device != x.device or t.shape != x.shape[:-1] or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(x.shape[:-1])} {dtype} tensor on {x.device}")
+    return t
+
+
+def _one_value(t, x, name, dtype):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != x.device or t.numel() != 1:
+        raise ValueError(f"{name} must be one {dtype} value on {x.device}")
+    return t
+
+
+def _scratch_bytes(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace
+
+
+def _drop(x, p, seed, offset, offset_dev):
+    return (p, seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF,
+            _ptr(_one_value(offset_dev, x, "offset_dev", torch.int64)))
+
+
+@_on_stream
+def dropout_fwd(x, p, seed, offset=0, *, out=None, offset_dev=None):
+    """Dropout over x as rows of its last dimension: y = x / (1 - p) where the
+    mask of (seed, offset, row, column) keeps the element, +0 elsewhere; p is
+    rounded to a multiple of 2^-16.  seed and offset are integers (modulo
+    2^64); offset_dev, an int64 tensor of one element, is added to offset when
+    the kernel runs.  out may be x.  Returns y."""
+    rows, n, ldx = _rows(x, "x")
+    y, ldy = _like(out, x, "out")
+    _launch("dropout_fwd_ld", x.device, x.data_ptr(), ldx, y.data_ptr(), ldy, rows, n,
+            *_drop(x, p, seed, offset, offset_dev), _dtype_code(x))
+    return y
+
+
+@_on_stream
+def dropout_bwd(dy, p, seed, offset=0, *, out=None, offset_dev=None):
+    """Gradient of dropout_fwd: the same places of dy dropped, the rest scaled.
+    Returns dx."""
+    return dropout_fwd(dy, p, seed, offset, out=out, offset_dev=offset_dev)
+
+
+@_on_stream
+def dropout_add_rms_fwd(x, residual, w=None, p=0.0, seed=0, offset=0, eps=1e-6, *,
+                        residual_out=None, out=None, rstd=None, offset_dev=None):
+    """residual_out = residual + dropout(x) (rounded to x.dtype); y =
+    RMSNorm(residual_out, w).  Returns (residual_out, y, rstd); the backward
+    takes residual_out and rstd.  Pass residual_out=residual to update the
+    residual stream in place."""
+    rows, n, ldx = _rows(x, "x")
+    ldr = _same_rows(residual, x, "residual")
+    w = _param(w, n, x.dtype, x.device, "w")
+    ro, ldro = _like(residual_out, x, "residual_out")
+    y, ldy = _like(out, x, "out")
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _row_values(rstd, x, "rstd")
+    _launch("dropout_add_rms_fwd_ld", x.device, x.data_ptr(), ldx, residual.data_ptr(), ldr, _ptr(w),
+            ro.data_ptr(), ldro, y.data_ptr(), ldy, rstd.data_ptr(), rows, n,
+            *_drop(x, p, seed, offset, offset_dev), eps, _dtype_code(x))
+    return ro, y, rstd
+
+
+def dropout_add_rms_bwd_workspace_size(rows, n, dtype) -> int:
+    return lib().dropout_add_rms_bwd_workspace_size(rows, n, _DT[dtype])
+
+
+@_on_stream
+def dropout_add_rms_bwd(dy, residual_out, rstd, w=None, p=0.0, seed=0, offset=0, *,
+                        dresidual_out=None, dx=None, dresidual=None, dw=None, want_dw=None,
+                        workspace=None, offset_dev=None):
+    """Backward of dropout_add_rms_fwd (with p = 0 of add_rms_fwd and, with
+    residual_out = x, of rms_fwd) from dy, the gradient of y, and optionally
+    dresidual_out, the gradient of residual_out.  Returns (dx, dresidual, dw):
+    dw is binary32, computed when w is given (or want_dw=True), else None.
+    Without dropout (p = 0) and without a dx to write to, dx is dresidual, the
+    same tensor.  dx=dy and dresidual=dresidual_out work in place."""
+    rows, n, lddy = _rows(dy, "dy")
+    ldh = _same_rows(residual_out, dy, "residual_out")
+    _row_values(rstd, dy, "rstd")
+    w = _param(w, n, dy.dtype, dy.device, "w")
+    ldu = n if dresidual_out is None else _same_rows(dresidual_out, dy, "dresidual_out")
+    dresidual, lddr = _like(dresidual, dy, "dresidual")
+    same = dx is None and p == 0
+    if not same:
+        dx, lddx = _like(dx, dy, "dx")
+    if dw is not None:
+        if dw.dtype != torch.float32 or dw.numel() != n or dw.device != dy.device or not dw.is_contiguous():
+            raise ValueError(f"dw must be [{n}] float32 on {dy.device}")
+    elif want_dw if want_dw is not None else w is not None:
+        dw = torch.empty(n, dtype=torch.float32, device=dy.device)
+    code = _dtype_code(dy)
+    workspace = _scratch_bytes(workspace, lib().dropout_add_rms_bwd_workspace_size(rows, n, code), dy.device)
+    _launch("dropout_add_rms_bwd_ld", dy.device, dy.data_ptr(), lddy, residual_out.data_ptr(), ldh,
+            rstd.data_ptr(), _ptr(w), _ptr(dresidual_out), ldu, None if same else dx.data_ptr(),
+            n if same else lddx, dresidual.data_ptr(), lddr, _ptr(dw), rows, n,
+            *_drop(dy, p, seed, offset, offset_dev), code, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return (dresidual if same else dx), dresidual, dw
+
+
+@_on_stream
+def logprob_fwd(logits, targets, inv_temp=1.0, *, logp=None, lse=None):
+    """Log-softmax of inv_temp * logits at one target (int64) per row of the
+    last dimension.  Returns (logp, lse), binary32, one value per row; rows
+    with a target outside [0, V) give 0 and are not read."""
+    rows, v, ldl = _rows(logits, "logits")
+    _row_values(targets, logits, "targets", torch.int64)
+    shape, dev = targets.shape, logits.device
+    logp = torch.empty(shape, dtype=torch.float32, device=dev) if logp is None else _row_values(logp, logits, "logp")
+    lse = torch.empty(shape, dtype=torch.float32, device=dev) if lse is None else _row_values(lse, logits, "lse")
+    _launch("logprob_fwd_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(),
+            lse.data_ptr(), rows, v, inv_temp, _dtype_code(logits))
+    return logp, lse
+
+
+@_on_stream
+def logprob_bwd(dlogp, logits, targets, lse, inv_temp=1.0, *, out=None):
+    """Gradient of the logits from dlogp, the gradient of logprob_fwd's logp
+    (one binary32 value per row), and its lse.  out may be logits.  Returns
+    dlogits."""
+    rows, v, ldl = _rows(logits, "logits")
+    _row_values(dlogp, logits, "dlogp")
+    _row_values(targets, logits, "targets", torch.int64)
+    _row_values(lse, logits, "lse")
+    out, lddl = _like(out, logits, "out")
+    _launch("logprob_bwd_ld", logits.device, dlogp.data_ptr(), logits.data_ptr(), ldl,
+            targets.data_ptr(), lse.data_ptr(), out.data_ptr(), lddl, rows, v, inv_temp,
+            _dtype_code(logits))
+    return out
+
+
+def policy_loss_workspace_size(rows) -> int:
+    return lib().policy_loss_workspace_size(rows)
+
+
+@_on_stream
+def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=None, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, inv_temp=1.0, *, grad_scale=None, want_grad=True,
+                out=None, logp=None, workspace=None):
+    """Clipped policy loss with a KL term over token rows, and the gradient of
+    the logits in the same pass.  Per row with a target in [0, V) and a weight
+    other than 0, ratio = exp(logp - old_logp):
+      max(-A ratio, -A clip(ratio, 1 - clip_low, 1 + clip_high))
+        + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1)
+    weighted and summed.  grad_scale (one binary32 value on the device)
+    multiplies the gradient.  out, the gradient's tensor, may be logits;
+    want_grad=False computes the loss only.  Returns (loss, logp, dlogits or
+    None)."""
+    rows, v, ldl = _rows(logits, "logits")
+    _row_values(targets, logits, "targets", torch.int64)
+    _row_values(old_logp, logits, "old_logp")
+    _row_values(advantages, logits, "advantages")
+    if weights is not None:
+        _row_values(weights, logits, "weights")
+    if ref_logp is not None:
+        _row_values(ref_logp, logits, "ref_logp")
+    _one_value(grad_scale, logits, "grad_scale", torch.float32)
+    dev, lddl = logits.device, v
+    logp = torch.empty(targets.shape, dtype=torch.float32, device=dev) if logp is None else _row_values(logp, logits, "logp")
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    if want_grad or out is not None:
+        out, lddl = _like(out, logits, "out")
+    workspace = _scratch_bytes(workspace, 4 * rows + 16, dev)
+    _launch("policy_loss_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), old_logp.data_ptr(),
+            advantages.data_ptr(), _ptr(weights), _ptr(ref_logp), clip_low, clip_high, kl_coef,
+            inv_temp, _ptr(grad_scale), loss.data_ptr(), logp.data_ptr(), _ptr(out), lddl, rows, v,
+            _dtype_code(logits), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return loss, logp, out
 
 
 # ---------------------------------------------------------------------------

@@ -988,6 +988,410 @@ int bn_bwd_apply_sums(const void *dy, const void *x, const void *gamma, const fl
     return record_bn(launch_bn_apply_sums(a, dtype, dev.sms, stream), PLAN_GENERIC);
 }
 
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Training operators: dropout and the residual path (drop.cuh), rows of
+// logits (logits.cuh).
+// ---------------------------------------------------------------------------
+
+// Outputs may overlap neither inputs nor each other.  An input that an output
+// replaces in place is left out of `ins` by the caller: what the other
+// outputs must keep clear of is then checked through that output.
+int check_alias(std::initializer_list<RSpan> outs, std::initializer_list<RSpan> ins) {
+    for (const RSpan *o = outs.begin(); o != outs.end(); ++o) {
+        for (const RSpan &i : ins)
+            if (roverlap(*o, i)) return NRM_ERR_ALIAS;
+        for (const RSpan *q = o + 1; q != outs.end(); ++q)
+            if (roverlap(*o, *q)) return NRM_ERR_ALIAS;
+    }
+    return NRM_OK;
+}
+
+// The generator's arguments.  Rows and column blocks are 32-bit words of its
+// counter.
+int drop_args(int64_t rows, int64_t N, double p, uint64_t seed, uint64_t offset,
+              const int64_t *offset_dev, DropArgs *d) {
+    if (!(p >= 0.0 && p <= 1.0)) return NRM_ERR_VALUE;
+    if (rows > ((int64_t)1 << 32) || N > ((int64_t)1 << 35)) return NRM_ERR_SHAPE;
+    if (offset_dev && !aligned(offset_dev, 8)) return NRM_ERR_VALUE;
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+    for (int r = 0; r < 10; ++r) {
+        d->key[2 * r] = k0;
+        d->key[2 * r + 1] = k1;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    const int64_t T = (int64_t)std::floor(p * 65536.0 + 0.5);
+    d->offset = offset;
+    d->offset_dev = offset_dev;
+    d->on = T > 0;
+    d->bar = (uint32_t)((T << 16) - 1);  // T = 65536: no word exceeds it
+    d->scale = T < 65536 ? (float)(65536.0 / (double)(65536 - T)) : 0.f;
+    return NRM_OK;
+}
+
+// Whether every row of every tensor is a run of whole 16-byte packs on a
+// 16-byte boundary.
+struct RowPtr {
+    const void *p;
+    int64_t ld;
+};
+bool rows_vec(int64_t N, size_t es, std::initializer_list<RowPtr> ts) {
+    const int64_t V = 16 / (int64_t)es;
+    if (N % V) return false;
+    for (const RowPtr &t : ts)
+        if (t.p && (!aligned(t.p, 16) || t.ld % V)) return false;
+    return true;
+}
+
+int record_plan(cudaError_t e, const Plan &p) {
+    if (e != cudaSuccess) return NRM_ERR_LAUNCH;
+    t_last_kind = p.kind;
+    t_last_threads = p.threads;
+    t_last_packs = p.packs;
+    t_last_stages = p.stages;
+    t_last_groups = p.groups;
+    return NRM_OK;
+}
+
+bool forced_generic() { return g_force_kind.load(std::memory_order_relaxed) == PLAN_GENERIC; }
+
+size_t round16(size_t v) { return (v + 15) & ~(size_t)15; }
+
+// Partial sums of dw and the long-row plan's row factors.
+void drop_bwd_layout(int64_t rows, int64_t N, size_t *part, size_t *k) {
+    *part = round16((size_t)(rows < kDropMaxParts ? rows : kDropMaxParts) * (size_t)N * 4);
+    *k = round16((size_t)rows * 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dropout_fwd_ld(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t rows, int64_t N,
+                   double p, uint64_t seed, uint64_t offset, const int64_t *offset_dev, int dtype,
+                   cudaStream_t stream) {
+    int st = validate_rows(rows, N, 0.f, dtype);
+    if (st != NRM_OK) return st;
+    DropoutArgs a{{}, x, y, rows, N, ldx, ldy};
+    if ((st = drop_args(rows, N, p, seed, offset, offset_dev, &a.d)) != NRM_OK) return st;
+    if (rows == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!x || !y) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, N, es, {ldx, ldy})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({x, y}, es)) != NRM_OK) return st;
+    const bool inplace = x == y && ldx == ldy;
+    const RSpan sx = rspan(inplace ? nullptr : x, ldx, rows, N, es), sy = rspan(y, ldy, rows, N, es),
+                so = rspan(offset_dev, 1, 1, 1, 8);
+    if ((st = check_alias({sy}, {sx, so})) != NRM_OK) return st;
+    if ((st = check_pointers({x, y, offset_dev})) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    Plan plan{};
+    plan.kind = PLAN_WARP;
+    plan.threads = 256;
+    return record_plan(launch_dropout(dtype, a, rows_vec(N, es, {{x, ldx}, {y, ldy}}), dev.sms, stream), plan);
+}
+
+int dropout_fwd(const void *x, void *y, int64_t rows, int64_t N, double p, uint64_t seed,
+                uint64_t offset, const int64_t *offset_dev, int dtype, cudaStream_t stream) {
+    return dropout_fwd_ld(x, N, y, N, rows, N, p, seed, offset, offset_dev, dtype, stream);
+}
+
+int dropout_add_rms_fwd_ld(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                           const void *w, void *residual_out, int64_t ldro, void *y, int64_t ldy,
+                           float *rstd, int64_t rows, int64_t N, double p, uint64_t seed,
+                           uint64_t offset, const int64_t *offset_dev, float eps, int dtype,
+                           cudaStream_t stream) {
+    int st = validate_rows(rows, N, eps, dtype);
+    if (st != NRM_OK) return st;
+    DropRmsArgs a{{}, x, residual, w, residual_out, y, rstd, rows, N, ldx, ldr, ldro, ldy, eps,
+                  1.0f / (float)N};
+    if ((st = drop_args(rows, N, p, seed, offset, offset_dev, &a.d)) != NRM_OK) return st;
+    if (rows == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!x || !residual || !residual_out || !y) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, N, es, {ldx, ldr, ldro, ldy})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({x, residual, w, residual_out, y}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({rstd}, 4)) != NRM_OK) return st;
+    // residual_out may be exactly residual, with the same row stride
+    const bool inplace = residual_out == residual && ldro == ldr;
+    const RSpan sx = rspan(x, ldx, rows, N, es),
+                sres = rspan(inplace ? nullptr : residual, ldr, rows, N, es),
+                sw = rspan(w, N, 1, N, es), sro = rspan(residual_out, ldro, rows, N, es),
+                sy = rspan(y, ldy, rows, N, es), sr = rspan(rstd, rows, 1, rows, 4),
+                so = rspan(offset_dev, 1, 1, 1, 8);
+    if ((st = check_alias({sro, sy, sr}, {sx, sres, sw, so})) != NRM_OK) return st;
+    if ((st = check_pointers({x, residual, w, residual_out, y, rstd, offset_dev})) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    const bool vec = rows_vec(N, es, {{x, ldx}, {residual, ldr}, {residual_out, ldro}, {y, ldy}, {w, 0}});
+    Plan plan{};
+    return record_plan(launch_drop_fwd(dtype, a, vec, forced_generic(), dev.sms, stream, &plan), plan);
+}
+
+int dropout_add_rms_fwd(const void *x, const void *residual, const void *w, void *residual_out,
+                        void *y, float *rstd, int64_t rows, int64_t N, double p, uint64_t seed,
+                        uint64_t offset, const int64_t *offset_dev, float eps, int dtype,
+                        cudaStream_t stream) {
+    return dropout_add_rms_fwd_ld(x, N, residual, N, w, residual_out, N, y, N, rstd, rows, N, p,
+                                  seed, offset, offset_dev, eps, dtype, stream);
+}
+
+size_t dropout_add_rms_bwd_workspace_size(int64_t rows, int64_t N, int dtype) {
+    if (rows < 1 || validate_rows(rows, N, 0.f, dtype) != NRM_OK) return 0;
+    if ((uint64_t)N > (uint64_t)INT64_MAX / 8 / kDropMaxParts) return 0;
+    size_t part, k;
+    drop_bwd_layout(rows, N, &part, &k);
+    return part + k;
+}
+
+int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_out, int64_t ldro,
+                           const float *rstd, const void *w, const void *dresidual_out,
+                           int64_t lddro, void *dx, int64_t lddx, void *dresidual, int64_t lddr,
+                           float *dw, int64_t rows, int64_t N, double p, uint64_t seed,
+                           uint64_t offset, const int64_t *offset_dev, int dtype, void *workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+    int st = validate_rows(rows, N, 0.f, dtype);
+    if (st != NRM_OK) return st;
+    DropRmsBwdArgs a{{}, dy, residual_out, dresidual_out, w, rstd, dx, dresidual, dw, nullptr,
+                     nullptr, rows, N, lddy, ldro, lddro, lddx, lddr, 1.0f / (float)N};
+    if ((st = drop_args(rows, N, p, seed, offset, offset_dev, &a.d)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({rstd, dw}, 4)) != NRM_OK) return st;
+    if (rows == 0) {  // no rows: the weight gradient is an empty sum, nothing else exists
+        if (!dw) return NRM_OK;
+        if ((st = check_pointers({dw})) != NRM_OK) return st;
+        return launch_dw_fold(nullptr, dw, 0, N, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+    }
+    if (!dy || !residual_out || !rstd || (!dx && !dresidual && !dw)) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, N, es, {lddy, ldro})) != NRM_OK) return st;
+    if (dresidual_out && (st = validate_ld(rows, N, es, {lddro})) != NRM_OK) return st;
+    if (dx && (st = validate_ld(rows, N, es, {lddx})) != NRM_OK) return st;
+    if (dresidual && (st = validate_ld(rows, N, es, {lddr})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({dy, residual_out, w, dresidual_out, dx, dresidual}, es)) != NRM_OK)
+        return st;
+    const size_t need = dropout_add_rms_bwd_workspace_size(rows, N, dtype);
+    if (!need) return NRM_ERR_SHAPE;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return NRM_ERR_WORKSPACE;
+    // in place, each with the same row stride: dx over dy, dresidual over dresidual_out
+    const bool in_dx = dx && dx == dy && lddx == lddy;
+    const bool in_dr = dresidual && dresidual == dresidual_out && lddr == lddro;
+    const RSpan sdy = rspan(in_dx ? nullptr : dy, lddy, rows, N, es),
+                sh = rspan(residual_out, ldro, rows, N, es), srs = rspan(rstd, rows, 1, rows, 4),
+                sw = rspan(w, N, 1, N, es),
+                sup = rspan(in_dr ? nullptr : dresidual_out, lddro, rows, N, es),
+                so = rspan(offset_dev, 1, 1, 1, 8), sdx = rspan(dx, lddx, rows, N, es),
+                sdr = rspan(dresidual, lddr, rows, N, es), sdw = rspan(dw, N, 1, N, 4),
+                sws = rspan(workspace, (int64_t)need, 1, (int64_t)need, 1);
+    if ((st = check_alias({sdx, sdr, sdw, sws}, {sdy, sh, srs, sw, sup, so})) != NRM_OK) return st;
+    if ((st = check_pointers({dy, residual_out, rstd, w, dresidual_out, dx, dresidual, dw, workspace,
+                              offset_dev})) != NRM_OK)
+        return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    size_t part, k;
+    drop_bwd_layout(rows, N, &part, &k);
+    a.part = static_cast<float *>(workspace);
+    a.k = reinterpret_cast<float *>(static_cast<char *>(workspace) + part);
+    const bool vec = rows_vec(N, es, {{dy, lddy}, {residual_out, ldro}, {dresidual_out, lddro}, {dx, lddx},
+                                      {dresidual, lddr}, {w, 0}});
+    Plan plan{};
+    int64_t parts = 0;
+    st = record_plan(launch_drop_bwd(dtype, a, vec, forced_generic(), dev.sms, stream, &plan, &parts), plan);
+    if (st != NRM_OK || !dw) return st;
+    return launch_dw_fold(a.part, dw, parts, N, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+}
+
+int dropout_add_rms_bwd(const void *dy, const void *residual_out, const float *rstd, const void *w,
+                        const void *dresidual_out, void *dx, void *dresidual, float *dw,
+                        int64_t rows, int64_t N, double p, uint64_t seed, uint64_t offset,
+                        const int64_t *offset_dev, int dtype, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+    return dropout_add_rms_bwd_ld(dy, N, residual_out, N, rstd, w, dresidual_out, N, dx, N, dresidual,
+                                  N, dw, rows, N, p, seed, offset, offset_dev, dtype, workspace,
+                                  workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Shared validation of the operators on rows of logits.
+int validate_logits(int64_t rows, int64_t V, float inv_temp, int dtype) {
+    const int st = validate_rows(rows, V, 0.f, dtype);
+    if (st != NRM_OK) return st;
+    if (V > 0x7fffffff) return NRM_ERR_SHAPE;  // a column is a 32-bit index in the kernels
+    if (!(std::isfinite(inv_temp) && inv_temp > 0.f)) return NRM_ERR_VALUE;
+    return NRM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
+                   int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream) {
+    int st = validate_logits(rows, V, inv_temp, dtype);
+    if (st != NRM_OK) return st;
+    if (rows == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!logits || !targets || (!logp && !lse)) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, V, es, {ldl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logp, lse}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({targets}, 8)) != NRM_OK) return st;
+    const RSpan sl = rspan(logits, ldl, rows, V, es), stg = rspan(targets, rows, 1, rows, 8),
+                sp = rspan(logp, rows, 1, rows, 4), ss = rspan(lse, rows, 1, rows, 4);
+    if ((st = check_alias({sp, ss}, {sl, stg})) != NRM_OK) return st;
+    if ((st = check_pointers({logits, targets, logp, lse})) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    LogitArgs a{};
+    a.z = logits;
+    a.ldz = ldl;
+    a.target = targets;
+    a.rows = rows;
+    a.V = V;
+    a.scale = inv_temp;
+    a.logp = logp;
+    a.lse = lse;
+    Plan plan{};
+    return record_plan(launch_logit_rows(dtype, a, false, dev.sms, stream, &plan), plan);
+}
+
+int logprob_fwd(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
+                int64_t V, float inv_temp, int dtype, cudaStream_t stream) {
+    return logprob_fwd_ld(logits, V, targets, logp, lse, rows, V, inv_temp, dtype, stream);
+}
+
+int logprob_bwd_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
+                   const float *lse, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
+                   float inv_temp, int dtype, cudaStream_t stream) {
+    int st = validate_logits(rows, V, inv_temp, dtype);
+    if (st != NRM_OK) return st;
+    if (rows == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!dlogp || !logits || !targets || !lse || !dlogits) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, V, es, {ldl, lddl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits, dlogits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({dlogp, lse}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({targets}, 8)) != NRM_OK) return st;
+    const bool inplace = logits == dlogits && ldl == lddl;
+    const RSpan sl = rspan(inplace ? nullptr : logits, ldl, rows, V, es),
+                stg = rspan(targets, rows, 1, rows, 8), sp = rspan(dlogp, rows, 1, rows, 4),
+                ss = rspan(lse, rows, 1, rows, 4), sd = rspan(dlogits, lddl, rows, V, es);
+    if ((st = check_alias({sd}, {sl, stg, sp, ss})) != NRM_OK) return st;
+    if ((st = check_pointers({dlogp, logits, targets, lse, dlogits})) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    LogitArgs a{};
+    a.z = logits;
+    a.ldz = ldl;
+    a.target = targets;
+    a.rows = rows;
+    a.V = V;
+    a.scale = inv_temp;
+    a.dlogp = dlogp;
+    a.lse_in = lse;
+    a.dz = dlogits;
+    a.lddz = lddl;
+    Plan plan{};
+    plan.kind = PLAN_CTA;
+    plan.threads = 256;
+    return record_plan(launch_logit_grad(dtype, a, stream), plan);
+}
+
+int logprob_bwd(const float *dlogp, const void *logits, const int64_t *targets, const float *lse,
+                void *dlogits, int64_t rows, int64_t V, float inv_temp, int dtype,
+                cudaStream_t stream) {
+    return logprob_bwd_ld(dlogp, logits, V, targets, lse, dlogits, V, rows, V, inv_temp, dtype, stream);
+}
+
+size_t policy_loss_workspace_size(int64_t rows) {
+    if (rows < 0 || rows > INT64_MAX / 8) return 0;
+    return round16(rows > 0 ? (size_t)rows * 4 : 16);
+}
+
+int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, const float *old_logp,
+                   const float *advantages, const float *weights, const float *ref_logp,
+                   double clip_low, double clip_high, float kl_coef, float inv_temp,
+                   const float *grad_scale, float *loss, float *logp, void *dlogits, int64_t lddl,
+                   int64_t rows, int64_t V, int dtype, void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+    int st = validate_logits(rows, V, inv_temp, dtype);
+    if (st != NRM_OK) return st;
+    if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(std::isfinite(clip_high) && clip_high >= 0.0) ||
+        !(std::isfinite(kl_coef) && kl_coef >= 0.f))
+        return NRM_ERR_VALUE;
+    if (!loss) return NRM_ERR_NULL;
+    if ((st = check_elem_alignment({old_logp, advantages, weights, ref_logp, grad_scale, loss, logp}, 4)) != NRM_OK)
+        return st;
+    if (rows == 0) {  // no rows: the loss is an empty sum
+        if ((st = check_pointers({loss})) != NRM_OK) return st;
+        return launch_loss_fold(nullptr, loss, 0, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+    }
+    if (!logits || !targets || !old_logp || !advantages || (kl_coef > 0.f && !ref_logp)) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, V, es, {ldl})) != NRM_OK) return st;
+    if (dlogits && (st = validate_ld(rows, V, es, {lddl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits, dlogits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({targets}, 8)) != NRM_OK) return st;
+    const size_t need = policy_loss_workspace_size(rows);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return NRM_ERR_WORKSPACE;
+    const bool inplace = dlogits && logits == dlogits && ldl == lddl;
+    const RSpan sl = rspan(inplace ? nullptr : logits, ldl, rows, V, es),
+                stg = rspan(targets, rows, 1, rows, 8), so = rspan(old_logp, rows, 1, rows, 4),
+                sa = rspan(advantages, rows, 1, rows, 4), sw = rspan(weights, rows, 1, rows, 4),
+                sr = rspan(ref_logp, rows, 1, rows, 4), sg = rspan(grad_scale, 1, 1, 1, 4),
+                sd = rspan(dlogits, lddl, rows, V, es), slo = rspan(loss, 1, 1, 1, 4),
+                sp = rspan(logp, rows, 1, rows, 4), sws = rspan(workspace, (int64_t)need, 1, (int64_t)need, 1);
+    if ((st = check_alias({sd, slo, sp, sws}, {sl, stg, so, sa, sw, sr, sg})) != NRM_OK) return st;
+    if ((st = check_pointers({logits, targets, old_logp, advantages, weights, ref_logp, grad_scale, loss,
+                              logp, dlogits, workspace})) != NRM_OK)
+        return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    LogitArgs a{};
+    a.z = logits;
+    a.ldz = ldl;
+    a.target = targets;
+    a.rows = rows;
+    a.V = V;
+    a.scale = inv_temp;
+    a.logp = logp;
+    a.old = old_logp;
+    a.adv = advantages;
+    a.weight = weights;
+    a.ref = kl_coef > 0.f ? ref_logp : nullptr;  // without the term its infinities do not count
+    a.kl = kl_coef;
+    a.ratio_lo = (float)(1.0 - clip_low);
+    a.ratio_hi = (float)(1.0 + clip_high);
+    a.log_lo = std::log1p(-clip_low);
+    a.log_hi = std::log1p(clip_high);
+    a.grad_scale = grad_scale;
+    a.row_loss = static_cast<float *>(workspace);
+    a.dz = dlogits;
+    a.lddz = lddl;
+    Plan plan{};
+    st = record_plan(launch_logit_rows(dtype, a, true, dev.sms, stream, &plan), plan);
+    if (st != NRM_OK) return st;
+    return launch_loss_fold(a.row_loss, loss, rows, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+}
+
+int policy_loss(const void *logits, const int64_t *targets, const float *old_logp,
+                const float *advantages, const float *weights, const float *ref_logp,
+                double clip_low, double clip_high, float kl_coef, float inv_temp,
+                const float *grad_scale, float *loss, float *logp, void *dlogits, int64_t rows,
+                int64_t V, int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    return policy_loss_ld(logits, V, targets, old_logp, advantages, weights, ref_logp, clip_low,
+                          clip_high, kl_coef, inv_temp, grad_scale, loss, logp, dlogits, V, rows, V,
+                          dtype, workspace, workspace_bytes, stream);
+}
+
 const char *nrm_status_string(int status) {
     switch (status) {
     case NRM_OK: return "ok";

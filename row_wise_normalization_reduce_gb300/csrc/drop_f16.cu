@@ -1,0 +1,18 @@
+// drop_f16.cu -- the dropout kernels for binary16 data.
+#include "drop.cuh"
+
+namespace nrm {
+
+cudaError_t launch_dropout_f16(const DropoutArgs &a, bool vec, int sms, cudaStream_t s) {
+    return launch_dropout_t<__half>(a, vec, sms, s);
+}
+cudaError_t launch_drop_fwd_f16(const DropRmsArgs &a, bool vec, bool longrow, int sms, cudaStream_t s,
+                                Plan *p) {
+    return launch_drop_fwd_t<__half>(a, vec, longrow, sms, s, p);
+}
+cudaError_t launch_drop_bwd_f16(const DropRmsBwdArgs &a, bool vec, bool longrow, int sms, cudaStream_t s,
+                                Plan *p, int64_t *parts) {
+    return launch_drop_bwd_t<__half>(a, vec, longrow, sms, s, p, parts);
+}
+
+}  // namespace nrm

@@ -1,0 +1,13 @@
+// logits_bf16.cu -- the kernels over rows of logits for bfloat16 data.
+#include "logits.cuh"
+
+namespace nrm {
+
+cudaError_t launch_logit_rows_bf16(const LogitArgs &a, bool policy, int sms, cudaStream_t s, Plan *p) {
+    return policy ? launch_logit_rows_t<__nv_bfloat16, true>(a, sms, s, p) : launch_logit_rows_t<__nv_bfloat16, false>(a, sms, s, p);
+}
+cudaError_t launch_logit_grad_bf16(const LogitArgs &a, cudaStream_t s) {
+    return launch_logit_grad_t<__nv_bfloat16>(a, s);
+}
+
+}  // namespace nrm

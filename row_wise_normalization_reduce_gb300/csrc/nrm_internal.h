@@ -257,4 +257,96 @@ cudaError_t launch_bn_apply_stats(const BnSyncArgs &a, int dtype, int num_sms, c
 cudaError_t launch_bn_cluster_stats(const BnArgs &a, int dtype, cudaStream_t s, bool *launched);
 cudaError_t launch_bn_apply_sums(const BnSyncArgs &a, int dtype, int num_sms, cudaStream_t s);
 
+// Dropout (drop.cuh): the generator's round keys and this call's counter, the
+// bar an element's 16-bit number (shifted to the top half of a word) has to
+// exceed to be kept, and the scale of what is kept.  on == 0: p rounds to 0,
+// the generator does not run.
+struct DropArgs {
+    uint32_t key[20];
+    uint64_t offset;
+    const int64_t *offset_dev;  // added to offset when the kernel runs, or NULL
+    uint32_t bar;
+    float scale;
+    int on;
+};
+struct DropoutArgs {
+    DropArgs d;
+    const void *x;
+    void *y;
+    int64_t rows, N, ldx, ldy;
+};
+struct DropRmsArgs {
+    DropArgs d;
+    const void *x, *res, *w;
+    void *h, *y;            // h: residual_out
+    float *rstd;
+    int64_t rows, N, ldx, ldr, ldh, ldy;
+    float eps, invN;
+};
+struct DropRmsBwdArgs {
+    DropArgs d;
+    const void *dy, *h, *up, *w;  // up: gradient of residual_out, or NULL
+    const float *rstd;
+    void *dx, *dres;        // either may be NULL
+    float *dw;              // NULL: no weight gradient
+    float *part;            // [parts][N] partial sums of dw
+    float *k;               // [rows], the long-row plan's row factors
+    int64_t rows, N, lddy, ldh, ldu, lddx, lddr;
+    float invN;
+};
+// Most row partials of dw a backward leaves (its grid is at most this), so
+// that the workspace size does not depend on the device: four CTAs for each
+// of 152 SMs.
+constexpr int64_t kDropMaxParts = 608;
+
+#define NRM_BY_TYPE(name, params, args)                       \
+    cudaError_t name##_f32 params;                            \
+    cudaError_t name##_f16 params;                            \
+    cudaError_t name##_bf16 params;                           \
+    inline cudaError_t name(int dtype, NRM_UNPAREN params) {  \
+        switch (dtype) {                                      \
+        case DT_F32: return name##_f32 args;                  \
+        case DT_F16: return name##_f16 args;                  \
+        case DT_BF16: return name##_bf16 args;                \
+        default: return cudaErrorInvalidValue;                \
+        }                                                     \
+    }
+#define NRM_UNPAREN(...) __VA_ARGS__
+// vec: rows of whole 16-byte packs on 16-byte boundaries; longrow: the plan
+// for rows that outgrow the registers (any length).  *p is what ran; *parts
+// the rows of dw partials left in a.part.
+NRM_BY_TYPE(launch_dropout, (const DropoutArgs &a, bool vec, int sms, cudaStream_t s), (a, vec, sms, s))
+NRM_BY_TYPE(launch_drop_fwd, (const DropRmsArgs &a, bool vec, bool longrow, int sms, cudaStream_t s, Plan *p),
+            (a, vec, longrow, sms, s, p))
+NRM_BY_TYPE(launch_drop_bwd,
+            (const DropRmsBwdArgs &a, bool vec, bool longrow, int sms, cudaStream_t s, Plan *p, int64_t *parts),
+            (a, vec, longrow, sms, s, p, parts))
+
+// Rows of logits (logits.cuh).  scale: the inverse temperature.
+struct LogitArgs {
+    const void *z;
+    int64_t ldz;
+    const int64_t *target;
+    int64_t rows, V;
+    float scale;
+    float *logp, *lse;          // outputs, either may be NULL
+    // policy loss
+    const float *old, *adv, *weight, *ref;  // weight, ref may be NULL
+    float kl, ratio_lo, ratio_hi;
+    double log_lo, log_hi;      // logarithms of the ratio's bounds
+    const float *grad_scale;    // [1], or NULL (= 1)
+    float *row_loss;            // [rows] workspace
+    void *dz;                   // NULL: no gradient
+    int64_t lddz;
+    // gradient of a given slope
+    const float *dlogp, *lse_in;
+};
+NRM_BY_TYPE(launch_logit_rows, (const LogitArgs &a, bool policy, int sms, cudaStream_t s, Plan *p),
+            (a, policy, sms, s, p))
+NRM_BY_TYPE(launch_logit_grad, (const LogitArgs &a, cudaStream_t s), (a, s))
+cudaError_t launch_loss_fold(const float *row_loss, float *loss, int64_t rows, cudaStream_t s);
+#undef NRM_UNPAREN
+#undef NRM_BY_TYPE
+cudaError_t launch_dw_fold(const float *part, float *dw, int64_t parts, int64_t N, cudaStream_t s);
+
 }  // namespace nrm
