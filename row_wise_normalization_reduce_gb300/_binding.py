@@ -7,7 +7,6 @@ library is missing the first call raises; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -540,38 +539,41 @@ def bn_bwd_apply_sums(dy, x, save_mean, save_rstd, parts, count, gamma=None, *, 
 # ---------------------------------------------------------------------------
 # Training operators.
 # ---------------------------------------------------------------------------
-def _on_stream(f):
-    """Keyword `stream` (a raw stream handle or a torch stream): everything the
-    call allocates and launches belongs to that stream."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        t = args[0] if args else next(v for v in kw.values() if isinstance(v, torch.Tensor))
-        if not t.is_cuda:
-            raise ValueError(f"{f.__name__}: the tensors must be CUDA tensors")
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+def _on_stream(stream, t):
+    """Context in which everything that a call allocates and launches belongs
+    to `stream` (a raw stream handle or a torch stream)."""
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    return torch.cuda.stream(stream)
+
+
+# The current stream's handle as an integer, without building a Stream object
+# (3 us a call on a Grace core).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+_fns = {}
 
 
 def _launch(name, device, *args):
     """One C call on `device`'s current stream."""
-    f = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream().cuda_stream)
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = f(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(device):
-            st = f(*args, torch.cuda.current_stream().cuda_stream)
-    _check(st, name)
+        with torch.cuda.device(i):
+            st = f(*args, _raw_stream(i))
+    if st != 0:
+        raise NrmError(st, name)
 
 
 def _like(t, x, name):
     """`t`, or a new contiguous tensor like x; and its row stride."""
     if t is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[-1]
+        return torch.empty_like(x, memory_format=torch.contiguous_format), x.shape[-1]
     return t, _same_rows(t, x, name)
 
 
@@ -580,6 +582,10 @@ def _row_values(t, x, name, dtype=torch.float32):
     if t.dtype != dtype or t.device != x.device or t.shape != x.shape[:-1] or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(x.shape[:-1])} {dtype} tensor on {x.device}")
     return t
+
+
+def _new_row_values(like):
+    return torch.empty_like(like, dtype=torch.float32)
 
 
 def _one_value(t, x, name, dtype):
@@ -603,13 +609,15 @@ def _drop(x, p, seed, offset, offset_dev):
             _ptr(_one_value(offset_dev, x, "offset_dev", torch.int64)))
 
 
-@_on_stream
-def dropout_fwd(x, p, seed, offset=0, *, out=None, offset_dev=None):
+def dropout_fwd(x, p, seed, offset=0, *, out=None, offset_dev=None, stream=None):
     """Dropout over x as rows of its last dimension: y = x / (1 - p) where the
     mask of (seed, offset, row, column) keeps the element, +0 elsewhere; p is
     rounded to a multiple of 2^-16.  seed and offset are integers (modulo
     2^64); offset_dev, an int64 tensor of one element, is added to offset when
     the kernel runs.  out may be x.  Returns y."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return dropout_fwd(x, p, seed, offset, out=out, offset_dev=offset_dev)
     rows, n, ldx = _rows(x, "x")
     y, ldy = _like(out, x, "out")
     _launch("dropout_fwd_ld", x.device, x.data_ptr(), ldx, y.data_ptr(), ldy, rows, n,
@@ -617,20 +625,23 @@ def dropout_fwd(x, p, seed, offset=0, *, out=None, offset_dev=None):
     return y
 
 
-@_on_stream
-def dropout_bwd(dy, p, seed, offset=0, *, out=None, offset_dev=None):
+def dropout_bwd(dy, p, seed, offset=0, *, out=None, offset_dev=None, stream=None):
     """Gradient of dropout_fwd: the same places of dy dropped, the rest scaled.
     Returns dx."""
-    return dropout_fwd(dy, p, seed, offset, out=out, offset_dev=offset_dev)
+    return dropout_fwd(dy, p, seed, offset, out=out, offset_dev=offset_dev, stream=stream)
 
 
-@_on_stream
 def dropout_add_rms_fwd(x, residual, w=None, p=0.0, seed=0, offset=0, eps=1e-6, *,
-                        residual_out=None, out=None, rstd=None, offset_dev=None):
+                        residual_out=None, out=None, rstd=None, offset_dev=None, stream=None):
     """residual_out = residual + dropout(x) (rounded to x.dtype); y =
     RMSNorm(residual_out, w).  Returns (residual_out, y, rstd); the backward
     takes residual_out and rstd.  Pass residual_out=residual to update the
     residual stream in place."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return dropout_add_rms_fwd(x, residual, w, p, seed, offset, eps,
+                                       residual_out=residual_out, out=out, rstd=rstd,
+                                       offset_dev=offset_dev)
     rows, n, ldx = _rows(x, "x")
     ldr = _same_rows(residual, x, "residual")
     w = _param(w, n, x.dtype, x.device, "w")
@@ -650,16 +661,21 @@ def dropout_add_rms_bwd_workspace_size(rows, n, dtype) -> int:
     return lib().dropout_add_rms_bwd_workspace_size(rows, n, _DT[dtype])
 
 
-@_on_stream
 def dropout_add_rms_bwd(dy, residual_out, rstd, w=None, p=0.0, seed=0, offset=0, *,
                         dresidual_out=None, dx=None, dresidual=None, dw=None, want_dw=None,
-                        workspace=None, offset_dev=None):
+                        workspace=None, offset_dev=None, stream=None):
     """Backward of dropout_add_rms_fwd (with p = 0 of add_rms_fwd and, with
     residual_out = x, of rms_fwd) from dy, the gradient of y, and optionally
     dresidual_out, the gradient of residual_out.  Returns (dx, dresidual, dw):
     dw is binary32, computed when w is given (or want_dw=True), else None.
     Without dropout (p = 0) and without a dx to write to, dx is dresidual, the
     same tensor.  dx=dy and dresidual=dresidual_out work in place."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return dropout_add_rms_bwd(dy, residual_out, rstd, w, p, seed, offset,
+                                       dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
+                                       dw=dw, want_dw=want_dw, workspace=workspace,
+                                       offset_dev=offset_dev)
     rows, n, lddy = _rows(dy, "dy")
     ldh = _same_rows(residual_out, dy, "residual_out")
     _row_values(rstd, dy, "rstd")
@@ -684,26 +700,30 @@ def dropout_add_rms_bwd(dy, residual_out, rstd, w=None, p=0.0, seed=0, offset=0,
     return (dresidual if same else dx), dresidual, dw
 
 
-@_on_stream
-def logprob_fwd(logits, targets, inv_temp=1.0, *, logp=None, lse=None):
+def logprob_fwd(logits, targets, inv_temp=1.0, *, logp=None, lse=None, stream=None):
     """Log-softmax of inv_temp * logits at one target (int64) per row of the
     last dimension.  Returns (logp, lse), binary32, one value per row; rows
     with a target outside [0, V) give 0 and are not read."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return logprob_fwd(logits, targets, inv_temp, logp=logp, lse=lse)
     rows, v, ldl = _rows(logits, "logits")
     _row_values(targets, logits, "targets", torch.int64)
-    shape, dev = targets.shape, logits.device
-    logp = torch.empty(shape, dtype=torch.float32, device=dev) if logp is None else _row_values(logp, logits, "logp")
-    lse = torch.empty(shape, dtype=torch.float32, device=dev) if lse is None else _row_values(lse, logits, "lse")
+    dev = logits.device
+    logp = _new_row_values(targets) if logp is None else _row_values(logp, logits, "logp")
+    lse = _new_row_values(targets) if lse is None else _row_values(lse, logits, "lse")
     _launch("logprob_fwd_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(),
             lse.data_ptr(), rows, v, inv_temp, _dtype_code(logits))
     return logp, lse
 
 
-@_on_stream
-def logprob_bwd(dlogp, logits, targets, lse, inv_temp=1.0, *, out=None):
+def logprob_bwd(dlogp, logits, targets, lse, inv_temp=1.0, *, out=None, stream=None):
     """Gradient of the logits from dlogp, the gradient of logprob_fwd's logp
     (one binary32 value per row), and its lse.  out may be logits.  Returns
     dlogits."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return logprob_bwd(dlogp, logits, targets, lse, inv_temp, out=out)
     rows, v, ldl = _rows(logits, "logits")
     _row_values(dlogp, logits, "dlogp")
     _row_values(targets, logits, "targets", torch.int64)
@@ -719,10 +739,9 @@ def policy_loss_workspace_size(rows) -> int:
     return lib().policy_loss_workspace_size(rows)
 
 
-@_on_stream
 def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=None, clip_low=0.2,
                 clip_high=0.2, kl_coef=0.0, inv_temp=1.0, *, grad_scale=None, want_grad=True,
-                out=None, logp=None, workspace=None):
+                out=None, logp=None, workspace=None, stream=None):
     """Clipped policy loss with a KL term over token rows, and the gradient of
     the logits in the same pass.  Per row with a target in [0, V) and a weight
     other than 0, ratio = exp(logp - old_logp):
@@ -732,6 +751,11 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
     multiplies the gradient.  out, the gradient's tensor, may be logits;
     want_grad=False computes the loss only.  Returns (loss, logp, dlogits or
     None)."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return policy_loss(logits, targets, old_logp, advantages, weights, ref_logp, clip_low,
+                               clip_high, kl_coef, inv_temp, grad_scale=grad_scale,
+                               want_grad=want_grad, out=out, logp=logp, workspace=workspace)
     rows, v, ldl = _rows(logits, "logits")
     _row_values(targets, logits, "targets", torch.int64)
     _row_values(old_logp, logits, "old_logp")
@@ -742,7 +766,7 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
         _row_values(ref_logp, logits, "ref_logp")
     _one_value(grad_scale, logits, "grad_scale", torch.float32)
     dev, lddl = logits.device, v
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=dev) if logp is None else _row_values(logp, logits, "logp")
+    logp = _new_row_values(targets) if logp is None else _row_values(logp, logits, "logp")
     loss = torch.empty((), dtype=torch.float32, device=dev)
     if want_grad or out is not None:
         out, lddl = _like(out, logits, "out")

@@ -1033,18 +1033,22 @@ int drop_args(int64_t rows, int64_t N, double p, uint64_t seed, uint64_t offset,
     return NRM_OK;
 }
 
-// Whether every row of every tensor is a run of whole 16-byte packs on a
-// 16-byte boundary.
+// How the rows of a call's tensors lie in memory (Map); `w`, a vector of
+// parameters, counts for whole packs only.
 struct RowPtr {
     const void *p;
     int64_t ld;
 };
-bool rows_vec(int64_t N, size_t es, std::initializer_list<RowPtr> ts) {
-    const int64_t V = 16 / (int64_t)es;
-    if (N % V) return false;
-    for (const RowPtr &t : ts)
-        if (t.p && (!aligned(t.p, 16) || t.ld % V)) return false;
-    return true;
+int rows_map(int64_t N, size_t es, std::initializer_list<RowPtr> ts, const void *w = nullptr) {
+    bool whole = N % (16 / (int64_t)es) == 0 && aligned(w, 16), same = true;
+    const RowPtr &t0 = *ts.begin();
+    for (const RowPtr &t : ts) {
+        if (!t.p) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(t.p), step = (uintptr_t)t.ld * es;
+        whole = whole && at % 16 == 0 && step % 16 == 0;
+        same = same && at % 16 == reinterpret_cast<uintptr_t>(t0.p) % 16 && step % 16 == (uintptr_t)t0.ld * es % 16;
+    }
+    return whole ? MAP_V : same ? MAP_A : MAP_S;
 }
 
 int record_plan(cudaError_t e, const Plan &p) {
@@ -1093,7 +1097,7 @@ int dropout_fwd_ld(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t row
     Plan plan{};
     plan.kind = PLAN_WARP;
     plan.threads = 256;
-    return record_plan(launch_dropout(dtype, a, rows_vec(N, es, {{x, ldx}, {y, ldy}}), dev.sms, stream), plan);
+    return record_plan(launch_dropout(dtype, a, rows_map(N, es, {{x, ldx}, {y, ldy}}), dev.sms, stream), plan);
 }
 
 int dropout_fwd(const void *x, void *y, int64_t rows, int64_t N, double p, uint64_t seed,
@@ -1128,9 +1132,9 @@ int dropout_add_rms_fwd_ld(const void *x, int64_t ldx, const void *residual, int
     if ((st = check_pointers({x, residual, w, residual_out, y, rstd, offset_dev})) != NRM_OK) return st;
     DevInfo dev;
     if ((st = device_info(&dev)) != NRM_OK) return st;
-    const bool vec = rows_vec(N, es, {{x, ldx}, {residual, ldr}, {residual_out, ldro}, {y, ldy}, {w, 0}});
+    const int map = rows_map(N, es, {{x, ldx}, {residual, ldr}, {residual_out, ldro}, {y, ldy}}, w);
     Plan plan{};
-    return record_plan(launch_drop_fwd(dtype, a, vec, forced_generic(), dev.sms, stream, &plan), plan);
+    return record_plan(launch_drop_fwd(dtype, a, map, forced_generic(), dev.sms, stream, &plan), plan);
 }
 
 int dropout_add_rms_fwd(const void *x, const void *residual, const void *w, void *residual_out,
@@ -1197,11 +1201,11 @@ int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_ou
     drop_bwd_layout(rows, N, &part, &k);
     a.part = static_cast<float *>(workspace);
     a.k = reinterpret_cast<float *>(static_cast<char *>(workspace) + part);
-    const bool vec = rows_vec(N, es, {{dy, lddy}, {residual_out, ldro}, {dresidual_out, lddro}, {dx, lddx},
-                                      {dresidual, lddr}, {w, 0}});
+    const int map = rows_map(N, es, {{dy, lddy}, {residual_out, ldro}, {dresidual_out, lddro}, {dx, lddx},
+                                     {dresidual, lddr}}, w);
     Plan plan{};
     int64_t parts = 0;
-    st = record_plan(launch_drop_bwd(dtype, a, vec, forced_generic(), dev.sms, stream, &plan, &parts), plan);
+    st = record_plan(launch_drop_bwd(dtype, a, map, forced_generic(), dev.sms, stream, &plan, &parts), plan);
     if (st != NRM_OK || !dw) return st;
     return launch_dw_fold(a.part, dw, parts, N, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
 }
@@ -1259,8 +1263,10 @@ int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, floa
     a.scale = inv_temp;
     a.logp = logp;
     a.lse = lse;
+    a.fault = fault_word();
+    a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     Plan plan{};
-    return record_plan(launch_logit_rows(dtype, a, false, dev.sms, stream, &plan), plan);
+    return record_plan(launch_logit_rows(dtype, a, false, forced_generic(), dev.sms, stream, &plan), plan);
 }
 
 int logprob_fwd(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
@@ -1370,14 +1376,16 @@ int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, cons
     a.kl = kl_coef;
     a.ratio_lo = (float)(1.0 - clip_low);
     a.ratio_hi = (float)(1.0 + clip_high);
-    a.log_lo = std::log1p(-clip_low);
-    a.log_hi = std::log1p(clip_high);
+    a.log_lo = (float)std::log1p(-clip_low);
+    a.log_hi = (float)std::log1p(clip_high);
     a.grad_scale = grad_scale;
     a.row_loss = static_cast<float *>(workspace);
     a.dz = dlogits;
     a.lddz = lddl;
+    a.fault = fault_word();
+    a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     Plan plan{};
-    st = record_plan(launch_logit_rows(dtype, a, true, dev.sms, stream, &plan), plan);
+    st = record_plan(launch_logit_rows(dtype, a, true, forced_generic(), dev.sms, stream, &plan), plan);
     if (st != NRM_OK) return st;
     return launch_loss_fold(a.row_loss, loss, rows, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
 }

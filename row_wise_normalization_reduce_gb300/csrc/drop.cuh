@@ -21,13 +21,23 @@
 // Work is cut into chunks of 256 columns, one warp each; lane l always
 // computes generator block l of the chunk (columns 8 l .. 8 l + 7) and holds 8
 // of the chunk's elements, placed so that its global accesses coalesce:
-//   MAP_V8  16-bit types, 16-byte aligned rows: columns 8 l + j, one 16-byte access
-//   MAP_V4  binary32, 16-byte aligned rows: columns 4 l + j and 128 + 4 l + j
-//   MAP_S   any N and alignment: columns 32 j + l, eight scalar accesses
-// For the last two the keep bits of a chunk travel by warp shuffles.
+//   MAP_V  rows of whole 16-byte packs on 16-byte boundaries: one 16-byte
+//          access (16-bit types: columns 8 l + j) or two (binary32: columns
+//          4 l + j and 128 + 4 l + j)
+//   MAP_A  any N, rows at any element alignment that all tensors share (odd N,
+//          contiguous): the same accesses on the 16-byte grid, so a lane's
+//          columns are those of MAP_V minus the row's `shift` (its start
+//          behind the grid, in elements).  A pack that a row's end cuts is
+//          read whole where it lies between the tensor's first and last
+//          element (its other half is the neighbouring row's) and trimmed,
+//          and written element by element.  A lane's columns straddle two
+//          generator blocks: its own and its lower neighbour's, by shuffle.
+//   MAP_S  tensors that differ in alignment: columns 32 j + l, eight scalar
+//          accesses, the keep bits gathered by shuffles
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "nrm_device.cuh"
 #include "nrm_internal.h"
@@ -35,9 +45,8 @@
 
 namespace nrm {
 
-enum Map { MAP_V8 = 0, MAP_V4 = 1, MAP_S = 2 };
-template <typename T> constexpr int vec_map() { return sizeof(T) == 2 ? MAP_V8 : MAP_V4; }
 constexpr int kChunk = 256;
+constexpr int kRowWarps = 4;  // rows (warps) per CTA of the warp plans
 
 // The offset words of this call: the host's plus the device counter's value.
 struct DropCtr {
@@ -49,66 +58,108 @@ __device__ __forceinline__ DropCtr drop_ctr(const DropArgs &d) {
     return DropCtr{(uint32_t)o, (uint32_t)(o >> 32)};
 }
 
-// One generator block.
-__device__ __forceinline__ uint4 drop_block(const DropArgs &d, const DropCtr &o, uint32_t block,
-                                            uint32_t row) {
-    uint32_t a = block, b = row, c = o.lo, e = o.hi;
+// What the generator's first two rounds make of the call's and the row's
+// words alone (2 of its 20 products).
+struct DropRow {
+    uint32_t x1, x2, x3, e2;
+};
+__device__ __forceinline__ DropRow drop_row(const DropArgs &d, const DropCtr &o, int64_t row) {
+    const uint64_t q1 = (uint64_t)o.lo * 0xCD9E8D57u;
+    const uint64_t p2 = (uint64_t)((uint32_t)(q1 >> 32) ^ (uint32_t)row ^ d.key[0]) * 0xD2511F53u;
+    return DropRow{o.hi ^ d.key[1], (uint32_t)q1 ^ d.key[2], (uint32_t)(p2 >> 32) ^ d.key[3], (uint32_t)p2};
+}
+
+// One generator block of a row.
+__device__ __forceinline__ uint4 drop_block(const DropArgs &d, const DropRow &r, uint32_t block) {
+    const uint64_t p1 = (uint64_t)block * 0xD2511F53u;
+    const uint64_t q2 = (uint64_t)((uint32_t)(p1 >> 32) ^ r.x1) * 0xCD9E8D57u;
+    uint32_t a = (uint32_t)(q2 >> 32) ^ r.x2, b = (uint32_t)q2, c = r.x3 ^ (uint32_t)p1, e = r.e2;
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
+    for (int i = 2; i < 10; ++i) {
         const uint64_t p = (uint64_t)a * 0xD2511F53u, q = (uint64_t)c * 0xCD9E8D57u;
-        a = (uint32_t)(q >> 32) ^ b ^ d.key[2 * r];
+        a = (uint32_t)(q >> 32) ^ b ^ d.key[2 * i];
         b = (uint32_t)q;
-        c = (uint32_t)(p >> 32) ^ e ^ d.key[2 * r + 1];
+        c = (uint32_t)(p >> 32) ^ e ^ d.key[2 * i + 1];
         e = (uint32_t)p;
     }
     return make_uint4(a, b, c, e);
 }
 
-// Which of a lane's 8 elements are kept.  MAP_V8 keeps the block's words (the
-// lane's elements are its own block); the others hold 8 bits gathered from
-// the lanes that computed them.
-template <int MAP> struct Keep {
-    uint32_t bits;
-    __device__ __forceinline__ bool operator()(int j, uint32_t) const { return (bits >> j) & 1u; }
-};
-template <> struct Keep<MAP_V8> {
-    uint32_t w[4];
+// Which of a lane's 8 elements are kept: the words of its own block (16-bit
+// types, MAP_V), or 8 bits gathered from the lanes that computed them.
+template <typename T, int MAP> struct Keep {
+    static constexpr bool WORDS = MAP == MAP_V && sizeof(T) == 2;
+    uint32_t w[WORDS ? 4 : 1];
     __device__ __forceinline__ bool operator()(int j, uint32_t bar) const {
-        return (j & 1 ? w[j >> 1] : w[j >> 1] << 16) > bar;
+        if constexpr (WORDS)
+            return (j & 1 ? w[j >> 1] : w[j >> 1] << 16) > bar;
+        else
+            return (w[0] >> j) & 1u;
     }
 };
 
-// The keep set of chunk `chunk` of `row` (the whole warp calls it).
-template <int MAP>
-__device__ __forceinline__ Keep<MAP> drop_keep(const DropArgs &d, const DropCtr &o, int64_t chunk,
-                                               int64_t row) {
-    const int lane = threadIdx.x & 31;
-    const uint4 w = drop_block(d, o, (uint32_t)(chunk * 32) + lane, (uint32_t)row);
-    Keep<MAP> k;
-    if constexpr (MAP == MAP_V8) {
-        k.w[0] = w.x; k.w[1] = w.y; k.w[2] = w.z; k.w[3] = w.w;
-    } else {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-        uint32_t mine = 0;
+__device__ __forceinline__ uint32_t keep_byte(const uint4 &w, uint32_t bar) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            mine |= (uint32_t)((j & 1 ? v[j >> 1] : v[j >> 1] << 16) > d.bar) << j;
-        if constexpr (MAP == MAP_V4) {
-            // pack p of the chunk is half (p & 1) of block p / 2
-            const int sh = (lane & 1) * 4;
-            const uint32_t lo = __shfl_sync(0xffffffffu, mine, lane >> 1) >> sh;
-            const uint32_t hi = __shfl_sync(0xffffffffu, mine, 16 + (lane >> 1)) >> sh;
-            k.bits = (lo & 15u) | (hi & 15u) << 4;
+    for (int j = 0; j < 8; ++j) m |= (uint32_t)((j & 1 ? v[j >> 1] : v[j >> 1] << 16) > bar) << j;
+    return m;
+}
+
+// The keep sets of one row's neighbouring chunks, in order from `chunk` (the
+// whole warp calls).
+template <typename T, int MAP> struct Masks {
+    const DropArgs &d;
+    DropRow r;
+    uint32_t block;  // this lane's next block
+    uint32_t prev;   // MAP_A: the byte of the block before the warp's next chunk
+    int shift;
+
+    __device__ __forceinline__ Masks(const DropArgs &d_, const DropCtr &o, int64_t row, int64_t chunk, int shift_)
+        : d(d_), r(drop_row(d_, o, row)), block((uint32_t)(chunk * 32) + (threadIdx.x & 31)), prev(0), shift(shift_) {
+        // columns before the row's first are nobody's: chunk 0 needs none
+        if (MAP == MAP_A && shift && chunk > 0)
+            prev = keep_byte(drop_block(d, r, (uint32_t)(chunk * 32) - 1), d.bar);
+    }
+    __device__ __forceinline__ Keep<T, MAP> next() {
+        const int lane = threadIdx.x & 31;
+        const uint4 w = drop_block(d, r, block);
+        block += 32;
+        Keep<T, MAP> k;
+        if constexpr (Keep<T, MAP>::WORDS) {
+            k.w[0] = w.x; k.w[1] = w.y; k.w[2] = w.z; k.w[3] = w.w;
+            return k;
         } else {
-            uint32_t b = 0;
+            const uint32_t mine = keep_byte(w, d.bar);
+            if constexpr (MAP == MAP_S) {
+                uint32_t b = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                b |= (__shfl_sync(0xffffffffu, mine, 4 * j + (lane >> 3)) >> (lane & 7) & 1u) << j;
-            k.bits = b;
+                for (int j = 0; j < 8; ++j)
+                    b |= (__shfl_sync(0xffffffffu, mine, 4 * j + (lane >> 3)) >> (lane & 7) & 1u) << j;
+                k.w[0] = b;
+            } else {
+                // columns 8 l - 8 .. 8 l + 7, then the window at -shift
+                uint32_t two = mine << 8;
+                if (MAP == MAP_A) {
+                    const uint32_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+                    two |= lane ? up : prev;
+                    prev = __shfl_sync(0xffffffffu, mine, 31);
+                }
+                const int sh = 8 - (MAP == MAP_A ? shift : 0);
+                if constexpr (sizeof(T) == 2) {
+                    k.w[0] = two >> sh;
+                } else {
+                    // pack p of the chunk starts at half (p & 1) of block p / 2
+                    const int at = sh + (lane & 1) * 4;
+                    const uint32_t lo = __shfl_sync(0xffffffffu, two, lane >> 1) >> at;
+                    const uint32_t hi = __shfl_sync(0xffffffffu, two, 16 + (lane >> 1)) >> at;
+                    k.w[0] = (lo & 15u) | (hi & 15u) << 4;
+                }
+            }
+            return k;
         }
     }
-    return k;
-}
+};
 
 // A lane's 8 elements of one chunk, in the storage type.
 template <typename T> struct Frag {
@@ -125,65 +176,189 @@ __device__ __forceinline__ uint4 ld_once(const void *p) {
     return r;
 }
 
-// Column of element j of this lane in a chunk.
-template <int MAP> __device__ __forceinline__ int frag_col(int j) {
+// Place of element j of this lane in a chunk (its column, plus the shift for
+// MAP_A).
+template <typename T, int MAP> __device__ __forceinline__ int frag_col(int j) {
     const int lane = threadIdx.x & 31;
-    return MAP == MAP_V8 ? 8 * lane + j : MAP == MAP_V4 ? 4 * lane + (j & 3) + 32 * (j & 4) : 32 * j + lane;
+    return MAP == MAP_S ? 32 * j + lane : sizeof(T) == 2 ? 8 * lane + j : 4 * lane + (j & 3) + 32 * (j & 4);
 }
 
-// p: the chunk's first element; left: columns from there to the row's end
-// (any value; lanes past it hold zeros and store nothing).
-template <typename T, int MAP, bool KEEP_CACHED = false>
-__device__ __forceinline__ void frag_load(Frag<T> &f, const T *p, int64_t left) {
+// A row's place on the 16-byte grid: elements from the grid to its start.
+template <typename T, int MAP> __device__ __forceinline__ int row_shift(const void *row) {
+    return MAP == MAP_A ? (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)) : 0;
+}
+
+// What of a chunk belongs to the row: places head (inclusive) to left
+// (exclusive; may be <= 0 or beyond the chunk).
+struct Part {
+    int head, left;
+};
+// chunk ch of a row of n elements.
+__device__ __forceinline__ Part chunk_part(int64_t ch, int64_t n, int shift) {
+    const int64_t left = n + shift - ch * kChunk;
+    return Part{ch == 0 ? shift : 0, left < kChunk ? (int)left : kChunk};
+}
+
+// Element e (0 .. sizeof-wise V - 1) of a pack as its bits.
+template <typename T> using Bits = typename std::conditional<sizeof(T) == 2, unsigned short, uint32_t>::type;
+
+template <typename T> constexpr int kPacks = sizeof(T) / 2;  // 16-byte packs of a fragment (MAP_V, MAP_A)
+
+// Place of a fragment's pack h in its chunk.
+template <typename T> __device__ __forceinline__ int pack_at(int h) {
     const int lane = threadIdx.x & 31;
-    if constexpr (MAP == MAP_V8) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (8 * lane < left) v = KEEP_CACHED ? ld_param(p + 8 * lane) : ld_once(p + 8 * lane);
-        f.r[0] = v.x; f.r[1] = v.y; f.r[2] = v.z; f.r[3] = v.w;
-    } else if constexpr (MAP == MAP_V4) {
+    return sizeof(T) == 2 ? 8 * lane : 128 * h + 4 * lane;
+}
+
+// Elements of a cut pack, one by one; the others are zeros, and are not stored.
+template <typename T> __device__ __forceinline__ uint4 cut_load(const T *p, int c, Part b) {
+    constexpr int V = IO<T>::V;
+    const Bits<T> *q = reinterpret_cast<const Bits<T> *>(p);
+    uint32_t e[V];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            const int c = 128 * h + 4 * lane;
-            if (c < left) v = KEEP_CACHED ? ld_param(p + c) : ld_once(p + c);
-            f.r[4 * h] = v.x; f.r[4 * h + 1] = v.y; f.r[4 * h + 2] = v.z; f.r[4 * h + 3] = v.w;
+    for (int j = 0; j < V; ++j) e[j] = c + j >= b.head && c + j < b.left ? (uint32_t)q[j] : 0u;
+    if constexpr (V == 8)
+        return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    else
+        return make_uint4(e[0], e[1], e[2], e[3]);
+}
+template <typename T> __device__ __forceinline__ void cut_store(T *p, int c, Part b, const uint4 &v) {
+    constexpr int V = IO<T>::V;
+    Bits<T> *q = reinterpret_cast<Bits<T> *>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (c + j >= b.head && c + j < b.left) q[j] = (Bits<T>)(V == 8 ? w[j >> 1] >> 16 * (j & 1) : w[j]);
+}
+
+// How a lane reaches its elements of U neighbouring chunks of a row: which of
+// its packs the row has whole, and which in part.  The same for all rows of
+// one shift.
+template <typename T, int MAP, int U> struct Access {
+    static constexpr int H = MAP == MAP_S ? 1 : kPacks<T>;
+    uint32_t whole, some;  // bit u * H + h; `some` includes the whole ones
+    int64_t ch0, n;
+    int shift;
+
+    __device__ __forceinline__ Access(int64_t ch0_, int64_t n_, int shift_) : whole(0), some(0), ch0(ch0_), n(n_), shift(shift_) {
+        if constexpr (MAP != MAP_S) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Part b = part(u);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int c = pack_at<T>(h);
+                    const bool s = c < b.left && c + IO<T>::V > b.head;
+                    some |= (uint32_t)s << (u * H + h);
+                    whole |= (uint32_t)(s && c >= b.head && c + IO<T>::V <= b.left) << (u * H + h);
+                }
+            }
         }
-    } else if constexpr (sizeof(T) == 2) {
-        const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
-        unsigned short e[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = 32 * j + lane < left ? q[32 * j + lane] : (unsigned short)0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f.r[j] = (uint32_t)e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
-    } else {
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f.r[j] = 32 * j + lane < left ? q[32 * j + lane] : 0u;
     }
-}
+    __device__ __forceinline__ Part part(int u) const { return chunk_part(ch0 + u, n, shift); }
+    // Element 0 of this lane in chunk 0 of the run, behind the row's first.
+    __device__ __forceinline__ int64_t first() const {
+        return ch0 * kChunk - shift + (MAP == MAP_S ? (int)(threadIdx.x & 31) : pack_at<T>(0));
+    }
+    // Packs that may be read whole in this row: a cut one reaches up to V - 1
+    // elements into the rows before or after.  That stays inside the tensor
+    // when as many lie on that side; rows are at least n elements apart.
+    __device__ __forceinline__ uint32_t readable(int64_t row, int64_t rows) const {
+        if (MAP != MAP_A) return whole;
+        constexpr int V = IO<T>::V;
+        const int over = (int)((V - (n + shift) % V) % V);  // places behind the row in its last pack
+        return row * n >= shift && (rows - 1 - row) * n >= over ? some : whole;
+    }
 
-template <typename T, int MAP>
-__device__ __forceinline__ void frag_store(const Frag<T> &f, T *p, int64_t left) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (MAP == MAP_V8) {
-        if (8 * lane < left) st_stream(p + 8 * lane, make_uint4(f.r[0], f.r[1], f.r[2], f.r[3]));
-    } else if constexpr (MAP == MAP_V4) {
+    // p: the row's element first().
+    template <bool KEEP_CACHED = false>
+    __device__ __forceinline__ void load(Frag<T> &f, const T *p, int u, uint32_t read) const {
+        if constexpr (MAP == MAP_S) {
+            const Part b = part(u);
+            const int lane = threadIdx.x & 31;
+            const Bits<T> *q = reinterpret_cast<const Bits<T> *>(p) + u * kChunk;
+            uint32_t e[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = 128 * h + 4 * lane;
-            if (c < left)
-                st_stream(p + c, make_uint4(f.r[4 * h], f.r[4 * h + 1], f.r[4 * h + 2], f.r[4 * h + 3]));
+            for (int j = 0; j < 8; ++j) e[j] = 32 * j + lane < b.left ? (uint32_t)q[32 * j] : 0u;
+#pragma unroll
+            for (int j = 0; j < 2 * (int)sizeof(T); ++j)
+                f.r[j] = sizeof(T) == 2 ? e[2 * j & 7] | e[(2 * j + 1) & 7] << 16 : e[j];
+        } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const uint32_t bit = 1u << (u * H + h);
+                const T *q = p + u * kChunk + 128 * h;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (read & bit)
+                    v = KEEP_CACHED ? ld_param(q) : ld_once(q);
+                else if (MAP == MAP_A && (some & bit))
+                    v = cut_load<T>(q, pack_at<T>(h), part(u));
+                f.r[4 * h] = v.x; f.r[4 * h + 1] = v.y; f.r[4 * h + 2] = v.z; f.r[4 * h + 3] = v.w;
+            }
         }
-    } else if constexpr (sizeof(T) == 2) {
-        unsigned short *q = reinterpret_cast<unsigned short *>(p);
+    }
+    // Zeros in the places of a loaded fragment that are not the row's.
+    __device__ __forceinline__ void trim(Frag<T> &f, int u) const {
+        if constexpr (MAP == MAP_A) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (32 * j + lane < left) q[32 * j + lane] = (unsigned short)(f.r[j >> 1] >> 16 * (j & 1));
+            for (int h = 0; h < H; ++h) {
+                const uint32_t bit = 1u << (u * H + h);
+                if ((some & ~whole) & bit) {
+                    const Part b = part(u);
+                    const int c = pack_at<T>(h);
+#pragma unroll
+                    for (int j = 0; j < IO<T>::V; ++j)
+                        if (c + j < b.head || c + j >= b.left) {
+                            if (sizeof(T) == 2)
+                                f.r[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+                            else
+                                f.r[(4 * h + j) % (2 * sizeof(T))] = 0u;
+                        }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const Frag<T> &f, T *p, int u) const {
+        if constexpr (MAP == MAP_S) {
+            const Part b = part(u);
+            const int lane = threadIdx.x & 31;
+            Bits<T> *q = reinterpret_cast<Bits<T> *>(p) + u * kChunk;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (32 * j + lane < b.left)
+                    q[32 * j] = (Bits<T>)(sizeof(T) == 2 ? f.r[j >> 1] >> 16 * (j & 1) : f.r[j % (2 * sizeof(T))]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const uint32_t bit = 1u << (u * H + h);
+                T *q = p + u * kChunk + 128 * h;
+                const uint4 v = make_uint4(f.r[4 * h], f.r[4 * h + 1], f.r[4 * h + 2], f.r[4 * h + 3]);
+                if (whole & bit)
+                    st_stream(q, v);
+                else if (MAP == MAP_A && (some & bit))
+                    cut_store<T>(q, pack_at<T>(h), part(u), v);
+            }
+        }
+    }
+};
+
+// The weights of a lane's columns.  Their vector has an alignment of its own:
+// element by element unless both are on the grid.
+template <typename T, int MAP, int U>
+__device__ __forceinline__ void frag_param(Frag<T> &f, const T *w, const Access<T, MAP, U> &at, int u) {
+    if (MAP != MAP_A || (at.shift == 0 && (reinterpret_cast<uintptr_t>(w) & 15) == 0)) {
+        at.template load<true>(f, w + at.first(), u, at.whole);
     } else {
-        uint32_t *q = reinterpret_cast<uint32_t *>(p);
+        const Part b = at.part(u);
+        const Bits<T> *q = reinterpret_cast<const Bits<T> *>(w) + ((at.ch0 + u) * kChunk - at.shift);
+        uint32_t e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (32 * j + lane < left) q[32 * j + lane] = f.r[j];
+        for (int j = 0; j < 8; ++j) {
+            const int c = frag_col<T, MAP>(j);
+            e[j] = c >= b.head && c < b.left ? (uint32_t)q[c] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * (int)sizeof(T); ++j) f.r[j] = sizeof(T) == 2 ? e[2 * j & 7] | e[(2 * j + 1) & 7] << 16 : e[j];
     }
 }
 
@@ -205,8 +380,8 @@ template <typename T> __device__ __forceinline__ Frag<T> frag_pack(const float2 
 
 // d(v) of 8 elements: the product rounded to binary32, or +0 (a select, so a
 // dropped infinity or NaN leaves nothing behind).
-template <int MAP>
-__device__ __forceinline__ void drop_apply(const DropArgs &d, const Keep<MAP> &k, float2 v[4]) {
+template <typename T, int MAP>
+__device__ __forceinline__ void drop_apply(const DropArgs &d, const Keep<T, MAP> &k, float2 v[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 s = __fmul2_rn(v[i], f2(d.scale));
@@ -223,106 +398,134 @@ template <typename T> __device__ __forceinline__ void prefetch_row(const T *p, i
 }
 
 // ---------------------------------------------------------------------------
-// Dropout alone: element-wise, bound by HBM (one read, one write).  Chunks of
-// the whole tensor are numbered row by row; a warp takes U at a time, loads
-// issued before the generator runs.
+// Dropout alone: element-wise, one read and one write.  A warp's item is U
+// neighbouring chunks of one row; all loads are issued before the generator
+// runs.  At 8192 x 8192 bf16 the generator's integer products and the ALU work
+// of the selects take 60 % of their pipes' time, so the kernel needs its
+// warps: five CTAs per SM (48 registers) 42.9 us, four 46.4, two 48.9, six
+// (spills) 54.9.
 // ---------------------------------------------------------------------------
 template <typename T, int MAP, int U>
-__global__ void __launch_bounds__(256) dropout_kernel(const DropArgs d, const T *x, const int64_t ldx,
-                                                      T *y, const int64_t ldy, const int64_t rows,
-                                                      const int64_t N, const int64_t cpr) {
+__global__ void __launch_bounds__(256, (MAP == MAP_V && sizeof(T) == 2 ? 5 : 3))
+    dropout_kernel(const DropArgs d, const T *x, const int64_t ldx, T *y, const int64_t ldy, const int64_t rows,
+                   const int64_t N, const uint32_t per_row) {
     pdl_wait();
     pdl_launch_dependents();
     const DropCtr o = drop_ctr(d);
-    const int64_t total = rows * cpr;
-    const int64_t step = (int64_t)gridDim.x * 8 * U;
-    for (int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * U; first < total; first += step) {
+    const int64_t total = rows * per_row;
+    const int64_t step = (int64_t)gridDim.x * 8;
+    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < total; item += step) {
+        const int64_t row = total <= 0xffffffffll ? (int64_t)((uint32_t)item / per_row) : item / per_row;
+        const int64_t ch = (item - row * per_row) * U;
+        const Access<T, MAP, U> at(ch, N, row_shift<T, MAP>(x + row * ldx));
+        const T *p = x + row * ldx + at.first();
+        T *q = y + row * ldy + at.first();
         Frag<T> f[U];
-        int64_t row[U], c[U];
-        row[0] = total <= 0xffffffffll ? (int64_t)((uint32_t)first / (uint32_t)cpr) : first / cpr;
-        c[0] = first - row[0] * cpr;
+        const uint32_t read = at.readable(row, rows);
 #pragma unroll
-        for (int u = 1; u < U; ++u) {
-            const bool wrap = c[u - 1] + 1 == cpr;
-            c[u] = wrap ? 0 : c[u - 1] + 1;
-            row[u] = row[u - 1] + wrap;
-        }
+        for (int u = 0; u < U; ++u) at.load(f[u], p, u, read);
+        if (d.on) {
+            Masks<T, MAP> m(d, o, row, ch, at.shift);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (row[u] < rows)
-                frag_load<T, MAP>(f[u], x + row[u] * ldx + c[u] * kChunk, N - c[u] * kChunk);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (row[u] < rows) {
+            for (int u = 0; u < U; ++u) {
                 float2 v[4];
                 frag_unpack<T>(f[u], v);
-                if (d.on) drop_apply<MAP>(d, drop_keep<MAP>(d, o, c[u], row[u]), v);
-                frag_store<T, MAP>(frag_pack<T>(v), y + row[u] * ldy + c[u] * kChunk, N - c[u] * kChunk);
+                drop_apply<T, MAP>(d, m.next(), v);
+                f[u] = frag_pack<T>(v);
             }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) at.store(f[u], q, u);
     }
 }
 
+// Sum over the CTA's warps (nw of them), returned to every thread; `slot` as
+// for cta_sum_all.
+__device__ __forceinline__ float warps_sum_all(float v, float *slot, int nw) {
+    const int lane = threadIdx.x & 31;
+    v = warp_sum_all(v);
+    if (lane == 0) slot[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum_all(lane < nw ? slot[lane] : 0.f);
+}
+
 // ---------------------------------------------------------------------------
-// Forward of the residual path, register plan: a group of GT threads per row
-// (a warp, or the whole CTA), the row in registers, x and the residual read
-// once.
+// Forward of the residual path, register plan: a row per warp (WARP) or per
+// CTA of as many warps as the row has U chunks; the row in registers, x and
+// the residual read once.  A group's rows are apart by a multiple of 8, so
+// that they share one shift (8 rows of any stride are a multiple of 16
+// bytes): its columns are the same in all of them, and w is fetched once.
 // ---------------------------------------------------------------------------
-template <typename T, int GT, int U, int MAP>
-__global__ void __launch_bounds__(GT < 128 ? 128 : GT) drop_add_rms_kernel(const DropRmsArgs a,
-                                                                          const int64_t pf) {
-    constexpr int CTA = GT < 128 ? 128 : GT, NW = GT / 32, G = CTA / GT;
-    __shared__ float slot[2][NW];
-    const int warp = (threadIdx.x % GT) >> 5;
-    const bool lead = threadIdx.x % GT == 0;
+template <typename T, bool WARP, int U, int MAP, int REGS>
+__global__ void __maxnreg__(REGS) drop_add_rms_kernel(const DropRmsArgs a, const int64_t pf) {
+    __shared__ float slot[2][32];
+    const int nw = WARP ? 1 : (int)blockDim.x / 32, groups = WARP ? (int)blockDim.x / 32 : 1;
+    const int warp = WARP ? 0 : (int)threadIdx.x >> 5;
+    const bool lead = WARP ? (threadIdx.x & 31) == 0 : threadIdx.x == 0;
     const int N = (int)a.N;
-    const T *X = static_cast<const T *>(a.x), *R = static_cast<const T *>(a.res);
     const T *W = static_cast<const T *>(a.w);
-    T *H = static_cast<T *>(a.h), *Y = static_cast<T *>(a.y);
+    int64_t row = (int64_t)blockIdx.x * groups + (WARP ? threadIdx.x >> 5 : 0);
+    const Access<T, MAP, U> at(warp * U, N, row_shift<T, MAP>(static_cast<const T *>(a.x) + row * a.ldx));
+    const T *X = static_cast<const T *>(a.x) + at.first(), *R = static_cast<const T *>(a.res) + at.first();
+    T *H = static_cast<T *>(a.h) + at.first(), *Y = static_cast<T *>(a.y) + at.first();
+    // a hint ahead of the wait, as the norm kernels give it: L2 is where the
+    // previous grid's writes arrive too
+    if (lead && row < a.rows) {
+        prefetch_row(static_cast<const T *>(a.x) + row * a.ldx, N);
+        prefetch_row(static_cast<const T *>(a.res) + row * a.ldr, N);
+    }
     pdl_wait();
     pdl_launch_dependents();
     const DropCtr o = drop_ctr(a.d);
     int parity = 0;
-    for (int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / GT; row < a.rows;
-         row += (int64_t)gridDim.x * G, parity ^= 1) {
+    Frag<T> fw[U];
+    if (MAP == MAP_A && W) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) frag_param(fw[u], W, at, u);
+    }
+    for (; row < a.rows; row += (int64_t)gridDim.x * groups, parity ^= 1) {
         if (pf > 0 && lead && row + pf < a.rows) {
-            prefetch_row(X + (row + pf) * a.ldx, N);
-            prefetch_row(R + (row + pf) * a.ldr, N);
+            prefetch_row(static_cast<const T *>(a.x) + (row + pf) * a.ldx, N);
+            prefetch_row(static_cast<const T *>(a.res) + (row + pf) * a.ldr, N);
         }
-        Frag<T> fx[U], fr[U], fw[U];
+        Frag<T> fx[U], fr[U];
+        const uint32_t read = at.readable(row, a.rows);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (u * NW + warp) * kChunk;
-            frag_load<T, MAP>(fx[u], X + row * a.ldx + c, N - c);
-            frag_load<T, MAP>(fr[u], R + row * a.ldr + c, N - c);
+            at.load(fx[u], X + row * a.ldx, u, read);
+            at.load(fr[u], R + row * a.ldr, u, read);
+        }
+        if (MAP != MAP_A && W) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) frag_param(fw[u], W, at, u);
         }
         float2 acc = f2(0.f);
+        Masks<T, MAP> m(a.d, o, row, at.ch0, at.shift);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int ch = u * NW + warp, c = ch * kChunk;
             float2 v[4], r[4];
-            Keep<MAP> k;
-            if (a.d.on) k = drop_keep<MAP>(a.d, o, ch, row);
+            Keep<T, MAP> k;
+            if (a.d.on) k = m.next();
+            at.trim(fx[u], u);
+            at.trim(fr[u], u);
             frag_unpack<T>(fx[u], v);
+            if (a.d.on) drop_apply<T, MAP>(a.d, k, v);
             frag_unpack<T>(fr[u], r);
-            if (a.d.on) drop_apply<MAP>(a.d, k, v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __fadd2_rn(v[i], r[i]);
             fr[u] = frag_pack<T>(v);  // the stream's value: the norm is of this rounding
-            frag_store<T, MAP>(fr[u], H + row * a.ldh + c, N - c);
+            at.store(fr[u], H + row * a.ldh, u);
             frag_unpack<T>(fr[u], v);
-            // columns past the row's end hold zeros and add nothing
+            // places outside the row hold zeros and add nothing
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc = __ffma2_rn(v[i], v[i], acc);
-            if (W) frag_load<T, MAP, true>(fw[u], W + c, N - c);
         }
         float ss = acc.x + acc.y;
-        ss = GT == 32 ? warp_sum_all(ss) : cta_sum_all<NW>(ss, slot[parity]);
+        ss = WARP ? warp_sum_all(ss) : warps_sum_all(ss, slot[parity], nw);
         const float rstd = rsqrtf(fmaf(ss, a.invN, a.eps));
         if (lead && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (u * NW + warp) * kChunk;
             float2 v[4], w[4];
             frag_unpack<T>(fr[u], v);
             if (W) frag_unpack<T>(fw[u], w);
@@ -331,13 +534,14 @@ __global__ void __launch_bounds__(GT < 128 ? 128 : GT) drop_add_rms_kernel(const
                 v[i] = __fmul2_rn(v[i], f2(rstd));
                 if (W) v[i] = __fmul2_rn(v[i], w[i]);
             }
-            frag_store<T, MAP>(frag_pack<T>(v), Y + row * a.ldy + c, N - c);
+            at.store(frag_pack<T>(v), Y + row * a.ldy, u);
         }
     }
 }
 
-// Rows longer than the register plan holds: the sum of squares while h is
-// written, then h read again (each lane re-reads what it wrote) for y.
+// Rows longer than the register plan holds, or tensors that differ in
+// alignment: the sum of squares while h is written, then h read again (each
+// lane re-reads what it wrote) for y.
 template <typename T, int MAP>
 __global__ void __launch_bounds__(512) drop_add_rms_long_kernel(const DropRmsArgs a) {
     constexpr int NW = 16;
@@ -354,18 +558,18 @@ __global__ void __launch_bounds__(512) drop_add_rms_long_kernel(const DropRmsArg
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
         float2 acc = f2(0.f);
         for (int64_t ch = warp; ch < chunks; ch += NW) {
-            const int64_t c = ch * kChunk;
+            const Access<T, MAP, 1> at(ch, a.N, 0);
             Frag<T> fx, fr;
-            frag_load<T, MAP>(fx, X + row * a.ldx + c, a.N - c);
-            frag_load<T, MAP>(fr, R + row * a.ldr + c, a.N - c);
+            at.load(fx, X + row * a.ldx + at.first(), 0, at.whole);
+            at.load(fr, R + row * a.ldr + at.first(), 0, at.whole);
             float2 v[4], r[4];
             frag_unpack<T>(fx, v);
+            if (a.d.on) drop_apply<T, MAP>(a.d, Masks<T, MAP>(a.d, o, row, ch, 0).next(), v);
             frag_unpack<T>(fr, r);
-            if (a.d.on) drop_apply<MAP>(a.d, drop_keep<MAP>(a.d, o, ch, row), v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __fadd2_rn(v[i], r[i]);
             fr = frag_pack<T>(v);
-            frag_store<T, MAP>(fr, H + row * a.ldh + c, a.N - c);
+            at.store(fr, H + row * a.ldh + at.first(), 0);
             frag_unpack<T>(fr, v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc = __ffma2_rn(v[i], v[i], acc);
@@ -374,11 +578,11 @@ __global__ void __launch_bounds__(512) drop_add_rms_long_kernel(const DropRmsArg
         const float rstd = rsqrtf(fmaf(ss, a.invN, a.eps));
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
         for (int64_t ch = warp; ch < chunks; ch += NW) {
-            const int64_t c = ch * kChunk;
+            const Access<T, MAP, 1> at(ch, a.N, 0);
             Frag<T> fh, fw;
             float2 v[4], w[4];
-            frag_load<T, MAP>(fh, H + row * a.ldh + c, a.N - c);
-            if (W) frag_load<T, MAP, true>(fw, W + c, a.N - c);
+            at.load(fh, H + row * a.ldh + at.first(), 0, at.whole);
+            if (W) frag_param(fw, W, at, 0);
             frag_unpack<T>(fh, v);
             if (W) frag_unpack<T>(fw, w);
 #pragma unroll
@@ -386,7 +590,7 @@ __global__ void __launch_bounds__(512) drop_add_rms_long_kernel(const DropRmsArg
                 v[i] = __fmul2_rn(v[i], f2(rstd));
                 if (W) v[i] = __fmul2_rn(v[i], w[i]);
             }
-            frag_store<T, MAP>(frag_pack<T>(v), Y + row * a.ldy + c, a.N - c);
+            at.store(frag_pack<T>(v), Y + row * a.ldy + at.first(), 0);
         }
     }
 }
@@ -395,13 +599,33 @@ __global__ void __launch_bounds__(512) drop_add_rms_long_kernel(const DropRmsArg
 // Backward.  With k = -rstd^3 / N * sum_j dy_j w_j h_j (one row-wide sum):
 //   dh = rstd * dy * w + k * h + dh_up
 // ---------------------------------------------------------------------------
-// The outputs of one lane's 8 elements of a row, and their share of dw.
-template <typename T, int MAP>
-__device__ __forceinline__ void drop_bwd_chunk(const DropRmsBwdArgs &a, const DropCtr &o, int64_t row,
-                                               int64_t ch, const Frag<T> &fd, const Frag<T> &fh,
-                                               const Frag<T> &fu, const Frag<T> &fw, float rstd,
-                                               float k, float2 dw[4]) {
-    const int64_t c = ch * kChunk;
+// A row's factor k from its sum; rstd^3 alone can leave binary32 where the
+// product does not.
+__device__ __forceinline__ float bwd_factor(float rstd, float dot, float invN) {
+    return -(rstd * dot) * invN * rstd * rstd;
+}
+// A lane's share of the row's sum.
+template <typename T>
+__device__ __forceinline__ float2 bwd_dot(const Frag<T> &fd, const Frag<T> &fh, const Frag<T> &fw, bool weighted,
+                                          float2 acc) {
+    float2 dy[4], h[4], w[4];
+    frag_unpack<T>(fd, dy);
+    frag_unpack<T>(fh, h);
+    if (weighted) frag_unpack<T>(fw, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (weighted) dy[i] = __fmul2_rn(dy[i], w[i]);
+        acc = __ffma2_rn(dy[i], h[i], acc);
+    }
+    return acc;
+}
+// The outputs of one lane's 8 elements of chunk u of a row, and their share of
+// dw.
+template <typename T, int MAP, int U>
+__device__ __forceinline__ void drop_bwd_chunk(const DropRmsBwdArgs &a, Masks<T, MAP> &m, const Access<T, MAP, U> &at,
+                                               T *dres, T *dx, int u, const Frag<T> &fd, const Frag<T> &fh,
+                                               const Frag<T> &fu, const Frag<T> &fw, float rstd, float k,
+                                               float2 dw[4]) {
     float2 dy[4], h[4], t[4];
     frag_unpack<T>(fd, dy);
     frag_unpack<T>(fh, h);
@@ -423,26 +647,42 @@ __device__ __forceinline__ void drop_bwd_chunk(const DropRmsBwdArgs &a, const Dr
 #pragma unroll
         for (int i = 0; i < 4; ++i) dy[i] = __fadd2_rn(dy[i], t[i]);
     }
-    if (a.dres) frag_store<T, MAP>(frag_pack<T>(dy), static_cast<T *>(a.dres) + row * a.lddr + c, a.N - c);
+    if (a.dres) at.store(frag_pack<T>(dy), dres, u);
     if (a.dx) {
-        if (a.d.on) drop_apply<MAP>(a.d, drop_keep<MAP>(a.d, o, ch, row), dy);
-        frag_store<T, MAP>(frag_pack<T>(dy), static_cast<T *>(a.dx) + row * a.lddx + c, a.N - c);
+        if (a.d.on) drop_apply<T, MAP>(a.d, m.next(), dy);
+        at.store(frag_pack<T>(dy), dx, u);
     }
 }
 
-// Register plan: persistent groups of GT threads, a row at a time; a thread's
-// columns are the same in every row, so dw accumulates in registers and each
-// CTA leaves one row of partial sums (folded in order by dw_fold_kernel: no
-// atomics, the same bits every time).
-template <typename T, int GT, int U, int MAP>
-__global__ void __launch_bounds__(GT < 128 ? 128 : GT) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a) {
-    constexpr int CTA = GT < 128 ? 128 : GT, NW = GT / 32, G = CTA / GT;
-    __shared__ float slot[2][NW];
-    __shared__ float part[G > 1 ? G - 1 : 1][G > 1 ? U * kChunk : 1];
-    const int warp = (threadIdx.x % GT) >> 5;
+// Register plan: persistent groups (as the forward's), a row at a time; a
+// thread's columns are the same in every row, so dw accumulates in registers
+// and each CTA leaves one row of partial sums (folded in order by
+// dw_fold_kernel: no atomics, the same bits every time).
+template <typename T, bool WARP, int U, int MAP, int REGS, bool AHEAD>
+__global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a) {
+    constexpr int G = WARP ? kRowWarps : 1;
+    __shared__ float slot[2][32];
+    __shared__ float part[WARP ? G - 1 : 1][WARP ? U * kChunk : 1];
+    const int nw = WARP ? 1 : (int)blockDim.x / 32;
+    const int warp = WARP ? 0 : (int)threadIdx.x >> 5;
+    const bool lead = WARP ? (threadIdx.x & 31) == 0 : threadIdx.x == 0;
     const int N = (int)a.N;
-    const T *DY = static_cast<const T *>(a.dy), *H = static_cast<const T *>(a.h);
-    const T *UP = static_cast<const T *>(a.up), *W = static_cast<const T *>(a.w);
+    const T *W = static_cast<const T *>(a.w);
+    int64_t row = (int64_t)blockIdx.x * G + (WARP ? threadIdx.x >> 5 : 0);
+    const Access<T, MAP, U> at(warp * U, N, row_shift<T, MAP>(static_cast<const T *>(a.dy) + row * a.lddy));
+    const T *DY = static_cast<const T *>(a.dy) + at.first(), *H = static_cast<const T *>(a.h) + at.first();
+    const T *UP = static_cast<const T *>(a.up) + at.first();
+    T *DR = static_cast<T *>(a.dres) + at.first(), *DX = static_cast<T *>(a.dx) + at.first();
+    const int64_t step = (int64_t)gridDim.x * G;
+    auto prefetch = [&](int64_t r) {
+        if (lead && r < a.rows) {
+            prefetch_row(static_cast<const T *>(a.dy) + r * a.lddy, N);
+            prefetch_row(static_cast<const T *>(a.h) + r * a.ldh, N);
+            if (a.up) prefetch_row(static_cast<const T *>(a.up) + r * a.ldu, N);
+        }
+    };
+    prefetch(row);
+    if (AHEAD) prefetch(row + step);
     pdl_wait();
     pdl_launch_dependents();
     const DropCtr o = drop_ctr(a.d);
@@ -450,82 +690,96 @@ __global__ void __launch_bounds__(GT < 128 ? 128 : GT) drop_add_rms_bwd_kernel(c
     float2 dw[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int c = (u * NW + warp) * kChunk;
-        if (W) frag_load<T, MAP, true>(fw[u], W + c, N - c);
+        if (W) frag_param(fw[u], W, at, u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dw[u][i] = f2(0.f);
     }
-    const int64_t step = (int64_t)gridDim.x * G;
-    int parity = 0;
-    for (int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / GT; row < a.rows; row += step, parity ^= 1) {
-        if (threadIdx.x % GT == 0 && row + step < a.rows) {
-            prefetch_row(DY + (row + step) * a.lddy, N);
-            prefetch_row(H + (row + step) * a.ldh, N);
-            if (UP) prefetch_row(UP + (row + step) * a.ldu, N);
-        }
-        Frag<T> fd[U], fh[U], fu[U];
+    Frag<T> fd[U], fh[U], fu[U];
+    float rstd = 0.f;
+    auto fetch = [&](int64_t r, Frag<T>(&xd)[U], Frag<T>(&xh)[U], Frag<T>(&xu)[U], float &xr) {
+        const uint32_t read = at.readable(r, a.rows);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (u * NW + warp) * kChunk;
-            frag_load<T, MAP>(fd[u], DY + row * a.lddy + c, N - c);
-            frag_load<T, MAP>(fh[u], H + row * a.ldh + c, N - c);
-            if (UP) frag_load<T, MAP>(fu[u], UP + row * a.ldu + c, N - c);
+            at.load(xd[u], DY + r * a.lddy, u, read);
+            at.load(xh[u], H + r * a.ldh, u, read);
+            if (a.up) at.load(xu[u], UP + r * a.ldu, u, read);
         }
-        const float rstd = a.rstd[row];
+        xr = a.rstd[r];
+    };
+    if (AHEAD && row < a.rows) fetch(row, fd, fh, fu, rstd);
+    int parity = 0;
+    for (; row < a.rows; row += step, parity ^= 1) {
+        prefetch(row + (AHEAD ? 2 : 1) * step);
+        if (!AHEAD) fetch(row, fd, fh, fu, rstd);
         float2 acc = f2(0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float2 dy[4], h[4], w[4];
-            frag_unpack<T>(fd[u], dy);
-            frag_unpack<T>(fh[u], h);
-            if (W) frag_unpack<T>(fw[u], w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (W) dy[i] = __fmul2_rn(dy[i], w[i]);
-                acc = __ffma2_rn(dy[i], h[i], acc);
-            }
+            // with zeros for dy what the others hold there reaches no output
+            // (0 times an infinity would: h too)
+            at.trim(fd[u], u);
+            at.trim(fh[u], u);
+            acc = bwd_dot<T>(fd[u], fh[u], fw[u], W != nullptr, acc);
         }
         float dot = acc.x + acc.y;
-        dot = GT == 32 ? warp_sum_all(dot) : cta_sum_all<NW>(dot, slot[parity]);
-        // rstd^3 can leave binary32 where rstd * (rstd * dot) * rstd does not
-        const float k = -(rstd * dot) * a.invN * rstd * rstd;
+        dot = WARP ? warp_sum_all(dot) : warps_sum_all(dot, slot[parity], nw);
+        Frag<T> nd[AHEAD ? U : 1], nh[AHEAD ? U : 1], nu[AHEAD ? U : 1];
+        float nr = 0.f;
+        if constexpr (AHEAD) {
+            if (row + step < a.rows) fetch(row + step, nd, nh, nu, nr);
+        }
+        const float k = bwd_factor(rstd, dot, a.invN);
+        Masks<T, MAP> m(a.d, o, row, at.ch0, at.shift);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            drop_bwd_chunk<T, MAP>(a, o, row, u * NW + warp, fd[u], fh[u], fu[u], fw[u], rstd, k, dw[u]);
+            drop_bwd_chunk(a, m, at, DR + row * a.lddr, DX + row * a.lddx, u, fd[u], fh[u], fu[u], fw[u], rstd, k,
+                           dw[u]);
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                fd[u] = nd[u];
+                fh[u] = nh[u];
+                fu[u] = nu[u];
+            }
+            rstd = nr;
+        }
     }
     if (!a.dw) return;
-    if constexpr (G > 1) {
-        // the CTA's groups meet in shared memory, added in group order
-        const int g = threadIdx.x / GT;
+    if constexpr (WARP) {
+        // the CTA's warps meet in shared memory by column, added in order
+        const int g = threadIdx.x >> 5;
         if (g > 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    part[g - 1][u * kChunk + frag_col<MAP>(j)] = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
+                for (int j = 0; j < 8; ++j) {
+                    const int c = u * kChunk + frag_col<T, MAP>(j) - at.shift;
+                    if (c >= 0 && c < N) part[g - 1][c] = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
+                }
         }
         __syncthreads();
         if (g > 0) return;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                for (int q = 0; q < G - 1; ++q) {
-                    float &s = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
-                    s += part[q][u * kChunk + frag_col<MAP>(j)];
-                }
+            for (int j = 0; j < 8; ++j) {
+                const int c = u * kChunk + frag_col<T, MAP>(j) - at.shift;
+                float &s = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
+                if (c >= 0 && c < N)
+                    for (int q = 0; q < G - 1; ++q) s += part[q][c];
+            }
     }
     float *P = a.part + (int64_t)blockIdx.x * a.N;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = (u * NW + warp) * kChunk + frag_col<MAP>(j);
-            if (c < N) P[c] = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
+            const int c = ((int)at.ch0 + u) * kChunk + frag_col<T, MAP>(j) - at.shift;
+            if (c >= 0 && c < N) P[c] = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
         }
 }
 
-// Long rows: the row sums first (k per row into the workspace) ...
+// Long rows (or tensors that differ in alignment): the row sums first (k per
+// row into the workspace) ...
 template <typename T, int MAP>
 __global__ void __launch_bounds__(512) drop_bwd_dot_kernel(const DropRmsBwdArgs a) {
     constexpr int NW = 16;
@@ -537,24 +791,16 @@ __global__ void __launch_bounds__(512) drop_bwd_dot_kernel(const DropRmsBwdArgs 
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
         float2 acc = f2(0.f);
         for (int64_t ch = warp; ch < chunks; ch += NW) {
-            const int64_t c = ch * kChunk;
+            const Access<T, MAP, 1> at(ch, a.N, 0);
             Frag<T> fd, fh, fw;
-            frag_load<T, MAP>(fd, static_cast<const T *>(a.dy) + row * a.lddy + c, a.N - c);
-            frag_load<T, MAP>(fh, static_cast<const T *>(a.h) + row * a.ldh + c, a.N - c);
-            if (a.w) frag_load<T, MAP, true>(fw, static_cast<const T *>(a.w) + c, a.N - c);
-            float2 dy[4], h[4], w[4];
-            frag_unpack<T>(fd, dy);
-            frag_unpack<T>(fh, h);
-            if (a.w) frag_unpack<T>(fw, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (a.w) dy[i] = __fmul2_rn(dy[i], w[i]);
-                acc = __ffma2_rn(dy[i], h[i], acc);
-            }
+            at.load(fd, static_cast<const T *>(a.dy) + row * a.lddy + at.first(), 0, at.whole);
+            at.load(fh, static_cast<const T *>(a.h) + row * a.ldh + at.first(), 0, at.whole);
+            if (a.w) frag_param(fw, static_cast<const T *>(a.w), at, 0);
+            acc = bwd_dot<T>(fd, fh, fw, a.w != nullptr, acc);
         }
         const float dot = cta_sum_all<NW>(acc.x + acc.y, slot[parity]);
         const float rstd = a.rstd[row];
-        if (threadIdx.x == 0) a.k[row] = -(rstd * dot) * a.invN * rstd * rstd;
+        if (threadIdx.x == 0) a.k[row] = bwd_factor(rstd, dot, a.invN);
     }
 }
 
@@ -565,25 +811,28 @@ __global__ void __launch_bounds__(256) drop_bwd_cols_kernel(const DropRmsBwdArgs
     pdl_wait();
     const DropCtr o = drop_ctr(a.d);
     const int64_t chunks = (a.N + kChunk - 1) / kChunk;
-    const int64_t ch = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), c = ch * kChunk;
+    const int64_t ch = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (ch >= chunks) return;
+    const Access<T, MAP, 1> at(ch, a.N, 0);
     Frag<T> fw;
-    if (a.w) frag_load<T, MAP, true>(fw, static_cast<const T *>(a.w) + c, a.N - c);
+    if (a.w) frag_param(fw, static_cast<const T *>(a.w), at, 0);
     float2 dw[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
     const int64_t r0 = (int64_t)blockIdx.y * rows_per;
     const int64_t r1 = r0 + rows_per < a.rows ? r0 + rows_per : a.rows;
     for (int64_t row = r0; row < r1; ++row) {
         Frag<T> fd, fh, fu;
-        frag_load<T, MAP>(fd, static_cast<const T *>(a.dy) + row * a.lddy + c, a.N - c);
-        frag_load<T, MAP>(fh, static_cast<const T *>(a.h) + row * a.ldh + c, a.N - c);
-        if (a.up) frag_load<T, MAP>(fu, static_cast<const T *>(a.up) + row * a.ldu + c, a.N - c);
-        drop_bwd_chunk<T, MAP>(a, o, row, ch, fd, fh, fu, fw, a.rstd[row], a.k[row], dw);
+        at.load(fd, static_cast<const T *>(a.dy) + row * a.lddy + at.first(), 0, at.whole);
+        at.load(fh, static_cast<const T *>(a.h) + row * a.ldh + at.first(), 0, at.whole);
+        if (a.up) at.load(fu, static_cast<const T *>(a.up) + row * a.ldu + at.first(), 0, at.whole);
+        Masks<T, MAP> m(a.d, o, row, ch, 0);
+        drop_bwd_chunk(a, m, at, static_cast<T *>(a.dres) + row * a.lddr + at.first(),
+                       static_cast<T *>(a.dx) + row * a.lddx + at.first(), 0, fd, fh, fu, fw, a.rstd[row], a.k[row], dw);
     }
     if (!a.dw) return;
     float *P = a.part + (int64_t)blockIdx.y * a.N;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t col = c + frag_col<MAP>(j);
+        const int64_t col = ch * kChunk + frag_col<T, MAP>(j);
         if (col < a.N) P[col] = j & 1 ? dw[j >> 1].y : dw[j >> 1].x;
     }
 }
@@ -591,96 +840,135 @@ __global__ void __launch_bounds__(256) drop_bwd_cols_kernel(const DropRmsBwdArgs
 // ---------------------------------------------------------------------------
 // Launchers, one instance of each per storage type (drop_<type>.cu).
 // ---------------------------------------------------------------------------
-template <typename T, int MAP>
-cudaError_t launch_dropout_m(const DropoutArgs &a, int sms, cudaStream_t s) {
-    constexpr int U = 4;
-    const int64_t cpr = (a.N + kChunk - 1) / kChunk;
-    int64_t ctas = (a.rows * cpr + 8 * U - 1) / (8 * U);
-    const int64_t most = (int64_t)sms * 64;
+template <typename T, int MAP, int U>
+cudaError_t launch_dropout_u(const DropoutArgs &a, int64_t per_row, int sms, cudaStream_t s) {
+    int64_t ctas = (a.rows * per_row + 7) / 8;
+    const int64_t most = (int64_t)sms * 256;
     if (ctas > most) ctas = most;
     return launch_row(dropout_kernel<T, MAP, U>, (unsigned)ctas, 256u, 0, s, a.d,
-                      static_cast<const T *>(a.x), a.ldx, static_cast<T *>(a.y), a.ldy, a.rows, a.N, cpr);
+                      static_cast<const T *>(a.x), a.ldx, static_cast<T *>(a.y), a.ldy, a.rows, a.N,
+                      (uint32_t)per_row);
 }
-template <typename T> cudaError_t launch_dropout_t(const DropoutArgs &a, bool vec, int sms, cudaStream_t s) {
-    return vec ? launch_dropout_m<T, vec_map<T>()>(a, sms, s) : launch_dropout_m<T, MAP_S>(a, sms, s);
+// Chunks of a row of n elements, wherever it starts.
+template <typename T> int64_t row_chunks(int64_t n, int map) {
+    return (n + (map == MAP_A ? IO<T>::V - 1 : 0) + kChunk - 1) / kChunk;
 }
-
-template <typename T, int GT, int U, int MAP>
-cudaError_t launch_drop_fwd_k(const DropRmsArgs &a, int sms, cudaStream_t s, Plan *p) {
-    constexpr int CTA = GT < 128 ? 128 : GT, G = CTA / GT;
-    auto kernel = drop_add_rms_kernel<T, GT, U, MAP>;
-    int per_sm = 0;
-    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), CTA, 0, &per_sm);
-    if (e != cudaSuccess) return e;
-    const int64_t need = (a.rows + G - 1) / G;
-    p->kind = GT == 32 ? PLAN_WARP : PLAN_CTA;
-    p->threads = CTA;
-    p->packs = U * 2 * (int)sizeof(T) / 4;
-    return launch_row(kernel, (unsigned)(need < 0x7fffffff ? need : 0x7fffffff), (unsigned)CTA, 0, s, a,
-                      (int64_t)sms * per_sm * G);
-}
-
-// The group and its share of the row: at least 128 threads a row where rows
-// are few (latency), a warp a row where they are many.
+// Chunks per item: the most whose last item of a row is not mostly empty.
 template <typename T, int MAP>
-cudaError_t launch_drop_fwd_m(const DropRmsArgs &a, bool longrow, int sms, cudaStream_t s, Plan *p) {
-    const int64_t C = (a.N + kChunk - 1) / kChunk;
-    if (!longrow) {
-        if (C <= 4 && a.rows >= 4 * (int64_t)sms) {
-            if (C <= 1) return launch_drop_fwd_k<T, 32, 1, MAP>(a, sms, s, p);
-            if (C <= 2) return launch_drop_fwd_k<T, 32, 2, MAP>(a, sms, s, p);
-            return launch_drop_fwd_k<T, 32, 4, MAP>(a, sms, s, p);
-        }
-        if (C <= 4) return launch_drop_fwd_k<T, 128, 1, MAP>(a, sms, s, p);
-        if (C <= 8) return launch_drop_fwd_k<T, 128, 2, MAP>(a, sms, s, p);
-        if (C <= 16) return launch_drop_fwd_k<T, 256, 2, MAP>(a, sms, s, p);
-        if (C <= 32) return launch_drop_fwd_k<T, 512, 2, MAP>(a, sms, s, p);
-        if (C <= 64) return launch_drop_fwd_k<T, 1024, 2, MAP>(a, sms, s, p);
+cudaError_t launch_dropout_m(const DropoutArgs &a, int sms, cudaStream_t s) {
+    const int64_t c = row_chunks<T>(a.N, MAP);
+    const int64_t i4 = (c + 3) / 4, i2 = (c + 1) / 2;
+    if (sizeof(T) == 2 && i4 * 4 * 8 <= c * 9) return launch_dropout_u<T, MAP, sizeof(T) == 2 ? 4 : 2>(a, i4, sms, s);
+    if (i2 * 2 * 8 <= c * 9) return launch_dropout_u<T, MAP, 2>(a, i2, sms, s);
+    return launch_dropout_u<T, MAP, 1>(a, c, sms, s);
+}
+template <typename T> cudaError_t launch_dropout_t(const DropoutArgs &a, int map, int sms, cudaStream_t s) {
+    return map == MAP_V   ? launch_dropout_m<T, MAP_V>(a, sms, s)
+           : map == MAP_A ? launch_dropout_m<T, MAP_A>(a, sms, s)
+                          : launch_dropout_m<T, MAP_S>(a, sms, s);
+}
+
+// Grid of the register plans: every row its group (MAP_V, forward), or
+// resident groups that step over the rows by a multiple of 8.
+inline int64_t stepped_grid(int64_t ctas, int64_t resident) {
+    ctas = (ctas + 7) / 8 * 8;
+    resident = resident / 8 * 8;
+    if (resident < 8) resident = 8;
+    return ctas < resident ? ctas : resident;
+}
+
+template <typename T, bool WARP, int U, int MAP, int REGS>
+cudaError_t launch_drop_fwd_k(const DropRmsArgs &a, int warps, int sms, cudaStream_t s, Plan *p) {
+    auto kernel = drop_add_rms_kernel<T, WARP, U, MAP, REGS>;
+    const int threads = 32 * warps, G = WARP ? warps : 1;
+    int per_sm = 0;
+    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), threads, 0, &per_sm);
+    if (e != cudaSuccess) return e;
+    int64_t ctas = (a.rows + G - 1) / G;
+    int64_t pf = (int64_t)sms * per_sm * G;
+    if (MAP == MAP_A) {
+        ctas = stepped_grid(ctas, (int64_t)sms * per_sm);
+        pf = ctas * G;
     }
+    if (ctas > 0x7fffffff) ctas = 0x7ffffff8;
+    p->kind = WARP ? PLAN_WARP : PLAN_CTA;
+    p->threads = threads;
+    p->packs = U * 2 * (int)sizeof(T) / 4;
+    return launch_row(kernel, (unsigned)ctas, (unsigned)threads, 0, s, a, pf);
+}
+
+// The group and its share of the row: a warp a row where rows are short and
+// many, else a CTA of as many warps as the row needs.
+template <typename T, int MAP>
+cudaError_t launch_drop_fwd_m(const DropRmsArgs &a, int sms, cudaStream_t s, Plan *p) {
+    const int C = (int)row_chunks<T>(a.N, MAP);
+    constexpr int R = MAP == MAP_V && sizeof(T) == 2 ? 64 : 96;
+    const int warps = (C + 1) / 2;
+    if (C <= 4 && a.rows >= 4 * (int64_t)sms) {
+        if (C <= 1) return launch_drop_fwd_k<T, true, 1, MAP, 128>(a, kRowWarps, sms, s, p);
+        if (C <= 2) return launch_drop_fwd_k<T, true, 2, MAP, 128>(a, kRowWarps, sms, s, p);
+        return launch_drop_fwd_k<T, true, 4, MAP, 128>(a, kRowWarps, sms, s, p);
+    }
+    if (C <= 4) return launch_drop_fwd_k<T, false, 1, MAP, 64>(a, C, sms, s, p);
+    if (warps * 32 * R <= 65536) return launch_drop_fwd_k<T, false, 2, MAP, R>(a, warps, sms, s, p);
+    return launch_drop_fwd_k<T, false, 2, MAP, 64>(a, warps, sms, s, p);
+}
+template <typename T, int MAP>
+cudaError_t launch_drop_fwd_long(const DropRmsArgs &a, cudaStream_t s, Plan *p) {
     p->kind = PLAN_GENERIC;
     p->threads = 512;
     p->packs = 1;
     return launch_row(drop_add_rms_long_kernel<T, MAP>, (unsigned)(a.rows < 0x7fffffff ? a.rows : 0x7fffffff),
                       512u, 0, s, a);
 }
+constexpr int kDropFwdChunks = 64, kDropBwdChunks = 32;
 template <typename T>
-cudaError_t launch_drop_fwd_t(const DropRmsArgs &a, bool vec, bool longrow, int sms, cudaStream_t s, Plan *p) {
-    return vec ? launch_drop_fwd_m<T, vec_map<T>()>(a, longrow, sms, s, p)
-               : launch_drop_fwd_m<T, MAP_S>(a, longrow, sms, s, p);
+cudaError_t launch_drop_fwd_t(const DropRmsArgs &a, int map, bool longrow, int sms, cudaStream_t s, Plan *p) {
+    longrow = longrow || row_chunks<T>(a.N, map) > kDropFwdChunks;
+    if (map == MAP_V) return longrow ? launch_drop_fwd_long<T, MAP_V>(a, s, p) : launch_drop_fwd_m<T, MAP_V>(a, sms, s, p);
+    if (map == MAP_A && !longrow) return launch_drop_fwd_m<T, MAP_A>(a, sms, s, p);
+    return launch_drop_fwd_long<T, MAP_S>(a, s, p);
 }
 
-template <typename T, int GT, int U, int MAP>
-cudaError_t launch_drop_bwd_k(const DropRmsBwdArgs &a, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
-    constexpr int CTA = GT < 128 ? 128 : GT, G = CTA / GT;
-    auto kernel = drop_add_rms_bwd_kernel<T, GT, U, MAP>;
+template <typename T, bool WARP, int U, int MAP, int REGS, bool AHEAD>
+cudaError_t launch_drop_bwd_k(const DropRmsBwdArgs &a, int warps, int sms, cudaStream_t s, Plan *p,
+                              int64_t *parts) {
+    auto kernel = drop_add_rms_bwd_kernel<T, WARP, U, MAP, REGS, AHEAD>;
+    const int threads = 32 * warps, G = WARP ? warps : 1;
     int per_sm = 0;
-    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), CTA, 0, &per_sm);
+    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), threads, 0, &per_sm);
     if (e != cudaSuccess) return e;
-    int64_t ctas = (a.rows + G - 1) / G;
-    if (ctas > (int64_t)sms * per_sm) ctas = (int64_t)sms * per_sm;
-    if (ctas > kDropMaxParts) ctas = kDropMaxParts;
-    p->kind = GT == 32 ? PLAN_WARP : PLAN_CTA;
-    p->threads = CTA;
+    int64_t ctas = (a.rows + G - 1) / G, most = (int64_t)sms * per_sm;
+    if (most > kDropMaxParts) most = kDropMaxParts;
+    if (MAP == MAP_A)
+        ctas = stepped_grid(ctas, most);
+    else if (ctas > most)
+        ctas = most;
+    p->kind = WARP ? PLAN_WARP : PLAN_CTA;
+    p->threads = threads;
     p->packs = U * 2 * (int)sizeof(T) / 4;
     *parts = ctas;
-    return launch_row(kernel, (unsigned)ctas, (unsigned)CTA, 0, s, a);
+    return launch_row(kernel, (unsigned)ctas, (unsigned)threads, 0, s, a);
 }
-
 template <typename T, int MAP>
-cudaError_t launch_drop_bwd_m(const DropRmsBwdArgs &a, bool longrow, int sms, cudaStream_t s, Plan *p,
-                              int64_t *parts) {
-    const int64_t C = (a.N + kChunk - 1) / kChunk;
-    if (!longrow) {
-        if (C <= 4 && a.rows >= 4 * (int64_t)sms) {
-            if (C <= 1) return launch_drop_bwd_k<T, 32, 1, MAP>(a, sms, s, p, parts);
-            if (C <= 2) return launch_drop_bwd_k<T, 32, 2, MAP>(a, sms, s, p, parts);
-            return launch_drop_bwd_k<T, 32, 4, MAP>(a, sms, s, p, parts);
-        }
-        if (C <= 4) return launch_drop_bwd_k<T, 128, 1, MAP>(a, sms, s, p, parts);
-        if (C <= 8) return launch_drop_bwd_k<T, 128, 2, MAP>(a, sms, s, p, parts);
-        if (C <= 16) return launch_drop_bwd_k<T, 256, 2, MAP>(a, sms, s, p, parts);
-        if (C <= 32) return launch_drop_bwd_k<T, 512, 2, MAP>(a, sms, s, p, parts);
+cudaError_t launch_drop_bwd_m(const DropRmsBwdArgs &a, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
+    const int C = (int)row_chunks<T>(a.N, MAP);
+    constexpr bool AHEAD = sizeof(T) == 2 && MAP == MAP_V;  // else the next row's registers spill
+    const int warps = (C + 1) / 2;
+    if (C <= 4 && a.rows >= 4 * (int64_t)sms) {
+        if (C <= 1) return launch_drop_bwd_k<T, true, 1, MAP, 128, AHEAD>(a, kRowWarps, sms, s, p, parts);
+        if (C <= 2) return launch_drop_bwd_k<T, true, 2, MAP, 160, AHEAD>(a, kRowWarps, sms, s, p, parts);
+        return launch_drop_bwd_k<T, true, 4, MAP, 255, AHEAD>(a, kRowWarps, sms, s, p, parts);
     }
+    if (C <= 4) return launch_drop_bwd_k<T, false, 1, MAP, 96, false>(a, C, sms, s, p, parts);
+    // two CTAs per SM matter more than the row ahead: up to 8 warps have both,
+    // up to 10 the former, beyond that one CTA fits either way
+    if (warps > 8 && warps <= 10) return launch_drop_bwd_k<T, false, 2, MAP, 96, false>(a, warps, sms, s, p, parts);
+    return launch_drop_bwd_k<T, false, 2, MAP, 128, AHEAD>(a, warps, sms, s, p, parts);
+}
+template <typename T, int MAP>
+cudaError_t launch_drop_bwd_long(const DropRmsBwdArgs &a, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
+    const int64_t C = row_chunks<T>(a.N, MAP);
     p->kind = PLAN_GENERIC;
     p->threads = 256;
     p->packs = 1;
@@ -707,10 +995,14 @@ cudaError_t launch_drop_bwd_m(const DropRmsBwdArgs &a, bool longrow, int sms, cu
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 template <typename T>
-cudaError_t launch_drop_bwd_t(const DropRmsBwdArgs &a, bool vec, bool longrow, int sms, cudaStream_t s,
+cudaError_t launch_drop_bwd_t(const DropRmsBwdArgs &a, int map, bool longrow, int sms, cudaStream_t s,
                               Plan *p, int64_t *parts) {
-    return vec ? launch_drop_bwd_m<T, vec_map<T>()>(a, longrow, sms, s, p, parts)
-               : launch_drop_bwd_m<T, MAP_S>(a, longrow, sms, s, p, parts);
+    longrow = longrow || row_chunks<T>(a.N, map) > kDropBwdChunks;
+    if (map == MAP_V)
+        return longrow ? launch_drop_bwd_long<T, MAP_V>(a, sms, s, p, parts)
+                       : launch_drop_bwd_m<T, MAP_V>(a, sms, s, p, parts);
+    if (map == MAP_A && !longrow) return launch_drop_bwd_m<T, MAP_A>(a, sms, s, p, parts);
+    return launch_drop_bwd_long<T, MAP_S>(a, sms, s, p, parts);
 }
 
 }  // namespace nrm

@@ -3,16 +3,16 @@
 
 namespace nrm {
 
-cudaError_t launch_dropout_f16(const DropoutArgs &a, bool vec, int sms, cudaStream_t s) {
-    return launch_dropout_t<__half>(a, vec, sms, s);
+cudaError_t launch_dropout_f16(const DropoutArgs &a, int map, int sms, cudaStream_t s) {
+    return launch_dropout_t<__half>(a, map, sms, s);
 }
-cudaError_t launch_drop_fwd_f16(const DropRmsArgs &a, bool vec, bool longrow, int sms, cudaStream_t s,
+cudaError_t launch_drop_fwd_f16(const DropRmsArgs &a, int map, bool longrow, int sms, cudaStream_t s,
                                 Plan *p) {
-    return launch_drop_fwd_t<__half>(a, vec, longrow, sms, s, p);
+    return launch_drop_fwd_t<__half>(a, map, longrow, sms, s, p);
 }
-cudaError_t launch_drop_bwd_f16(const DropRmsBwdArgs &a, bool vec, bool longrow, int sms, cudaStream_t s,
+cudaError_t launch_drop_bwd_f16(const DropRmsBwdArgs &a, int map, bool longrow, int sms, cudaStream_t s,
                                 Plan *p, int64_t *parts) {
-    return launch_drop_bwd_t<__half>(a, vec, longrow, sms, s, p, parts);
+    return launch_drop_bwd_t<__half>(a, map, longrow, sms, s, p, parts);
 }
 
 }  // namespace nrm

@@ -20,9 +20,15 @@ __global__ void __launch_bounds__(32 * kFoldWarps) dw_fold_kernel(const float *p
     for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < N; c0 += (int64_t)gridDim.x * 32) {
         const int64_t c = c0 + lane;
         float s = 0.f;
-        if (c < N) {
-#pragma unroll 8
-            for (int64_t p = warp; p < parts; p += kFoldWarps) s += part[p * N + c];
+        for (int64_t p0 = warp; p0 < parts; p0 += kFoldWarps * 16) {
+            float v[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int64_t p = p0 + u * kFoldWarps;
+                v[u] = c < N && p < parts ? part[p * N + c] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u) s += v[u];
         }
         sh[warp][lane] = s;
         __syncthreads();

@@ -20,6 +20,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "nrm_device.cuh"
 #include "nrm_internal.h"
@@ -64,14 +65,38 @@ __device__ __forceinline__ RowMax cta_row_max(RowMax v, float c, float2 *slot) {
     return v;
 }
 
-// log d as a sum of a part in binary64 and a binary32 part below 0.41: d =
-// 2^e f with f in [0.75, 1.5), log d = e log 2 + log1p(f - 1).  A binary32
-// log would cost the log-probability half an ulp of log d (2.4e-7 at 10).
-__device__ __forceinline__ double log_sum(float d) {
-    if (!(d < INFINITY)) return (double)d;  // NaN stays NaN
-    const int e = ((__float_as_int(d) - 0x3f400000) >> 23);
-    const float f = __int_as_float(__float_as_int(d) - (e << 23));
-    return fma((double)e, 0.693147180559945309, (double)log1pf(f - 1.f));
+// Send a pair to `rank`'s copy of a shared variable and count its 8 bytes on
+// that CTA's copy of an mbarrier.
+__device__ __forceinline__ void send_pair(float2 *p, float2 v, uint64_t *bar, uint32_t rank) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                 ::"r"(dsmem_addr(p, rank)), "f"(v.x), "f"(v.y), "r"(dsmem_addr(bar, rank))
+                 : "memory");
+}
+
+// What a row's factors are computed in: a value as the unevaluated sum of two
+// binary32 numbers.  One rounding to binary32 of a log-probability of -12 is
+// 5e-7, as much as everything else together, and the clip has a border; the
+// binary64 units would take 64 cycles for each operation of this one thread.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+// s (z - m) - log d, with log d = e log 2 + log1p(f - 1) for d = 2^e f, f in
+// [0.75, 1.5), and log 2 in two parts, e times the first exact.
+__device__ __forceinline__ Two log_prob(float z, float m, float d, float s) {
+    const Two x = two_sum(z, -m);
+    if (!(d < INFINITY) || !(fabsf(x.hi) < INFINITY)) return Two{s * x.hi - logf(d), 0.f};
+    const int e = (__float_as_int(d) - 0x3f400000) >> 23;
+    const float f = __int_as_float(__float_as_int(d) - (e << 23)), fe = (float)e;
+    const float p = __fmul_rn(s, x.hi);
+    const float pl = fmaf(s, x.lo, fmaf(s, x.hi, -p));
+    const Two y = two_sum(p, -fe * 0.693145751953125f);
+    const float l = y.lo + (pl - fmaf(fe, 1.42860677e-6f, log1pf(f - 1.f)));
+    const float hi = __fadd_rn(y.hi, l);
+    return Two{hi, __fadd_rn(__fsub_rn(y.hi, hi), l)};
 }
 
 // exp(q) - q - 1 without the cancellation at small q: its Taylor series to
@@ -90,23 +115,28 @@ __device__ __forceinline__ float kl_term(float q) {
 }
 
 // One row's policy term and its slope in logp.  The clip is decided on the
-// logarithm of the ratio, against the logarithms of the bounds in binary64:
-// the ratio itself carries expf's rounding.
-__device__ __forceinline__ void policy_row(const LogitArgs &a, int64_t row, double logp, float *loss,
+// logarithm of the ratio, against the logarithms of the bounds: the ratio
+// itself carries expf's rounding.
+struct RowTerms {
+    float adv, weight, old, ref;
+};
+__device__ __forceinline__ RowTerms row_terms(const LogitArgs &a, int64_t row) {
+    return RowTerms{a.adv[row], a.weight ? a.weight[row] : 1.f, a.old[row], a.ref ? a.ref[row] : 0.f};
+}
+__device__ __forceinline__ void policy_row(const LogitArgs &a, const RowTerms &r, Two logp, float *loss,
                                            float *slope) {
-    const float A = a.adv[row], w = a.weight ? a.weight[row] : 1.f;
-    const double q = logp - (double)a.old[row];
-    const bool held = A > 0.f ? q > a.log_hi : A < 0.f && q < a.log_lo;
-    const float free_ = -A * expf((float)q);
-    float l = held ? -A * (A > 0.f ? a.ratio_hi : a.ratio_lo) : free_;
+    const float q = (logp.hi - r.old) + logp.lo;
+    const bool held = r.adv > 0.f ? q > a.log_hi : r.adv < 0.f && q < a.log_lo;
+    const float free_ = -r.adv * expf(q);
+    float l = held ? -r.adv * (r.adv > 0.f ? a.ratio_hi : a.ratio_lo) : free_;
     float g = held ? 0.f : free_;
     if (a.ref) {
-        const float k = (float)((double)a.ref[row] - logp);
+        const float k = (r.ref - logp.hi) - logp.lo;
         l = fmaf(a.kl, kl_term(k), l);
         g = fmaf(a.kl, -expm1f(k), g);
     }
-    *loss = w * l;
-    *slope = w * g;
+    *loss = r.weight * l;
+    *slope = r.weight * g;
 }
 
 // Elements of a row before its first 16-byte boundary, whole packs after it,
@@ -117,13 +147,13 @@ template <typename T> struct RowCut {
     int tail;   // elements after the last
 };
 template <typename T> __device__ __forceinline__ RowCut<T> cut_row(const T *p, int64_t n) {
-    constexpr int V = IO<T>::V;
+    constexpr uint32_t V = IO<T>::V;
     RowCut<T> c;
-    const int off = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-    c.head = off ? V - off : 0;
-    if (c.head > n) c.head = (int)n;
-    c.packs = (int)((n - c.head) / V);
-    c.tail = (int)(n - c.head) - c.packs * V;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (V - 1);
+    const uint32_t head = (V - off) & (V - 1), m = (uint32_t)n;  // n < 2^31
+    c.head = (int)(head < m ? head : m);
+    c.packs = (int)((m - c.head) / V);
+    c.tail = (int)((m - c.head) & (V - 1));
     return c;
 }
 
@@ -169,6 +199,39 @@ __device__ __forceinline__ uint4 grad_pack(const uint4 &z, float a, float b, flo
         v[i] = __fmul2_rn(v[i], f2(k));
     }
     return IO2<T>::pack(v);
+}
+
+// The same as k * 2^(a z + b).
+template <typename T> __device__ __forceinline__ uint4 grad_pack1(const uint4 &z, float a, float b, float k) {
+    float2 v[IO2<T>::H];
+    IO2<T>::unpack(z, v);
+#pragma unroll
+    for (int i = 0; i < IO2<T>::H; ++i) {
+        v[i] = __ffma2_rn(v[i], f2(a), f2(b));
+        v[i].x = exp2_fast(v[i].x);
+        v[i].y = exp2_fast(v[i].y);
+        v[i] = __fmul2_rn(v[i], f2(k));
+    }
+    return IO2<T>::pack(v);
+}
+
+// A live row's scalar outputs and its slope (by one thread; `write`: this is
+// the rank that stores them).
+template <bool POLICY>
+__device__ __forceinline__ void finish_row(const LogitArgs &a, int64_t row, const RowMax &r, float za, bool write,
+                                           const RowTerms &terms, float *loss, float *slope) {
+    const bool empty = r.m == -INFINITY && r.d == 0.f;
+    const Two logp = empty ? Two{-INFINITY, 0.f} : log_prob(za, r.m, r.d, a.scale);
+    if (POLICY && !empty) policy_row(a, terms, logp, loss, slope);
+    if (write) {
+        if (a.logp) a.logp[row] = logp.hi;
+        // the log-sum as that of the row's own maximum
+        if (a.lse) {
+            const Two top = empty ? Two{INFINITY, 0.f} : log_prob(r.m, r.m, r.d, a.scale);
+            a.lse[row] = fmaf(a.scale, r.m, -top.hi);
+        }
+        if (POLICY) a.row_loss[row] = *loss;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -264,17 +327,8 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
                     r = rm_merge(r, RowMax{__shfl_sync(0xffffffffu, mine.x, q), __shfl_sync(0xffffffffu, mine.y, q)}, c);
             }
             if (t == 0) {
-                const bool empty = r.m == -INFINITY && r.d == 0.f;
-                const double ls = empty ? 0.0 : log_sum(r.d);
-                const double sm = (double)a.scale * (double)r.m;
-                const double logp = empty ? -INFINITY : (double)a.scale * (double)za - sm - ls;
                 float l = 0.f, g = 0.f;
-                if (POLICY && !empty) policy_row(a, row, logp, &l, &g);
-                if (rank == 0) {
-                    if (a.logp) a.logp[row] = (float)logp;
-                    if (a.lse) a.lse[row] = empty ? -INFINITY : (float)(sm + ls);
-                    if (POLICY) a.row_loss[row] = l;
-                }
+                finish_row<POLICY>(a, row, r, za, rank == 0, POLICY ? row_terms(a, row) : RowTerms{}, &l, &g);
                 if (POLICY) {
                     sh[parity][0] = g * gs * a.scale;
                     sh[parity][1] = za;
@@ -326,6 +380,428 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
         // stay resident until every peer has read this CTA's pairs
         cluster_arrive();
         cluster_wait();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Register plan.  A group of TH threads (a warp, a CTA, or the CTAs of a
+// cluster with a slice each) takes a batch of rows.  The row at hand is in
+// registers, at most PK packs a thread, so it is read once; the packs of the
+// batch's next live row are on their way into shared memory meanwhile (each
+// thread copies and reads back its own, so nothing but its own copies has to
+// be waited for).
+// ---------------------------------------------------------------------------
+// (max, sum) over a set of pairs, two butterflies: the maximum, then the sums
+// rescaled to it.  Every lane gets the same bits.
+__device__ __forceinline__ RowMax lanes_row_max(float m, float d, float c) {
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    // nothing finite: the pairs are (-inf, 0) or (-inf, NaN), rescaled from 0
+    d *= exp2_fast((m - (M == -INFINITY ? 0.f : M)) * c);
+    return RowMax{M, warp_sum_all(d)};
+}
+
+// Arrival at the cluster barrier that orders nothing: a releasing one would
+// wait for the CTA's stores of dlogits to reach L2.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+// Accesses under a predicate without a branch: a pack is one instruction, and
+// the branches around eight of them cost more than the packs' arithmetic.
+__device__ __forceinline__ void cp_async16_if(bool on, void *dst, const void *src) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"((uint32_t)on)
+                 : "memory");
+}
+__device__ __forceinline__ void st_stream_if(bool on, void *p, const uint4 &v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};\n\t}"
+                 ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((uint32_t)on)
+                 : "memory");
+}
+
+// A pack of -inf: what a place without a logit holds, it adds nothing.
+template <typename T> __device__ __forceinline__ uint4 no_pack() {
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+// The largest value of a set of packs (NaN are passed over; none: -inf).
+// 16-bit types compare in their own type, two at a time.
+template <int PK> __device__ __forceinline__ float packs_max(const uint4 (&raw)[PK], float) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < PK; ++k) {
+        m = fmaxf(fmaxf(m, __uint_as_float(raw[k].x)), __uint_as_float(raw[k].y));
+        m = fmaxf(fmaxf(m, __uint_as_float(raw[k].z)), __uint_as_float(raw[k].w));
+    }
+    return m;
+}
+template <int PK, typename T> __device__ __forceinline__ float packs_max(const uint4 (&raw)[PK], T) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    auto as2 = [](const uint32_t &w) { return *reinterpret_cast<const T2 *>(&w); };
+    T2 m = __hmax2(__hmax2(as2(raw[0].x), as2(raw[0].y)), __hmax2(as2(raw[0].z), as2(raw[0].w)));
+#pragma unroll
+    for (int k = 1; k < PK; ++k)
+        m = __hmax2(m, __hmax2(__hmax2(as2(raw[k].x), as2(raw[k].y)), __hmax2(as2(raw[k].z), as2(raw[k].w))));
+    const float a = IO<T>::to_f(m.x), b = IO<T>::to_f(m.y);
+    const float r = fmaxf(a, b);
+    return r != r ? -INFINITY : r;
+}
+
+// 2^((z - m) c) takes one fused multiply-add an element as 2^(z c - b), b = m c
+// rounded; what b's rounding leaves, 2^(b - m c), is one factor for all of
+// them.  For |m c| beyond binary32 (logits at the type's lowest value) the
+// difference comes first instead.
+struct Shift {
+    float b, left;
+    bool direct;
+    __device__ __forceinline__ Shift(float m, float c) {
+        const float p = m * c;
+        direct = !(fabsf(p) < INFINITY) && fabsf(m) < INFINITY;
+        b = m == -INFINITY || direct ? 0.f : p;
+        // (an infinite or NaN m reaches the sum through b)
+        left = m == -INFINITY || direct ? 1.f : exp2_fast(-fmaf(m, c, -b));
+    }
+};
+// Sum of 2^((z - m) c) over a set of packs.
+template <typename T, int PK>
+__device__ __forceinline__ float packs_sum(const uint4 (&raw)[PK], float m, float c) {
+    constexpr int H = IO2<T>::H;
+    const Shift s(m, c);
+    float2 acc = f2(0.f);
+    if (!s.direct) {
+#pragma unroll
+        for (int k = 0; k < PK; ++k) {
+            float2 v[H];
+            IO2<T>::unpack(raw[k], v);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                float2 e = __ffma2_rn(v[h], f2(c), f2(-s.b));
+                e.x = exp2_fast(e.x);
+                e.y = exp2_fast(e.y);
+                acc = __fadd2_rn(acc, e);
+            }
+        }
+        return (acc.x + acc.y) * s.left;
+    }
+#pragma unroll 1
+    for (int k = 0; k < PK; ++k) {
+        uint4 q = raw[0];
+#pragma unroll
+        for (int j = 1; j < PK; ++j)
+            if (j == k) q = raw[j];
+        float2 v[H];
+        IO2<T>::unpack(q, v);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            acc = __fadd2_rn(acc, make_float2(exp2_fast((v[h].x - m) * c), exp2_fast((v[h].y - m) * c)));
+    }
+    return acc.x + acc.y;
+}
+
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Tries of the wait for pairs still on their way after a wait gave up.
+constexpr uint32_t kDrainTries = 1u << 16;
+
+// A row as a thread sees it: its packs (k * TH apart, `mine` of them in all
+// counting from its first), and its scalar element of the row's ends, if any.
+template <typename T> struct RowView {
+    const T *z, *body;
+    T *d, *out;
+    int p0, p1, mine, ns, head, tail;
+    int64_t sc;
+    bool wide;
+    __device__ __forceinline__ RowView(const LogitArgs &a, int64_t row, int rank, int log_cs, int t) {
+        constexpr int V = IO<T>::V;
+        z = static_cast<const T *>(a.z) + row * a.ldz;
+        d = a.dz ? static_cast<T *>(a.dz) + row * a.lddz : nullptr;
+        const RowCut<T> cut = cut_row(z, a.V);
+        head = cut.head;
+        tail = cut.tail;
+        p0 = cut.packs * rank >> log_cs;  // packs < 2^28, ranks <= 8
+        p1 = cut.packs * (rank + 1) >> log_cs;
+        body = z + head + (int64_t)(p0 + t) * V;
+        out = d + head + (int64_t)(p0 + t) * V;
+        mine = p1 - p0 - t;
+        ns = rank == 0 ? head + tail : 0;
+        sc = t < head ? t : a.V - tail + (t - head);
+        wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    }
+};
+
+template <typename T, bool POLICY, int TH, int PK, int MINB>
+__global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
+    logit_reg_kernel(const LogitArgs a, const int log_cs, const int batch) {
+    constexpr int CTA = TH < 128 ? 128 : TH, G = CTA / TH, NW = TH / 32, V = IO<T>::V, H = IO2<T>::H;
+    constexpr int CSMAX = 8, PAIRS = (CSMAX * NW + 31) / 32;
+    extern __shared__ __align__(16) uint4 next_row[];  // [PK][CTA]
+    // every warp of the cluster sends its pair to every CTA of it, counted on
+    // that CTA's barrier
+    __shared__ float2 pairs[2][CSMAX * NW];
+    __shared__ uint64_t arrived[2];
+    __shared__ float sh[2][2];  // the row's gradient factor; the target's logit
+    const int t = threadIdx.x % TH, lane = threadIdx.x & 31, warp = t >> 5;
+    const int cs = 1 << log_cs, rank = log_cs ? (int)cluster_rank() : 0;
+    // the first pair may go to a peer only once its barriers stand: the other
+    // half of this cluster barrier is before that
+    bool joined = log_cs == 0;
+    uint32_t phases = 0;  // bit p: the parity of arrived[p]'s next phase
+    bool broken = false;  // a pair never came: no further waits
+    if (!joined) {
+        if (threadIdx.x == 0) {
+            mbar_init(&arrived[0], 1);
+            mbar_init(&arrived[1], 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        cluster_arrive_relaxed();  // the fence has released the barriers' state
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const float c = a.scale * kLog2e;
+    const float gs = POLICY && a.grad_scale ? *a.grad_scale : 1.f;
+    int parity = 1;  // the exchange slots alternate between live rows
+    const int64_t group = (int64_t)(blockIdx.x >> log_cs) * G + threadIdx.x / TH,
+                  step = (int64_t)(gridDim.x >> log_cs) * G;
+    for (int64_t r0 = group * batch; r0 < a.rows; r0 += step * batch) {
+        // lane i keeps the target of row r0 + i
+        const bool have = lane < batch && r0 + lane < a.rows;
+        const int64_t my_target = have ? a.target[r0 + lane] : -1;
+        const bool takes_part = my_target >= 0 && my_target < a.V && !(POLICY && a.weight && a.weight[r0 + lane] == 0.f);
+        uint32_t live = __ballot_sync(0xffffffffu, takes_part);
+        uint32_t dead = __ballot_sync(0xffffffffu, have && !takes_part);
+        auto fetch = [&](int64_t row) {
+            const RowView<T> w(a, row, rank, log_cs, t);
+#pragma unroll
+            for (int k = 0; k < PK; ++k)
+                cp_async16_if(k * TH < w.mine, &next_row[k * CTA + threadIdx.x], w.body + k * TH * V);
+        };
+        auto zero_fill = [&](const RowView<T> &w) {
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            if (w.wide) {
+#pragma unroll
+                for (int k = 0; k < PK; ++k) st_stream_if(k * TH < w.mine, w.out + k * TH * V, z);
+            } else {
+                for (int k = 0; k * TH < w.mine; ++k) st_pack(w.out + k * TH * V, z, false);
+            }
+            if (t < w.ns) w.d[w.sc] = IO<T>::from_f(0.f);
+        };
+        if (live) fetch(r0 + __ffs(live) - 1);
+        for (; dead; dead &= dead - 1) {
+            const int64_t row = r0 + __ffs(dead) - 1;
+            if (t == 0 && rank == 0) {
+                if (a.logp) a.logp[row] = 0.f;
+                if (a.lse) a.lse[row] = 0.f;
+                if (POLICY) a.row_loss[row] = 0.f;
+            }
+            if (POLICY && a.dz) zero_fill(RowView<T>(a, row, rank, log_cs, t));
+        }
+        while (live) {
+            const int at = __ffs(live) - 1;
+            const int64_t row = r0 + at, tgt = __shfl_sync(0xffffffffu, my_target, at);
+            live &= live - 1;
+            parity ^= 1;
+            const RowView<T> w(a, row, rank, log_cs, t);
+            float zs = 0.f, za = 0.f;
+            if (t < w.ns) zs = IO<T>::to_f(w.z[w.sc]);
+            RowTerms terms = {};
+            if (t == 0) {
+                za = IO<T>::to_f(w.z[tgt]);
+                if (POLICY) terms = row_terms(a, row);
+            }
+            cp_async_wait();
+            uint4 raw[PK];
+#pragma unroll
+            for (int k = 0; k < PK; ++k) {
+                raw[k] = no_pack<T>();
+                if (k * TH < w.mine) raw[k] = next_row[k * CTA + threadIdx.x];
+            }
+            float m = packs_max<PK>(raw, T());
+            // the maximum is there, so the packs have left shared memory
+            asm volatile("" : "+f"(m)::"memory");
+            if (live) fetch(r0 + __ffs(live) - 1);
+            if (t < w.ns) m = fmaxf(m, zs);
+            float d = packs_sum<T, PK>(raw, m, c);
+            if (t < w.ns) d += exp2_fast((zs - (m == -INFINITY ? 0.f : m)) * c);
+            RowMax r = lanes_row_max(m, d, c);
+            if constexpr (TH > 32) {
+                if (log_cs) {
+                    if (!joined) {
+                        cluster_wait();
+                        joined = true;
+                    }
+                    uint64_t *bar = &arrived[parity];
+                    if (threadIdx.x == 0 && !broken) mbar_arrive_expect_tx(bar, (uint32_t)(cs * NW * sizeof(float2)));
+                    // lane q sends the warp's pair to CTA q.  A peer sends the
+                    // pair of the next row but one, into the same place, only
+                    // after it has this warp's pair of the next row, which
+                    // this warp sends after it has read the place
+                    if (lane < cs) send_pair(&pairs[parity][rank * NW + warp], make_float2(r.m, r.d), bar, (uint32_t)lane);
+                    const uint32_t ph = phases >> parity & 1u;
+                    phases ^= 1u << parity;
+                    if (!broken && !mbar_wait_bounded(bar, ph, a.wait_limit)) {
+                        // the wait gave up: say so, and stay for what is still
+                        // on its way here
+                        if (a.fault && lane == 0) atomicOr(a.fault, (unsigned)FAULT_WAIT);
+                        broken = !mbar_wait_bounded(bar, ph, kDrainTries);
+                        if (broken && a.fault && lane == 0) atomicOr(a.fault, (unsigned)FAULT_DRAIN);
+                    }
+                } else {
+                    if (lane == 0) pairs[parity][warp] = make_float2(r.m, r.d);
+                    __syncthreads();
+                }
+                float pm[PAIRS], pd[PAIRS], M = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    const int q = i * 32 + lane;
+                    const float2 v = q < cs * NW ? pairs[parity][q] : make_float2(-INFINITY, 0.f);
+                    pm[i] = v.x;
+                    pd[i] = v.y;
+                    M = fmaxf(M, v.x);
+                }
+                const float mr = M == -INFINITY ? 0.f : M;
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) s += pd[i] * exp2_fast((pm[i] - mr) * c);
+                r = lanes_row_max(M, s, c);
+            }
+            float g = 0.f;
+            if (t == 0) {
+                float l = 0.f;
+                finish_row<POLICY>(a, row, r, za, rank == 0, terms, &l, &g);
+                g *= gs * a.scale;
+                if (POLICY && TH > 32) {
+                    sh[parity][0] = g;
+                    sh[parity][1] = za;
+                }
+            }
+            if (POLICY && a.dz) {
+                if constexpr (TH > 32) {
+                    __syncthreads();
+                    g = sh[parity][0];
+                    za = sh[parity][1];
+                } else {
+                    g = __shfl_sync(0xffffffffu, g, 0);
+                    za = __shfl_sync(0xffffffffu, za, 0);
+                }
+                if (g == 0.f) {
+                    zero_fill(w);
+                    continue;
+                }
+                const float f = -g / r.d;
+                const Shift sf(r.m, c);
+                if (w.wide && !sf.direct) {
+#pragma unroll
+                    for (int k = 0; k < PK; ++k)
+                        st_stream_if(k * TH < w.mine, w.out + k * TH * V, grad_pack1<T>(raw[k], c, -sf.b, f * sf.left));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < PK; ++k)
+                        if (k * TH < w.mine)
+                            st_pack(w.out + k * TH * V,
+                                    sf.direct ? grad_pack<T>(raw[k], 1.f, -r.m, c, f)
+                                              : grad_pack1<T>(raw[k], c, -sf.b, f * sf.left),
+                                    w.wide);
+                }
+                if (t < w.ns) w.d[w.sc] = IO<T>::from_f(grad_one(zs, 1.f, -r.m, c, f));
+                // the target's own element, by the thread that wrote it just now
+                const int ip = (int)(tgt - w.head) / V;
+                const bool scalar = tgt < w.head || tgt >= a.V - w.tail;
+                const bool owner = scalar ? (t < w.ns && w.sc == tgt) : (ip >= w.p0 && ip < w.p1 && (ip - w.p0) % TH == t);
+                if (owner) w.d[tgt] = IO<T>::from_f(g + grad_one(za, 1.f, -r.m, c, f));
+            }
+        }
+    }
+    if (log_cs) {
+        // no CTA leaves before its peers have sent all they send
+        if (!joined) cluster_wait();
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Log-probabilities alone, rows longer than a CTA's registers: nothing of the
+// row is needed again, so a CTA passes over it in segments of TH x PK packs
+// with a running (max, sum) per thread, the next segment (of this row or of
+// the batch's next live one) on its way meanwhile; one exchange a row.
+// ---------------------------------------------------------------------------
+template <typename T, int TH, int PK, int MINB>
+__global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, const int batch) {
+    constexpr int NW = TH / 32, V = IO<T>::V;
+    extern __shared__ __align__(16) uint4 next_row[];  // [PK][TH]
+    __shared__ float2 slot[2][NW];
+    const int t = threadIdx.x, lane = t & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float c = a.scale * kLog2e;
+    int parity = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * batch; r0 < a.rows; r0 += (int64_t)gridDim.x * batch) {
+        const bool have = lane < batch && r0 + lane < a.rows;
+        const int64_t my_target = have ? a.target[r0 + lane] : -1;
+        const bool takes_part = my_target >= 0 && my_target < a.V;
+        uint32_t live = __ballot_sync(0xffffffffu, takes_part);
+        if (t < 32 && have && !takes_part) {
+            if (a.logp) a.logp[r0 + lane] = 0.f;
+            if (a.lse) a.lse[r0 + lane] = 0.f;
+        }
+        auto fetch = [&](int64_t row, int seg) {
+            const RowView<T> w(a, row, 0, 0, t);
+#pragma unroll
+            for (int k = 0; k < PK; ++k) {
+                const int at = (seg * PK + k) * TH;
+                cp_async16_if(at < w.mine, &next_row[k * TH + t], w.body + (int64_t)at * V);
+            }
+        };
+        if (live) fetch(r0 + __ffs(live) - 1, 0);
+        while (live) {
+            const int at = __ffs(live) - 1;
+            const int64_t row = r0 + at, tgt = __shfl_sync(0xffffffffu, my_target, at);
+            live &= live - 1;
+            const RowView<T> w(a, row, 0, 0, t);
+            float za = 0.f;
+            RowMax r{-INFINITY, 0.f};
+            if (t < w.ns) {
+                const float z = IO<T>::to_f(w.z[w.sc]);
+                r.m = z != z ? -INFINITY : z;
+                r.d = exp2_fast((z - (r.m == -INFINITY ? 0.f : r.m)) * c);
+            }
+            if (t == 0) za = IO<T>::to_f(w.z[tgt]);
+            const int segs = w.p1 > 0 ? (w.p1 + TH * PK - 1) / (TH * PK) : 1;
+            for (int seg = 0; seg < segs; ++seg) {
+                cp_async_wait();
+                uint4 raw[PK];
+#pragma unroll
+                for (int k = 0; k < PK; ++k) {
+                    raw[k] = no_pack<T>();
+                    if ((seg * PK + k) * TH < w.mine) raw[k] = next_row[k * TH + t];
+                }
+                float m = packs_max<PK>(raw, T());
+                // the maximum is there, so the packs have left shared memory
+                asm volatile("" : "+f"(m)::"memory");
+                if (seg + 1 < segs)
+                    fetch(row, seg + 1);
+                else if (live)
+                    fetch(r0 + __ffs(live) - 1, 0);
+                // a segment below the running maximum is summed from that
+                m = fmaxf(m, r.m);
+                if (m > r.m) {
+                    r.d *= exp2_fast((r.m - m) * c);
+                    r.m = m;
+                }
+                r.d += packs_sum<T, PK>(raw, m, c);
+            }
+            r = lanes_row_max(r.m, r.d, c);
+            if (lane == 0) slot[parity][t >> 5] = make_float2(r.m, r.d);
+            __syncthreads();
+            const float2 v = lane < NW ? slot[parity][lane] : make_float2(-INFINITY, 0.f);
+            r = lanes_row_max(v.x, v.y, c);
+            parity ^= 1;
+            float l, g;
+            if (t == 0) finish_row<false>(a, row, r, za, true, RowTerms{}, &l, &g);
+        }
     }
 }
 
@@ -385,20 +861,13 @@ __global__ void __launch_bounds__(256) logit_grad_kernel(const LogitArgs a, cons
 // ---------------------------------------------------------------------------
 // Launchers, one instance of each per storage type (logits_<type>.cu).
 // ---------------------------------------------------------------------------
-template <typename T, bool POLICY>
-cudaError_t launch_logit_rows_t(const LogitArgs &a, int sms, cudaStream_t s, Plan *p) {
-    // a row over more CTAs while the SMs are not twice covered and each CTA
-    // keeps a pack per thread
-    int cs = 1;
-    while (cs < 8 && a.rows * cs < 2 * (int64_t)sms && a.V / IO<T>::V >= 2 * cs * (int64_t)kLogitThreads) cs *= 2;
+template <typename K, typename... Args>
+cudaError_t launch_clusters(K kernel, int64_t rows, int cs, int threads, size_t smem, cudaStream_t s, Args... args) {
     const int64_t most = 0x7fffffff / cs;
-    p->kind = cs > 1 ? PLAN_CLUSTER : PLAN_CTA;
-    p->threads = kLogitThreads;
-    p->packs = 1;
-    p->groups = cs > 1 ? cs : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.rows < most ? a.rows : most) * cs));
-    cfg.blockDim = dim3(kLogitThreads);
+    cfg.gridDim = dim3((unsigned)((rows < most ? rows : most) * cs));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -409,8 +878,79 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, int sms, cudaStream_t s, Pla
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, logit_rows_kernel<T, POLICY>, a, cs);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// Batches per resident group: at 2048 x 50001 bf16 with its gradient 86.0 us
+// at three, 87.8 at six and 96.4 at ten (each batch starts with nothing on its
+// way); at 4096 x 131072 with 30 % of the rows taking no part 296, 288 and 285.
+constexpr int kTurns = 4;
+
+template <typename T, bool POLICY, int TH, int PK, int MINB>
+cudaError_t launch_logit_reg(const LogitArgs &a, int cs, int sms, cudaStream_t s, Plan *p) {
+    constexpr int CTA = TH < 128 ? 128 : TH, G = CTA / TH;
+    constexpr size_t smem = (size_t)PK * CTA * 16;
+    auto kernel = logit_reg_kernel<T, POLICY, TH, PK, MINB>;
+    int per_sm = 0;
+    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), CTA, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    p->kind = cs > 1 ? PLAN_CLUSTER : TH == 32 ? PLAN_WARP : PLAN_CTA;
+    p->threads = CTA;
+    p->packs = PK;
+    p->groups = cs > 1 ? cs : 0;
+    // rows per batch: the most that leaves the resident groups kTurns each,
+    // which evens out rows that take no part
+    const int64_t groups = (int64_t)sms * per_sm / cs * G;
+    int64_t batch = a.rows / (groups * kTurns);
+    batch = batch < 1 ? 1 : batch > 32 ? 32 : batch;
+    int log_cs = 0;
+    while (1 << log_cs < cs) ++log_cs;
+    return launch_clusters(kernel, (a.rows + batch * G - 1) / (batch * G), cs, CTA, smem, s, a, log_cs, (int)batch);
+}
+
+template <typename T, int TH, int PK, int MINB>
+cudaError_t launch_logit_seg(const LogitArgs &a, int sms, cudaStream_t s, Plan *p) {
+    constexpr size_t smem = (size_t)PK * TH * 16;
+    auto kernel = logit_seg_kernel<T, TH, PK, MINB>;
+    int per_sm = 0;
+    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), TH, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    p->kind = PLAN_CTA;
+    p->threads = TH;
+    p->packs = PK;
+    int64_t batch = a.rows / ((int64_t)sms * per_sm * kTurns);
+    batch = batch < 1 ? 1 : batch > 32 ? 32 : batch;
+    const int64_t n = (a.rows + batch - 1) / batch;
+    return launch_row(kernel, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), (unsigned)TH, smem, s, a, (int)batch);
+}
+
+template <typename T, bool POLICY>
+cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaStream_t s, Plan *p) {
+    const int64_t packs = a.V / IO<T>::V;
+    // a row over more CTAs while the SMs are not twice covered and each CTA
+    // keeps a pack per thread
+    auto spread = [&](int cs, int threads) {
+        while (cs < 8 && a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * (int64_t)threads) cs *= 2;
+        return cs;
+    };
+    if (!stream) {
+        if (packs <= 32 * 4) return launch_logit_reg<T, POLICY, 32, 4, 1>(a, 1, sms, s, p);
+        if (packs <= 32 * 8 && a.rows >= 4 * (int64_t)sms) return launch_logit_reg<T, POLICY, 32, 8, 1>(a, 1, sms, s, p);
+        if (packs <= 128 * 8 && a.rows >= 2 * (int64_t)sms) return launch_logit_reg<T, POLICY, 128, 8, 8>(a, 1, sms, s, p);
+        if (!POLICY && packs > 256 * 8 && a.rows >= 2 * (int64_t)sms) return launch_logit_seg<T, 256, 8, 4>(a, sms, s, p);
+        int cs = 1;
+        while (cs < 8 && packs > 256 * 8 * cs) cs *= 2;
+        if (packs <= 256 * 8 * cs)
+            return launch_logit_reg<T, POLICY, 256, 8, 4>(a, spread(cs, 256), sms, s, p);
+        if (packs <= 8 * 512 * 8) return launch_logit_reg<T, POLICY, 512, 8, 2>(a, 8, sms, s, p);
+    }
+    const int cs = spread(1, kLogitThreads);
+    p->kind = PLAN_GENERIC;
+    p->threads = kLogitThreads;
+    p->packs = 1;
+    p->groups = cs > 1 ? cs : 0;
+    return launch_clusters(logit_rows_kernel<T, POLICY>, a.rows, cs, kLogitThreads, 0, s, a, cs);
 }
 
 template <typename T> cudaError_t launch_logit_grad_t(const LogitArgs &a, cudaStream_t s) {

@@ -312,15 +312,17 @@ constexpr int64_t kDropMaxParts = 608;
         }                                                     \
     }
 #define NRM_UNPAREN(...) __VA_ARGS__
-// vec: rows of whole 16-byte packs on 16-byte boundaries; longrow: the plan
-// for rows that outgrow the registers (any length).  *p is what ran; *parts
-// the rows of dw partials left in a.part.
-NRM_BY_TYPE(launch_dropout, (const DropoutArgs &a, bool vec, int sms, cudaStream_t s), (a, vec, sms, s))
-NRM_BY_TYPE(launch_drop_fwd, (const DropRmsArgs &a, bool vec, bool longrow, int sms, cudaStream_t s, Plan *p),
-            (a, vec, longrow, sms, s, p))
+// How a call's rows lie in memory (drop.cuh): MAP_V rows of whole 16-byte
+// packs on 16-byte boundaries, MAP_A rows whose tensors share their alignment,
+// MAP_S anything else.  longrow: the plan for rows that outgrow the registers
+// (any length).  *p is what ran; *parts the rows of dw partials left in a.part.
+enum Map { MAP_V = 0, MAP_A = 1, MAP_S = 2 };
+NRM_BY_TYPE(launch_dropout, (const DropoutArgs &a, int map, int sms, cudaStream_t s), (a, map, sms, s))
+NRM_BY_TYPE(launch_drop_fwd, (const DropRmsArgs &a, int map, bool longrow, int sms, cudaStream_t s, Plan *p),
+            (a, map, longrow, sms, s, p))
 NRM_BY_TYPE(launch_drop_bwd,
-            (const DropRmsBwdArgs &a, bool vec, bool longrow, int sms, cudaStream_t s, Plan *p, int64_t *parts),
-            (a, vec, longrow, sms, s, p, parts))
+            (const DropRmsBwdArgs &a, int map, bool longrow, int sms, cudaStream_t s, Plan *p, int64_t *parts),
+            (a, map, longrow, sms, s, p, parts))
 
 // Rows of logits (logits.cuh).  scale: the inverse temperature.
 struct LogitArgs {
@@ -333,16 +335,19 @@ struct LogitArgs {
     // policy loss
     const float *old, *adv, *weight, *ref;  // weight, ref may be NULL
     float kl, ratio_lo, ratio_hi;
-    double log_lo, log_hi;      // logarithms of the ratio's bounds
+    float log_lo, log_hi;       // logarithms of the ratio's bounds
     const float *grad_scale;    // [1], or NULL (= 1)
     float *row_loss;            // [rows] workspace
     void *dz;                   // NULL: no gradient
     int64_t lddz;
     // gradient of a given slope
     const float *dlogp, *lse_in;
+    unsigned *fault;            // device fault word, or NULL
+    unsigned wait_limit;        // tries per bounded wait
 };
-NRM_BY_TYPE(launch_logit_rows, (const LogitArgs &a, bool policy, int sms, cudaStream_t s, Plan *p),
-            (a, policy, sms, s, p))
+// stream: the plan for rows that outgrow a cluster's registers (any length).
+NRM_BY_TYPE(launch_logit_rows, (const LogitArgs &a, bool policy, bool stream, int sms, cudaStream_t s, Plan *p),
+            (a, policy, stream, sms, s, p))
 NRM_BY_TYPE(launch_logit_grad, (const LogitArgs &a, cudaStream_t s), (a, s))
 cudaError_t launch_loss_fold(const float *row_loss, float *loss, int64_t rows, cudaStream_t s);
 #undef NRM_UNPAREN

@@ -126,6 +126,29 @@ def test_rows_that_take_no_part_and_masked_entries(v, dtype):
     check_grad(z[live], t[live], lse[live], dlogp[live], 1.0, dz[live])
 
 
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,v", [(6, 40), (6, 1003), (6, 5000), (3, 40001), (2, 300001)])
+def test_masks_of_the_lowest_value(rows, v, dtype):
+    # the type's lowest value instead of -inf: where it is all a row has, the
+    # row is uniform; elsewhere it has probability 0
+    low = torch.finfo(dtype).min
+    z, t = make(rows, v, dtype, 8)
+    z[0] = low
+    z[1, ::3] = low
+    t[1] = 1
+    logp, lse = nrm.logprob_fwd(z, t)
+    # -log v at a lse of -3.4e38 is all rounding there; logp keeps it
+    assert abs(float(logp[0]) + np.log(v)) < (v / 512 + 120) * R.U + 1e-6
+    check_logprob(z[1:], t[1:], 1.0, (logp[1:], lse[1:]))
+    one = torch.ones(rows, device="cuda")
+    loss, lp, dz = nrm.policy_loss(z, t, logp, -one, one)
+    assert torch.equal(lp, logp)
+    ref = np.full(v, -1.0 / v)
+    ref[int(t[0])] += 1.0
+    R.check(dz[0], ref, R.out_bound(dtype, ref, np.abs(ref) * (v / 512 + 200) * R.U), "dlogits")
+    assert not (dz[1, ::3] != 0).any()
+
+
 def test_nan_and_infinite_logits_are_not_hidden():
     z, t = make(4, 5000, torch.float32)
     z[0, 4000] = float("nan")
@@ -288,6 +311,24 @@ def test_leading_dimensions_stream_and_graph():
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(cap, want))
+
+
+def test_bounded_waits_give_up_and_report():
+    # wait limit 0: every wait for a peer's pair gives up at once, raises the
+    # fault bit and the kernel ends; the next call is unaffected
+    args = policy_inputs(5, 50001, torch.bfloat16, 6)
+    assert nrm.device_fault(clear=True) == 0
+    old = nrm.set_wait_limit(0)
+    try:
+        nrm.policy_loss(*args, 0.2, 0.3, 0.1)
+        plan = nrm.last_plan()
+        torch.cuda.synchronize()
+        bits = nrm.device_fault(clear=True)
+    finally:
+        nrm.set_wait_limit(old)
+    assert plan[0] == nrm.PLAN_CLUSTER and bits & 1
+    check_policy(*args, 0.2, 0.3, 0.1, 1.0, nrm.policy_loss(*args, 0.2, 0.3, 0.1))
+    assert nrm.device_fault(clear=True) == 0
 
 
 def test_refused_tensors():
