@@ -549,64 +549,84 @@ def _on_stream(stream, t):
     return torch.cuda.stream(stream)
 
 
-# The current stream's handle as an integer, without building a Stream object
-# (3 us a call on a Grace core).
+# These calls take 10 to 20 us of kernel at ordinary sizes, so their checks are
+# written for few attribute reads (0.1 us each): shape, type and device index
+# are taken from the first tensor once.
+_F32 = torch.float32
+# The current stream's handle and the current device as integers, without
+# building Stream and device objects (3 us a call on a Grace core).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _fns = {}
 
 
-def _launch(name, device, *args):
-    """One C call on `device`'s current stream."""
+def _launch(name, dev, *args):
+    """One C call on the current stream of device number `dev`."""
     f = _fns.get(name)
     if f is None:
         f = _fns[name] = getattr(lib(), name)
-    i = device.index
-    if i == torch.cuda.current_device():
-        st = f(*args, _raw_stream(i))
+    if dev == _current():
+        st = f(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(i):
-            st = f(*args, _raw_stream(i))
+        with torch.cuda.device(dev):
+            st = f(*args, _raw_stream(dev))
     if st != 0:
         raise NrmError(st, name)
 
 
-def _like(t, x, name):
+def _code(dtype):
+    code = _DT.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _match(t, shape, dtype, dev, name):
+    """Row stride of a tensor that has to be like the first one."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on device {dev}")
+    return shape[-1] if t.is_contiguous() else _rows(t, name)[2]
+
+
+def _like(t, x, shape, dtype, dev, name):
     """`t`, or a new contiguous tensor like x; and its row stride."""
     if t is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format), x.shape[-1]
-    return t, _same_rows(t, x, name)
+        return torch.empty_like(x, memory_format=torch.contiguous_format), shape[-1]
+    return t, _match(t, shape, dtype, dev, name)
 
 
-def _row_values(t, x, name, dtype=torch.float32):
-    """One value per row of x."""
-    if t.dtype != dtype or t.device != x.device or t.shape != x.shape[:-1] or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(x.shape[:-1])} {dtype} tensor on {x.device}")
+def _flat(t, shape, dtype, dev, name):
+    """A contiguous tensor of exactly this shape and type."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on device {dev}")
     return t
 
 
-def _new_row_values(like):
-    return torch.empty_like(like, dtype=torch.float32)
+def _weight(w, n, dtype, dev, name):
+    if w is not None and (w.dtype is not dtype or w.get_device() != dev or w.numel() != n or not w.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous [{n}] {dtype} on device {dev}")
+    return w
 
 
-def _one_value(t, x, name, dtype):
+def _one_value(t, dtype, dev, name):
+    """Address of one value on the device, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != x.device or t.numel() != 1:
-        raise ValueError(f"{name} must be one {dtype} value on {x.device}")
-    return t
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != 1:
+        raise ValueError(f"{name} must be one {dtype} value on device {dev}")
+    return t.data_ptr()
 
 
-def _scratch_bytes(workspace, need, device):
+def _scratch_bytes(workspace, need, x):
+    """Address and size of a workspace, and what keeps it alive."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {device}")
-    return workspace
+        workspace = torch.empty(need if need > 16 else 16, dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the tensors' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _drop(x, p, seed, offset, offset_dev):
-    return (p, seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF,
-            _ptr(_one_value(offset_dev, x, "offset_dev", torch.int64)))
+_M64 = 0xFFFFFFFFFFFFFFFF
 
 
 def dropout_fwd(x, p, seed, offset=0, *, out=None, offset_dev=None, stream=None):
@@ -619,9 +639,11 @@ def dropout_fwd(x, p, seed, offset=0, *, out=None, offset_dev=None, stream=None)
         with _on_stream(stream, x):
             return dropout_fwd(x, p, seed, offset, out=out, offset_dev=offset_dev)
     rows, n, ldx = _rows(x, "x")
-    y, ldy = _like(out, x, "out")
-    _launch("dropout_fwd_ld", x.device, x.data_ptr(), ldx, y.data_ptr(), ldy, rows, n,
-            *_drop(x, p, seed, offset, offset_dev), _dtype_code(x))
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    code = _code(dtype)
+    y, ldy = _like(out, x, shape, dtype, dev, "out")
+    _launch("dropout_fwd_ld", dev, x.data_ptr(), ldx, y.data_ptr(), ldy, rows, n, p, seed & _M64,
+            offset & _M64, _one_value(offset_dev, torch.int64, dev, "offset_dev"), code)
     return y
 
 
@@ -643,17 +665,19 @@ def dropout_add_rms_fwd(x, residual, w=None, p=0.0, seed=0, offset=0, eps=1e-6, 
                                        residual_out=residual_out, out=out, rstd=rstd,
                                        offset_dev=offset_dev)
     rows, n, ldx = _rows(x, "x")
-    ldr = _same_rows(residual, x, "residual")
-    w = _param(w, n, x.dtype, x.device, "w")
-    ro, ldro = _like(residual_out, x, "residual_out")
-    y, ldy = _like(out, x, "out")
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    code = _code(dtype)
+    ldr = _match(residual, shape, dtype, dev, "residual")
+    w = _weight(w, n, dtype, dev, "w")
+    ro, ldro = _like(residual_out, x, shape, dtype, dev, "residual_out")
+    y, ldy = _like(out, x, shape, dtype, dev, "out")
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty(shape[:-1], dtype=_F32, device=x.device)
     else:
-        _row_values(rstd, x, "rstd")
-    _launch("dropout_add_rms_fwd_ld", x.device, x.data_ptr(), ldx, residual.data_ptr(), ldr, _ptr(w),
-            ro.data_ptr(), ldro, y.data_ptr(), ldy, rstd.data_ptr(), rows, n,
-            *_drop(x, p, seed, offset, offset_dev), eps, _dtype_code(x))
+        _flat(rstd, shape[:-1], _F32, dev, "rstd")
+    _launch("dropout_add_rms_fwd_ld", dev, x.data_ptr(), ldx, residual.data_ptr(), ldr, _ptr(w),
+            ro.data_ptr(), ldro, y.data_ptr(), ldy, rstd.data_ptr(), rows, n, p, seed & _M64,
+            offset & _M64, _one_value(offset_dev, torch.int64, dev, "offset_dev"), eps, code)
     return ro, y, rstd
 
 
@@ -677,26 +701,25 @@ def dropout_add_rms_bwd(dy, residual_out, rstd, w=None, p=0.0, seed=0, offset=0,
                                        dw=dw, want_dw=want_dw, workspace=workspace,
                                        offset_dev=offset_dev)
     rows, n, lddy = _rows(dy, "dy")
-    ldh = _same_rows(residual_out, dy, "residual_out")
-    _row_values(rstd, dy, "rstd")
-    w = _param(w, n, dy.dtype, dy.device, "w")
-    ldu = n if dresidual_out is None else _same_rows(dresidual_out, dy, "dresidual_out")
-    dresidual, lddr = _like(dresidual, dy, "dresidual")
+    shape, dtype, dev = dy.shape, dy.dtype, dy.get_device()
+    code = _code(dtype)
+    ldh = _match(residual_out, shape, dtype, dev, "residual_out")
+    _flat(rstd, shape[:-1], _F32, dev, "rstd")
+    w = _weight(w, n, dtype, dev, "w")
+    ldu = n if dresidual_out is None else _match(dresidual_out, shape, dtype, dev, "dresidual_out")
+    dresidual, lddr = _like(dresidual, dy, shape, dtype, dev, "dresidual")
     same = dx is None and p == 0
     if not same:
-        dx, lddx = _like(dx, dy, "dx")
+        dx, lddx = _like(dx, dy, shape, dtype, dev, "dx")
     if dw is not None:
-        if dw.dtype != torch.float32 or dw.numel() != n or dw.device != dy.device or not dw.is_contiguous():
-            raise ValueError(f"dw must be [{n}] float32 on {dy.device}")
+        _weight(dw, n, _F32, dev, "dw")
     elif want_dw if want_dw is not None else w is not None:
-        dw = torch.empty(n, dtype=torch.float32, device=dy.device)
-    code = _dtype_code(dy)
-    workspace = _scratch_bytes(workspace, lib().dropout_add_rms_bwd_workspace_size(rows, n, code), dy.device)
-    _launch("dropout_add_rms_bwd_ld", dy.device, dy.data_ptr(), lddy, residual_out.data_ptr(), ldh,
+        dw = torch.empty(n, dtype=_F32, device=dy.device)
+    ws, wsb, workspace = _scratch_bytes(workspace, lib().dropout_add_rms_bwd_workspace_size(rows, n, code), dy)
+    _launch("dropout_add_rms_bwd_ld", dev, dy.data_ptr(), lddy, residual_out.data_ptr(), ldh,
             rstd.data_ptr(), _ptr(w), _ptr(dresidual_out), ldu, None if same else dx.data_ptr(),
-            n if same else lddx, dresidual.data_ptr(), lddr, _ptr(dw), rows, n,
-            *_drop(dy, p, seed, offset, offset_dev), code, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            n if same else lddx, dresidual.data_ptr(), lddr, _ptr(dw), rows, n, p, seed & _M64,
+            offset & _M64, _one_value(offset_dev, torch.int64, dev, "offset_dev"), code, ws, wsb)
     return (dresidual if same else dx), dresidual, dw
 
 
@@ -708,12 +731,13 @@ def logprob_fwd(logits, targets, inv_temp=1.0, *, logp=None, lse=None, stream=No
         with _on_stream(stream, logits):
             return logprob_fwd(logits, targets, inv_temp, logp=logp, lse=lse)
     rows, v, ldl = _rows(logits, "logits")
-    _row_values(targets, logits, "targets", torch.int64)
-    dev = logits.device
-    logp = _new_row_values(targets) if logp is None else _row_values(logp, logits, "logp")
-    lse = _new_row_values(targets) if lse is None else _row_values(lse, logits, "lse")
+    shape, dev = logits.shape[:-1], logits.get_device()
+    code = _code(logits.dtype)
+    _flat(targets, shape, torch.int64, dev, "targets")
+    logp = torch.empty_like(targets, dtype=_F32) if logp is None else _flat(logp, shape, _F32, dev, "logp")
+    lse = torch.empty_like(targets, dtype=_F32) if lse is None else _flat(lse, shape, _F32, dev, "lse")
     _launch("logprob_fwd_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(),
-            lse.data_ptr(), rows, v, inv_temp, _dtype_code(logits))
+            lse.data_ptr(), rows, v, inv_temp, code)
     return logp, lse
 
 
@@ -725,13 +749,15 @@ def logprob_bwd(dlogp, logits, targets, lse, inv_temp=1.0, *, out=None, stream=N
         with _on_stream(stream, logits):
             return logprob_bwd(dlogp, logits, targets, lse, inv_temp, out=out)
     rows, v, ldl = _rows(logits, "logits")
-    _row_values(dlogp, logits, "dlogp")
-    _row_values(targets, logits, "targets", torch.int64)
-    _row_values(lse, logits, "lse")
-    out, lddl = _like(out, logits, "out")
-    _launch("logprob_bwd_ld", logits.device, dlogp.data_ptr(), logits.data_ptr(), ldl,
-            targets.data_ptr(), lse.data_ptr(), out.data_ptr(), lddl, rows, v, inv_temp,
-            _dtype_code(logits))
+    shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
+    code = _code(dtype)
+    per_row = shape[:-1]
+    _flat(dlogp, per_row, _F32, dev, "dlogp")
+    _flat(targets, per_row, torch.int64, dev, "targets")
+    _flat(lse, per_row, _F32, dev, "lse")
+    out, lddl = _like(out, logits, shape, dtype, dev, "out")
+    _launch("logprob_bwd_ld", dev, dlogp.data_ptr(), logits.data_ptr(), ldl, targets.data_ptr(),
+            lse.data_ptr(), out.data_ptr(), lddl, rows, v, inv_temp, code)
     return out
 
 
@@ -757,24 +783,26 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
                                clip_high, kl_coef, inv_temp, grad_scale=grad_scale,
                                want_grad=want_grad, out=out, logp=logp, workspace=workspace)
     rows, v, ldl = _rows(logits, "logits")
-    _row_values(targets, logits, "targets", torch.int64)
-    _row_values(old_logp, logits, "old_logp")
-    _row_values(advantages, logits, "advantages")
+    shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
+    code = _code(dtype)
+    per_row = shape[:-1]
+    _flat(targets, per_row, torch.int64, dev, "targets")
+    _flat(old_logp, per_row, _F32, dev, "old_logp")
+    _flat(advantages, per_row, _F32, dev, "advantages")
     if weights is not None:
-        _row_values(weights, logits, "weights")
+        _flat(weights, per_row, _F32, dev, "weights")
     if ref_logp is not None:
-        _row_values(ref_logp, logits, "ref_logp")
-    _one_value(grad_scale, logits, "grad_scale", torch.float32)
-    dev, lddl = logits.device, v
-    logp = _new_row_values(targets) if logp is None else _row_values(logp, logits, "logp")
-    loss = torch.empty((), dtype=torch.float32, device=dev)
+        _flat(ref_logp, per_row, _F32, dev, "ref_logp")
+    logp = torch.empty_like(targets, dtype=_F32) if logp is None else _flat(logp, per_row, _F32, dev, "logp")
+    loss = torch.empty((), dtype=_F32, device=logits.device)
+    lddl = v
     if want_grad or out is not None:
-        out, lddl = _like(out, logits, "out")
-    workspace = _scratch_bytes(workspace, 4 * rows + 16, dev)
+        out, lddl = _like(out, logits, shape, dtype, dev, "out")
+    ws, wsb, workspace = _scratch_bytes(workspace, 4 * rows + 16, logits)
     _launch("policy_loss_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), old_logp.data_ptr(),
             advantages.data_ptr(), _ptr(weights), _ptr(ref_logp), clip_low, clip_high, kl_coef,
-            inv_temp, _ptr(grad_scale), loss.data_ptr(), logp.data_ptr(), _ptr(out), lddl, rows, v,
-            _dtype_code(logits), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            inv_temp, _one_value(grad_scale, _F32, dev, "grad_scale"), loss.data_ptr(),
+            logp.data_ptr(), _ptr(out), lddl, rows, v, code, ws, wsb)
     return loss, logp, out
 
 

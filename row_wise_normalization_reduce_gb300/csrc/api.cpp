@@ -1029,6 +1029,9 @@ int drop_args(int64_t rows, int64_t N, double p, uint64_t seed, uint64_t offset,
     d->offset_dev = offset_dev;
     d->on = T > 0;
     d->bar = (uint32_t)((T << 16) - 1);  // T = 65536: no word exceeds it
+    d->low2 = (uint32_t)(T & 0x7fff) * 0x10001u;
+    d->any2 = T < 65536 ? 0x80008000u : 0u;
+    d->top = (T & 0x8000) != 0;
     d->scale = T < 65536 ? (float)(65536.0 / (double)(65536 - T)) : 0.f;
     return NRM_OK;
 }

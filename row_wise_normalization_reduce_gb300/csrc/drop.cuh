@@ -98,12 +98,20 @@ template <typename T, int MAP> struct Keep {
     }
 };
 
-__device__ __forceinline__ uint32_t keep_byte(const uint4 &w, uint32_t bar) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-    uint32_t m = 0;
+// The 8 keep bits of a block, bit j for number j.  Two numbers are compared
+// with T at a time: with H the halves' top bits, (x | H) - (T & ~H) borrows
+// nothing across the halves, and its top bit says x & ~H >= T & ~H.
+__device__ __forceinline__ uint32_t keep_byte(const uint4 &w, const DropArgs &d) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    uint32_t ge[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m |= (uint32_t)((j & 1 ? v[j >> 1] : v[j >> 1] << 16) > bar) << j;
-    return m;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t e = (x[i] | 0x80008000u) - d.low2;
+        ge[i] = (d.top ? x[i] & e : x[i] | e) & d.any2;
+    }
+    // the halves' bits to places 2 i and 2 i + 16, then together
+    const uint32_t t = ge[0] >> 15 | ge[1] >> 13 | ge[2] >> 11 | ge[3] >> 9;
+    return (t | t >> 15) & 0xffu;
 }
 
 // The keep sets of one row's neighbouring chunks, in order from `chunk` (the
@@ -119,44 +127,56 @@ template <typename T, int MAP> struct Masks {
         : d(d_), r(drop_row(d_, o, row)), block((uint32_t)(chunk * 32) + (threadIdx.x & 31)), prev(0), shift(shift_) {
         // columns before the row's first are nobody's: chunk 0 needs none
         if (MAP == MAP_A && shift && chunk > 0)
-            prev = keep_byte(drop_block(d, r, (uint32_t)(chunk * 32) - 1), d.bar);
+            prev = keep_byte(drop_block(d, r, (uint32_t)(chunk * 32) - 1), d);
+    }
+    // The byte of this lane's next block, and the keep set of a chunk from its
+    // lanes' bytes.
+    __device__ __forceinline__ uint32_t next_byte() {
+        const uint32_t m = keep_byte(drop_block(d, r, block), d);
+        block += 32;
+        return m;
+    }
+    __device__ __forceinline__ Keep<T, MAP> window(uint32_t mine) {
+        static_assert(!Keep<T, MAP>::WORDS && MAP != MAP_S, "shifted or binary32 rows");
+        const int lane = threadIdx.x & 31;
+        Keep<T, MAP> k;
+        // columns 8 l - 8 .. 8 l + 7, then the window at -shift
+        uint32_t two = mine << 8;
+        if (MAP == MAP_A) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+            two |= lane ? up : prev;
+            prev = __shfl_sync(0xffffffffu, mine, 31);
+        }
+        const int sh = 8 - (MAP == MAP_A ? shift : 0);
+        if constexpr (sizeof(T) == 2) {
+            k.w[0] = two >> sh;
+        } else {
+            // pack p of the chunk starts at half (p & 1) of block p / 2
+            const int at = sh + (lane & 1) * 4;
+            const uint32_t lo = __shfl_sync(0xffffffffu, two, lane >> 1) >> at;
+            const uint32_t hi = __shfl_sync(0xffffffffu, two, 16 + (lane >> 1)) >> at;
+            k.w[0] = (lo & 15u) | (hi & 15u) << 4;
+        }
+        return k;
     }
     __device__ __forceinline__ Keep<T, MAP> next() {
-        const int lane = threadIdx.x & 31;
-        const uint4 w = drop_block(d, r, block);
-        block += 32;
-        Keep<T, MAP> k;
         if constexpr (Keep<T, MAP>::WORDS) {
+            const uint4 w = drop_block(d, r, block);
+            block += 32;
+            Keep<T, MAP> k;
             k.w[0] = w.x; k.w[1] = w.y; k.w[2] = w.z; k.w[3] = w.w;
             return k;
-        } else {
-            const uint32_t mine = keep_byte(w, d.bar);
-            if constexpr (MAP == MAP_S) {
-                uint32_t b = 0;
+        } else if constexpr (MAP == MAP_S) {
+            const int lane = threadIdx.x & 31;
+            const uint32_t mine = next_byte();
+            Keep<T, MAP> k;
+            k.w[0] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    b |= (__shfl_sync(0xffffffffu, mine, 4 * j + (lane >> 3)) >> (lane & 7) & 1u) << j;
-                k.w[0] = b;
-            } else {
-                // columns 8 l - 8 .. 8 l + 7, then the window at -shift
-                uint32_t two = mine << 8;
-                if (MAP == MAP_A) {
-                    const uint32_t up = __shfl_up_sync(0xffffffffu, mine, 1);
-                    two |= lane ? up : prev;
-                    prev = __shfl_sync(0xffffffffu, mine, 31);
-                }
-                const int sh = 8 - (MAP == MAP_A ? shift : 0);
-                if constexpr (sizeof(T) == 2) {
-                    k.w[0] = two >> sh;
-                } else {
-                    // pack p of the chunk starts at half (p & 1) of block p / 2
-                    const int at = sh + (lane & 1) * 4;
-                    const uint32_t lo = __shfl_sync(0xffffffffu, two, lane >> 1) >> at;
-                    const uint32_t hi = __shfl_sync(0xffffffffu, two, 16 + (lane >> 1)) >> at;
-                    k.w[0] = (lo & 15u) | (hi & 15u) << 4;
-                }
-            }
+            for (int j = 0; j < 8; ++j)
+                k.w[0] |= (__shfl_sync(0xffffffffu, mine, 4 * j + (lane >> 3)) >> (lane & 7) & 1u) << j;
             return k;
+        } else {
+            return window(next_byte());
         }
     }
 };
@@ -210,6 +230,15 @@ template <typename T> __device__ __forceinline__ int pack_at(int h) {
     return sizeof(T) == 2 ? 8 * lane : 128 * h + 4 * lane;
 }
 
+// Which of a pack's elements belong to the part, bit j for element j.
+template <typename T> __device__ __forceinline__ uint32_t cut_bits(int c, Part b) {
+    constexpr int V = IO<T>::V;
+    const int lo = b.head - c, hi = b.left - c;
+    uint32_t m = (1u << V) - 1u;
+    if (lo > 0) m = lo < V ? m >> lo << lo : 0u;
+    if (hi < V) m &= hi > 0 ? (1u << hi) - 1u : 0u;
+    return m;
+}
 // Elements of a cut pack, one by one; the others are zeros, and are not stored.
 template <typename T> __device__ __forceinline__ uint4 cut_load(const T *p, int c, Part b) {
     constexpr int V = IO<T>::V;
@@ -222,13 +251,13 @@ template <typename T> __device__ __forceinline__ uint4 cut_load(const T *p, int 
     else
         return make_uint4(e[0], e[1], e[2], e[3]);
 }
-template <typename T> __device__ __forceinline__ void cut_store(T *p, int c, Part b, const uint4 &v) {
+template <typename T> __device__ __forceinline__ void cut_store(T *p, uint32_t bits, const uint4 &v) {
     constexpr int V = IO<T>::V;
     Bits<T> *q = reinterpret_cast<Bits<T> *>(p);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (c + j >= b.head && c + j < b.left) q[j] = (Bits<T>)(V == 8 ? w[j >> 1] >> 16 * (j & 1) : w[j]);
+        if (bits >> j & 1u) q[j] = (Bits<T>)(V == 8 ? w[j >> 1] >> 16 * (j & 1) : w[j]);
 }
 
 // How a lane reaches its elements of U neighbouring chunks of a row: which of
@@ -237,10 +266,13 @@ template <typename T> __device__ __forceinline__ void cut_store(T *p, int c, Par
 template <typename T, int MAP, int U> struct Access {
     static constexpr int H = MAP == MAP_S ? 1 : kPacks<T>;
     uint32_t whole, some;  // bit u * H + h; `some` includes the whole ones
+    uint32_t bits;         // MAP_A: the elements of a cut pack, in the byte of its chunk (a
+                           // chunk's second pack, binary32: the upper half of it)
     int64_t ch0, n;
     int shift;
 
-    __device__ __forceinline__ Access(int64_t ch0_, int64_t n_, int shift_) : whole(0), some(0), ch0(ch0_), n(n_), shift(shift_) {
+    __device__ __forceinline__ Access(int64_t ch0_, int64_t n_, int shift_)
+        : whole(0), some(0), bits(0), ch0(ch0_), n(n_), shift(shift_) {
         if constexpr (MAP != MAP_S) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -250,6 +282,7 @@ template <typename T, int MAP, int U> struct Access {
                     const int c = pack_at<T>(h);
                     const bool s = c < b.left && c + IO<T>::V > b.head;
                     some |= (uint32_t)s << (u * H + h);
+                    if (MAP == MAP_A) bits |= cut_bits<T>(c, b) << (8 * u + 4 * h);
                     whole |= (uint32_t)(s && c >= b.head && c + IO<T>::V <= b.left) << (u * H + h);
                 }
             }
@@ -304,16 +337,14 @@ template <typename T, int MAP, int U> struct Access {
             for (int h = 0; h < H; ++h) {
                 const uint32_t bit = 1u << (u * H + h);
                 if ((some & ~whole) & bit) {
-                    const Part b = part(u);
-                    const int c = pack_at<T>(h);
+                    const uint32_t m = bits >> (8 * u + 4 * h);
 #pragma unroll
-                    for (int j = 0; j < IO<T>::V; ++j)
-                        if (c + j < b.head || c + j >= b.left) {
-                            if (sizeof(T) == 2)
-                                f.r[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
-                            else
-                                f.r[(4 * h + j) % (2 * sizeof(T))] = 0u;
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        if (sizeof(T) == 2)
+                            f.r[i] &= (m >> (2 * i) & 1u ? 0xffffu : 0u) | (m >> (2 * i + 1) & 1u ? 0xffff0000u : 0u);
+                        else if (!(m >> i & 1u))
+                            f.r[(4 * h + i) % (2 * sizeof(T))] = 0u;
+                    }
                 }
             }
         }
@@ -336,7 +367,7 @@ template <typename T, int MAP, int U> struct Access {
                 if (whole & bit)
                     st_stream(q, v);
                 else if (MAP == MAP_A && (some & bit))
-                    cut_store<T>(q, pack_at<T>(h), part(u), v);
+                    cut_store<T>(q, bits >> (8 * u + 4 * h), v);
             }
         }
     }
@@ -654,6 +685,23 @@ __device__ __forceinline__ void drop_bwd_chunk(const DropRmsBwdArgs &a, Masks<T,
     }
 }
 
+// A warp's sums of one chunk into row P of the partials: through shared memory
+// (the warp's own), so that the stores are of neighbouring columns.  c0: the
+// column of the chunk's place 0.
+template <typename T, int MAP>
+__device__ __forceinline__ void store_sums(float *stage, const float2 dw[4], float *P, int64_t c0, int64_t n) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) stage[frag_col<T, MAP>(j)] = j & 1 ? dw[j >> 1].y : dw[j >> 1].x;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t c = c0 + 32 * j + lane;
+        if (c >= 0 && c < n) P[c] = stage[32 * j + lane];
+    }
+}
+
 // Register plan: persistent groups (as the forward's), a row at a time; a
 // thread's columns are the same in every row, so dw accumulates in registers
 // and each CTA leaves one row of partial sums (folded in order by
@@ -663,6 +711,7 @@ __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a
     constexpr int G = WARP ? kRowWarps : 1;
     __shared__ float slot[2][32];
     __shared__ float part[WARP ? G - 1 : 1][WARP ? U * kChunk : 1];
+    __shared__ float stage[WARP ? 1 : 16][kChunk];
     const int nw = WARP ? 1 : (int)blockDim.x / 32;
     const int warp = WARP ? 0 : (int)threadIdx.x >> 5;
     const bool lead = WARP ? (threadIdx.x & 31) == 0 : threadIdx.x == 0;
@@ -743,7 +792,8 @@ __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a
             rstd = nr;
         }
     }
-    if (!a.dw) return;
+    // (a stepped grid is rounded up: a CTA past the last row has no partial row)
+    if (!a.dw || (int64_t)blockIdx.x * G >= a.rows) return;
     if constexpr (WARP) {
         // the CTA's warps meet in shared memory by column, added in order
         const int g = threadIdx.x >> 5;
@@ -770,12 +820,7 @@ __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a
     }
     float *P = a.part + (int64_t)blockIdx.x * a.N;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = ((int)at.ch0 + u) * kChunk + frag_col<T, MAP>(j) - at.shift;
-            if (c >= 0 && c < N) P[c] = j & 1 ? dw[u][j >> 1].y : dw[u][j >> 1].x;
-        }
+    for (int u = 0; u < U; ++u) store_sums<T, MAP>(stage[warp], dw[u], P, (at.ch0 + u) * kChunk - at.shift, a.N);
 }
 
 // Long rows (or tensors that differ in alignment): the row sums first (k per
@@ -808,6 +853,7 @@ __global__ void __launch_bounds__(512) drop_bwd_dot_kernel(const DropRmsBwdArgs 
 // the rows, so dw accumulates in registers as in the register plan.
 template <typename T, int MAP>
 __global__ void __launch_bounds__(256) drop_bwd_cols_kernel(const DropRmsBwdArgs a, const int64_t rows_per) {
+    __shared__ float stage[8][kChunk];
     pdl_wait();
     const DropCtr o = drop_ctr(a.d);
     const int64_t chunks = (a.N + kChunk - 1) / kChunk;
@@ -829,12 +875,7 @@ __global__ void __launch_bounds__(256) drop_bwd_cols_kernel(const DropRmsBwdArgs
                        static_cast<T *>(a.dx) + row * a.lddx + at.first(), 0, fd, fh, fu, fw, a.rstd[row], a.k[row], dw);
     }
     if (!a.dw) return;
-    float *P = a.part + (int64_t)blockIdx.y * a.N;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int64_t col = ch * kChunk + frag_col<T, MAP>(j);
-        if (col < a.N) P[col] = j & 1 ? dw[j >> 1].y : dw[j >> 1].x;
-    }
+    store_sums<T, MAP>(stage[threadIdx.x >> 5], dw, a.part + (int64_t)blockIdx.y * a.N, ch * kChunk, a.N);
 }
 
 // ---------------------------------------------------------------------------
@@ -947,7 +988,7 @@ cudaError_t launch_drop_bwd_k(const DropRmsBwdArgs &a, int warps, int sms, cudaS
     p->kind = WARP ? PLAN_WARP : PLAN_CTA;
     p->threads = threads;
     p->packs = U * 2 * (int)sizeof(T) / 4;
-    *parts = ctas;
+    *parts = ctas < (a.rows + G - 1) / G ? ctas : (a.rows + G - 1) / G;
     return launch_row(kernel, (unsigned)ctas, (unsigned)threads, 0, s, a);
 }
 template <typename T, int MAP>

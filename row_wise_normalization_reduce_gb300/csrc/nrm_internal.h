@@ -266,6 +266,8 @@ struct DropArgs {
     uint64_t offset;
     const int64_t *offset_dev;  // added to offset when the kernel runs, or NULL
     uint32_t bar;
+    uint32_t low2, any2;        // the bar's low 15 bits in both halves of a word; the halves' top
+    int top;                    // bits, or 0 when nothing is kept; whether the bar's bit 15 is set
     float scale;
     int on;
 };

@@ -257,6 +257,22 @@ def test_backward_workspace_is_scratch_and_graphs_can_share_it():
         assert all(same_bits(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("plan", [nrm.PLAN_AUTO, nrm.PLAN_GENERIC])
+@pytest.mark.parametrize("rows,n", [(1, 5001), (3, 4096), (9, 5001), (9, 1001), (700, 257), (1, 20001), (613, 40)])
+def test_backward_stays_inside_its_workspace(rows, n, plan):
+    nrm.force_plan(plan)
+    for dtype in (torch.float16, torch.float32):
+        _, h, w = inputs(rows, n, dtype)
+        dy = make(rows, n, dtype, 5)
+        rstd = 1 / torch.sqrt(h.float().square().mean(-1) + 1e-6)
+        need = nrm.dropout_add_rms_bwd_workspace_size(rows, n, dtype)
+        buf = torch.full((need + 16 * 4 * n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        got = nrm.dropout_add_rms_bwd(dy, h, rstd, w, 0.2, SEED, OFF, workspace=buf[:need])
+        torch.cuda.synchronize()
+        assert (buf[need:] == 0xA5).all()
+        check_bwd(dy, h, rstd, w, None, R.keep(rows, n, 0.2, SEED, OFF), 0.2, got)
+
+
 def test_side_stream():
     x, res, w = inputs(64, 1024, torch.bfloat16)
     side = torch.cuda.Stream()
