@@ -962,7 +962,8 @@ cudaError_t launch_drop_fwd_long(const DropRmsArgs &a, cudaStream_t s, Plan *p) 
     return launch_row(drop_add_rms_long_kernel<T, MAP>, (unsigned)(a.rows < 0x7fffffff ? a.rows : 0x7fffffff),
                       512u, 0, s, a);
 }
-constexpr int kDropFwdChunks = 64, kDropBwdChunks = 32;
+constexpr int kDropFwdChunks = 64;
+template <typename T> constexpr int kDropBwdChunks = sizeof(T) == 2 ? 64 : 32;
 template <typename T>
 cudaError_t launch_drop_fwd_t(const DropRmsArgs &a, int map, bool longrow, int sms, cudaStream_t s, Plan *p) {
     longrow = longrow || row_chunks<T>(a.N, map) > kDropFwdChunks;
@@ -994,17 +995,29 @@ cudaError_t launch_drop_bwd_k(const DropRmsBwdArgs &a, int warps, int sms, cudaS
 template <typename T, int MAP>
 cudaError_t launch_drop_bwd_m(const DropRmsBwdArgs &a, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
     const int C = (int)row_chunks<T>(a.N, MAP);
-    constexpr bool AHEAD = sizeof(T) == 2 && MAP == MAP_V;  // else the next row's registers spill
+    // The row ahead in registers while this one's outputs are made: 31.0 us
+    // against 32.3 at 4096 x 4096 bf16; binary32 and shifted rows have no
+    // registers left for it.
+    constexpr bool AHEAD = sizeof(T) == 2 && MAP == MAP_V;
     const int warps = (C + 1) / 2;
     if (C <= 4 && a.rows >= 4 * (int64_t)sms) {
         if (C <= 1) return launch_drop_bwd_k<T, true, 1, MAP, 128, AHEAD>(a, kRowWarps, sms, s, p, parts);
         if (C <= 2) return launch_drop_bwd_k<T, true, 2, MAP, 160, AHEAD>(a, kRowWarps, sms, s, p, parts);
         return launch_drop_bwd_k<T, true, 4, MAP, 255, AHEAD>(a, kRowWarps, sms, s, p, parts);
     }
-    if (C <= 4) return launch_drop_bwd_k<T, false, 1, MAP, 96, false>(a, C, sms, s, p, parts);
+    // a chunk a warp up to 6 chunks (10922 x 1536 bf16 34.3 us against 39.8 with
+    // two, 8192 x 2048 33.8 against 32.4)
+    if (C <= 6) return launch_drop_bwd_k<T, false, 1, MAP, 80, false>(a, C, sms, s, p, parts);
     // two CTAs per SM matter more than the row ahead: up to 8 warps have both,
-    // up to 10 the former, beyond that one CTA fits either way
+    // up to 10 the former (4096 x 5120 bf16 38.3 us against 47.1), beyond that
+    // one CTA fits either way
     if (warps > 8 && warps <= 10) return launch_drop_bwd_k<T, false, 2, MAP, 96, false>(a, warps, sms, s, p, parts);
+    if constexpr (kDropBwdChunks<T> > 32) {
+        // rows of 16-bit data beyond 32 chunks: some spills, but read once
+        // (2048 x 16384 bf16 70.5 us against 99.0 through the long-row plan)
+        if (C > 48) return launch_drop_bwd_k<T, false, 4, MAP, 128, false>(a, (C + 3) / 4, sms, s, p, parts);
+        if (C > 32) return launch_drop_bwd_k<T, false, 4, MAP, 168, false>(a, (C + 3) / 4, sms, s, p, parts);
+    }
     return launch_drop_bwd_k<T, false, 2, MAP, 128, AHEAD>(a, warps, sms, s, p, parts);
 }
 template <typename T, int MAP>
@@ -1038,7 +1051,7 @@ cudaError_t launch_drop_bwd_long(const DropRmsBwdArgs &a, int sms, cudaStream_t 
 template <typename T>
 cudaError_t launch_drop_bwd_t(const DropRmsBwdArgs &a, int map, bool longrow, int sms, cudaStream_t s,
                               Plan *p, int64_t *parts) {
-    longrow = longrow || row_chunks<T>(a.N, map) > kDropBwdChunks;
+    longrow = longrow || row_chunks<T>(a.N, map) > kDropBwdChunks<T>;
     if (map == MAP_V)
         return longrow ? launch_drop_bwd_long<T, MAP_V>(a, sms, s, p, parts)
                        : launch_drop_bwd_m<T, MAP_V>(a, sms, s, p, parts);

@@ -885,6 +885,8 @@ cudaError_t launch_clusters(K kernel, int64_t rows, int cs, int threads, size_t 
 // Batches per resident group: at 2048 x 50001 bf16 with its gradient 86.0 us
 // at three, 87.8 at six and 96.4 at ten (each batch starts with nothing on its
 // way); at 4096 x 131072 with 30 % of the rows taking no part 296, 288 and 285.
+// Groups of less than 256 threads take two: 8192 x 4096 36.4 us, at one 40.6,
+// at four 42.6.
 constexpr int kTurns = 4;
 
 template <typename T, bool POLICY, int TH, int PK, int MINB>
@@ -902,7 +904,7 @@ cudaError_t launch_logit_reg(const LogitArgs &a, int cs, int sms, cudaStream_t s
     // rows per batch: the most that leaves the resident groups kTurns each,
     // which evens out rows that take no part
     const int64_t groups = (int64_t)sms * per_sm / cs * G;
-    int64_t batch = a.rows / (groups * kTurns);
+    int64_t batch = a.rows / (groups * (TH >= 256 ? kTurns : 2));
     batch = batch < 1 ? 1 : batch > 32 ? 32 : batch;
     int log_cs = 0;
     while (1 << log_cs < cs) ++log_cs;
@@ -936,7 +938,11 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
     };
     if (!stream) {
         if (packs <= 32 * 4) return launch_logit_reg<T, POLICY, 32, 4, 1>(a, 1, sms, s, p);
-        if (packs <= 32 * 8 && a.rows >= 4 * (int64_t)sms) return launch_logit_reg<T, POLICY, 32, 8, 1>(a, 1, sms, s, p);
+        if (a.rows >= 4 * (int64_t)sms) {
+            if (packs <= 32 * 8) return launch_logit_reg<T, POLICY, 32, 8, 1>(a, 1, sms, s, p);
+            if (packs <= 32 * 12) return launch_logit_reg<T, POLICY, 32, 12, 1>(a, 1, sms, s, p);
+            if (packs <= 32 * 16) return launch_logit_reg<T, POLICY, 32, 16, 1>(a, 1, sms, s, p);
+        }
         if (packs <= 128 * 8 && a.rows >= 2 * (int64_t)sms) return launch_logit_reg<T, POLICY, 128, 8, 8>(a, 1, sms, s, p);
         if (!POLICY && packs > 256 * 8 && a.rows >= 2 * (int64_t)sms) return launch_logit_seg<T, 256, 8, 4>(a, sms, s, p);
         int cs = 1;
