@@ -274,6 +274,10 @@ template <typename T, int MAP, int U> struct Access {
     __device__ __forceinline__ Access(int64_t ch0_, int64_t n_, int shift_)
         : whole(0), some(0), bits(0), ch0(ch0_), n(n_), shift(shift_) {
         if constexpr (MAP != MAP_S) {
+            if ((MAP == MAP_V || ch0 > 0) && n + shift - ch0 * kChunk >= U * kChunk) {  // inside the row
+                whole = some = (1u << (U * H)) - 1u;
+                return;
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const Part b = part(u);
@@ -299,8 +303,11 @@ template <typename T, int MAP, int U> struct Access {
     __device__ __forceinline__ uint32_t readable(int64_t row, int64_t rows) const {
         if (MAP != MAP_A) return whole;
         constexpr int V = IO<T>::V;
-        const int over = (int)((V - (n + shift) % V) % V);  // places behind the row in its last pack
-        return row * n >= shift && (rows - 1 - row) * n >= over ? some : whole;
+        const int over = (int)((V - ((uint32_t)n + shift) % V) % V);  // places behind the row in its last pack
+        // rows that hold as many elements as are needed on a side
+        const int before = n >= V ? shift > 0 : (shift + (int)n - 1) / (int)n;
+        const int behind = n >= V ? over > 0 : (over + (int)n - 1) / (int)n;
+        return row >= before && row + behind < rows ? some : whole;
     }
 
     // p: the row's element first().

@@ -273,6 +273,19 @@ def test_backward_stays_inside_its_workspace(rows, n, plan):
         check_bwd(dy, h, rstd, w, None, R.keep(rows, n, 0.2, SEED, OFF), 0.2, got)
 
 
+@pytest.mark.parametrize("rows,n", [(66001, 65536), (140000, 30727)])
+def test_more_than_2_to_the_32_elements(rows, n):
+    # row offsets beyond 32 bits, aligned and not; the last rows against the definition
+    x = torch.ones(rows, n, dtype=torch.bfloat16, device="cuda")
+    y = nrm.dropout_fwd(x, 0.25, SEED, OFF)
+    del x
+    last = R.keep(rows, 64, 0.25, SEED, OFF)[-3:]
+    got = y[-3:, :64].float().cpu().numpy()
+    assert np.array_equal(got != 0, last) and (got[last] == np.float32(1.3359375)).all()
+    first = R.keep(2, n, 0.25, SEED, OFF)
+    assert np.array_equal(y[:2].float().cpu().numpy() != 0, first)
+
+
 def test_side_stream():
     x, res, w = inputs(64, 1024, torch.bfloat16)
     side = torch.cuda.Stream()

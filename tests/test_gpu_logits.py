@@ -313,6 +313,25 @@ def test_leading_dimensions_stream_and_graph():
     assert all(torch.equal(a, b) for a, b in zip(cap, want))
 
 
+def test_more_than_2_to_the_31_logits():
+    rows, v = 21000, 110001
+    z = torch.zeros(rows, v, dtype=torch.bfloat16, device="cuda")
+    z[:, 5] = 3.0
+    t = torch.full((rows,), 5, device="cuda")
+    old = torch.full((rows,), np.log(np.exp(3.0) / (v - 1 + np.exp(3.0))), device="cuda")
+    adv = torch.full((rows,), -1.0, device="cuda")
+    loss, logp, dz = nrm.policy_loss(z, t, old, adv, out=z)  # ratio 1: the slope is 1 everywhere
+    prob = np.exp(3.0) / (v - 1 + np.exp(3.0))
+    lp, slack = np.log(prob), (v / 512 + 130) * R.U
+    assert float((logp.double() - lp).abs().max()) <= slack + 12 * R.U
+    assert abs(float(loss) - rows) <= rows * (2 * slack + 16 * R.U)
+    for r in (0, 1, 11000, rows - 2, rows - 1):
+        row = dz[r].double().cpu().numpy()
+        ref = np.full(v, -1.0 / (v - 1 + np.exp(3.0)))
+        ref[5] = 1 - prob
+        R.check(row, ref, R.out_bound(torch.bfloat16, ref, np.abs(ref) * 4 * slack), "dlogits")
+
+
 def test_bounded_waits_give_up_and_report():
     # wait limit 0: every wait for a peer's pair gives up at once, raises the
     # fault bit and the kernel ends; the next call is unaffected
