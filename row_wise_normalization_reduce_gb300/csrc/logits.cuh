@@ -8,9 +8,17 @@
 //   logp = s z_a - lse
 //   dz_j = g s (delta_ja - 2^((z_j - m) c) / d)       g: the gradient of logp
 //
-// The row's policy term needs g before any dz_j, so a row is passed over
-// twice.  A row of logits is 64 KB to 600 KB; the second pass of a CTA finds
-// in L2 what its first pass read from HBM.
+// The policy loss' slope g needs the whole row's (m, d), so dz_j can only be
+// written once the row has been seen to its end; a row of logits is 2 KB to
+// 640 KB.  All of it is bound by HBM (the log-probability reads a row, its
+// gradient and the loss read and write one), and which kernel comes nearest
+// depends on where the row can wait:
+//
+//   logit_reg_kernel   in the registers of a warp, a CTA or a cluster of CTAs
+//   logit_seg_kernel   nowhere: the log-probability alone needs no second look
+//   logit_grad_kernel  the gradient for a slope and lse that are there already
+//   logit_rows_kernel  in L2, passed over twice: rows longer than a cluster's
+//                      registers
 //
 // A row takes part ("is live") when its target lies in [0, V) (and, for the
 // loss, its weight is not 0); of the others nothing is read and their gradient
@@ -235,9 +243,13 @@ __device__ __forceinline__ void finish_row(const LogitArgs &a, int64_t row, cons
 }
 
 // ---------------------------------------------------------------------------
-// One row per cluster of CTAs (1 where rows are many; up to 8 where they are
-// few, each CTA a slice of the row's packs, the pairs joined over distributed
-// shared memory in rank order).
+// Streaming plan, any length.  One row per cluster of CTAs (1 where rows are
+// many; up to 8 where they are few, each CTA a slice of the row's packs, the
+// pairs joined over distributed shared memory in rank order).  The loss reads
+// the row again for its gradient, newest packs first; 152 x 4 resident CTAs
+// hold more rows than the L2 does, so much of that comes from HBM again: 516 us
+// for the loss of 4096 x 131072 bf16 (10 % of the rows out) where the register
+// plan takes 303; the log-probability alone 162, in segments 137.
 // ---------------------------------------------------------------------------
 constexpr int kLogitThreads = 512;
 
@@ -390,6 +402,18 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
 // batch's next live row are on their way into shared memory meanwhile (each
 // thread copies and reads back its own, so nothing but its own copies has to
 // be waited for).
+//
+// What a cluster has to exchange is one (max, sum) a warp: the sum is taken
+// around the warp's own maximum and rescaled, so there is a single exchange a
+// row.  The pairs travel as st.async counted on the receiver's mbarrier; with
+// barrier.cluster, whose arrival waits for the previous row's stores, 4096 x
+// 131072 bf16 took 417 us.
+//
+// 4096 x 131072 bf16, 30 % of the rows out, loss and gradient: 289 us, 6.3
+// TB/s, 93 % of the measured copy rate.
+// 152 x 32 warps issue 56 % of the cycles, 26 % of them exponentials.  Rows
+// of a few thousand logits are bound by the latency of a row's scalar part
+// instead (log, exp, one thread): 8192 x 4096 bf16 31.0 us, 61 %.
 // ---------------------------------------------------------------------------
 // (max, sum) over a set of pairs, two butterflies: the maximum, then the sums
 // rescaled to it.  Every lane gets the same bits.
@@ -726,7 +750,11 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
 // Log-probabilities alone, rows longer than a CTA's registers: nothing of the
 // row is needed again, so a CTA passes over it in segments of TH x PK packs
 // with a running (max, sum) per thread, the next segment (of this row or of
-// the batch's next live one) on its way meanwhile; one exchange a row.
+// the batch's next live one) on its way meanwhile; one exchange a row.  Held
+// in a cluster's registers instead, a row waits for eight CTAs' exchange:
+// 4096 x 131072 bf16 (10 % of the rows out) 137 us against 169, 4096 x 32000
+// 38.2 against 47.8, f32 2048 x 50001 61.0 against 77.7.  Reads alone run at
+// 7.0 TB/s, a little above the copy rate.
 // ---------------------------------------------------------------------------
 template <typename T, int TH, int PK, int MINB>
 __global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, const int batch) {
@@ -807,16 +835,20 @@ __global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, 
 
 // ---------------------------------------------------------------------------
 // The gradient for a given slope dlogp and the forward's lse: element-wise.
-// A CTA takes one tile of a row.
+// A group of TH threads (the CTA, or a warp where rows are short) takes one
+// tile of 4 x TH packs of a row, so there is nothing to wait for but the loads
+// of one tile: 2048 x 131072 bf16 137 us, 6.9 TB/s.  An element at its row's
+// lse takes exp(s z - lse), no max: lse is the maximum's own upper bound.
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, int TH>
 __global__ void __launch_bounds__(256) logit_grad_kernel(const LogitArgs a, const int tiles) {
-    constexpr int TH = 256, V = IO<T>::V, U = 4;
-    const int t = threadIdx.x;
+    constexpr int G = 256 / TH, V = IO<T>::V, U = 4;
+    const int t = threadIdx.x % TH;
     pdl_wait();
     pdl_launch_dependents();
-    for (int64_t id = blockIdx.x; id < a.rows * tiles; id += gridDim.x) {
-        const int64_t row = id / tiles;
+    const int64_t total = a.rows * tiles;
+    for (int64_t id = (int64_t)blockIdx.x * G + threadIdx.x / TH; id < total; id += (int64_t)gridDim.x * G) {
+        const int64_t row = total <= 0xffffffffll ? (int64_t)((uint32_t)id / (uint32_t)tiles) : id / tiles;
         const int tile = (int)(id - row * tiles);
         const T *Z = static_cast<const T *>(a.z) + row * a.ldz;
         T *D = static_cast<T *>(a.dz) + row * a.lddz;
@@ -882,12 +914,13 @@ cudaError_t launch_clusters(K kernel, int64_t rows, int cs, int threads, size_t 
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// Batches per resident group: at 2048 x 50001 bf16 with its gradient 86.0 us
-// at three, 87.8 at six and 96.4 at ten (each batch starts with nothing on its
-// way); at 4096 x 131072 with 30 % of the rows taking no part 296, 288 and 285.
-// Groups of less than 256 threads take two: 8192 x 4096 36.4 us, at one 40.6,
-// at four 42.6.
-constexpr int kTurns = 4;
+// Batches per resident group.  Each starts with nothing on its way; few leave
+// the SMs unevenly loaded where rows take no part.  Loss and gradient at four,
+// six, eight and twelve: 4096 x 131072 bf16 308.8, 303.2, 301.7 and 303.2 us,
+// 8192 x 32000 170.8, 166.8, 167.2 and 171.5, f32 4096 x 16000 86.6, 87.2, 95.4
+// and 95.6.  Groups of less than 256 threads take two: 8192 x 4096 bf16 31.0
+// us, at one 33.1.
+constexpr int kTurns = 6;
 
 template <typename T, bool POLICY, int TH, int PK, int MINB>
 cudaError_t launch_logit_reg(const LogitArgs &a, int cs, int sms, cudaStream_t s, Plan *p) {
@@ -930,28 +963,41 @@ cudaError_t launch_logit_seg(const LogitArgs &a, int sms, cudaStream_t s, Plan *
 template <typename T, bool POLICY>
 cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaStream_t s, Plan *p) {
     const int64_t packs = a.V / IO<T>::V;
-    // a row over more CTAs while the SMs are not twice covered and each CTA
-    // keeps a pack per thread
-    auto spread = [&](int cs, int threads) {
-        while (cs < 8 && a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * (int64_t)threads) cs *= 2;
-        return cs;
-    };
+    // The fewest threads that hold the row, while rows are enough for every SM:
+    // what a row costs beside its packs (the exchange, the scalar part) costs a
+    // warp least.  Loss and gradient, 8192 rows bf16, by a warp and by a CTA of
+    // 128: 1000 logits 16.6 and 40.3 us, 2501 30.6 and 42.3; by a CTA of 128
+    // and of 256: 4096 x 8192 bf16 28.9 and 43.2, f32 4096 x 4096 27.8 and 38.2.
+    // With 304 rows of 2501 a warp still wins (6.6 us, a CTA 7.4); with 64 rows
+    // of 4000 a CTA does (log-probability 2.5, a warp 2.8).  The CTAs per SM are
+    // those that the registers of the packs leave: without that bound the
+    // compiler took 172 for sixteen packs (8192 x 4096 37.6 us, 31.0 with 128).
+    // More CTAs a row than its packs need do not help: 200 x 16000 bf16 8.0 us
+    // by one, 8.6 by two.
     if (!stream) {
-        if (packs <= 32 * 4) return launch_logit_reg<T, POLICY, 32, 4, 1>(a, 1, sms, s, p);
-        if (a.rows >= 4 * (int64_t)sms) {
-            if (packs <= 32 * 8) return launch_logit_reg<T, POLICY, 32, 8, 1>(a, 1, sms, s, p);
-            if (packs <= 32 * 12) return launch_logit_reg<T, POLICY, 32, 12, 1>(a, 1, sms, s, p);
-            if (packs <= 32 * 16) return launch_logit_reg<T, POLICY, 32, 16, 1>(a, 1, sms, s, p);
+        if (packs <= 32 * 4) return launch_logit_reg<T, POLICY, 32, 4, 8>(a, 1, sms, s, p);
+        if (a.rows >= 2 * (int64_t)sms) {
+            if (packs <= 32 * 8) return launch_logit_reg<T, POLICY, 32, 8, 6>(a, 1, sms, s, p);
+            if (packs <= 32 * 12) return launch_logit_reg<T, POLICY, 32, 12, 5>(a, 1, sms, s, p);
+            if (packs <= 32 * 16) return launch_logit_reg<T, POLICY, 32, 16, (POLICY ? 4 : 5)>(a, 1, sms, s, p);
+            if (packs <= 128 * 8) return launch_logit_reg<T, POLICY, 128, 8, 8>(a, 1, sms, s, p);
+            if (!POLICY && packs > 256 * 8) return launch_logit_seg<T, 256, 8, 4>(a, sms, s, p);
         }
-        if (packs <= 128 * 8 && a.rows >= 2 * (int64_t)sms) return launch_logit_reg<T, POLICY, 128, 8, 8>(a, 1, sms, s, p);
-        if (!POLICY && packs > 256 * 8 && a.rows >= 2 * (int64_t)sms) return launch_logit_seg<T, 256, 8, 4>(a, sms, s, p);
         int cs = 1;
         while (cs < 8 && packs > 256 * 8 * cs) cs *= 2;
-        if (packs <= 256 * 8 * cs)
-            return launch_logit_reg<T, POLICY, 256, 8, 4>(a, spread(cs, 256), sms, s, p);
-        if (packs <= 8 * 512 * 8) return launch_logit_reg<T, POLICY, 512, 8, 2>(a, 8, sms, s, p);
+        if (packs <= 256 * 8 * cs) return launch_logit_reg<T, POLICY, 256, 8, 4>(a, cs, sms, s, p);
+        // longer rows: more packs a thread, fewer CTAs per SM.  1024 x 150001
+        // bf16 at twelve packs 132 us, by CTAs of 512 threads at eight 168;
+        // f32 1024 x 120000 at sixteen 160 and 182; 700 x 151936 at twenty 141,
+        // in the streaming plan 197
+        if (packs <= 8 * 256 * 12) return launch_logit_reg<T, POLICY, 256, 12, 3>(a, 8, sms, s, p);
+        if (packs <= 8 * 256 * 16) return launch_logit_reg<T, POLICY, 256, 16, 2>(a, 8, sms, s, p);
+        if (packs <= 8 * 256 * 20) return launch_logit_reg<T, POLICY, 256, 20, 2>(a, 8, sms, s, p);
     }
-    const int cs = spread(1, kLogitThreads);
+    // a row over more CTAs while the SMs are not twice covered and each CTA
+    // keeps a pack per thread
+    int cs = 1;
+    while (cs < 8 && a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * (int64_t)kLogitThreads) cs *= 2;
     p->kind = PLAN_GENERIC;
     p->threads = kLogitThreads;
     p->packs = 1;
@@ -959,12 +1005,18 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
     return launch_clusters(logit_rows_kernel<T, POLICY>, a.rows, cs, kLogitThreads, 0, s, a, cs);
 }
 
-template <typename T> cudaError_t launch_logit_grad_t(const LogitArgs &a, cudaStream_t s) {
+template <typename T, int TH> cudaError_t launch_logit_grad_g(const LogitArgs &a, cudaStream_t s) {
+    constexpr int G = 256 / TH;
     const int64_t packs = a.V / IO<T>::V + 1;
-    const int64_t tiles = (packs + 1023) / 1024;
-    const int64_t n = a.rows * tiles;
-    return launch_row(logit_grad_kernel<T>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), 256u, 0, s, a,
+    const int64_t tiles = (packs + 4 * TH - 1) / (4 * TH);
+    const int64_t n = (a.rows * tiles + G - 1) / G;
+    return launch_row(logit_grad_kernel<T, TH>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), 256u, 0, s, a,
                       (int)tiles);
+}
+// Rows of up to 512 packs by warps: 8192 x 1000 bf16 5.8 us, by CTAs 17.4; 8192
+// x 4096 23.3 and 23.9; at 750 packs (8192 x 6000) 32.7 and 30.9.
+template <typename T> cudaError_t launch_logit_grad_t(const LogitArgs &a, cudaStream_t s) {
+    return a.V / IO<T>::V <= 512 ? launch_logit_grad_g<T, 32>(a, s) : launch_logit_grad_g<T, 256>(a, s);
 }
 
 }  // namespace nrm

@@ -263,6 +263,45 @@ def test_policy_loss_masked_rows_and_edges():
     check_policy(*sub, one, ref[live], 0.2, 0.3, 0.0, 1.0, nrm.policy_loss(*sub, clip_high=0.3))
 
 
+# rows by warps at each of their register budgets, and the cluster's from its
+# smallest to the rows it has no room for; the last of a budget and the first
+# of the next
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,packs", [(305, 128), (305, 129), (304, 257), (307, 385), (305, 512), (303, 300),
+                                        (3, 16385), (2, 24577), (2, 32768), (1, 32769), (2, 40959), (1, 41000)])
+def test_every_budget_of_packs(rows, packs, dtype):
+    v = packs * (4 if dtype == torch.float32 else 8) + 3
+    args = policy_inputs(rows, v, dtype, packs)
+    z, t, old, adv, wt, ref = args
+    check_policy(*args, 0.2, 0.3, 0.1, 1.0, nrm.policy_loss(z, t, old, adv, wt, ref, 0.2, 0.3, 0.1))
+    got = nrm.logprob_fwd(z, t)
+    live = (t >= 0) & (t < v)
+    check_logprob(z[live], t[live], 1.0, [x[live] for x in got])
+    dlogp = torch.linspace(-1, 1, rows).cuda()
+    check_grad(z[live], t[live], got[1][live], dlogp[live], 1.0, nrm.logprob_bwd(dlogp, z, t, got[1])[live])
+
+
+def test_the_loss_of_many_rows_that_cancel():
+    # one logit a row: its log-probability is 0 and the ratio 1, exactly, so the
+    # loss is -sum(adv) with nothing but the sum's own rounding.  A thread adds
+    # rows / 1024 terms; each addition's error is kept, at most u A of the sum A
+    # of the magnitudes, and what adding those up loses is (rows / 1024)^2 2 u^2 A
+    rows = 300_001
+    g = torch.Generator().manual_seed(3)
+    adv = torch.randn(rows, generator=g)
+    adv[1000], adv[250_000] = 3e6, -3e6
+    zero = torch.zeros(rows, device="cuda")
+    z, t = torch.ones(rows, 1, device="cuda"), torch.zeros(rows, dtype=torch.int64, device="cuda")
+    loss, logp, _ = nrm.policy_loss(z, t, zero, adv.cuda())
+    assert not logp.any()
+    want, total = float(-adv.double().sum()), float(adv.double().abs().sum())
+    assert abs(float(loss) - want) <= R.U * abs(want) + ((rows / 1024) ** 2 + 64) * 2 * R.U ** 2 * total
+    for bad in (INF, -INF, float("nan")):
+        adv[77] = bad
+        got = float(nrm.policy_loss(z, t, zero, adv.cuda())[0])
+        assert got == -bad or (bad != bad and got != got)
+
+
 def test_clipped_rows_have_no_gradient_without_kl():
     z, t = make(6, 3000, torch.float32, 9)
     logp, _ = nrm.logprob_fwd(z, t)
