@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
     __shared__ float2 pairs[2][CSMAX * NW];
     __shared__ uint64_t arrived[2];
     __shared__ float sh[2][2];  // the row's gradient factor; the target's logit
-    const int t = threadIdx.x % TH, lane = threadIdx.x & 31, warp = t >> 5;
+    const int t = G > 1 ? threadIdx.x % TH : threadIdx.x, lane = threadIdx.x & 31, warp = t >> 5;
     const int cs = 1 << log_cs, rank = log_cs ? (int)cluster_rank() : 0;
     // the first pair may go to a peer only once its barriers stand: the other
     // half of this cluster barrier is before that
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
     const float c = a.scale * kLog2e;
     const float gs = POLICY && a.grad_scale ? *a.grad_scale : 1.f;
     int parity = 1;  // the exchange slots alternate between live rows
-    const int64_t group = (int64_t)(blockIdx.x >> log_cs) * G + threadIdx.x / TH,
+    const int64_t group = (int64_t)(blockIdx.x >> log_cs) * G + (G > 1 ? threadIdx.x / TH : 0),
                   step = (int64_t)(gridDim.x >> log_cs) * G;
     for (int64_t r0 = group * batch; r0 < a.rows; r0 += step * batch) {
         // lane i keeps the target of row r0 + i
@@ -596,8 +596,10 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
         const bool takes_part = my_target >= 0 && my_target < a.V && !(POLICY && a.weight && a.weight[r0 + lane] == 0.f);
         uint32_t live = __ballot_sync(0xffffffffu, takes_part);
         uint32_t dead = __ballot_sync(0xffffffffu, have && !takes_part);
+        float zn = 0.f;  // the next row's scalar element
         auto fetch = [&](int64_t row) {
             const RowView<T> w(a, row, rank, log_cs, t);
+            if (t < w.ns) zn = IO<T>::to_f(w.z[w.sc]);
 #pragma unroll
             for (int k = 0; k < PK; ++k)
                 cp_async16_if(k * TH < w.mine, &next_row[k * CTA + threadIdx.x], w.body + k * TH * V);
@@ -628,8 +630,8 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
             live &= live - 1;
             parity ^= 1;
             const RowView<T> w(a, row, rank, log_cs, t);
-            float zs = 0.f, za = 0.f;
-            if (t < w.ns) zs = IO<T>::to_f(w.z[w.sc]);
+            const float zs = zn;
+            float za = 0.f;
             RowTerms terms = {};
             if (t == 0) {
                 za = IO<T>::to_f(w.z[tgt]);
@@ -775,8 +777,10 @@ __global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, 
             if (a.logp) a.logp[r0 + lane] = 0.f;
             if (a.lse) a.lse[r0 + lane] = 0.f;
         }
+        float zn = 0.f;  // the next row's scalar element
         auto fetch = [&](int64_t row, int seg) {
             const RowView<T> w(a, row, 0, 0, t);
+            if (seg == 0 && t < w.ns) zn = IO<T>::to_f(w.z[w.sc]);
 #pragma unroll
             for (int k = 0; k < PK; ++k) {
                 const int at = (seg * PK + k) * TH;
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, 
             float za = 0.f;
             RowMax r{-INFINITY, 0.f};
             if (t < w.ns) {
-                const float z = IO<T>::to_f(w.z[w.sc]);
+                const float z = zn;
                 r.m = z != z ? -INFINITY : z;
                 r.d = exp2_fast((z - (r.m == -INFINITY ? 0.f : r.m)) * c);
             }
@@ -985,11 +989,25 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
         }
         int cs = 1;
         while (cs < 8 && packs > 256 * 8 * cs) cs *= 2;
+        // packs that a CTA has room for and the row does not fill cost their
+        // instructions all the same, so a CTA is no larger than the slice needs:
+        // 6710 x 10001 bf16 by 160 threads 52.4 us, by 256 68.7; 1365 x 49152
+        // by 192 50.7 and 61.7; 1335 x 50257 by 224 59.9 and 63.2.  With less
+        // than four rows or slices for each resident CTA the larger one is
+        // ahead (333 x 50001 f16 16.9 us, by 224 17.9).  The strides stay
+        // constants: with the CTA's size read at run time 4096 x 131072 took
+        // 344 us, not 289
+        if (a.rows * cs >= 16 * (int64_t)sms) {
+            if (packs <= 160 * 8 * cs) return launch_logit_reg<T, POLICY, 160, 8, 6>(a, cs, sms, s, p);
+            if (packs <= 192 * 8 * cs) return launch_logit_reg<T, POLICY, 192, 8, 5>(a, cs, sms, s, p);
+            if (packs <= 224 * 8 * cs) return launch_logit_reg<T, POLICY, 224, 8, 4>(a, cs, sms, s, p);
+        }
         if (packs <= 256 * 8 * cs) return launch_logit_reg<T, POLICY, 256, 8, 4>(a, cs, sms, s, p);
         // longer rows: more packs a thread, fewer CTAs per SM.  1024 x 150001
-        // bf16 at twelve packs 132 us, by CTAs of 512 threads at eight 168;
+        // bf16 at ten packs 125 us, twelve 132, by 512 threads at eight 168;
         // f32 1024 x 120000 at sixteen 160 and 182; 700 x 151936 at twenty 141,
         // in the streaming plan 197
+        if (packs <= 8 * 256 * 10) return launch_logit_reg<T, POLICY, 256, 10, 3>(a, 8, sms, s, p);
         if (packs <= 8 * 256 * 12) return launch_logit_reg<T, POLICY, 256, 12, 3>(a, 8, sms, s, p);
         if (packs <= 8 * 256 * 16) return launch_logit_reg<T, POLICY, 256, 16, 2>(a, 8, sms, s, p);
         if (packs <= 8 * 256 * 20) return launch_logit_reg<T, POLICY, 256, 20, 2>(a, 8, sms, s, p);

@@ -268,7 +268,8 @@ def test_policy_loss_masked_rows_and_edges():
 # of the next
 @pytest.mark.parametrize("dtype", R.DTYPES)
 @pytest.mark.parametrize("rows,packs", [(305, 128), (305, 129), (304, 257), (307, 385), (305, 512), (303, 300),
-                                        (3, 16385), (2, 24577), (2, 32768), (1, 32769), (2, 40959), (1, 41000)])
+                                        (2433, 1100), (1217, 2100), (1217, 2600), (1217, 3400),
+                                        (3, 16385), (2, 20481), (2, 24577), (2, 32768), (1, 32769), (2, 40959), (1, 41000)])
 def test_every_budget_of_packs(rows, packs, dtype):
     v = packs * (4 if dtype == torch.float32 else 8) + 3
     args = policy_inputs(rows, v, dtype, packs)
