@@ -507,6 +507,12 @@ __device__ __forceinline__ float warps_sum_all(float v, float *slot, int nw) {
 // the residual read once.  A group's rows are apart by a multiple of 8, so
 // that they share one shift (8 rows of any stride are a multiple of 16
 // bytes): its columns are the same in all of them, and w is fetched once.
+//
+// Bound by HBM on the 16-byte grid: 4096 x 4096 bf16 19.0 us, 7.1 TB/s, with
+// 73 % of the issue slots used, so off the grid (half as many instructions
+// again: shuffles, cut packs) it is bound by those: 2795 x 6001 bf16 35.5 us,
+// 56 % of the copy rate, binary32 81 %.  The L2 hint for the row that the next
+// resident group starts with hides the ramp between rows of one SM.
 // ---------------------------------------------------------------------------
 template <typename T, bool WARP, int U, int MAP, int REGS>
 __global__ void __maxnreg__(REGS) drop_add_rms_kernel(const DropRmsArgs a, const int64_t pf) {
@@ -593,7 +599,7 @@ __global__ void __maxnreg__(REGS) drop_add_rms_kernel(const DropRmsArgs a, const
 
 // Rows longer than the register plan holds, or tensors that differ in
 // alignment: the sum of squares while h is written, then h read again (each
-// lane re-reads what it wrote) for y.
+// lane re-reads what it wrote, mostly from L2) for y.
 template <typename T, int MAP>
 __global__ void __launch_bounds__(512) drop_add_rms_long_kernel(const DropRmsArgs a) {
     constexpr int NW = 16;
@@ -726,7 +732,13 @@ __device__ __forceinline__ void store_sums(float *stage, const float2 dw[4], flo
 // Register plan: persistent groups (as the forward's), a row at a time; a
 // thread's columns are the same in every row, so dw accumulates in registers
 // and each CTA leaves one row of partial sums (folded in order by
-// dw_fold_kernel: no atomics, the same bits every time).
+// dw_fold_kernel: no atomics, the same bits every time).  The mask is made
+// again from the seed: reading one back would add 1 to 16 bits an element.
+//
+// 4096 x 4096 bf16 with dh_up 28.9 us (26.7 before the fold), 5.8 TB/s, 86 % of
+// the copy rate: dw, w and two rows fill 119 registers, so an SM has 16 warps,
+// at 58 % of its issue slots, and their waits are not all covered.  Off the
+// 16-byte grid instructions bound it: 1999 x 5001 f16 26.8 us, 44 %.
 template <typename T, bool WARP, int U, int MAP, int REGS, bool AHEAD>
 __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a) {
     constexpr int G = WARP ? kRowWarps : 1;
@@ -845,7 +857,9 @@ __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a
 }
 
 // Long rows (or tensors that differ in alignment): the row sums first (k per
-// row into the workspace) ...
+// row into the workspace), which reads dy and h once more than the register
+// plan: binary32 1024 x 16384 88.5 us, 56 % of the copy rate by the bytes that a
+// single pass needs ...
 template <typename T, int MAP>
 __global__ void __launch_bounds__(512) drop_bwd_dot_kernel(const DropRmsBwdArgs a) {
     constexpr int NW = 16;
@@ -960,16 +974,21 @@ cudaError_t launch_drop_fwd_k(const DropRmsArgs &a, int warps, int sms, cudaStre
 }
 
 // The group and its share of the row: a warp a row where rows are short and
-// many, else a CTA of as many warps as the row needs.
+// many (16384 x 1024 bf16 20.8 us, by CTAs of a chunk a warp 26.6; binary32 up
+// to two chunks, 16384 x 640 26.2 us by warps, 24.2 by CTAs), else a CTA of as
+// many warps as the row needs.  The bounds on the registers buy rows in flight:
+// 16384 x 256 bf16 8.8 us with 64, 10.0 with the 84 that the compiler took.
 template <typename T, int MAP>
 cudaError_t launch_drop_fwd_m(const DropRmsArgs &a, int sms, cudaStream_t s, Plan *p) {
     const int C = (int)row_chunks<T>(a.N, MAP);
     constexpr int R = MAP == MAP_V && sizeof(T) == 2 ? 64 : 96;
     const int warps = (C + 1) / 2;
     if (C <= 4 && a.rows >= 4 * (int64_t)sms) {
-        if (C <= 1) return launch_drop_fwd_k<T, true, 1, MAP, 128>(a, kRowWarps, sms, s, p);
-        if (C <= 2) return launch_drop_fwd_k<T, true, 2, MAP, 128>(a, kRowWarps, sms, s, p);
-        return launch_drop_fwd_k<T, true, 4, MAP, 128>(a, kRowWarps, sms, s, p);
+        constexpr int E = MAP == MAP_V ? 0 : 24;
+        constexpr bool H = sizeof(T) == 2;
+        if (C <= 1) return launch_drop_fwd_k<T, true, 1, MAP, 64 + E>(a, kRowWarps, sms, s, p);
+        if (C <= 2) return launch_drop_fwd_k<T, true, 2, MAP, H ? 72 + E : 128>(a, kRowWarps, sms, s, p);
+        if constexpr (H) return launch_drop_fwd_k<T, true, 4, MAP, 128>(a, kRowWarps, sms, s, p);
     }
     if (C <= 4) return launch_drop_fwd_k<T, false, 1, MAP, 64>(a, C, sms, s, p);
     if (warps * 32 * R <= 65536) return launch_drop_fwd_k<T, false, 2, MAP, R>(a, warps, sms, s, p);
