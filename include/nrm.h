@@ -565,9 +565,9 @@ typedef enum {
  * NRM_PLAN_PERSIST as its one-pass plan (dy and x read once) and anything
  * else as its streaming plan where the layout allows it;
  * bn_fwd_infer takes NRM_PLAN_GENERIC as its scalar element-wise kernel;
- * dropout_add_rms_fwd and dropout_add_rms_bwd take NRM_PLAN_GENERIC as the
- * plan of rows that outgrow the registers (any length), and the training
- * operators follow no other forced plan.
+ * dropout_add_rms_fwd, dropout_add_rms_bwd, logprob_fwd and policy_loss take
+ * NRM_PLAN_GENERIC as their plan for rows that outgrow the registers (any
+ * length), and the training operators follow no other forced plan.
  * Returns NRM_OK or NRM_ERR_UNSUPPORTED for
  * an unknown plan.  Process-wide; not meant to change while calls run.
  */
@@ -585,8 +585,9 @@ int nrm_force_plan(int plan, int threads, int packs, int stages, int groups);
 void nrm_last_plan(int *plan, int *threads, int *packs, int *stages, int *groups);
 
 /*
- * Kernels that wait on asynchronous copies (NRM_PLAN_TMA) bound every wait:
- * after `tries` unsuccessful polls they give up, record a fault bit, drain
+ * Kernels that wait on asynchronous copies (NRM_PLAN_TMA) or on what another
+ * CTA of their cluster sends (logprob_fwd and policy_loss where a row takes
+ * several CTAs) bound every wait: after `tries` unsuccessful polls they give up, record a fault bit, drain
  * their copies in flight (again bounded) and return, leaving the outputs of
  * that call undefined.  Sets the number of polls (default 2^20; 0 makes every
  * such wait give up at once, which tests use to exercise the path) and
