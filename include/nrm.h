@@ -415,8 +415,8 @@ int dropout_add_rms_fwd_ld(const void *x, int64_t ldx, const void *residual, int
  *   dresidual = dh,   dx = d(dh),   dw = sum over rows of dy * xhat
  * The mask is made again from p, seed and offset (the forward's).  With p = 0
  * this is the backward of add_rms_fwd (dx == dresidual) and of rms_fwd
- * (h = x).  Sums are binary32 in an order that depends on the shape alone:
- * the same call gives the same bits.
+ * (h = x).  Sums are binary32 in an order that depends on the shape and the
+ * alignment alone: the same call gives the same bits.
  *   dy, residual_out   [rows, N] dtype, read only
  *   rstd               [rows] binary32
  *   w                  [N] dtype or NULL (= 1)

@@ -47,6 +47,7 @@ namespace nrm {
 
 constexpr int kChunk = 256;
 constexpr int kRowWarps = 4;  // rows (warps) per CTA of the warp plans
+constexpr int kBwdWarps = 16;  // the most warps a CTA of the backward's register plan has
 
 // The offset words of this call: the host's plus the device counter's value.
 struct DropCtr {
@@ -744,7 +745,7 @@ __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a
     constexpr int G = WARP ? kRowWarps : 1;
     __shared__ float slot[2][32];
     __shared__ float part[WARP ? G - 1 : 1][WARP ? U * kChunk : 1];
-    __shared__ float stage[WARP ? 1 : 16][kChunk];
+    __shared__ float stage[WARP ? 1 : kBwdWarps][kChunk];
     const int nw = WARP ? 1 : (int)blockDim.x / 32;
     const int warp = WARP ? 0 : (int)threadIdx.x >> 5;
     const bool lead = WARP ? (threadIdx.x & 31) == 0 : threadIdx.x == 0;
@@ -858,8 +859,8 @@ __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a
 
 // Long rows (or tensors that differ in alignment): the row sums first (k per
 // row into the workspace), which reads dy and h once more than the register
-// plan: binary32 1024 x 16384 88.5 us, 56 % of the copy rate by the bytes that a
-// single pass needs ...
+// plan: binary32 1638 x 10240 90.9 us, 54 % of the copy rate by the bytes that a
+// single pass needs (register plan: 61.9, 80 %) ...
 template <typename T, int MAP>
 __global__ void __launch_bounds__(512) drop_bwd_dot_kernel(const DropRmsBwdArgs a) {
     constexpr int NW = 16;
@@ -1003,7 +1004,7 @@ cudaError_t launch_drop_fwd_long(const DropRmsArgs &a, cudaStream_t s, Plan *p) 
                       512u, 0, s, a);
 }
 constexpr int kDropFwdChunks = 64;
-template <typename T> constexpr int kDropBwdChunks = sizeof(T) == 2 ? 64 : 32;
+constexpr int kDropBwdChunks = 64;
 template <typename T>
 cudaError_t launch_drop_fwd_t(const DropRmsArgs &a, int map, bool longrow, int sms, cudaStream_t s, Plan *p) {
     longrow = longrow || row_chunks<T>(a.N, map) > kDropFwdChunks;
@@ -1015,6 +1016,7 @@ cudaError_t launch_drop_fwd_t(const DropRmsArgs &a, int map, bool longrow, int s
 template <typename T, bool WARP, int U, int MAP, int REGS, bool AHEAD>
 cudaError_t launch_drop_bwd_k(const DropRmsBwdArgs &a, int warps, int sms, cudaStream_t s, Plan *p,
                               int64_t *parts) {
+    if (warps > kBwdWarps) return cudaErrorInvalidConfiguration;
     auto kernel = drop_add_rms_bwd_kernel<T, WARP, U, MAP, REGS, AHEAD>;
     const int threads = 32 * warps, G = WARP ? warps : 1;
     int per_sm = 0;
@@ -1052,12 +1054,10 @@ cudaError_t launch_drop_bwd_m(const DropRmsBwdArgs &a, int sms, cudaStream_t s, 
     // up to 10 the former (4096 x 5120 bf16 38.3 us against 47.1), beyond that
     // one CTA fits either way
     if (warps > 8 && warps <= 10) return launch_drop_bwd_k<T, false, 2, MAP, 96, false>(a, warps, sms, s, p, parts);
-    if constexpr (kDropBwdChunks<T> > 32) {
-        // rows of 16-bit data beyond 32 chunks: some spills, but read once
-        // (2048 x 16384 bf16 70.5 us against 99.0 through the long-row plan)
-        if (C > 48) return launch_drop_bwd_k<T, false, 4, MAP, 128, false>(a, (C + 3) / 4, sms, s, p, parts);
-        if (C > 32) return launch_drop_bwd_k<T, false, 4, MAP, 168, false>(a, (C + 3) / 4, sms, s, p, parts);
-    }
+    // beyond 32 chunks: some spills, but read once (1024 x 16384 bf16 40.3 us,
+    // 51.5 through the long-row plan; binary32 1398 x 12000 63.8 and 91.4)
+    if (C > 48) return launch_drop_bwd_k<T, false, 4, MAP, 128, false>(a, (C + 3) / 4, sms, s, p, parts);
+    if (C > 32) return launch_drop_bwd_k<T, false, 4, MAP, 168, false>(a, (C + 3) / 4, sms, s, p, parts);
     return launch_drop_bwd_k<T, false, 2, MAP, 128, AHEAD>(a, warps, sms, s, p, parts);
 }
 template <typename T, int MAP>
@@ -1091,7 +1091,11 @@ cudaError_t launch_drop_bwd_long(const DropRmsBwdArgs &a, int sms, cudaStream_t 
 template <typename T>
 cudaError_t launch_drop_bwd_t(const DropRmsBwdArgs &a, int map, bool longrow, int sms, cudaStream_t s,
                               Plan *p, int64_t *parts) {
-    longrow = longrow || row_chunks<T>(a.N, map) > kDropBwdChunks<T>;
+    const int64_t C = row_chunks<T>(a.N, map);
+    // the most chunks of binary32 spill most: that pays while every SM has rows
+    // to go on with (1024 x 16384 80.3 us, by the long-row plan 88.4; 300 rows
+    // 30.6 and 27.4)
+    longrow = longrow || C > kDropBwdChunks || (sizeof(T) == 4 && C > 48 && a.rows < 4 * (int64_t)sms);
     if (map == MAP_V)
         return longrow ? launch_drop_bwd_long<T, MAP_V>(a, sms, s, p, parts)
                        : launch_drop_bwd_m<T, MAP_V>(a, sms, s, p, parts);

@@ -197,7 +197,7 @@ def check_bwd(dy, h, rstd, w, up, mask, p, got):
 
 @pytest.mark.parametrize("plan", [nrm.PLAN_AUTO, nrm.PLAN_GENERIC])
 @pytest.mark.parametrize("dtype", R.DTYPES)
-@pytest.mark.parametrize("rows,n", SIZES + [(2500, 384), (1999, 130)])
+@pytest.mark.parametrize("rows,n", SIZES + [(2500, 384), (1999, 130), (5, 9001), (40, 12288), (612, 16384), (611, 15999)])
 def test_backward(rows, n, dtype, plan):
     _, h, w = inputs(rows, n, dtype)
     dy, up = make(rows, n, dtype, 5), make(rows, n, dtype, 6)
