@@ -1055,7 +1055,10 @@ int rows_map(int64_t N, size_t es, std::initializer_list<RowPtr> ts, const void 
 }
 
 int record_plan(cudaError_t e, const Plan &p) {
-    if (e != cudaSuccess) return NRM_ERR_LAUNCH;
+    if (e != cudaSuccess) {
+        cudaGetLastError();  // this call's, not the next one's
+        return NRM_ERR_LAUNCH;
+    }
     t_last_kind = p.kind;
     t_last_threads = p.threads;
     t_last_packs = p.packs;

@@ -992,7 +992,8 @@ cudaError_t launch_drop_fwd_m(const DropRmsArgs &a, int sms, cudaStream_t s, Pla
         if constexpr (H) return launch_drop_fwd_k<T, true, 4, MAP, 128>(a, kRowWarps, sms, s, p);
     }
     if (C <= 4) return launch_drop_fwd_k<T, false, 1, MAP, 64>(a, C, sms, s, p);
-    if (warps * 32 * R <= 65536) return launch_drop_fwd_k<T, false, 2, MAP, R>(a, warps, sms, s, p);
+    // the registers of a CTA's warps come from four banks of 16384, whole warps each
+    if (warps <= 4 * (16384 / (32 * R))) return launch_drop_fwd_k<T, false, 2, MAP, R>(a, warps, sms, s, p);
     return launch_drop_fwd_k<T, false, 2, MAP, 64>(a, warps, sms, s, p);
 }
 template <typename T, int MAP>

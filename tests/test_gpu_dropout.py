@@ -210,6 +210,22 @@ def test_backward(rows, n, dtype, plan):
     assert all(same_bits(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [2, 610])
+def test_every_number_of_256_columns(rows, dtype):
+    # each is its own CTA size: whole packs and rows off the 16-byte grid
+    for c in range(1, 67):
+        if rows > 2 and c > 6 and c not in (32, 33, 48, 49, 64, 65):
+            continue
+        for n in (256 * c, 256 * c - 7):
+            x, res, w = inputs(rows, n, dtype)
+            mask = R.keep(rows, n, 0.2, SEED, OFF)
+            got = nrm.dropout_add_rms_fwd(x, res, w, 0.2, SEED, OFF, 1e-6)
+            check_fwd(x, res, w, 0.2, 1e-6, mask, got)
+            check_bwd(x, got[0], got[2], w, res, mask, 0.2,
+                      nrm.dropout_add_rms_bwd(x, got[0], got[2], w, 0.2, SEED, OFF, dresidual_out=res))
+
+
 @pytest.mark.parametrize("plan", [nrm.PLAN_AUTO, nrm.PLAN_GENERIC])
 @pytest.mark.parametrize("dtype", R.DTYPES)
 @pytest.mark.parametrize("n", [264, 1001, 4096])
