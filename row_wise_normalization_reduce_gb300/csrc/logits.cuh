@@ -969,15 +969,15 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
     const int64_t packs = a.V / IO<T>::V;
     // The fewest threads that hold the row, while rows are enough for every SM:
     // what a row costs beside its packs (the exchange, the scalar part) costs a
-    // warp least.  Loss and gradient, 8192 rows bf16, by a warp and by a CTA of
-    // 128: 1000 logits 16.6 and 40.3 us, 2501 30.6 and 42.3; by a CTA of 128
-    // and of 256: 4096 x 8192 bf16 28.9 and 43.2, f32 4096 x 4096 27.8 and 38.2.
-    // With 304 rows of 2501 a warp still wins (6.6 us, a CTA 7.4); with 64 rows
-    // of 4000 a CTA does (log-probability 2.5, a warp 2.8).  The CTAs per SM are
-    // those that the registers of the packs leave: without that bound the
-    // compiler took 172 for sixteen packs (8192 x 4096 37.6 us, 31.0 with 128).
-    // More CTAs a row than its packs need do not help: 200 x 16000 bf16 8.0 us
-    // by one, 8.6 by two.
+    // warp least.  Loss and gradient of 8192 rows bf16, by a warp and by a CTA
+    // of 128: 1000 logits 10.7 and 35.4 us, 2501 21.0 and 37.5; by a CTA of 128
+    // and the next larger: 4096 x 8192 bf16 26.1 and 29.9, f32 4096 x 4096 24.7
+    // and 26.1.  With 304 rows of 2501 a warp is still ahead (5.0 us, a CTA of
+    // 256 6.1); with 64 rows of 4000 the CTA is (log-probability 2.4, a warp
+    // 2.7).  The CTAs per SM are those that the registers of the packs leave:
+    // without that bound the compiler took 172 for sixteen packs (8192 x 4096
+    // 37.6 us, 31.0 with 128).  More CTAs a row than its packs need do not help:
+    // 200 x 16000 bf16 takes 0.7 us more by two.
     if (!stream) {
         if (packs <= 32 * 4) return launch_logit_reg<T, POLICY, 32, 4, 8>(a, 1, sms, s, p);
         if (a.rows >= 2 * (int64_t)sms) {
