@@ -918,13 +918,19 @@ cudaError_t launch_clusters(K kernel, int64_t rows, int cs, int threads, size_t 
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// Batches per resident group.  Each starts with nothing on its way; few leave
-// the SMs unevenly loaded where rows take no part.  Loss and gradient at four,
-// six, eight and twelve: 4096 x 131072 bf16 308.8, 303.2, 301.7 and 303.2 us,
-// 8192 x 32000 170.8, 166.8, 167.2 and 171.5, f32 4096 x 16000 86.6, 87.2, 95.4
-// and 95.6.  Groups of less than 256 threads take two: 8192 x 4096 bf16 31.0
-// us, at one 33.1.
-constexpr int kTurns = 6;
+// Rows per batch.  A batch starts with nothing on its way, but few batches
+// leave the SMs unevenly loaded where rows take no part: six per resident
+// group, and where that leaves less than three rows each, down to two.  Loss and
+// gradient at one row a batch, at three and at four: 1335 x 50257 bf16 60.1, 53.6
+// and 55.2 us, 8192 x 6000 39.3, 37.8 and 37.7; with rows enough for six batches,
+// at four, six and twelve of them: 4096 x 131072 bf16 308.8, 303.2 and 303.2,
+// 8192 x 32000 170.8, 166.8 and 171.5.
+inline int64_t rows_per_batch(int64_t rows, int64_t groups, int64_t least) {
+    if (groups < 1) groups = 1;
+    const int64_t even = rows / (groups * 6), ahead = rows / (groups * 2);
+    const int64_t batch = even >= least ? even : ahead < least ? ahead : least;
+    return batch < 1 ? 1 : batch > 32 ? 32 : batch;
+}
 
 template <typename T, bool POLICY, int TH, int PK, int MINB>
 cudaError_t launch_logit_reg(const LogitArgs &a, int cs, int sms, cudaStream_t s, Plan *p) {
@@ -938,11 +944,8 @@ cudaError_t launch_logit_reg(const LogitArgs &a, int cs, int sms, cudaStream_t s
     p->threads = CTA;
     p->packs = PK;
     p->groups = cs > 1 ? cs : 0;
-    // rows per batch: the most that leaves the resident groups kTurns each,
-    // which evens out rows that take no part
     const int64_t groups = (int64_t)sms * per_sm / cs * G;
-    int64_t batch = a.rows / (groups * (TH >= 256 ? kTurns : 2));
-    batch = batch < 1 ? 1 : batch > 32 ? 32 : batch;
+    const int64_t batch = rows_per_batch(a.rows, groups, 3);
     int log_cs = 0;
     while (1 << log_cs < cs) ++log_cs;
     return launch_clusters(kernel, (a.rows + batch * G - 1) / (batch * G), cs, CTA, smem, s, a, log_cs, (int)batch);
@@ -958,8 +961,9 @@ cudaError_t launch_logit_seg(const LogitArgs &a, int sms, cudaStream_t s, Plan *
     p->kind = PLAN_CTA;
     p->threads = TH;
     p->packs = PK;
-    int64_t batch = a.rows / ((int64_t)sms * per_sm * kTurns);
-    batch = batch < 1 ? 1 : batch > 32 ? 32 : batch;
+    // (a row's own segments follow one another: batches of one row will do, 4096
+    // x 32000 bf16 32.7 us, of three 34.9)
+    const int64_t batch = rows_per_batch(a.rows, (int64_t)sms * per_sm, 1);
     const int64_t n = (a.rows + batch - 1) / batch;
     return launch_row(kernel, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), (unsigned)TH, smem, s, a, (int)batch);
 }
