@@ -1,0 +1,171 @@
+"""Many rows of logits of mixed kinds (live, clipped, without a target, without
+a weight, without a finite logit) through every kernel that takes them, against
+the 64-bit definitions, and in place against out of place.  The definitions are
+those of train_ref.py in torch on the GPU, a part of the rows at a time."""
+import numpy as np
+import pytest
+import torch
+
+import train_ref as R
+
+pytestmark = pytest.mark.gpu
+
+import row_wise_normalization_reduce_gb300 as nrm  # noqa: E402
+
+INF = float("inf")
+LO, HI = 0.2, 0.3
+# distances of log(ratio) from 0: on both sides of both bounds (-0.22 and 0.26)
+STEPS = [-0.6, -0.1, 0.0, 0.1, 0.2, 0.6]
+
+
+@pytest.fixture(autouse=True)
+def _setup():
+    nrm.build()
+    nrm.force_plan(nrm.PLAN_AUTO)
+    yield
+    nrm.force_plan(nrm.PLAN_AUTO)
+
+
+def packs(n, dtype, more=3):
+    """Columns of n packs of 16 bytes and a few more."""
+    return n * (4 if dtype == torch.float32 else 8) + more
+
+
+def parts(rows, v):
+    step = max(1, 2 ** 24 // v)
+    return [slice(a, min(a + step, rows)) for a in range(0, rows, step)]
+
+
+def logprob64(z, t, s):
+    """logp, lse and the bound of log d (train_ref.logprob) of rows with a target; rows without a finite logit -inf."""
+    x = z.double() * s
+    m = x.amax(-1, keepdim=True)
+    none = m[:, 0] == -INF
+    e = torch.exp(x - torch.where(none[:, None], 0.0, m))
+    d = e.sum(-1)
+    lse = m[:, 0] + torch.log(d)
+    logp = torch.where(none, -INF, x.gather(-1, t[:, None])[:, 0] - lse)
+    arg = torch.where(e > 0, (x - m).abs() * e, 0.0).sum(-1) / torch.where(none, 1.0, d)
+    return logp, lse, (z.shape[1] / 512 + 104 + 3 * arg) * R.U
+
+
+def mixed(rows, v, dtype, seed, s=1.0, scale=2.5):
+    """Logits, targets and a policy's other inputs; of 16 rows in a row: two without a target, one without a weight, one
+    without a finite logit, the others live, some of them clipped."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.empty(rows, v, dtype=dtype, device="cuda")
+    t = torch.randint(0, v, (rows,), generator=g, device="cuda")
+    logp = torch.empty(rows, dtype=torch.float64, device="cuda")
+    kind = torch.randint(0, 16, (rows,), generator=g, device="cuda")
+    for p in parts(rows, v):
+        x = scale * torch.randn(p.stop - p.start, v, generator=g, device="cuda")
+        x[torch.arange(len(x), device="cuda"), t[p]] += 6 * torch.rand(len(x), generator=g, device="cuda")
+        x[kind[p] == 3] = -INF
+        z[p] = x.to(dtype)
+        logp[p] = logprob64(z[p], t[p], s)[0]
+    step = torch.tensor(STEPS, device="cuda")[torch.randint(0, len(STEPS), (rows,), generator=g, device="cuda")]
+    logp = torch.where(kind == 3, -3.0, logp).float()
+    old, ref = logp - step, logp + 0.4 * torch.randn(rows, generator=g, device="cuda")
+    adv, wt = torch.randn(rows, generator=g, device="cuda"), (0.5 + torch.rand(rows, generator=g, device="cuda")) / rows
+    t[kind == 0], t[kind == 1], wt[kind == 2] = -100, v + 5, 0.0
+    # what rows that take no part hold is not read
+    old[kind == 0] = adv[kind == 1] = float("nan")
+    return z, t, old, adv, wt, ref
+
+
+def near(got, want, room, what):
+    bad = ~((got.double() - want).abs() <= room)
+    assert not bad.any(), (what, int(bad.sum()), torch.nonzero(bad)[:3].tolist(), got[bad][:3].tolist(), want[bad][:3].tolist())
+
+
+def out_room(dtype, want, extra):
+    return (want.abs() + extra) * (R.EPS[dtype] / 2) + extra + R.TINY[dtype] / 2
+
+
+def check_logprob(z, t, s, got):
+    v = z.shape[1]
+    ok = (t >= 0) & (t < v)
+    assert not got[0][~ok].any() and not got[1][~ok].any()
+    for p in parts(*z.shape):
+        o = ok[p]
+        logp, lse, slack = logprob64(z[p][o], t[p][o], s)
+        fin = torch.isfinite(logp)
+        for a, want in ((got[0][p][o], logp), (got[1][p][o], lse)):
+            assert (a[~fin] == -INF).all()
+            near(a[fin], want[fin], (slack + R.U * want.abs())[fin] + 1e-45, "logp, lse")
+
+
+def check_policy(z, t, old, adv, wt, ref, kl, s, got, scale=1.0):
+    """The bounds of check_policy in test_gpu_logits.py, over all rows."""
+    dtype, v = z.dtype, z.shape[1]
+    live = (t >= 0) & (t < v) & (wt != 0)
+    assert not got[1][~live].any()
+    total = room = 0.0
+    for p in parts(*z.shape):
+        i = torch.nonzero(live[p])[:, 0]
+        assert not (got[2][p][~live[p]] != 0).any()
+        x, a = z[p][i], t[p][i]
+        logp, lse, slack = logprob64(x, a, s)
+        none = logp == -INF
+        assert (got[1][p][i][none] == -INF).all() and not (got[2][p][i][none] != 0).any()
+        i, x, a, logp, lse, slack = (q[~none] for q in (i, x, a, logp, lse, slack))
+        near(got[1][p][i], logp, slack + R.U * logp.abs() + 1e-45, "logp")
+        o, A, w, r = (q[p][i].double() for q in (old, adv, wt, ref))
+        d, e = logp - o, r - logp
+        ratio = torch.exp(d)
+        free, held = -A * ratio, -A * ratio.clamp(1 - LO, 1 + HI)
+        clipped = held > free
+        term, g = torch.maximum(free, held), torch.where(clipped, 0.0, free)
+        wrong = (w * free).abs() * (slack + 16 * R.U * (1 + d.abs()))
+        room += float(((w * free).abs() * (slack + 10 * R.U * (1 + d.abs()))).sum())
+        if kl:
+            term, g = term + kl * (torch.exp(e) - e - 1), g + kl * (1 - torch.exp(e))
+            wrong += w.abs() * kl * torch.exp(e) * (slack + 16 * R.U * (1 + e.abs()))
+            room += float((w.abs() * kl * (torch.exp(e) + 1) * (slack + 8 * R.U * (1 + e.abs()))).sum())
+        else:
+            assert not (got[2][p][i][clipped] != 0).any()
+        total += float((w * term).sum())
+        g = w * g * scale * s
+        wrong = wrong * abs(scale) * s
+        arg = x.double() * s - lse[:, None]
+        soft = torch.exp(arg)
+        out = -g[:, None] * soft
+        out.scatter_add_(-1, a[:, None], g[:, None])
+        mag = out.abs()
+        mag.scatter_(-1, a[:, None], g.abs()[:, None])
+        soft.scatter_(-1, a[:, None], 1.0)
+        arg = torch.where(torch.isfinite(arg), arg.abs(), 0.0)
+        extra = mag * ((3 * arg + 16) * R.U + slack[:, None]) + wrong[:, None] * soft.clamp(min=1e-30)
+        near(got[2][p][i], out, out_room(dtype, out, extra), "dlogits")
+    assert abs(float(got[0]) - total) <= room + 5 * R.U * abs(total) + 1e-45
+
+
+# --- in place ----------------------------------------------------------------
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,n,cs", [(3001, 2100, 2), (2003, 5000, 4), (2003, 10000, 8), (613, 19000, 8), (311, 5000, 4)])
+def test_policy_loss_in_place_where_a_row_takes_a_cluster(rows, n, cs, dtype):
+    # every CTA of the cluster overwrites its slice while others may be a step
+    # behind: the same bits as out of place, everywhere
+    v = packs(n, dtype)
+    z, t, old, adv, wt, ref = mixed(rows, v, dtype, n)
+    want = nrm.policy_loss(z, t, old, adv, wt, ref, LO, HI, 0.1, out=torch.full_like(z, 3.0))
+    plan = nrm.last_plan()
+    assert plan[0] == nrm.PLAN_CLUSTER and plan[4] == cs
+    for _ in range(3):
+        x = z.clone()
+        got = nrm.policy_loss(x, t, old, adv, wt, ref, LO, HI, 0.1, out=x)
+        assert got[2].data_ptr() == x.data_ptr()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert torch.isfinite(want[0]) and (want[2] != 0).any(-1).sum() > rows / 2
+    # targets at the row's ends and at the borders of the CTAs' slices
+    edge = torch.tensor([0, 1, v - 1, v - 2, *(v * q // cs + k for q in range(1, cs) for k in (-9, -1, 0, 1, 9))], device="cuda")
+    t = edge[torch.arange(rows, device="cuda") % len(edge)]
+    want = nrm.policy_loss(z, t, old.nan_to_num(-9.0), adv.nan_to_num(1.0), wt, None, LO, 9.0)
+    x = z.clone()
+    got = nrm.policy_loss(x, t, old.nan_to_num(-9.0), adv.nan_to_num(1.0), wt, None, LO, 9.0, out=x)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    live = torch.nonzero((wt != 0) & torch.isfinite(want[1]))[:, 0]
+    logp = torch.cat([logprob64(z[live[q]], t[live[q]], 1.0)[0] for q in torch.arange(len(live)).split(64)])
+    near(want[1][live], logp, (v / 512 + 150) * R.U + R.U * logp.abs(), "logp")
