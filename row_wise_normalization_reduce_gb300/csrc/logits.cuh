@@ -475,14 +475,16 @@ template <int PK, typename T> __device__ __forceinline__ float packs_max(const u
 
 // 2^((z - m) c) takes one fused multiply-add an element as 2^(z c - b), b = m c
 // rounded; what b's rounding leaves, 2^(b - m c), is one factor for all of
-// them.  For |m c| beyond binary32 (logits at the type's lowest value) the
+// them.  That factor has to stay near 1: below |m c| = 2^24 the rounding leaves
+// at most 1/2, at 1e10 it leaves hundreds (2^-440 times a sum of terms 2^440).
+// Beyond that (masked logits of -1e10, -1e30 or the type's lowest value) the
 // difference comes first instead.
 struct Shift {
     float b, left;
     bool direct;
     __device__ __forceinline__ Shift(float m, float c) {
         const float p = m * c;
-        direct = !(fabsf(p) < INFINITY) && fabsf(m) < INFINITY;
+        direct = !(fabsf(p) < 16777216.f) && fabsf(m) < INFINITY;
         b = m == -INFINITY || direct ? 0.f : p;
         // (an infinite or NaN m reaches the sum through b)
         left = m == -INFINITY || direct ? 1.f : exp2_fast(-fmaf(m, c, -b));

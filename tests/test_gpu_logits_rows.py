@@ -36,22 +36,34 @@ def parts(rows, v):
     return [slice(a, min(a + step, rows)) for a in range(0, rows, step)]
 
 
+def logsoftmax64(z, s):
+    """s z less the row's log-sum-exp (as its maximum and log d: their sum loses log d at large logits), lse, and the bound
+    of log d (train_ref.logprob); rows without a finite logit -inf."""
+    z = z.double()
+    m = z.amax(-1, keepdim=True)
+    none = m == -INF
+    x = (z - torch.where(none, 0.0, m)) * s
+    d = torch.exp(x).sum(-1, keepdim=True)
+    arg = torch.where(torch.exp(x) > 0, x.abs() * torch.exp(x), 0.0).sum(-1) / torch.where(none, 1.0, d)[:, 0]
+    logd = torch.log(d)
+    return torch.where(none, -INF, x - logd), (m * s)[:, 0], logd[:, 0], (z.shape[1] / 512 + 104 + 3 * arg) * R.U
+
+
 def logprob64(z, t, s):
-    """logp, lse and the bound of log d (train_ref.logprob) of rows with a target; rows without a finite logit -inf."""
-    x = z.double() * s
-    m = x.amax(-1, keepdim=True)
-    none = m[:, 0] == -INF
-    e = torch.exp(x - torch.where(none[:, None], 0.0, m))
-    d = e.sum(-1)
-    lse = m[:, 0] + torch.log(d)
-    logp = torch.where(none, -INF, x.gather(-1, t[:, None])[:, 0] - lse)
-    arg = torch.where(e > 0, (x - m).abs() * e, 0.0).sum(-1) / torch.where(none, 1.0, d)
-    return logp, lse, (z.shape[1] / 512 + 104 + 3 * arg) * R.U
+    x, top, logd, slack = logsoftmax64(z, s)
+    return x.gather(-1, t[:, None])[:, 0], top + logd, slack
 
 
-def mixed(rows, v, dtype, seed, s=1.0, scale=2.5):
-    """Logits, targets and a policy's other inputs; of 16 rows in a row: two without a target, one without a weight, one
-    without a finite logit, the others live, some of them clipped."""
+def away64(zt, top, logd, other):
+    """zt - top - logd - other; where zt and other are large (a masked target: -1e30 each), what 64 bits keep of
+    zt - top alone is not enough, so the two that are nearest cancel first."""
+    return torch.where((zt - top).abs() <= (zt - other).abs(), zt - top - other, zt - other - top) - logd
+
+
+def mixed(rows, v, dtype, seed, s=1.0, scale=2.5, low=None):
+    """Logits, targets and a policy's other inputs; of 16 rows two have no target, one no weight, one no finite logit; the
+    others are live, some of them clipped.  low: the value of masked logits of some live rows: a third in one piece, every
+    third, all of them; and a logit of -low."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     z = torch.empty(rows, v, dtype=dtype, device="cuda")
     t = torch.randint(0, v, (rows,), generator=g, device="cuda")
@@ -61,6 +73,14 @@ def mixed(rows, v, dtype, seed, s=1.0, scale=2.5):
         x = scale * torch.randn(p.stop - p.start, v, generator=g, device="cuda")
         x[torch.arange(len(x), device="cuda"), t[p]] += 6 * torch.rand(len(x), generator=g, device="cuda")
         x[kind[p] == 3] = -INF
+        if low is not None:
+            one, every, whole, hot = ((kind[p] == k) for k in (4, 5, 6, 7))
+            x[one, v // 3:2 * v // 3] = low
+            t[p][one] %= max(1, v // 3)
+            x[every, ::3] = low
+            t[p][every] = (t[p][every] // 3 * 3 + 1).clamp(max=v - 1)
+            x[whole] = low
+            x[hot, t[p][hot]] = -low
         z[p] = x.to(dtype)
         logp[p] = logprob64(z[p], t[p], s)[0]
     step = torch.tensor(STEPS, device="cuda")[torch.randint(0, len(STEPS), (rows,), generator=g, device="cuda")]
@@ -105,13 +125,15 @@ def check_policy(z, t, old, adv, wt, ref, kl, s, got, scale=1.0):
         i = torch.nonzero(live[p])[:, 0]
         assert not (got[2][p][~live[p]] != 0).any()
         x, a = z[p][i], t[p][i]
-        logp, lse, slack = logprob64(x, a, s)
+        zt = x.gather(-1, a[:, None])[:, 0].double() * s
+        x, top, logd, slack = logsoftmax64(x, s)
+        logp = x.gather(-1, a[:, None])[:, 0]
         none = logp == -INF
         assert (got[1][p][i][none] == -INF).all() and not (got[2][p][i][none] != 0).any()
-        i, x, a, logp, lse, slack = (q[~none] for q in (i, x, a, logp, lse, slack))
+        i, x, a, logp, zt, top, logd, slack = (q[~none] for q in (i, x, a, logp, zt, top, logd, slack))
         near(got[1][p][i], logp, slack + R.U * logp.abs() + 1e-45, "logp")
         o, A, w, r = (q[p][i].double() for q in (old, adv, wt, ref))
-        d, e = logp - o, r - logp
+        d, e = away64(zt, top, logd, o), -away64(zt, top, logd, r)
         ratio = torch.exp(d)
         free, held = -A * ratio, -A * ratio.clamp(1 - LO, 1 + HI)
         clipped = held > free
@@ -127,14 +149,13 @@ def check_policy(z, t, old, adv, wt, ref, kl, s, got, scale=1.0):
         total += float((w * term).sum())
         g = w * g * scale * s
         wrong = wrong * abs(scale) * s
-        arg = x.double() * s - lse[:, None]
-        soft = torch.exp(arg)
+        soft = torch.exp(x)
         out = -g[:, None] * soft
         out.scatter_add_(-1, a[:, None], g[:, None])
         mag = out.abs()
         mag.scatter_(-1, a[:, None], g.abs()[:, None])
         soft.scatter_(-1, a[:, None], 1.0)
-        arg = torch.where(torch.isfinite(arg), arg.abs(), 0.0)
+        arg = torch.where(soft > 0, x.abs(), 0.0)
         extra = mag * ((3 * arg + 16) * R.U + slack[:, None]) + wrong[:, None] * soft.clamp(min=1e-30)
         near(got[2][p][i], out, out_room(dtype, out, extra), "dlogits")
     assert abs(float(got[0]) - total) <= room + 5 * R.U * abs(total) + 1e-45
@@ -169,3 +190,25 @@ def test_policy_loss_in_place_where_a_row_takes_a_cluster(rows, n, cs, dtype):
     live = torch.nonzero((wt != 0) & torch.isfinite(want[1]))[:, 0]
     logp = torch.cat([logprob64(z[live[q]], t[live[q]], 1.0)[0] for q in torch.arange(len(live)).split(64)])
     near(want[1][live], logp, (v / 512 + 150) * R.U + R.U * logp.abs(), "logp")
+
+
+# --- masked logits that are finite -------------------------------------------
+# one of each kernel: rows by warps, by CTAs, by clusters, in segments (the
+# log-probability of many long rows), and forced through the streaming plan
+KINDS = [(400, 20, 0), (310, 500, 0), (400, 900, 0), (310, 1900, 0), (24, 1500, 0), (24, 3000, 0), (20, 20000, 0),
+         (310, 2500, 0), (24, 5000, 1), (310, 1500, 1)]
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("low", [-1e4, -1e9, -1e10, -1e30, None])
+@pytest.mark.parametrize("rows,n,stream", KINDS)
+def test_masks_of_large_finite_values(rows, n, stream, low, dtype):
+    if low is not None and abs(low) > torch.finfo(dtype).max:
+        low = -5e4
+    low = torch.finfo(dtype).min if low is None else low
+    v = packs(n, dtype)
+    z, t, old, adv, wt, ref = mixed(rows, v, dtype, n, low=low)
+    if stream:
+        nrm.force_plan(nrm.PLAN_GENERIC)
+    check_logprob(z, t, 1.0, nrm.logprob_fwd(z, t))
+    check_policy(z, t, old, adv, wt, ref, 0.1, 1.0, nrm.policy_loss(z, t, old, adv, wt, ref, LO, HI, 0.1))
