@@ -96,10 +96,12 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
 // [0.75, 1.5), and log 2 in two parts, e times the first exact.
 __device__ __forceinline__ Two log_prob(float z, float m, float d, float s) {
     const Two x = two_sum(z, -m);
-    if (!(d < INFINITY) || !(fabsf(x.hi) < INFINITY)) return Two{s * x.hi - logf(d), 0.f};
+    const float p = __fmul_rn(s, x.hi);
+    // no remainder where the product is not finite (z at the type's lowest value
+    // and s > 1 suffice)
+    if (!(d < INFINITY) || !(fabsf(p) < INFINITY)) return Two{p - logf(d), 0.f};
     const int e = (__float_as_int(d) - 0x3f400000) >> 23;
     const float f = __int_as_float(__float_as_int(d) - (e << 23)), fe = (float)e;
-    const float p = __fmul_rn(s, x.hi);
     const float pl = fmaf(s, x.lo, fmaf(s, x.hi, -p));
     const Two y = two_sum(p, -fe * 0.693145751953125f);
     const float l = y.lo + (pl - fmaf(fe, 1.42860677e-6f, log1pf(f - 1.f)));

@@ -212,3 +212,38 @@ def test_masks_of_large_finite_values(rows, n, stream, low, dtype):
         nrm.force_plan(nrm.PLAN_GENERIC)
     check_logprob(z, t, 1.0, nrm.logprob_fwd(z, t))
     check_policy(z, t, old, adv, wt, ref, 0.1, 1.0, nrm.policy_loss(z, t, old, adv, wt, ref, LO, HI, 0.1))
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("s", [0.5, 1.0, 1.4, 3.0, 1e6])
+@pytest.mark.parametrize("rows,n,stream", [(40, 5, 0), (400, 900, 0), (24, 5000, 0), (310, 2500, 0), (24, 5000, 1)])
+def test_a_masked_target_at_any_temperature(rows, n, stream, s, dtype):
+    # s (z - max) of a target at the type's lowest value can leave binary32: its
+    # log-probability is -inf then, not NaN, and the ratio 0
+    v = packs(n, dtype)
+    z, t, old, adv, wt, _ = mixed(rows, v, dtype, n, s=s)
+    z[::5] = z[::5].clamp(-20, 20)
+    at = torch.arange(0, rows, 5, device="cuda")
+    t[at] = at % v
+    z[at, t[at]] = torch.finfo(dtype).min
+    old, adv, wt = old.nan_to_num(-1.0), adv.nan_to_num(1.0).abs(), wt.clamp(min=0.1 / rows)
+    if stream:
+        nrm.force_plan(nrm.PLAN_GENERIC)
+    logp, lse = nrm.logprob_fwd(z, t, s)
+    want, lse64, slack = logprob64(z[at], t[at], s)
+    # the type's lowest value times s beyond binary32: rounds to -inf
+    over = want < -(2.0 - 2.0 ** -24) * 2.0 ** 127
+    assert over.any() == (dtype != torch.float16 and s > 1)
+    assert (logp[at][over] == -INF).all()
+    near(logp[at][~over], want[~over], (slack + R.U * want.abs())[~over], "logp")
+    near(lse[at], lse64, slack + R.U * lse64.abs(), "lse")
+    # nothing of such a row is left for a positive advantage: as without it
+    got = nrm.policy_loss(z, t, old, adv, wt, None, LO, HI, 0.0, s)
+    w0 = wt.clone()
+    w0[at] = 0.0
+    ref = nrm.policy_loss(z, t, old, adv, w0, None, LO, HI, 0.0, s)
+    assert torch.isfinite(got[0]) and torch.equal(got[0], ref[0]) and torch.equal(got[2], ref[2])
+    # the log-probability of many long rows sums in another order (segments): each is within its bound of the exact value
+    assert torch.equal(got[1][at] == -INF, logp[at] == -INF)
+    fin = torch.isfinite(logp[at])
+    near(got[1][at][fin], logp[at][fin].double(), 2 * (slack + R.U * want.abs())[fin], "logp of both")
