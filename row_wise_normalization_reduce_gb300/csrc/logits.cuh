@@ -92,19 +92,29 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
     return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-// s (z - m) - log d, with log d = e log 2 + log1p(f - 1) for d = 2^e f, f in
-// [0.75, 1.5), and log 2 in two parts, e times the first exact.
+// s (z - m) - log d.  The logarithm's range reduction is that of W. J. Cody and
+// W. Waite, "Software Manual for the Elementary Functions" (1980), ALOG:
+// d = 2^e f with f in [sqrt(1/2), sqrt 2), log d = e log 2 + log f, and log 2 =
+// C1 + C2 with C1 = 355/512.  C1 has nine bits and e is below 2^15, so e C1 is
+// exact; C2 = log 2 - 355/512 = -2.12194440054690583e-4, rounded to binary32,
+// leaves an error of e 2^-37.  f - 1 is exact.  What is not exact is log f and
+// two sums of its size: 2^-24 in all, an eighth of the last place of a
+// log-probability of -8, and most of it stays in the low part.
 __device__ __forceinline__ Two log_prob(float z, float m, float d, float s) {
     const Two x = two_sum(z, -m);
     const float p = __fmul_rn(s, x.hi);
     // no remainder where the product is not finite (z at the type's lowest value
     // and s > 1 suffice)
     if (!(d < INFINITY) || !(fabsf(p) < INFINITY)) return Two{p - logf(d), 0.f};
-    const int e = (__float_as_int(d) - 0x3f400000) >> 23;
-    const float f = __int_as_float(__float_as_int(d) - (e << 23)), fe = (float)e;
+    const int bits = __float_as_int(d);
+    float f = __int_as_float((bits & 0x007fffff) | 0x3f800000), fe = (float)((bits >> 23) - 127);  // d is normal
+    if (f >= 1.41421356f) {
+        f *= 0.5f;
+        fe += 1.f;
+    }
     const float pl = fmaf(s, x.lo, fmaf(s, x.hi, -p));
-    const Two y = two_sum(p, -fe * 0.693145751953125f);
-    const float l = y.lo + (pl - fmaf(fe, 1.42860677e-6f, log1pf(f - 1.f)));
+    const Two y = two_sum(p, -fe * (355.f / 512.f));
+    const float l = y.lo + (pl - fmaf(fe, -2.12194440e-4f, log1pf(f - 1.f)));
     const float hi = __fadd_rn(y.hi, l);
     return Two{hi, __fadd_rn(__fsub_rn(y.hi, hi), l)};
 }

@@ -247,3 +247,41 @@ def test_a_masked_target_at_any_temperature(rows, n, stream, s, dtype):
     assert torch.equal(got[1][at] == -INF, logp[at] == -INF)
     fin = torch.isfinite(logp[at])
     near(got[1][at][fin], logp[at][fin].double(), 2 * (slack + R.U * want.abs())[fin], "logp of both")
+
+
+# --- the log-probability's two parts -----------------------------------------
+# sums of 1 to 98305 ones: around the powers of two, 0.75 and 1.5 times one and
+# sqrt(2) times one
+ONES = sorted({max(1, int(f * 2 ** k) + e) for k in (0, 1, 2, 3, 5, 8, 10, 13, 16) for f in (1, 1.5, 2 ** 0.5) for e in (-1, 0, 1)})
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+def test_log_probability_of_equal_logits(dtype):
+    # every exponential is 1 and their sum v exactly, so logp = -log v with the
+    # error of the logarithm alone: log f (at most 1 ulp of a value below 0.35:
+    # 2^-25) and the roundings of two sums of that size (2^-26 each) make 2^-24
+    # in the low part, and the high part is the sum's rounding
+    for v in ONES:
+        z = torch.zeros(2, v, dtype=dtype, device="cuda")
+        t = torch.tensor([0, v - 1], device="cuda")
+        logp, lse = nrm.logprob_fwd(z, t)
+        want = -np.log(v)
+        ulp = float(np.spacing(np.float32(abs(want)))) if v > 1 else 0.0
+        assert abs(R.f64(logp) - want).max() <= ulp / 2 + 2.0 ** -24 * (v > 1), v
+        assert abs(R.f64(lse) + want).max() <= ulp / 2 + 2.0 ** -24 * (v > 1), v
+        # the low part: with clip bounds of 0, old = the rounded log-probability
+        # and advantages of both signs, the side of the border that the exact
+        # remainder lies on decides which row has a gradient
+        old = np.float32(want)
+        rest = want - float(old)
+        if abs(rest) > 2.0 ** -24:
+            olds = torch.full((2,), float(old), device="cuda")
+            dz = nrm.policy_loss(z, t, olds, torch.tensor([1.0, -1.0], device="cuda"), clip_low=0.0, clip_high=0.0)[2]
+            has = (dz != 0).any(-1).tolist()
+            assert has == [rest < 0, rest > 0], (v, rest, has)
+
+
+def test_equal_logits_reach_the_low_part():
+    # the test above says something: of its sums more than half have a remainder that decides
+    rest = [abs(-np.log(v) - float(np.float32(-np.log(v)))) for v in ONES if v > 1]
+    assert sum(r > 2.0 ** -24 for r in rest) > len(rest) / 2
