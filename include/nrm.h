@@ -452,11 +452,20 @@ int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_ou
  *   logp, lse  [rows] binary32, written; one of them may be NULL
  *   V < 2^31 (NRM_ERR_SHAPE); inv_temp > 0, finite
  * A row whose entries are all -inf gives logp = lse = -inf.
+ * The stats form writes for the backward also
+ *   stats    [rows][2] binary32, per row max_j z_j and log sum_j exp(s (z_j - max));
+ *            rows that take no part 0 and 0, rows of -inf twice -inf
+ *   (one at least of logp, lse and stats)
  */
 int logprob_fwd(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
                 int64_t V, float inv_temp, int dtype, cudaStream_t stream);
 int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
                    int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream);
+int logprob_fwd_stats(const void *logits, const int64_t *targets, float *logp, float *lse, float *stats,
+                      int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream);
+int logprob_fwd_stats_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
+                         float *stats, int64_t rows, int64_t V, float inv_temp, int dtype,
+                         cudaStream_t stream);
 
 /*
  * Gradient of the logits for a gradient dlogp [rows] (binary32) of the
@@ -465,6 +474,15 @@ int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, floa
  * Rows without a target in [0, V), rows with dlogp = 0 and rows without a
  * finite logit (lse = -inf) get zeros, their logits are not read.
  *   dlogits  [rows, V] dtype, written; may be logits (same row stride)
+ * The given lse is taken as it is.  Its rounding to binary32 is a factor on the
+ * whole row: up to |lse| 2^-24 relative, 6e-4 at an lse of 1e4, and at 2^24 and
+ * beyond nothing is left (a row whose logits are all masked by the type's lowest
+ * value: its lse is that value, log V is lost, and each probability counts as 1).
+ * The stats form takes logprob_fwd_stats' two numbers instead of lse and has no
+ * such error:
+ *   dlogits_j = dlogp * s * ((j == target) - exp(s (z_j - stats[0]) - stats[1]))
+ * (rows with stats[1] = -inf get zeros).  Use it where logits carry a large common
+ * offset or rows may be masked as a whole by a finite value.
  */
 int logprob_bwd(const float *dlogp, const void *logits, const int64_t *targets, const float *lse,
                 void *dlogits, int64_t rows, int64_t V, float inv_temp, int dtype,
@@ -472,6 +490,12 @@ int logprob_bwd(const float *dlogp, const void *logits, const int64_t *targets, 
 int logprob_bwd_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
                    const float *lse, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
                    float inv_temp, int dtype, cudaStream_t stream);
+int logprob_bwd_stats(const float *dlogp, const void *logits, const int64_t *targets, const float *stats,
+                      void *dlogits, int64_t rows, int64_t V, float inv_temp, int dtype,
+                      cudaStream_t stream);
+int logprob_bwd_stats_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
+                         const float *stats, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
+                         float inv_temp, int dtype, cudaStream_t stream);
 
 /*
  * Clipped policy loss with a KL term over token rows, and its gradient, in

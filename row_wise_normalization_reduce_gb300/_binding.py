@@ -97,15 +97,19 @@ def _declare(lib):
                                            _I64, _P, _I64, _I64, *drop, _INT, _P, _SZ, _P]
     lib.logprob_fwd.argtypes = [_P] * 4 + [_I64, _I64, _F, _INT, _P]
     lib.logprob_fwd_ld.argtypes = [_P, _I64, _P, _P, _P, _I64, _I64, _F, _INT, _P]
+    lib.logprob_fwd_stats.argtypes = [_P] * 5 + [_I64, _I64, _F, _INT, _P]
+    lib.logprob_fwd_stats_ld.argtypes = [_P, _I64, _P, _P, _P, _P, _I64, _I64, _F, _INT, _P]
     lib.logprob_bwd.argtypes = [_P] * 5 + [_I64, _I64, _F, _INT, _P]
     lib.logprob_bwd_ld.argtypes = [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P]
+    lib.logprob_bwd_stats.argtypes = lib.logprob_bwd.argtypes
+    lib.logprob_bwd_stats_ld.argtypes = lib.logprob_bwd_ld.argtypes
     lib.policy_loss_workspace_size.argtypes = [_I64]
     lib.policy_loss_workspace_size.restype = _SZ
     lib.policy_loss.argtypes = [_P] * 6 + [_D, _D, _F, _F] + [_P] * 4 + [_I64, _I64, _INT, _P, _SZ, _P]
     lib.policy_loss_ld.argtypes = [_P, _I64] + [_P] * 5 + [_D, _D, _F, _F] + [_P] * 4 + [
         _I64, _I64, _I64, _INT, _P, _SZ, _P]
     for f in ("dropout_fwd", "dropout_add_rms_fwd", "dropout_add_rms_bwd", "logprob_fwd",
-              "logprob_bwd", "policy_loss"):
+              "logprob_fwd_stats", "logprob_bwd", "logprob_bwd_stats", "policy_loss"):
         getattr(lib, f).restype = getattr(lib, f + "_ld").restype = _INT
     lib.nrm_status_string.argtypes = [_INT]
     lib.nrm_status_string.restype = ctypes.c_char_p
@@ -723,41 +727,53 @@ def dropout_add_rms_bwd(dy, residual_out, rstd, w=None, p=0.0, seed=0, offset=0,
     return (dresidual if same else dx), dresidual, dw
 
 
-def logprob_fwd(logits, targets, inv_temp=1.0, *, logp=None, lse=None, stream=None):
+def logprob_fwd(logits, targets, inv_temp=1.0, *, logp=None, lse=None, stats=None, stream=None):
     """Log-softmax of inv_temp * logits at one target (int64) per row of the
     last dimension.  Returns (logp, lse), binary32, one value per row; rows
-    with a target outside [0, V) give 0 and are not read."""
+    with a target outside [0, V) give 0 and are not read.  stats, a contiguous
+    binary32 tensor of targets' shape and 2, takes each row's maximum and log
+    sum exp(inv_temp * (logits - maximum)) for logprob_bwd."""
     if stream is not None:
         with _on_stream(stream, logits):
-            return logprob_fwd(logits, targets, inv_temp, logp=logp, lse=lse)
+            return logprob_fwd(logits, targets, inv_temp, logp=logp, lse=lse, stats=stats)
     rows, v, ldl = _rows(logits, "logits")
     shape, dev = logits.shape[:-1], logits.get_device()
     code = _code(logits.dtype)
     _flat(targets, shape, torch.int64, dev, "targets")
     logp = torch.empty_like(targets, dtype=_F32) if logp is None else _flat(logp, shape, _F32, dev, "logp")
     lse = torch.empty_like(targets, dtype=_F32) if lse is None else _flat(lse, shape, _F32, dev, "lse")
-    _launch("logprob_fwd_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(),
-            lse.data_ptr(), rows, v, inv_temp, code)
+    if stats is not None:
+        _flat(stats, (*shape, 2), _F32, dev, "stats")
+    _launch("logprob_fwd_stats_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(),
+            lse.data_ptr(), _ptr(stats), rows, v, inv_temp, code)
     return logp, lse
 
 
-def logprob_bwd(dlogp, logits, targets, lse, inv_temp=1.0, *, out=None, stream=None):
+def logprob_bwd(dlogp, logits, targets, lse, inv_temp=1.0, *, stats=None, out=None, stream=None):
     """Gradient of the logits from dlogp, the gradient of logprob_fwd's logp
-    (one binary32 value per row), and its lse.  out may be logits.  Returns
+    (one binary32 value per row), and its lse, or its stats (then lse is not
+    used and may be None).  lse's rounding is a factor of up to |lse| 2^-24 on
+    its row (6e-4 at 1e4, and a row masked as a whole by the type's lowest value
+    loses log V); stats have no such error.  out may be logits.  Returns
     dlogits."""
     if stream is not None:
         with _on_stream(stream, logits):
-            return logprob_bwd(dlogp, logits, targets, lse, inv_temp, out=out)
+            return logprob_bwd(dlogp, logits, targets, lse, inv_temp, stats=stats, out=out)
     rows, v, ldl = _rows(logits, "logits")
     shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
     code = _code(dtype)
     per_row = shape[:-1]
     _flat(dlogp, per_row, _F32, dev, "dlogp")
     _flat(targets, per_row, torch.int64, dev, "targets")
-    _flat(lse, per_row, _F32, dev, "lse")
+    if stats is None:
+        if lse is None:
+            raise ValueError("lse or stats must be given")
+        name, from_fwd = "logprob_bwd_ld", _flat(lse, per_row, _F32, dev, "lse")
+    else:
+        name, from_fwd = "logprob_bwd_stats_ld", _flat(stats, (*per_row, 2), _F32, dev, "stats")
     out, lddl = _like(out, logits, shape, dtype, dev, "out")
-    _launch("logprob_bwd_ld", dev, dlogp.data_ptr(), logits.data_ptr(), ldl, targets.data_ptr(),
-            lse.data_ptr(), out.data_ptr(), lddl, rows, v, inv_temp, code)
+    _launch(name, dev, dlogp.data_ptr(), logits.data_ptr(), ldl, targets.data_ptr(),
+            from_fwd.data_ptr(), out.data_ptr(), lddl, rows, v, inv_temp, code)
     return out
 
 

@@ -1243,21 +1243,22 @@ int validate_logits(int64_t rows, int64_t V, float inv_temp, int dtype) {
 
 extern "C" {
 
-int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
-                   int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream) {
+int logprob_fwd_stats_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
+                         float *stats, int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream) {
     int st = validate_logits(rows, V, inv_temp, dtype);
     if (st != NRM_OK) return st;
     if (rows == 0) return NRM_OK;  // empty input: no pointer is used
-    if (!logits || !targets || (!logp && !lse)) return NRM_ERR_NULL;
+    if (!logits || !targets || (!logp && !lse && !stats)) return NRM_ERR_NULL;
     const size_t es = elem_size(dtype);
     if ((st = validate_ld(rows, V, es, {ldl})) != NRM_OK) return st;
     if ((st = check_elem_alignment({logits}, es)) != NRM_OK) return st;
-    if ((st = check_elem_alignment({logp, lse}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logp, lse, stats}, 4)) != NRM_OK) return st;
     if ((st = check_elem_alignment({targets}, 8)) != NRM_OK) return st;
     const RSpan sl = rspan(logits, ldl, rows, V, es), stg = rspan(targets, rows, 1, rows, 8),
-                sp = rspan(logp, rows, 1, rows, 4), ss = rspan(lse, rows, 1, rows, 4);
-    if ((st = check_alias({sp, ss}, {sl, stg})) != NRM_OK) return st;
-    if ((st = check_pointers({logits, targets, logp, lse})) != NRM_OK) return st;
+                sp = rspan(logp, rows, 1, rows, 4), ss = rspan(lse, rows, 1, rows, 4),
+                st2 = rspan(stats, 2 * rows, 1, 2 * rows, 4);
+    if ((st = check_alias({sp, ss, st2}, {sl, stg})) != NRM_OK) return st;
+    if ((st = check_pointers({logits, targets, logp, lse, stats})) != NRM_OK) return st;
     DevInfo dev;
     if ((st = device_info(&dev)) != NRM_OK) return st;
     LogitArgs a{};
@@ -1269,10 +1270,21 @@ int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, floa
     a.scale = inv_temp;
     a.logp = logp;
     a.lse = lse;
+    a.stats = stats;
     a.fault = fault_word();
     a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     Plan plan{};
     return record_plan(launch_logit_rows(dtype, a, false, forced_generic(), dev.sms, stream, &plan), plan);
+}
+
+int logprob_fwd_stats(const void *logits, const int64_t *targets, float *logp, float *lse, float *stats,
+                      int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream) {
+    return logprob_fwd_stats_ld(logits, V, targets, logp, lse, stats, rows, V, inv_temp, dtype, stream);
+}
+
+int logprob_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *lse,
+                   int64_t rows, int64_t V, float inv_temp, int dtype, cudaStream_t stream) {
+    return logprob_fwd_stats_ld(logits, ldl, targets, logp, lse, nullptr, rows, V, inv_temp, dtype, stream);
 }
 
 int logprob_fwd(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
@@ -1280,24 +1292,30 @@ int logprob_fwd(const void *logits, const int64_t *targets, float *logp, float *
     return logprob_fwd_ld(logits, V, targets, logp, lse, rows, V, inv_temp, dtype, stream);
 }
 
-int logprob_bwd_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
-                   const float *lse, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
-                   float inv_temp, int dtype, cudaStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// The gradient from lse [rows], or from stats [rows][2].
+int logprob_bwd_any(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets, const float *lse,
+                    const float *stats, void *dlogits, int64_t lddl, int64_t rows, int64_t V, float inv_temp,
+                    int dtype, cudaStream_t stream) {
     int st = validate_logits(rows, V, inv_temp, dtype);
     if (st != NRM_OK) return st;
     if (rows == 0) return NRM_OK;  // empty input: no pointer is used
-    if (!dlogp || !logits || !targets || !lse || !dlogits) return NRM_ERR_NULL;
+    if (!dlogp || !logits || !targets || (!lse && !stats) || !dlogits) return NRM_ERR_NULL;
     const size_t es = elem_size(dtype);
     if ((st = validate_ld(rows, V, es, {ldl, lddl})) != NRM_OK) return st;
     if ((st = check_elem_alignment({logits, dlogits}, es)) != NRM_OK) return st;
-    if ((st = check_elem_alignment({dlogp, lse}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({dlogp, lse, stats}, 4)) != NRM_OK) return st;
     if ((st = check_elem_alignment({targets}, 8)) != NRM_OK) return st;
     const bool inplace = logits == dlogits && ldl == lddl;
     const RSpan sl = rspan(inplace ? nullptr : logits, ldl, rows, V, es),
                 stg = rspan(targets, rows, 1, rows, 8), sp = rspan(dlogp, rows, 1, rows, 4),
-                ss = rspan(lse, rows, 1, rows, 4), sd = rspan(dlogits, lddl, rows, V, es);
-    if ((st = check_alias({sd}, {sl, stg, sp, ss})) != NRM_OK) return st;
-    if ((st = check_pointers({dlogp, logits, targets, lse, dlogits})) != NRM_OK) return st;
+                ss = rspan(lse, rows, 1, rows, 4), st2 = rspan(stats, 2 * rows, 1, 2 * rows, 4),
+                sd = rspan(dlogits, lddl, rows, V, es);
+    if ((st = check_alias({sd}, {sl, stg, sp, ss, st2})) != NRM_OK) return st;
+    if ((st = check_pointers({dlogp, logits, targets, lse, stats, dlogits})) != NRM_OK) return st;
     DevInfo dev;
     if ((st = device_info(&dev)) != NRM_OK) return st;
     LogitArgs a{};
@@ -1309,12 +1327,35 @@ int logprob_bwd_ld(const float *dlogp, const void *logits, int64_t ldl, const in
     a.scale = inv_temp;
     a.dlogp = dlogp;
     a.lse_in = lse;
+    a.stats_in = stats;
     a.dz = dlogits;
     a.lddz = lddl;
     Plan plan{};
     plan.kind = PLAN_CTA;
     plan.threads = 256;
     return record_plan(launch_logit_grad(dtype, a, stream), plan);
+}
+
+}  // namespace
+
+extern "C" {
+
+int logprob_bwd_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
+                   const float *lse, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
+                   float inv_temp, int dtype, cudaStream_t stream) {
+    return logprob_bwd_any(dlogp, logits, ldl, targets, lse, nullptr, dlogits, lddl, rows, V, inv_temp, dtype, stream);
+}
+
+int logprob_bwd_stats_ld(const float *dlogp, const void *logits, int64_t ldl, const int64_t *targets,
+                         const float *stats, void *dlogits, int64_t lddl, int64_t rows, int64_t V,
+                         float inv_temp, int dtype, cudaStream_t stream) {
+    return logprob_bwd_any(dlogp, logits, ldl, targets, nullptr, stats, dlogits, lddl, rows, V, inv_temp, dtype, stream);
+}
+
+int logprob_bwd_stats(const float *dlogp, const void *logits, const int64_t *targets, const float *stats,
+                      void *dlogits, int64_t rows, int64_t V, float inv_temp, int dtype,
+                      cudaStream_t stream) {
+    return logprob_bwd_stats_ld(dlogp, logits, V, targets, stats, dlogits, V, rows, V, inv_temp, dtype, stream);
 }
 
 int logprob_bwd(const float *dlogp, const void *logits, const int64_t *targets, const float *lse,

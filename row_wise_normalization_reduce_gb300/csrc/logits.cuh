@@ -203,16 +203,17 @@ template <typename T> __device__ __forceinline__ void st_pack(T *p, const uint4 
 }
 
 // dz of one element and of a pack: k * 2^((a z + b) c); a, b, c and k are the
-// row's.
+// row's.  BASE: (z - base) in the place of z.
 __device__ __forceinline__ float grad_one(float z, float a, float b, float c, float k) {
     return k * exp2_fast(fmaf(z, a, b) * c);
 }
-template <typename T>
-__device__ __forceinline__ uint4 grad_pack(const uint4 &z, float a, float b, float c, float k) {
+template <typename T, bool BASE = false>
+__device__ __forceinline__ uint4 grad_pack(const uint4 &z, float a, float b, float c, float k, float base = 0.f) {
     float2 v[IO2<T>::H];
     IO2<T>::unpack(z, v);
 #pragma unroll
     for (int i = 0; i < IO2<T>::H; ++i) {
+        if (BASE) v[i] = __fadd2_rn(v[i], f2(-base));
         v[i] = __fmul2_rn(__ffma2_rn(v[i], f2(a), f2(b)), f2(c));
         v[i].x = exp2_fast(v[i].x);
         v[i].y = exp2_fast(v[i].y);
@@ -246,12 +247,24 @@ __device__ __forceinline__ void finish_row(const LogitArgs &a, int64_t row, cons
     if (write) {
         if (a.logp) a.logp[row] = logp.hi;
         // the log-sum as that of the row's own maximum
-        if (a.lse) {
-            const Two top = empty ? Two{INFINITY, 0.f} : log_prob(r.m, r.m, r.d, a.scale);
-            a.lse[row] = fmaf(a.scale, r.m, -top.hi);
+        if (!POLICY) {
+            const float logd = empty ? -INFINITY : -log_prob(r.m, r.m, r.d, a.scale).hi;
+            if (a.lse) a.lse[row] = fmaf(a.scale, r.m, logd);
+            if (a.stats) {
+                a.stats[2 * row] = r.m;
+                a.stats[2 * row + 1] = logd;
+            }
         }
         if (POLICY) a.row_loss[row] = *loss;
     }
+}
+
+// The scalar outputs of a row that takes no part.
+template <bool POLICY> __device__ __forceinline__ void no_row(const LogitArgs &a, int64_t row) {
+    if (a.logp) a.logp[row] = 0.f;
+    if (!POLICY && a.lse) a.lse[row] = 0.f;
+    if (!POLICY && a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.f;
+    if (POLICY) a.row_loss[row] = 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -389,9 +402,7 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
                 if (g != 0.f) continue;
             }
         } else if (t == 0 && rank == 0) {
-            if (a.logp) a.logp[row] = 0.f;
-            if (a.lse) a.lse[row] = 0.f;
-            if (POLICY) a.row_loss[row] = 0.f;
+            no_row<POLICY>(a, row);
         }
         if (POLICY && D) {  // no gradient: zeros
             const bool wide = (reinterpret_cast<uintptr_t>(D + cut.head) & 15) == 0;
@@ -631,11 +642,7 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
         if (live) fetch(r0 + __ffs(live) - 1);
         for (; dead; dead &= dead - 1) {
             const int64_t row = r0 + __ffs(dead) - 1;
-            if (t == 0 && rank == 0) {
-                if (a.logp) a.logp[row] = 0.f;
-                if (a.lse) a.lse[row] = 0.f;
-                if (POLICY) a.row_loss[row] = 0.f;
-            }
+            if (t == 0 && rank == 0) no_row<POLICY>(a, row);
             if (POLICY && a.dz) zero_fill(RowView<T>(a, row, rank, log_cs, t));
         }
         while (live) {
@@ -798,10 +805,7 @@ __global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, 
         const int64_t my_target = have ? a.target[r0 + lane] : -1;
         const bool takes_part = my_target >= 0 && my_target < a.V;
         uint32_t live = __ballot_sync(0xffffffffu, takes_part);
-        if (t < 32 && have && !takes_part) {
-            if (a.logp) a.logp[r0 + lane] = 0.f;
-            if (a.lse) a.lse[r0 + lane] = 0.f;
-        }
+        if (t < 32 && have && !takes_part) no_row<false>(a, r0 + lane);
         float zn = 0.f;  // the next row's scalar element
         auto fetch = [&](int64_t row, int seg) {
             const RowView<T> w(a, row, 0, 0, t);
@@ -863,13 +867,16 @@ __global__ void __launch_bounds__(TH, MINB) logit_seg_kernel(const LogitArgs a, 
 }
 
 // ---------------------------------------------------------------------------
-// The gradient for a given slope dlogp and the forward's lse: element-wise.
+// The gradient for a given slope dlogp and the forward's lse, or (STATS) the
+// row's maximum m and log d, lse = s m + log d: element-wise.  With lse the
+// rounding of that one number is a factor on the whole row, |lse| 2^-24 of it;
+// s (z - m) - log d costs one more subtraction an element, which HBM hides.
 // A group of TH threads (the CTA, or a warp where rows are short) takes one
 // tile of 4 x TH packs of a row, so there is nothing to wait for but the loads
 // of one tile: 2048 x 131072 bf16 137 us, 6.9 TB/s.  An element at its row's
 // lse takes exp(s z - lse), no max: lse is the maximum's own upper bound.
 // ---------------------------------------------------------------------------
-template <typename T, int TH>
+template <typename T, int TH, bool STATS>
 __global__ void __launch_bounds__(256) logit_grad_kernel(const LogitArgs a, const int tiles) {
     constexpr int G = 256 / TH, V = IO<T>::V, U = 4;
     const int t = threadIdx.x % TH;
@@ -882,7 +889,8 @@ __global__ void __launch_bounds__(256) logit_grad_kernel(const LogitArgs a, cons
         const T *Z = static_cast<const T *>(a.z) + row * a.ldz;
         T *D = static_cast<T *>(a.dz) + row * a.lddz;
         const int64_t tgt = a.target[row];
-        const float lse = a.lse_in[row];
+        const float lse = STATS ? a.stats_in[2 * row + 1] : a.lse_in[row];  // STATS: log d
+        const float top = STATS ? a.stats_in[2 * row] : 0.f;
         const bool in = tgt >= 0 && tgt < a.V;
         const float g = in && lse != -INFINITY ? a.dlogp[row] * a.scale : 0.f;
         const RowCut<T> cut = cut_row(Z, a.V);
@@ -906,9 +914,10 @@ __global__ void __launch_bounds__(256) logit_grad_kernel(const LogitArgs a, cons
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (p0 + u * TH < cut.packs)
-                    st_pack(out + (int64_t)(p0 + u * TH) * V, grad_pack<T>(raw[u], a.scale, -lse, kLog2e, -g), wide);
-            if (t < ns) D[sc] = IO<T>::from_f(grad_one(IO<T>::to_f(Z[sc]), a.scale, -lse, kLog2e, -g));
-            if (owner) D[tgt] = IO<T>::from_f(g + grad_one(za, a.scale, -lse, kLog2e, -g));
+                    st_pack(out + (int64_t)(p0 + u * TH) * V,
+                            grad_pack<T, STATS>(raw[u], a.scale, -lse, kLog2e, -g, top), wide);
+            if (t < ns) D[sc] = IO<T>::from_f(grad_one(IO<T>::to_f(Z[sc]) - top, a.scale, -lse, kLog2e, -g));
+            if (owner) D[tgt] = IO<T>::from_f(g + grad_one(za - top, a.scale, -lse, kLog2e, -g));
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -1052,18 +1061,20 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
     return launch_clusters(logit_rows_kernel<T, POLICY>, a.rows, cs, kLogitThreads, 0, s, a, cs);
 }
 
-template <typename T, int TH> cudaError_t launch_logit_grad_g(const LogitArgs &a, cudaStream_t s) {
+template <typename T, int TH, bool STATS> cudaError_t launch_logit_grad_g(const LogitArgs &a, cudaStream_t s) {
     constexpr int G = 256 / TH;
     const int64_t packs = a.V / IO<T>::V + 1;
     const int64_t tiles = (packs + 4 * TH - 1) / (4 * TH);
     const int64_t n = (a.rows * tiles + G - 1) / G;
-    return launch_row(logit_grad_kernel<T, TH>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), 256u, 0, s, a,
+    return launch_row(logit_grad_kernel<T, TH, STATS>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), 256u, 0, s, a,
                       (int)tiles);
 }
 // Rows of up to 512 packs by warps: 8192 x 1000 bf16 5.8 us, by CTAs 17.4; 8192
 // x 4096 23.3 and 23.9; at 750 packs (8192 x 6000) 32.7 and 30.9.
 template <typename T> cudaError_t launch_logit_grad_t(const LogitArgs &a, cudaStream_t s) {
-    return a.V / IO<T>::V <= 512 ? launch_logit_grad_g<T, 32>(a, s) : launch_logit_grad_g<T, 256>(a, s);
+    const bool warps = a.V / IO<T>::V <= 512;
+    if (a.stats_in) return warps ? launch_logit_grad_g<T, 32, true>(a, s) : launch_logit_grad_g<T, 256, true>(a, s);
+    return warps ? launch_logit_grad_g<T, 32, false>(a, s) : launch_logit_grad_g<T, 256, false>(a, s);
 }
 
 }  // namespace nrm

@@ -333,7 +333,8 @@ struct LogitArgs {
     const int64_t *target;
     int64_t rows, V;
     float scale;
-    float *logp, *lse;          // outputs, either may be NULL
+    float *logp, *lse;          // outputs, each may be NULL
+    float *stats;               // [rows][2]: the row's maximum and log d
     // policy loss
     const float *old, *adv, *weight, *ref;  // weight, ref may be NULL
     float kl, ratio_lo, ratio_hi;
@@ -343,7 +344,7 @@ struct LogitArgs {
     void *dz;                   // NULL: no gradient
     int64_t lddz;
     // gradient of a given slope
-    const float *dlogp, *lse_in;
+    const float *dlogp, *lse_in, *stats_in;  // stats_in, or lse_in where it is NULL
     unsigned *fault;            // device fault word, or NULL
     unsigned wait_limit;        // tries per bounded wait
 };

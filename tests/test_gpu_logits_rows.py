@@ -285,3 +285,73 @@ def test_equal_logits_reach_the_low_part():
     # the test above says something: of its sums more than half have a remainder that decides
     rest = [abs(-np.log(v) - float(np.float32(-np.log(v)))) for v in ONES if v > 1]
     assert sum(r > 2.0 ** -24 for r in rest) > len(rest) / 2
+
+
+# --- the gradient end to end, from the forward's stats -----------------------
+def check_logprob_bwd(z, t, g, s, dz):
+    """dz against g s (onehot - softmax(s z)) of the logits themselves, with the bounds of check_policy."""
+    v = z.shape[1]
+    ok = (t >= 0) & (t < v) & (g != 0)
+    for p in parts(*z.shape):
+        assert not (dz[p][~ok[p]] != 0).any()
+        i = torch.nonzero(ok[p])[:, 0]
+        x, _, _, slack = logsoftmax64(z[p][i], s)
+        none, nan = x.amax(-1) == -INF, x.isnan().any(-1)  # no finite logit; an infinite one (NaN as anywhere)
+        assert not (dz[p][i][none] != 0).any() and dz[p][i][nan].isnan().all()
+        i, x, slack = (q[~none & ~nan] for q in (i, x, slack))
+        k, a = g[p][i].double()[:, None] * s, t[p][i][:, None]
+        soft = torch.exp(x)
+        out = (-k * soft).scatter_add_(-1, a, k)
+        mag = out.abs().scatter_(-1, a, k.abs())
+        arg = torch.where(soft > 0, x.abs(), 0.0)
+        near(dz[p][i], out, out_room(z.dtype, out, mag * ((3 * arg + 16) * R.U + slack[:, None])), "dlogits")
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("s", [1.0, 0.7, 2.5])
+@pytest.mark.parametrize("rows,n,stream", [(40, 1, 0), (400, 20, 0), (310, 900, 0), (24, 5000, 0), (310, 2500, 0), (24, 5000, 1)])
+def test_gradient_from_stats(rows, n, stream, s, dtype):
+    # rows with a common offset of up to 1e4 and rows masked as a whole by
+    # finite values, the type's lowest among them: what one binary32 lse loses
+    v = packs(n, dtype)
+    z, t = mixed(rows, v, dtype, n, low=torch.finfo(dtype).min)[:2]
+    for i, off in enumerate((1e3, -1e3, 1e4, -1e4)):
+        z[8 + i::12] = (z[8 + i::12].float() + off).to(dtype)
+    if dtype != torch.float16:
+        z[3::12] = -1e30
+    if stream:
+        nrm.force_plan(nrm.PLAN_GENERIC)
+    plain = nrm.logprob_fwd(z, t, s)
+    stats = torch.full((rows, 2), 7.0, device="cuda")
+    logp, lse = nrm.logprob_fwd(z, t, s, stats=stats)
+    same = lambda a, b: torch.equal(a.nan_to_num(9.0), b.nan_to_num(9.0))  # noqa: E731  (binary16's largest + 1e4: NaN rows)
+    assert same(logp, plain[0]) and same(lse, plain[1])
+    ok = (t >= 0) & (t < v)
+    assert not stats[~ok].any() and torch.equal(stats[ok][:, 0], z[ok].amax(-1).float())
+    g = torch.linspace(-1.0, 1.0, rows, device="cuda")
+    g[rows // 2] = 0.0
+    dz = nrm.logprob_bwd(g, z, t, None, s, stats=stats)
+    check_logprob_bwd(z, t, g, s, dz)
+    # rows at another alignment, and in place
+    flat = torch.empty(rows * (v + 1) + 1, dtype=dtype, device="cuda")
+    other = flat[1:].view(rows, v + 1)[:, :v]
+    other.copy_(z)
+    assert same(nrm.logprob_bwd(g, other, t, None, s, stats=stats), dz)
+    x = z.clone()
+    got = nrm.logprob_bwd(g, x, t, None, s, stats=stats, out=x)
+    assert got.data_ptr() == x.data_ptr() and same(x, dz)
+
+
+def test_stats_are_refused_in_other_forms():
+    z, t, old = (q.cuda() for q in (torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(4)))
+    good = torch.zeros(4, 2, device="cuda")
+    for bad in (good.half(), good[:3], good.t().contiguous(), torch.zeros(4, 4, device="cuda")[:, ::2], good.cpu()):
+        with pytest.raises(ValueError):
+            nrm.logprob_fwd(z, t, stats=bad)
+        with pytest.raises(ValueError):
+            nrm.logprob_bwd(old, z, t, None, stats=bad)
+    with pytest.raises(ValueError):
+        nrm.logprob_bwd(old, z, t, None)
+    with pytest.raises(nrm.NrmError) as e:
+        nrm.logprob_fwd(z, t, stats=z.view(-1)[:8].view(4, 2))
+    assert e.value.status == 4
