@@ -1054,11 +1054,17 @@ int rows_map(int64_t N, size_t es, std::initializer_list<RowPtr> ts, const void 
     return whole ? MAP_V : same ? MAP_A : MAP_S;
 }
 
+// Status of a launch.  The runtime keeps a failed one's error until it is read:
+// it is this call's, not the next one's.
+int launched(cudaError_t e) {
+    if (e == cudaSuccess) return NRM_OK;
+    cudaGetLastError();
+    return NRM_ERR_LAUNCH;
+}
+
 int record_plan(cudaError_t e, const Plan &p) {
-    if (e != cudaSuccess) {
-        cudaGetLastError();  // this call's, not the next one's
-        return NRM_ERR_LAUNCH;
-    }
+    const int st = launched(e);
+    if (st != NRM_OK) return st;
     t_last_kind = p.kind;
     t_last_threads = p.threads;
     t_last_packs = p.packs;
@@ -1174,7 +1180,7 @@ int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_ou
     if (rows == 0) {  // no rows: the weight gradient is an empty sum, nothing else exists
         if (!dw) return NRM_OK;
         if ((st = check_pointers({dw})) != NRM_OK) return st;
-        return launch_dw_fold(nullptr, dw, 0, N, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+        return launched(launch_dw_fold(nullptr, dw, 0, N, stream));
     }
     if (!dy || !residual_out || !rstd || (!dx && !dresidual && !dw)) return NRM_ERR_NULL;
     const size_t es = elem_size(dtype);
@@ -1213,7 +1219,7 @@ int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_ou
     int64_t parts = 0;
     st = record_plan(launch_drop_bwd(dtype, a, map, forced_generic(), dev.sms, stream, &plan, &parts), plan);
     if (st != NRM_OK || !dw) return st;
-    return launch_dw_fold(a.part, dw, parts, N, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+    return launched(launch_dw_fold(a.part, dw, parts, N, stream));
 }
 
 int dropout_add_rms_bwd(const void *dy, const void *residual_out, const float *rstd, const void *w,
@@ -1385,7 +1391,7 @@ int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, cons
         return st;
     if (rows == 0) {  // no rows: the loss is an empty sum
         if ((st = check_pointers({loss})) != NRM_OK) return st;
-        return launch_loss_fold(nullptr, loss, 0, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+        return launched(launch_loss_fold(nullptr, loss, 0, stream));
     }
     if (!logits || !targets || !old_logp || !advantages || (kl_coef > 0.f && !ref_logp)) return NRM_ERR_NULL;
     const size_t es = elem_size(dtype);
@@ -1434,7 +1440,7 @@ int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, cons
     Plan plan{};
     st = record_plan(launch_logit_rows(dtype, a, true, forced_generic(), dev.sms, stream, &plan), plan);
     if (st != NRM_OK) return st;
-    return launch_loss_fold(a.row_loss, loss, rows, stream) == cudaSuccess ? NRM_OK : NRM_ERR_LAUNCH;
+    return launched(launch_loss_fold(a.row_loss, loss, rows, stream));
 }
 
 int policy_loss(const void *logits, const int64_t *targets, const float *old_logp,
