@@ -355,3 +355,101 @@ def test_stats_are_refused_in_other_forms():
     with pytest.raises(nrm.NrmError) as e:
         nrm.logprob_fwd(z, t, stats=z.view(-1)[:8].view(4, 2))
     assert e.value.status == 4
+
+
+# --- the loss' gradient against differences ----------------------------------
+@pytest.mark.parametrize("kl", [0.0, 0.1])
+@pytest.mark.parametrize("rows,v", [(10, 700), (6, 5003), (5, 40001)])
+def test_gradient_against_differences_along_itself(rows, v, kl):
+    # along the gradient's signs the slope is its 1-norm, the largest there is.
+    # Central differences of the library's loss differ from it by the formula's
+    # own truncation at this step (taken in 64 bits, from the same two points),
+    # by the loss' bound at either point over 2 h and by the gradient's bound
+    g = torch.Generator().manual_seed(rows)
+    z = 2 * torch.randn(rows, v, generator=g)
+    t = torch.randint(0, v, (rows,), generator=g)
+    z[torch.arange(rows), t] += 8
+    logp = torch.from_numpy(R.logprob(z.double().numpy(), t.numpy(), 1.0)[0]).float()
+    old = logp - torch.tensor([-0.6, -0.1, 0.1, 0.6, 0.0])[torch.arange(rows) % 5]
+    adv = torch.where(torch.arange(rows) % 2 == 0, 1.0, -1.0) * (0.5 + torch.rand(rows, generator=g))
+    ref, wt = logp + 0.4 * torch.randn(rows, generator=g), 0.5 + torch.rand(rows, generator=g)
+    rest = [x.cuda() for x in (t, old, adv, wt, ref)]
+    rest64 = [t.numpy(), *(x.double().numpy() for x in (old, adv, wt, ref))]
+    loss = lambda q: float(nrm.policy_loss(q, *rest, LO, HI, kl, want_grad=False)[0])  # noqa: E731
+    exact = lambda q: R.policy(R.f64(q), *rest64, LO, HI, kl, 1.0)  # noqa: E731
+    dz = nrm.policy_loss(z.cuda(), *rest, LO, HI, kl)[2]
+    h = 2.0 ** -5
+    hi, lo = z.cuda() + h * dz.sign(), z.cuda() - h * dz.sign()
+    # the step that binary32 took, and the slope along it
+    d = (hi.double() - lo.double()) / (2 * h)
+    slope = float((dz.double() * d).sum())
+    out64 = exact(z)
+    dz64 = torch.from_numpy(R.grad(z.double().numpy(), rest64[0], out64[3], out64[2], 1.0)[0])
+    e_hi, e_lo = exact(hi), exact(lo)
+    truncation = abs((e_hi[0] - e_lo[0]) / (2 * h) - float((dz64 * d.cpu()).sum()))
+    room = truncation + (e_hi[5] + e_lo[5] + R.U * (abs(e_hi[0]) + abs(e_lo[0]))) / (2 * h) + 512 * R.U * float(dz.double().abs().sum())
+    assert room < 0.01 * slope  # nothing less than the whole gradient passes
+    assert abs((loss(hi) - loss(lo)) / (2 * h) - slope) <= room
+
+
+# --- batches of rows ---------------------------------------------------------
+# A group (warp, CTA, cluster) takes a batch of up to 32 rows and fetches the
+# next live one ahead: live, dead, clipped and empty rows side by side, in each
+# kernel, batches of two and more.  (rows, packs, plan, threads, packs a thread)
+BATCHES = [(950_001, 3, "warp", 128, 4), (30_011, 100, "warp", 128, 4), (22_003, 250, "warp", 128, 8),
+           (15_001, 380, "warp", 128, 12), (15_001, 500, "warp", 128, 16), (7_501, 600, "cta", 128, 8),
+           (5_603, 1200, "cta", 160, 8), (4_703, 1500, "cta", 192, 8), (3_701, 1700, "cta", 224, 8),
+           (3_701, 1900, "cta", 256, 8), (2_903, 2400, "cluster", 160, 8), (1_201, 6000, "cluster", 192, 8),
+           (483, 14000, "cluster", 224, 8), (353, 19000, "cluster", 256, 10)]
+KIND = {"warp": nrm.PLAN_WARP, "cta": nrm.PLAN_CTA, "cluster": nrm.PLAN_CLUSTER}
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,n,kind,threads,per", BATCHES)
+def test_batches_of_mixed_rows(rows, n, kind, threads, per, dtype):
+    v = packs(n, dtype)
+    z, t, old, adv, wt, ref = mixed(rows, v, dtype, n + 1)
+    z[(t < 0) | (t >= v)] = float("nan")  # not read
+    got = nrm.policy_loss(z, t, old, adv, wt, ref, LO, HI, 0.1)
+    assert nrm.last_plan()[:3] == (KIND[kind], threads, per)
+    check_policy(z, t, old, adv, wt, ref, 0.1, 1.0, got)
+    x = z.clone()
+    for a, b in zip(nrm.policy_loss(x, t, old, adv, wt, ref, LO, HI, 0.1, out=x), got):
+        assert torch.equal(a, b)
+    # at another temperature, without the KL term, the gradient scaled
+    z, t, old, adv, wt, ref = mixed(rows, v, dtype, n + 2, s=0.6)
+    gs = torch.tensor(-3.0, device="cuda")
+    check_policy(z, t, old, adv, wt, ref, 0.0, 0.6, nrm.policy_loss(z, t, old, adv, wt, None, LO, HI, 0.0, 0.6, grad_scale=gs), -3.0)
+    check_logprob(z, t, 0.6, nrm.logprob_fwd(z, t, 0.6))
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,n", [(7_401, 2300), (3_701, 5001)])
+def test_batches_of_rows_in_segments(rows, n, dtype):
+    # the log-probability alone, rows longer than a CTA's registers, batches of two and of one
+    v = packs(n, dtype)
+    z, t = mixed(rows, v, dtype, n + 1, s=1.3)[:2]
+    z[(t < 0) | (t >= v)] = float("nan")
+    got = nrm.logprob_fwd(z, t, 1.3)
+    assert nrm.last_plan()[:3] == (nrm.PLAN_CTA, 256, 8)
+    check_logprob(z, t, 1.3, got)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,n,cs", [(1009, 300, 1), (311, 1500, 1), (200, 1300, 2), (100, 2500, 4), (20, 5000, 8), (70, 4200, 8)])
+def test_the_streaming_plan(rows, n, cs, dtype):
+    # forced: a row by one, two, four and eight CTAs, also in place
+    v = packs(n, dtype)
+    z, t, old, adv, wt, ref = mixed(rows, v, dtype, n + 1, s=1.2)
+    z[(t < 0) | (t >= v)] = float("nan")
+    nrm.force_plan(nrm.PLAN_GENERIC)
+    got = nrm.logprob_fwd(z, t, 1.2)
+    assert nrm.last_plan()[0] == nrm.PLAN_GENERIC and max(1, nrm.last_plan()[4]) == cs
+    check_logprob(z, t, 1.2, got)
+    got = nrm.policy_loss(z, t, old, adv, wt, ref, LO, HI, 0.1, 1.2)
+    assert nrm.last_plan()[0] == nrm.PLAN_GENERIC and max(1, nrm.last_plan()[4]) == cs
+    check_policy(z, t, old, adv, wt, ref, 0.1, 1.2, got)
+    for _ in range(2):
+        x = z.clone()
+        for a, b in zip(nrm.policy_loss(x, t, old, adv, wt, ref, LO, HI, 0.1, 1.2, out=x), got):
+            assert torch.equal(a, b)
