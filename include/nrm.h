@@ -450,7 +450,7 @@ int dropout_add_rms_bwd_ld(const void *dy, int64_t lddy, const void *residual_ou
  *   targets  [rows] int64.  A row whose target is outside [0, V) (padding,
  *            conventionally -100) takes no part: its logits are not read, logp = lse = 0
  *   logp, lse  [rows] binary32, written; one of them may be NULL
- *   V < 2^31 (NRM_ERR_SHAPE); inv_temp > 0, finite
+ *   V < 2^31 (NRM_ERR_SHAPE); inv_temp > 0, inv_temp * log2(e) finite (up to 2.3e38)
  * A row whose entries are all -inf gives logp = lse = -inf.
  * The stats form writes for the backward also
  *   stats    [rows][2] binary32, per row max_j z_j and log sum_j exp(s (z_j - max));

@@ -1241,7 +1241,8 @@ int validate_logits(int64_t rows, int64_t V, float inv_temp, int dtype) {
     const int st = validate_rows(rows, V, 0.f, dtype);
     if (st != NRM_OK) return st;
     if (V > 0x7fffffff) return NRM_ERR_SHAPE;  // a column is a 32-bit index in the kernels
-    if (!(std::isfinite(inv_temp) && inv_temp > 0.f)) return NRM_ERR_VALUE;
+    // the kernels' factor on logits is inv_temp log2(e)
+    if (!(std::isfinite(inv_temp * 1.442695f) && inv_temp > 0.f)) return NRM_ERR_VALUE;
     return NRM_OK;
 }
 

@@ -39,3 +39,12 @@ def test_what_one_number_loses(offset):
         assert abs(one * v - 1) <= abs(float(lse)) * 2.0 ** -24 + 2.0 ** -21
     else:
         assert one == 1.0
+
+
+@pytest.mark.parametrize("s,want", [(2.3e38, (OK, DEVICE)), (2.5e38, VALUE), (3.4e38, VALUE), (1e-45, (OK, DEVICE))])
+def test_the_largest_inverse_temperatures(lib, s, want):  # noqa: F811
+    # s log2(e), the kernels' factor, has to be finite: infinite, it makes 0 times infinity of the row's maximum
+    want = want if isinstance(want, tuple) else (want,)
+    assert lib.logprob_fwd(A, 2 * A, 3 * A, 4 * A, 4, 8, s, 0, None) in want
+    assert lib.logprob_bwd(A, 2 * A, 3 * A, 4 * A, 5 * A, 4, 8, s, 0, None) in want
+    assert lib.policy_loss(A, 2 * A, 3 * A, 4 * A, None, None, 0.2, 0.2, 0.0, s, None, 5 * A, 6 * A, 7 * A, 4, 8, 0, 8 * A, 16, None) in want
