@@ -198,16 +198,6 @@ template <typename T> struct Frag {
     uint32_t r[2 * sizeof(T)];
 };
 
-// Streaming 16-byte load that stays coherent (an output may be the input).
-__device__ __forceinline__ uint4 ld_once(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-    return r;
-}
-
 // Place of element j of this lane in a chunk (its column, plus the shift for
 // MAP_A).
 template <typename T, int MAP> __device__ __forceinline__ int frag_col(int j) {

@@ -177,15 +177,6 @@ template <typename T> __device__ __forceinline__ RowCut<T> cut_row(const T *p, i
     return c;
 }
 
-// 16-byte load of data that may be overwritten in place later.
-__device__ __forceinline__ uint4 ld_pack(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-    return r;
-}
 template <typename T> __device__ __forceinline__ void st_pack(T *p, const uint4 &v, bool wide) {
     if (wide) {
         st_stream(p, v);
@@ -319,7 +310,7 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
                 uint4 raw[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (p + u * TH < p1) raw[u] = ld_pack(body + (int64_t)(p + u * TH) * V);
+                    if (p + u * TH < p1) raw[u] = ld_once(body + (int64_t)(p + u * TH) * V);
                 float bm = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -386,7 +377,7 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
                         uint4 raw[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            if (p - u * TH >= p0) raw[u] = ld_pack(body + (int64_t)(p - u * TH) * V);
+                            if (p - u * TH >= p0) raw[u] = ld_once(body + (int64_t)(p - u * TH) * V);
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
                             if (p - u * TH >= p0)
@@ -910,7 +901,7 @@ __global__ void __launch_bounds__(256) logit_grad_kernel(const LogitArgs a, cons
             uint4 raw[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (p0 + u * TH < cut.packs) raw[u] = ld_pack(body + (int64_t)(p0 + u * TH) * V);
+                if (p0 + u * TH < cut.packs) raw[u] = ld_once(body + (int64_t)(p0 + u * TH) * V);
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (p0 + u * TH < cut.packs)

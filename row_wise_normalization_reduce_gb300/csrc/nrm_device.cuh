@@ -146,6 +146,16 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
     return r;
 }
 
+// The same, coherent: for data that an output may replace in place.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
 // 16-byte load of data every CTA re-reads (parameters): keep it cached.
 __device__ __forceinline__ uint4 ld_param(const void *p) {
     return __ldg(reinterpret_cast<const uint4 *>(p));
