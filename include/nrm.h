@@ -473,7 +473,8 @@ int logprob_fwd_stats_ld(const void *logits, int64_t ldl, const int64_t *targets
  *   dlogits_j = dlogp * s * ((j == target) - exp(s z_j - lse))
  * Rows without a target in [0, V), rows with dlogp = 0 and rows without a
  * finite logit (lse = -inf) get zeros, their logits are not read.
- *   dlogits  [rows, V] dtype, written; may be logits (same row stride)
+ *   dlogits  [rows, V] dtype, written; may be logits (same row stride).  In
+ *            binary16 scale dlogp against underflow (below 2^-25 nothing is held)
  * The given lse is taken as it is.  Its rounding to binary32 is a factor on the
  * whole row: up to |lse| 2^-24 relative, 6e-4 at an lse of 1e4, and at 2^24 and
  * beyond nothing is left (a row whose logits are all masked by the type's lowest
@@ -515,7 +516,10 @@ int logprob_bwd_stats_ld(const float *dlogp, const void *logits, int64_t ldl, co
  *   grad_scale  device binary32 [1] or NULL (= 1): the gradient of the loss
  *   loss        [1] binary32, written (0 when no row takes part)
  *   logp        [rows] binary32 or NULL
- *   dlogits     [rows, V] dtype or NULL (loss only); may be logits (same row stride)
+ *   dlogits     [rows, V] dtype or NULL (loss only); may be logits (same row stride).
+ *               Binary16 holds nothing below 2^-25: with weights of 1 / rows and a
+ *               large vocabulary most of a row's gradient rounds to 0 or to single
+ *               steps of 2^-24 there.  grad_scale is the loss scale against that
  *   0 <= clip_low <= 1, clip_high >= 0 and finite, kl_coef >= 0 and finite
  *   workspace   device memory, 16-byte aligned, policy_loss_workspace_size(rows)
  *               bytes, scratch; calls sharing one must be ordered on the GPU

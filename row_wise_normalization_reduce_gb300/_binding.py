@@ -790,7 +790,8 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
       max(-A ratio, -A clip(ratio, 1 - clip_low, 1 + clip_high))
         + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1)
     weighted and summed.  grad_scale (one binary32 value on the device)
-    multiplies the gradient.  out, the gradient's tensor, may be logits;
+    multiplies the gradient: the loss scale that binary16 gradients need, most
+    of which are below 2^-24 at weights of 1 / rows and a large vocabulary.  out, the gradient's tensor, may be logits;
     want_grad=False computes the loss only.  Returns (loss, logp, dlogits or
     None)."""
     if stream is not None:

@@ -501,8 +501,9 @@ __device__ __forceinline__ float warps_sum_all(float v, float *slot, int nw) {
 //
 // Bound by HBM on the 16-byte grid: 4096 x 4096 bf16 19.0 us, 7.1 TB/s, with
 // 73 % of the issue slots used, so off the grid (half as many instructions
-// again: shuffles, cut packs) it is bound by those: 2795 x 6001 bf16 35.5 us,
-// 56 % of the copy rate, binary32 81 %.  The L2 hint for the row that the next
+// again: a third generator block for a warp's two chunks, shuffles, cut packs) it
+// is bound by those: 2795 x 6001 bf16 35.5 us, 56 % of the copy rate, binary32
+// 81 %.  The L2 hint for the row that the next
 // resident group starts with hides the ramp between rows of one SM.
 // ---------------------------------------------------------------------------
 template <typename T, bool WARP, int U, int MAP, int REGS>

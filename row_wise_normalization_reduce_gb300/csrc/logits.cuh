@@ -120,7 +120,7 @@ __device__ __forceinline__ Two log_prob(float z, float m, float d, float s) {
 }
 
 // exp(q) - q - 1 without the cancellation at small q: its Taylor series to
-// q^8 below 1/2 (the next term is under 4e-8 of the sum).
+// q^8 below 1/2 (the rest is at most 5.1e-8 of the sum, at q = -1/2).
 __device__ __forceinline__ float kl_term(float q) {
     if (fabsf(q) < 0.5f) {
         float t = fmaf(q, 1.f / 40320, 1.f / 5040);
@@ -560,7 +560,9 @@ template <typename T> struct RowView {
         const RowCut<T> cut = cut_row(z, a.V);
         head = cut.head;
         tail = cut.tail;
-        p0 = cut.packs * rank >> log_cs;  // packs < 2^28, ranks <= 8
+        // fits 32 bits: a cluster's rows have at most 8 x 256 x 20 packs, any
+        // others are all rank 0's
+        p0 = cut.packs * rank >> log_cs;
         p1 = cut.packs * (rank + 1) >> log_cs;
         body = z + head + (int64_t)(p0 + t) * V;
         out = d + head + (int64_t)(p0 + t) * V;
@@ -777,8 +779,8 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
 // with a running (max, sum) per thread, the next segment (of this row or of
 // the batch's next live one) on its way meanwhile; one exchange a row.  Held
 // in a cluster's registers instead, a row waits for eight CTAs' exchange:
-// 4096 x 131072 bf16 (10 % of the rows out) 137 us against 169, 4096 x 32000
-// 38.2 against 47.8, f32 2048 x 50001 61.0 against 77.7.  Reads alone run at
+// 4096 x 131072 bf16 (10 % of the rows out) 137 us against 170, 4096 x 32000
+// 39.5 against 47.7, f32 2048 x 50001 61.5 against 71.8.  Reads alone run at
 // 7.0 TB/s, a little above the copy rate.
 // ---------------------------------------------------------------------------
 template <typename T, int TH, int PK, int MINB>
@@ -946,10 +948,10 @@ cudaError_t launch_clusters(K kernel, int64_t rows, int cs, int threads, size_t 
 // Rows per batch.  A batch starts with nothing on its way, but few batches
 // leave the SMs unevenly loaded where rows take no part: six per resident
 // group, and where that leaves less than three rows each, down to two.  Loss and
-// gradient at one row a batch, at three and at four: 1335 x 50257 bf16 60.1, 53.6
-// and 55.2 us, 8192 x 6000 39.3, 37.8 and 37.7; with rows enough for six batches,
-// at four, six and twelve of them: 4096 x 131072 bf16 308.8, 303.2 and 303.2,
-// 8192 x 32000 170.8, 166.8 and 171.5.
+// gradient, inputs beyond L2, at one row a batch, at three and at four: 1335 x
+// 50257 bf16 66.0, 59.6 and 62.0 us, 8192 x 6000 45.6, 42.9 and 43.0; with rows
+// enough for six batches, at four, six and twelve of them (10 % of the rows out):
+// 4096 x 131072 bf16 308.8, 303.2 and 303.2, 8192 x 32000 170.8, 166.8 and 171.5.
 inline int64_t rows_per_batch(int64_t rows, int64_t groups, int64_t least) {
     if (groups < 1) groups = 1;
     const int64_t even = rows / (groups * 6), ahead = rows / (groups * 2);
@@ -987,7 +989,7 @@ cudaError_t launch_logit_seg(const LogitArgs &a, int sms, cudaStream_t s, Plan *
     p->threads = TH;
     p->packs = PK;
     // (a row's own segments follow one another: batches of one row will do, 4096
-    // x 32000 bf16 32.7 us, of three 34.9)
+    // x 32000 bf16 with 10 % of the rows out 39.5 us, of three 42.7)
     const int64_t batch = rows_per_batch(a.rows, (int64_t)sms * per_sm, 1);
     const int64_t n = (a.rows + batch - 1) / batch;
     return launch_row(kernel, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), (unsigned)TH, smem, s, a, (int)batch);
@@ -1020,8 +1022,8 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
         while (cs < 8 && packs > 256 * 8 * cs) cs *= 2;
         // packs that a CTA has room for and the row does not fill cost their
         // instructions all the same, so a CTA is no larger than the slice needs:
-        // 6710 x 10001 bf16 by 160 threads 52.4 us, by 256 68.7; 1365 x 49152
-        // by 192 50.7 and 61.7; 1335 x 50257 by 224 59.9 and 63.2.  With less
+        // 6710 x 10001 bf16 by 160 threads 53.7 us, by 256 66.7; 1365 x 49152
+        // by 192 53.6 and 60.4; 1335 x 50257 by 224 59.5 and 62.5.  With less
         // than four rows or slices for each resident CTA the larger one is
         // ahead (333 x 50001 f16 16.9 us, by 224 17.9).  The strides stay
         // constants: with the CTA's size read at run time 4096 x 131072 took
