@@ -526,6 +526,9 @@ int logprob_bwd_stats_ld(const float *dlogp, const void *logits, int64_t ldl, co
  * A row with a target outside [0, V) or weight 0 takes no part: its logits,
  * old_logp, advantage and ref_logp are not read, logp = 0, dlogits = 0.  A row
  * without a finite logit adds nothing either: logp = -inf, dlogits = 0.
+ * Each row's term is binary32, from a logp good to some 1e-7, and their sum loses
+ * nothing more: a loss whose terms cancel is good to about 1e-8 of the sum of
+ * their magnitudes, and a ratio nearer than that to its bound may take either branch.
  */
 size_t policy_loss_workspace_size(int64_t rows);
 int policy_loss(const void *logits, const int64_t *targets, const float *old_logp,

@@ -499,7 +499,7 @@ __device__ __forceinline__ float warps_sum_all(float v, float *slot, int nw) {
 // that they share one shift (8 rows of any stride are a multiple of 16
 // bytes): its columns are the same in all of them, and w is fetched once.
 //
-// Bound by HBM on the 16-byte grid: 4096 x 4096 bf16 19.0 us, 7.1 TB/s, with
+// Bound by HBM on the 16-byte grid: 4096 x 4096 bf16 19.7 us, 6.8 TB/s, with
 // 73 % of the issue slots used, so off the grid (half as many instructions
 // again: a third generator block for a warp's two chunks, shuffles, cut packs) it
 // is bound by those: 2795 x 6001 bf16 35.5 us, 56 % of the copy rate, binary32
@@ -727,10 +727,10 @@ __device__ __forceinline__ void store_sums(float *stage, const float2 dw[4], flo
 // dw_fold_kernel: no atomics, the same bits every time).  The mask is made
 // again from the seed: reading one back would add 1 to 16 bits an element.
 //
-// 4096 x 4096 bf16 with dh_up 28.9 us (26.7 before the fold), 5.8 TB/s, 86 % of
+// 4096 x 4096 bf16 with dh_up 29.3 us (2.3 of them the fold), 5.7 TB/s, 84 % of
 // the copy rate: dw, w and two rows fill 119 registers, so an SM has 16 warps,
 // at 58 % of its issue slots, and their waits are not all covered.  Off the
-// 16-byte grid instructions bound it: 1999 x 5001 f16 26.8 us, 44 %.
+// 16-byte grid instructions bound it: 1999 x 5001 f16 27.5 us, 43 %.
 template <typename T, bool WARP, int U, int MAP, int REGS, bool AHEAD>
 __global__ void __maxnreg__(REGS) drop_add_rms_bwd_kernel(const DropRmsBwdArgs a) {
     constexpr int G = WARP ? kRowWarps : 1;

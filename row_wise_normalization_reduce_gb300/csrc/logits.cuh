@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kLogitThreads) logit_rows_kernel(const LogitAr
 // barrier.cluster, whose arrival waits for the previous row's stores, 4096 x
 // 131072 bf16 took 417 us.
 //
-// 4096 x 131072 bf16, 30 % of the rows out, loss and gradient: 289 us, 6.3
+// 4096 x 131072 bf16, 30 % of the rows out, loss and gradient: 290 us, 6.3
 // TB/s, 93 % of the measured copy rate.
 // 152 x 32 warps issue 56 % of the cycles, 26 % of them exponentials.  Rows
 // of a few thousand logits are bound by the latency of a row's scalar part
@@ -779,8 +779,8 @@ __global__ void __launch_bounds__(TH < 128 ? 128 : TH, MINB)
 // with a running (max, sum) per thread, the next segment (of this row or of
 // the batch's next live one) on its way meanwhile; one exchange a row.  Held
 // in a cluster's registers instead, a row waits for eight CTAs' exchange:
-// 4096 x 131072 bf16 (10 % of the rows out) 137 us against 170, 4096 x 32000
-// 39.5 against 47.7, f32 2048 x 50001 61.5 against 71.8.  Reads alone run at
+// 4096 x 131072 bf16 (10 % of the rows out) 136 us against 170, 4096 x 32000
+// 37.9 against 46.3, f32 2048 x 50001 60.7 against 70.4.  Reads alone run at
 // 7.0 TB/s, a little above the copy rate.
 // ---------------------------------------------------------------------------
 template <typename T, int TH, int PK, int MINB>
@@ -949,7 +949,7 @@ cudaError_t launch_clusters(K kernel, int64_t rows, int cs, int threads, size_t 
 // leave the SMs unevenly loaded where rows take no part: six per resident
 // group, and where that leaves less than three rows each, down to two.  Loss and
 // gradient, inputs beyond L2, at one row a batch, at three and at four: 1335 x
-// 50257 bf16 66.0, 59.6 and 62.0 us, 8192 x 6000 45.6, 42.9 and 43.0; with rows
+// 50257 bf16 64.8, 58.2 and 60.8 us, 8192 x 6000 44.8, 42.3 and 42.3; with rows
 // enough for six batches, at four, six and twelve of them (10 % of the rows out):
 // 4096 x 131072 bf16 308.8, 303.2 and 303.2, 8192 x 32000 170.8, 166.8 and 171.5.
 inline int64_t rows_per_batch(int64_t rows, int64_t groups, int64_t least) {
@@ -989,7 +989,7 @@ cudaError_t launch_logit_seg(const LogitArgs &a, int sms, cudaStream_t s, Plan *
     p->threads = TH;
     p->packs = PK;
     // (a row's own segments follow one another: batches of one row will do, 4096
-    // x 32000 bf16 with 10 % of the rows out 39.5 us, of three 42.7)
+    // x 32000 bf16 with 10 % of the rows out 37.9 us, of three 41.0)
     const int64_t batch = rows_per_batch(a.rows, (int64_t)sms * per_sm, 1);
     const int64_t n = (a.rows + batch - 1) / batch;
     return launch_row(kernel, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), (unsigned)TH, smem, s, a, (int)batch);
@@ -1022,8 +1022,8 @@ cudaError_t launch_logit_rows_t(const LogitArgs &a, bool stream, int sms, cudaSt
         while (cs < 8 && packs > 256 * 8 * cs) cs *= 2;
         // packs that a CTA has room for and the row does not fill cost their
         // instructions all the same, so a CTA is no larger than the slice needs:
-        // 6710 x 10001 bf16 by 160 threads 53.7 us, by 256 66.7; 1365 x 49152
-        // by 192 53.6 and 60.4; 1335 x 50257 by 224 59.5 and 62.5.  With less
+        // 6710 x 10001 bf16 by 160 threads 52.7 us, by 256 65.6; 1365 x 49152
+        // by 192 52.2 and 59.1; 1335 x 50257 by 224 58.2 and 60.9.  With less
         // than four rows or slices for each resident CTA the larger one is
         // ahead (333 x 50001 f16 16.9 us, by 224 17.9).  The strides stay
         // constants: with the CTA's size read at run time 4096 x 131072 took
