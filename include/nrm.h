@@ -527,8 +527,8 @@ int logprob_bwd_stats_ld(const float *dlogp, const void *logits, int64_t ldl, co
  * old_logp, advantage and ref_logp are not read, logp = 0, dlogits = 0.  A row
  * without a finite logit adds nothing either: logp = -inf, dlogits = 0.
  * Each row's term is binary32, from a logp good to some 1e-7, and their sum loses
- * nothing more: a loss whose terms cancel is good to about 1e-8 of the sum of
- * their magnitudes, and a ratio nearer than that to its bound may take either branch.
+ * nothing more: a loss whose terms cancel keeps the terms' own errors (some
+ * 1e-7 of each), and a ratio nearer than some 1e-7 to its bound may take either branch.
  */
 size_t policy_loss_workspace_size(int64_t rows);
 int policy_loss(const void *logits, const int64_t *targets, const float *old_logp,
