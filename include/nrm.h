@@ -475,7 +475,8 @@ int logprob_fwd_stats_ld(const void *logits, int64_t ldl, const int64_t *targets
  * finite logit (lse = -inf) get zeros, their logits are not read.
  *   dlogits  [rows, V] dtype, written; may be logits (same row stride).  In
  *            binary16 scale dlogp against underflow (below 2^-25 nothing is held)
- * The given lse is taken as it is.  Its rounding to binary32 is a factor on the
+ * The given lse is taken as it is (one of -inf, whether of a row without a finite
+ * logit or because s max_j z_j left binary32, gives zeros).  Its rounding to binary32 is a factor on the
  * whole row: up to |lse| 2^-24 relative, 6e-4 at an lse of 1e4, and at 2^24 and
  * beyond nothing is left (a row whose logits are all masked by the type's lowest
  * value: its lse is that value, log V is lost, and each probability counts as 1).
