@@ -476,10 +476,11 @@ int logprob_fwd_stats_ld(const void *logits, int64_t ldl, const int64_t *targets
  *   dlogits  [rows, V] dtype, written; may be logits (same row stride).  In
  *            binary16 scale dlogp against underflow (below 2^-25 nothing is held)
  * The given lse is taken as it is (one of -inf, whether of a row without a finite
- * logit or because s max_j z_j left binary32, gives zeros).  Its rounding to binary32 is a factor on the
- * whole row: up to |lse| 2^-24 relative, 6e-4 at an lse of 1e4, and at 2^24 and
- * beyond nothing is left (a row whose logits are all masked by the type's lowest
- * value: its lse is that value, log V is lost, and each probability counts as 1).
+ * logit or because s max_j z_j left binary32, gives zeros).  Its rounding to
+ * binary32 is a factor on the whole row: up to |lse| 2^-24 relative, 6e-4 at an
+ * lse of 1e4, and at 2^24 and beyond nothing is left (a row whose logits are all
+ * masked by the type's lowest value: its lse is that value, log V is lost, and
+ * each probability counts as 1).
  * The stats form takes logprob_fwd_stats' two numbers instead of lse and has no
  * such error:
  *   dlogits_j = dlogp * s * ((j == target) - exp(s (z_j - stats[0]) - stats[1]))
@@ -527,9 +528,10 @@ int logprob_bwd_stats_ld(const float *dlogp, const void *logits, int64_t ldl, co
  * A row with a target outside [0, V) or weight 0 takes no part: its logits,
  * old_logp, advantage and ref_logp are not read, logp = 0, dlogits = 0.  A row
  * without a finite logit adds nothing either: logp = -inf, dlogits = 0.
- * Each row's term is binary32, from a logp good to some 1e-7, and their sum loses
- * nothing more: a loss whose terms cancel keeps the terms' own errors (some
- * 1e-7 of each), and a ratio nearer than some 1e-7 to its bound may take either branch.
+ * Each row's term is binary32, from a logp good to some 1e-7, and adding them up
+ * loses nothing but the result's own rounding: a loss whose terms cancel keeps the
+ * terms' errors (some 1e-7 of each), and a ratio nearer than some 1e-7 to its
+ * bound may take either branch.
  */
 size_t policy_loss_workspace_size(int64_t rows);
 int policy_loss(const void *logits, const int64_t *targets, const float *old_logp,
