@@ -546,6 +546,56 @@ int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, cons
                    int64_t rows, int64_t V, int dtype, void *workspace, size_t workspace_bytes,
                    cudaStream_t stream);
 
+/*
+ * Norms of queries and keys for each head with the position rotation in the
+ * same pass, and the gradient.  Per token t with 0 <= positions[t] < max_pos and
+ * each of its heads, a row x of D entries:
+ *   r = 1 / sqrt(sum x_i^2 / D + eps),  y_i = x_i r w_i
+ *   out_a = y_a c - y_b s,  out_b = y_b c + y_a s    for the rot / 2 pairs (a, b)
+ *   out_i = y_i                                      for i >= rot
+ * Pair i is (i, i + rot / 2), or with `interleaved` (2i, 2i + 1); its cosine and
+ * sine are table[p][i] and table[p][rot / 2 + i], p the token's position.
+ *   q, k        [tokens, q_heads, D] and [tokens, k_heads, D], dtype, the entries of
+ *               a head contiguous.  Strides in elements: *_token from a token to the
+ *               next, *_head from a head to the next (of an extent of 1 they are not
+ *               used), so q and k may be slices of one projection's output.  Heads
+ *               may lie within tokens or tokens within heads; rows may not overlap.
+ *               k_heads may be 0 (then the k pointers are not used)
+ *   table       [max_pos, rot] binary32; not used with rot = 0
+ *   positions   [tokens] int64
+ *   wq, wk      [D] dtype, or NULL (= 1)
+ *   q_out, k_out  as q and k with strides of their own; may be q and k in place
+ *               (the same pointer and strides)
+ *   0 <= rot <= D, rot even; 1 <= D <= 512 (else NRM_ERR_UNSUPPORTED); eps >= 0
+ * A token whose position lies outside the table takes no part: its rows are not
+ * read, its outputs are 0.  All arithmetic is binary32, rounded once at the end.
+ *
+ * The backward takes the gradients of q_out and k_out and q, k as the forward got
+ * them.  With g = the output's gradient turned back and u = g w:
+ *   dx_i = r (u_i - x_i r^2 sum_j (u_j x_j) / D)
+ *   dwq  = sum over tokens and heads of g x r, binary32 [D]; dwk the same
+ *   dwq, dwk    either may be NULL; both are written, not added to, and the same
+ *               bits for the same call on the same device
+ *   dq, dk      may be dq_out and dk_out, or q and k, in place
+ *   workspace   device memory, 16-byte aligned, of
+ *               qk_norm_rope_bwd_workspace_size(...) bytes, scratch; not used
+ *               without dwq and dwk.  Calls sharing one must be ordered on the GPU
+ * Tokens that take no part get zero gradients and have no share in dwq and dwk.
+ */
+int qk_norm_rope_fwd(const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token, int64_t k_head,
+                     const float *table, const int64_t *positions, const void *wq, const void *wk, void *q_out,
+                     int64_t qo_token, int64_t qo_head, void *k_out, int64_t ko_token, int64_t ko_head,
+                     int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D, int64_t rot, int64_t max_pos,
+                     float eps, int interleaved, int dtype, cudaStream_t stream);
+size_t qk_norm_rope_bwd_workspace_size(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D);
+int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, const void *dk_out, int64_t dko_token,
+                     int64_t dko_head, const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
+                     int64_t k_head, const float *table, const int64_t *positions, const void *wq, const void *wk,
+                     void *dq, int64_t dq_token, int64_t dq_head, void *dk, int64_t dk_token, int64_t dk_head,
+                     float *dwq, float *dwk, int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D, int64_t rot,
+                     int64_t max_pos, float eps, int interleaved, int dtype, void *workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char *nrm_status_string(int status);
 

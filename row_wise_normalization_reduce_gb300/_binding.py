@@ -111,6 +111,14 @@ def _declare(lib):
     for f in ("dropout_fwd", "dropout_add_rms_fwd", "dropout_add_rms_bwd", "logprob_fwd",
               "logprob_fwd_stats", "logprob_bwd", "logprob_bwd_stats", "policy_loss"):
         getattr(lib, f).restype = getattr(lib, f + "_ld").restype = _INT
+    heads = [_P, _I64, _I64]  # pointer, token stride, head stride
+    lib.qk_norm_rope_fwd.argtypes = heads * 2 + [_P] * 4 + heads * 2 + [_I64] * 6 + [_F, _INT, _INT, _P]
+    lib.qk_norm_rope_bwd_workspace_size.argtypes = [_I64] * 4
+    lib.qk_norm_rope_bwd_workspace_size.restype = _SZ
+    lib.qk_norm_rope_bwd.argtypes = heads * 4 + [_P] * 4 + heads * 2 + [_P] * 2 + [_I64] * 6 + [
+        _F, _INT, _INT, _P, _SZ, _P]
+    for f in ("qk_norm_rope_fwd", "qk_norm_rope_bwd"):
+        getattr(lib, f).restype = _INT
     lib.nrm_status_string.argtypes = [_INT]
     lib.nrm_status_string.restype = ctypes.c_char_p
     lib.nrm_force_plan.argtypes = [_INT, _INT, _INT, _INT, _INT]
@@ -821,6 +829,136 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
             inv_temp, _one_value(grad_scale, _F32, dev, "grad_scale"), loss.data_ptr(),
             logp.data_ptr(), _ptr(out), lddl, rows, v, code, ws, wsb)
     return loss, logp, out
+
+
+# ---------------------------------------------------------------------------
+# Inside a block: head norms with the position rotation.
+# ---------------------------------------------------------------------------
+def _heads(t, shape, dtype, dev, name):
+    """(token stride, head stride) of a tensor [..., heads, D] whose leading
+    dimensions have one stride between tokens."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on device {dev}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"the entries of a head of {name} must be contiguous")
+    step, n = None, 1
+    for d in range(t.dim() - 3, -1, -1):
+        if shape[d] == 1:
+            continue
+        if step is None:
+            step, n = st[d], shape[d]
+        elif st[d] == step * n:
+            n *= shape[d]
+        else:
+            raise ValueError(f"the tokens of {name} must have one stride")
+    return step or 0, st[-2]
+
+
+def _heads_out(t, shape, dtype, dev, device, name):
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr(), *_heads(t, shape, dtype, dev, name)
+
+
+def _qk_inputs(q, k, table, positions, wq, wk):
+    """Checks of what both directions take.  Returns (shape of k or None, dtype,
+    device index, tokens, (q_heads, k_heads, D, rot, max_pos), [k and its strides])."""
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    _code(dtype)
+    if len(shape) < 2:
+        raise ValueError("q must be [..., heads, D]")
+    lead, hq, d = shape[:-2], shape[-2], shape[-1]
+    tokens = lead.numel()
+    if positions.shape != lead:
+        raise ValueError(f"positions must be {tuple(lead)}")
+    _flat(positions, lead, torch.int64, dev, "positions")
+    if table.dim() != 2:
+        raise ValueError("table must be [positions, rotated entries]")
+    _flat(table, table.shape, _F32, dev, "table")
+    _weight(wq, d, dtype, dev, "wq")
+    if k is None:
+        if wk is not None:
+            raise ValueError("wk without k")
+        hk, kshape, kk = 0, None, (None, 0, 0)
+    else:
+        if k.dim() != len(shape) or k.shape[:-2] != lead or k.shape[-1] != d:
+            raise ValueError("k must be like q but for its heads")
+        hk, kshape = k.shape[-2], k.shape
+        kk = (k.data_ptr(), *_heads(k, kshape, dtype, dev, "k"))
+        _weight(wk, d, dtype, dev, "wk")
+    return kshape, dtype, dev, tokens, (hq, hk, d, table.shape[1], table.shape[0]), kk
+
+
+def qk_norm_rope_fwd(q, k, table, positions, wq=None, wk=None, eps=1e-6, *, interleaved=False, q_out=None,
+                     k_out=None, stream=None):
+    """RMSNorm of each head of q [..., heads, D] and k [..., key heads, D] with
+    weights wq and wk [D], then the position rotation of the first R entries by
+    table [P, R] (binary32: R / 2 cosines, then R / 2 sines) at positions [...]
+    (int64).  Pairs are (i, i + R / 2), interleaved (2i, 2i + 1).  q and k may be
+    slices of one projection's output, k may be None.  Tokens whose position is
+    outside [0, P) are not read and get zeros.  Returns (q_out, k_out); they may
+    be q and k in place."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return qk_norm_rope_fwd(q, k, table, positions, wq, wk, eps, interleaved=interleaved, q_out=q_out,
+                                    k_out=k_out)
+    kshape, dtype, dev, tokens, sizes, kk = _qk_inputs(q, k, table, positions, wq, wk)
+    qs = _heads(q, q.shape, dtype, dev, "q")
+    q_out, *qo = _heads_out(q_out, q.shape, dtype, dev, q.device, "q_out")
+    if kshape is not None:
+        k_out, *ko = _heads_out(k_out, kshape, dtype, dev, q.device, "k_out")
+    else:
+        k_out, ko = None, (None, 0, 0)
+    _launch("qk_norm_rope_fwd", dev, q.data_ptr(), *qs, *kk, table.data_ptr(), positions.data_ptr(), _ptr(wq), _ptr(wk),
+            *qo, *ko, tokens, *sizes, eps, 1 if interleaved else 0, _code(dtype))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_size(tokens, q_heads, k_heads, d) -> int:
+    return lib().qk_norm_rope_bwd_workspace_size(tokens, q_heads, k_heads, d)
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, positions, wq=None, wk=None, eps=1e-6, *, interleaved=False,
+                     dq=None, dk=None, dwq=None, dwk=None, want_dw=None, workspace=None, stream=None):
+    """Backward of qk_norm_rope_fwd from the gradients of q_out and k_out and
+    the forward's other arguments.  Returns (dq, dk, dwq, dwk): the weights'
+    gradients are binary32, computed for the weights that are given (want_dw:
+    for both, or neither), else None.  dq and dk may be dq_out and dk_out, or q
+    and k, in place."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, table, positions, wq, wk, eps, interleaved=interleaved, dq=dq,
+                                    dk=dk, dwq=dwq, dwk=dwk, want_dw=want_dw, workspace=workspace)
+    kshape, dtype, dev, tokens, sizes, kk = _qk_inputs(q, k, table, positions, wq, wk)
+    d = sizes[2]
+    qs = _heads(q, q.shape, dtype, dev, "q")
+    dqs = _heads(dq_out, q.shape, dtype, dev, "dq_out")
+    dq, *dqo = _heads_out(dq, q.shape, dtype, dev, q.device, "dq")
+    if kshape is not None:
+        dks = (dk_out.data_ptr(), *_heads(dk_out, kshape, dtype, dev, "dk_out"))
+        dk, *dko = _heads_out(dk, kshape, dtype, dev, q.device, "dk")
+    else:
+        if dk_out is not None or dk is not None or dwk is not None:
+            raise ValueError("gradients of k without k")
+        dks, dko = (None, 0, 0), (None, 0, 0)
+    new_q = dwq is None and (want_dw if want_dw is not None else wq is not None)
+    new_k = kshape is not None and dwk is None and (want_dw if want_dw is not None else wk is not None)
+    _weight(dwq, d, _F32, dev, "dwq")
+    _weight(dwk, d, _F32, dev, "dwk")
+    if new_q or new_k:
+        both = torch.empty(2, d, dtype=_F32, device=q.device)
+        dwq = both[0] if new_q else dwq
+        dwk = both[1] if new_k else dwk
+    ws, wsb = None, 0
+    if dwq is not None or dwk is not None:
+        ws, wsb, workspace = _scratch_bytes(workspace, lib().qk_norm_rope_bwd_workspace_size(tokens, *sizes[:3]), q)
+    _launch("qk_norm_rope_bwd", dev, dq_out.data_ptr(), *dqs, *dks, q.data_ptr(), *qs, *kk, table.data_ptr(),
+            positions.data_ptr(), _ptr(wq), _ptr(wk), *dqo, *dko, _ptr(dwq), _ptr(dwk), tokens, *sizes, eps,
+            1 if interleaved else 0, _code(dtype), ws, wsb)
+    return dq, dk, dwq, dwk
 
 
 # ---------------------------------------------------------------------------

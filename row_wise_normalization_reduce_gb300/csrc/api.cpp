@@ -1454,6 +1454,204 @@ int policy_loss(const void *logits, const int64_t *targets, const float *old_log
                           dtype, workspace, workspace_bytes, stream);
 }
 
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Head norms with the position rotation (qk.cuh).
+// ---------------------------------------------------------------------------
+
+// The strides of one tensor [tokens, heads, D]: those of an extent of one are
+// not used.  Rows may not overlap, tokens may lie within heads or heads within
+// tokens.
+struct HeadSpan {
+    const void *p;
+    int64_t t, h;
+};
+int head_span(HeadSpan *a, int64_t tokens, int64_t heads, int64_t D, size_t es, RSpan *span) {
+    *span = RSpan{};
+    if (heads == 0) return NRM_OK;
+    if (!a->p) return NRM_ERR_NULL;
+    if (!aligned(a->p, es)) return NRM_ERR_VALUE;
+    if (heads == 1) a->h = D;
+    if (tokens == 1) a->t = heads * a->h;
+    if (a->t < D || a->h < D) return NRM_ERR_SHAPE;
+    const uint64_t most = (uint64_t)INT64_MAX / 4 / es;
+    if ((uint64_t)a->t > most / (uint64_t)tokens || (uint64_t)a->h > most / (uint64_t)heads) return NRM_ERR_SHAPE;
+    const int64_t by_t = (tokens - 1) * a->t + D, by_h = (heads - 1) * a->h + D;
+    if (a->t == heads * a->h)
+        *span = rspan(a->p, a->h, tokens * heads, D, es);
+    else if (a->t >= by_h)
+        *span = rspan(a->p, a->t, tokens, by_h, es);
+    else if (a->h >= by_t)
+        *span = rspan(a->p, a->h, heads, by_t, es);
+    else
+        return NRM_ERR_SHAPE;
+    return NRM_OK;
+}
+
+// Values per access: the widest that every row, weight and table row allows.
+int head_access(const QkArgs &q, bool back, size_t es) {
+    for (int ve = 16 / (int)es; ve > 1; ve /= 2) {
+        const size_t bytes = ve * es, angles = 4 * (size_t)(q.near ? ve / 2 : ve);
+        bool ok = q.D % ve == 0 && (q.near ? 2 * q.half : q.half) % ve == 0 &&
+                  (q.half == 0 || aligned(q.table, angles < 16 ? angles : 16));
+        for (const QkSide &s : q.side) {
+            if (s.heads == 0) continue;
+            ok = ok && aligned(s.x, bytes) && aligned(s.out, bytes) && aligned(s.w, bytes) && s.xt % ve == 0 &&
+                 s.xh % ve == 0 && s.ot % ve == 0 && s.oh % ve == 0;
+            if (back) ok = ok && aligned(s.dy, bytes) && s.dt % ve == 0 && s.dh % ve == 0;
+        }
+        if (ok) return ve;
+    }
+    return 1;
+}
+
+bool qk_shape_ok(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D) {
+    return tokens >= 0 && q_heads >= 1 && k_heads >= 0 && D >= 1 && q_heads <= 65536 && k_heads <= 65536 &&
+           tokens <= ((int64_t)1 << 40);
+}
+
+// Everything both directions check; fills q and the extents of the inputs and
+// outputs.  The in-place forms (an output that is exactly one of its side's
+// row inputs) leave that input out of the comparison.
+int qk_check(QkArgs *q, int64_t max_pos, int64_t D, int64_t rot, bool back, int dtype) {
+    const size_t es = elem_size(dtype);
+    RSpan in[8], out[2];
+    int st;
+    for (int i = 0; i < 2; ++i) {
+        QkSide &s = q->side[i];
+        HeadSpan x{s.x, s.xt, s.xh}, o{s.out, s.ot, s.oh}, dy{s.dy, s.dt, s.dh};
+        if ((st = head_span(&x, q->tokens, s.heads, D, es, &in[4 * i])) != NRM_OK) return st;
+        if ((st = head_span(&o, q->tokens, s.heads, D, es, &out[i])) != NRM_OK) return st;
+        s.xt = x.t, s.xh = x.h, s.ot = o.t, s.oh = o.h;
+        if (s.out == s.x && s.ot == s.xt && s.oh == s.xh) in[4 * i] = RSpan{};
+        if (back) {
+            if ((st = head_span(&dy, q->tokens, s.heads, D, es, &in[4 * i + 1])) != NRM_OK) return st;
+            s.dt = dy.t, s.dh = dy.h;
+            if (s.out == s.dy && s.ot == s.dt && s.oh == s.dh) in[4 * i + 1] = RSpan{};
+        }
+        if ((st = check_elem_alignment({s.w}, es)) != NRM_OK) return st;
+        in[4 * i + 2] = rspan(s.heads ? s.w : nullptr, D, 1, D, es);
+    }
+    if (!q->pos || (rot > 0 && max_pos > 0 && !q->table)) return NRM_ERR_NULL;
+    if ((st = check_elem_alignment({q->pos}, 8)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({q->table}, 4)) != NRM_OK) return st;
+    in[3] = rspan(q->pos, q->tokens, 1, q->tokens, 8);
+    in[7] = rspan(rot ? q->table : nullptr, max_pos * rot, 1, max_pos * rot, 4);
+    if ((st = check_alias({out[0], out[1]}, {in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7]})) != NRM_OK)
+        return st;
+    return check_pointers({q->side[0].x, q->side[0].w, q->side[0].dy, q->side[0].out, q->side[1].x, q->side[1].w,
+                           q->side[1].dy, q->side[1].out, q->table, q->pos});
+}
+
+int qk_values(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D, int64_t rot, int64_t max_pos, float eps,
+              int dtype) {
+    if (!dtype_ok(dtype)) return NRM_ERR_DTYPE;
+    if (!qk_shape_ok(tokens, q_heads, k_heads, D) || rot < 0 || rot > D || rot % 2 || max_pos < 0) return NRM_ERR_SHAPE;
+    if (rot && max_pos > INT64_MAX / 8 / rot) return NRM_ERR_SHAPE;
+    if (!eps_ok(eps)) return NRM_ERR_VALUE;
+    return D > kQkMaxDim ? NRM_ERR_UNSUPPORTED : NRM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qk_norm_rope_fwd(const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token, int64_t k_head,
+                     const float *table, const int64_t *positions, const void *wq, const void *wk, void *q_out,
+                     int64_t qo_token, int64_t qo_head, void *k_out, int64_t ko_token, int64_t ko_head,
+                     int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D, int64_t rot, int64_t max_pos,
+                     float eps, int interleaved, int dtype, cudaStream_t stream) {
+    int st = qk_values(tokens, q_heads, k_heads, D, rot, max_pos, eps, dtype);
+    if (st != NRM_OK) return st;
+    if (tokens == 0) return NRM_OK;  // empty input: no pointer is used
+    QkArgs a{};
+    a.side[0] = QkSide{q, wq, nullptr, q_out, q_token, q_head, 0, 0, qo_token, qo_head, (int)q_heads};
+    a.side[1] = QkSide{k, wk, nullptr, k_out, k_token, k_head, 0, 0, ko_token, ko_head, (int)k_heads};
+    a.table = table;
+    a.pos = positions;
+    a.tokens = tokens;
+    a.max_pos = max_pos;
+    a.D = (int)D;
+    a.half = (int)rot / 2;
+    a.near = interleaved != 0;
+    a.eps = eps;
+    a.invD = 1.0f / (float)D;
+    if ((st = qk_check(&a, max_pos, D, rot, false, dtype)) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    Plan plan{};
+    return record_plan(launch_qk(dtype, a, head_access(a, false, elem_size(dtype)), false, dev.sms, stream, &plan, nullptr),
+                       plan);
+}
+
+size_t qk_norm_rope_bwd_workspace_size(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D) {
+    if (!qk_shape_ok(tokens, q_heads, k_heads, D) || D > kQkMaxDim) return 0;
+    return (size_t)kDropMaxParts * 2 * (size_t)D * 4;
+}
+
+int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, const void *dk_out, int64_t dko_token,
+                     int64_t dko_head, const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
+                     int64_t k_head, const float *table, const int64_t *positions, const void *wq, const void *wk,
+                     void *dq, int64_t dq_token, int64_t dq_head, void *dk, int64_t dk_token, int64_t dk_head,
+                     float *dwq, float *dwk, int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D, int64_t rot,
+                     int64_t max_pos, float eps, int interleaved, int dtype, void *workspace, size_t workspace_bytes,
+                     cudaStream_t stream) {
+    int st = qk_values(tokens, q_heads, k_heads, D, rot, max_pos, eps, dtype);
+    if (st != NRM_OK) return st;
+    if ((st = check_elem_alignment({dwq, dwk}, 4)) != NRM_OK) return st;
+    if (k_heads == 0 && dwk) return NRM_ERR_SHAPE;
+    if (tokens == 0) {  // no rows: the weights' gradients are empty sums, nothing else exists
+        if (!dwq && !dwk) return NRM_OK;
+        if ((st = check_pointers({dwq, dwk})) != NRM_OK) return st;
+        return launched(launch_qk_fold(nullptr, dwq, dwk, 0, (int)D, stream));
+    }
+    QkArgs a{};
+    a.side[0] = QkSide{q, wq, dq_out, dq, q_token, q_head, dqo_token, dqo_head, dq_token, dq_head, (int)q_heads};
+    a.side[1] = QkSide{k, wk, dk_out, dk, k_token, k_head, dko_token, dko_head, dk_token, dk_head, (int)k_heads};
+    a.table = table;
+    a.pos = positions;
+    a.tokens = tokens;
+    a.max_pos = max_pos;
+    a.D = (int)D;
+    a.half = (int)rot / 2;
+    a.near = interleaved != 0;
+    a.eps = eps;
+    a.invD = 1.0f / (float)D;
+    if ((st = qk_check(&a, max_pos, D, rot, true, dtype)) != NRM_OK) return st;
+    if (dwq || dwk) {
+        const size_t need = qk_norm_rope_bwd_workspace_size(tokens, q_heads, k_heads, D), es = elem_size(dtype);
+        if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return NRM_ERR_WORKSPACE;
+        // the workspace and the weights' gradients against all the rest
+        const RSpan swq = rspan(dwq, D, 1, D, 4), swk = rspan(dwk, D, 1, D, 4),
+                    sws = rspan(workspace, (int64_t)need, 1, (int64_t)need, 1);
+        RSpan t[6];
+        for (int i = 0; i < 2; ++i) {
+            const QkSide &s = a.side[i];
+            HeadSpan x{s.x, s.xt, s.xh}, o{s.out, s.ot, s.oh}, dy{s.dy, s.dt, s.dh};
+            head_span(&x, tokens, s.heads, D, es, &t[3 * i]);
+            head_span(&o, tokens, s.heads, D, es, &t[3 * i + 1]);
+            head_span(&dy, tokens, s.heads, D, es, &t[3 * i + 2]);
+        }
+        if ((st = check_alias({swq, swk, sws},
+                              {t[0], t[1], t[2], t[3], t[4], t[5], rspan(wq, D, 1, D, es), rspan(k_heads ? wk : nullptr, D, 1, D, es),
+                               rspan(positions, tokens, 1, tokens, 8),
+                               rspan(rot ? table : nullptr, max_pos * rot, 1, max_pos * rot, 4)})) != NRM_OK)
+            return st;
+        if ((st = check_pointers({dwq, dwk, workspace})) != NRM_OK) return st;
+        a.part = static_cast<float *>(workspace);
+    }
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    Plan plan{};
+    int64_t parts = 0;
+    st = record_plan(launch_qk(dtype, a, head_access(a, true, elem_size(dtype)), true, dev.sms, stream, &plan, &parts), plan);
+    if (st != NRM_OK || (!dwq && !dwk)) return st;
+    return launched(launch_qk_fold(a.part, dwq, dwk, parts, (int)D, stream));
+}
+
 const char *nrm_status_string(int status) {
     switch (status) {
     case NRM_OK: return "ok";

@@ -353,6 +353,35 @@ NRM_BY_TYPE(launch_logit_rows, (const LogitArgs &a, bool policy, bool stream, in
             (a, policy, stream, sms, s, p))
 NRM_BY_TYPE(launch_logit_grad, (const LogitArgs &a, cudaStream_t s), (a, s))
 cudaError_t launch_loss_fold(const float *row_loss, float *loss, int64_t rows, cudaStream_t s);
+
+// Entries of a head that the kernels hold in a warp's registers.
+constexpr int64_t kQkMaxDim = 512;
+
+// Norms of each head's queries (side 0) and keys (side 1) with the position
+// rotation (qk.cuh).  Strides in elements: of a token, of a head.
+struct QkSide {
+    const void *x, *w;      // w NULL: ones
+    const void *dy;         // backward only
+    void *out;              // y, or dx
+    int64_t xt, xh, dt, dh, ot, oh;
+    int heads;
+};
+struct QkArgs {
+    QkSide side[2];
+    const float *table;     // [max_pos][2 * half]: cosines, then sines
+    const int64_t *pos;     // [tokens]
+    int64_t tokens, max_pos;
+    int D, half;            // half of the entries that turn
+    int near;               // pairs are neighbours, not half and half
+    float eps, invD;
+    float *part;            // [parts][2][D] partial sums of dw, NULL: no weight gradient
+};
+// ve: values per access.  back: the gradient; *parts, the rows left in a.part
+// (at most kDropMaxParts).
+NRM_BY_TYPE(launch_qk, (const QkArgs &a, int ve, bool back, int sms, cudaStream_t s, Plan *p, int64_t *parts),
+            (a, ve, back, sms, s, p, parts))
+// dwq[c] (c < D) and dwk[c - D]: the parts' sums; either may be NULL.
+cudaError_t launch_qk_fold(const float *part, float *dwq, float *dwk, int64_t parts, int D, cudaStream_t s);
 #undef NRM_UNPAREN
 #undef NRM_BY_TYPE
 cudaError_t launch_dw_fold(const float *part, float *dw, int64_t parts, int64_t N, cudaStream_t s);
