@@ -596,6 +596,94 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
                      int64_t max_pos, float eps, int interleaved, int dtype, void *workspace, size_t workspace_bytes,
                      cudaStream_t stream);
 
+/*
+ * Routing of tokens to experts, and the gradient.  Per token with logits x:
+ *   s = softmax(x), or 1 / (1 + exp(-x)) each        the scores
+ *   c = s + bias                                     what is chosen by
+ * With top_groups < groups only the top_groups groups of experts / groups
+ * neighbouring experts stay that have the largest sums of their group_top (1 or 2)
+ * largest c.  Of those that stay the k largest c are taken, largest first; their
+ * weights are scale s, or with `renormalize` scale s / (the sum of the chosen s).
+ * The order is that of the exact c (differences below binary32's are found, in
+ * binary64), among equal ones that of the index, lowest first.
+ *   logits      [tokens, experts] dtype (row stride ldl)
+ *   bias        [experts] binary32 or NULL (= 0); it has no part in the weights
+ *   weights     [tokens, k] binary32
+ *   ids         [tokens, k] int64
+ *   scores      [tokens, experts] binary32 or NULL: all s, for a balance term
+ *   1 <= k <= experts / groups * top_groups, scale finite; at most 1024 experts,
+ *   k 32, and where groups limit the choice 32 groups, group_top 2 and 32 times the
+ *   largest power of two in 32 / groups experts a group (else NRM_ERR_UNSUPPORTED)
+ * An expert whose logit or bias is -inf, or whose c is NaN, is not available.  A
+ * group's sum counts those it has; one without any comes last.  Places that no
+ * available expert is left for get id -1 and weight 0, and where the sum of the
+ * chosen s is 0 (sigmoids below binary32's range) all weights are 0.
+ *
+ * The backward takes the gradient of the weights, the forward's logits and ids and
+ * optionally the gradient of the scores, and writes the gradient of the logits.
+ * The choice itself has no gradient, nor has the bias.
+ *   ids         entries outside [0, experts) have no part; an expert listed more than
+ *               once gets the sum of its gradients
+ *   dscores     [tokens, experts] binary32 or NULL (= 0)
+ *   dlogits     [tokens, experts] dtype (row stride lddl); may be logits (same stride)
+ */
+typedef enum {
+    NRM_SCORE_SOFTMAX = 0,
+    NRM_SCORE_SIGMOID = 1
+} nrm_score;
+
+int route_fwd(const void *logits, int64_t ldl, const float *bias, float *weights, int64_t *ids, float *scores,
+              int64_t tokens, int64_t experts, int64_t k, int score, int64_t groups, int64_t top_groups,
+              int64_t group_top, int renormalize, float scale, int dtype, cudaStream_t stream);
+int route_bwd(const float *dweights, const void *logits, int64_t ldl, const int64_t *ids, const float *dscores,
+              void *dlogits, int64_t lddl, int64_t tokens, int64_t experts, int64_t k, int score, int renormalize,
+              float scale, int dtype, cudaStream_t stream);
+
+/*
+ * Log-probability of one target per row of logits with the row's entropy and its k
+ * largest alternatives, from one pass over the logits, and the gradient of all
+ * three.  With s = inv_temp and lp_j = log softmax(s z)_j, per row:
+ *   logp     = lp_target
+ *   entropy  = -sum_j exp(lp_j) lp_j
+ *   top_ids  = the k columns with the largest z, largest first, among equal ones the
+ *              lowest column first; top_logp = their lp
+ *   stats    = max z, log sum_j exp(s (z_j - max z))
+ *   logits      [rows, V] dtype (row stride ldl), V < 2^31
+ *   targets     [rows] int64, as logprob_fwd
+ *   logp, entropy  [rows] binary32, each may be NULL
+ *   top_ids     [rows, k] int64;  top_logp [rows, k] binary32; not used with k = 0
+ *   stats       [rows, 2] binary32 or NULL; the backward needs them
+ *   0 <= k <= 32 (else NRM_ERR_UNSUPPORTED); inv_temp as logprob_fwd
+ * A row with a target outside [0, V) takes no part: its logits are not read, its ids
+ * are -1 and all else is 0.  Logits of -inf are no alternatives, nor are NaN: places
+ * without one get id -1 and -inf.  A row without a finite logit has logp = stats[1] =
+ * -inf and entropy 0.  A NaN or an inf among the logits makes logp and entropy NaN.
+ *
+ * The backward, for the gradients g of logp, h of entropy and a_i of top_logp_i:
+ *   dlogits_j = s (g [j = target] + sum_i a_i [j = top_ids_i]
+ *                  - p_j (g + sum_i a_i + h (lp_j + entropy)))
+ *   dlogp, dentropy, dtop_logp   binary32 as the forward's outputs; each may be NULL
+ *               (= 0), not all
+ *   stats       the forward's; entropy the forward's, not used without dentropy
+ *   top_ids     not used without dtop_logp; entries outside [0, V) have no part, an
+ *               entry may be named more than once and may be the target
+ *   dlogits     [rows, V] dtype (row stride lddl); may be logits (same stride)
+ * Rows that take no part and rows with stats[1] = -inf get zeros.
+ */
+int logprob_top_fwd(const void *logits, const int64_t *targets, float *logp, float *entropy, int64_t *top_ids,
+                    float *top_logp, float *stats, int64_t rows, int64_t V, int64_t k, float inv_temp, int dtype,
+                    cudaStream_t stream);
+int logprob_top_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *entropy,
+                       int64_t *top_ids, float *top_logp, float *stats, int64_t rows, int64_t V, int64_t k,
+                       float inv_temp, int dtype, cudaStream_t stream);
+int logprob_top_bwd(const float *dlogp, const float *dentropy, const float *dtop_logp, const void *logits,
+                    const int64_t *targets, const float *stats, const float *entropy, const int64_t *top_ids,
+                    void *dlogits, int64_t rows, int64_t V, int64_t k, float inv_temp, int dtype, cudaStream_t stream);
+int logprob_top_bwd_ld(const float *dlogp, const float *dentropy, const float *dtop_logp, const void *logits,
+                       int64_t ldl, const int64_t *targets, const float *stats, const float *entropy,
+                       const int64_t *top_ids, void *dlogits, int64_t lddl, int64_t rows, int64_t V, int64_t k,
+                       float inv_temp, int dtype, cudaStream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char *nrm_status_string(int status);
 

@@ -19,7 +19,7 @@ from ._binding import (  # noqa: F401
     dropout_fwd, dropout_bwd, dropout_add_rms_fwd, dropout_add_rms_bwd,
     dropout_add_rms_bwd_workspace_size, logprob_fwd, logprob_bwd, policy_loss,
     policy_loss_workspace_size, qk_norm_rope_fwd, qk_norm_rope_bwd,
-    qk_norm_rope_bwd_workspace_size)
+    qk_norm_rope_bwd_workspace_size, route_fwd, route_bwd, logprob_top_fwd, logprob_top_bwd)
 from .sync import exchange_parts, global_count, sync_bn_bwd, sync_bn_fwd_train  # noqa: F401
 
 

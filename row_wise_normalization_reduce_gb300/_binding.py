@@ -117,7 +117,14 @@ def _declare(lib):
     lib.qk_norm_rope_bwd_workspace_size.restype = _SZ
     lib.qk_norm_rope_bwd.argtypes = heads * 4 + [_P] * 4 + heads * 2 + [_P] * 2 + [_I64] * 6 + [
         _F, _INT, _INT, _P, _SZ, _P]
-    for f in ("qk_norm_rope_fwd", "qk_norm_rope_bwd"):
+    lib.route_fwd.argtypes = [_P, _I64] + [_P] * 4 + [_I64] * 3 + [_INT] + [_I64] * 3 + [_INT, _F, _INT, _P]
+    lib.route_bwd.argtypes = [_P, _P, _I64, _P, _P, _P] + [_I64] * 4 + [_INT, _INT, _F, _INT, _P]
+    lib.logprob_top_fwd.argtypes = [_P] * 7 + [_I64] * 3 + [_F, _INT, _P]
+    lib.logprob_top_fwd_ld.argtypes = [_P, _I64] + [_P] * 6 + [_I64] * 3 + [_F, _INT, _P]
+    lib.logprob_top_bwd.argtypes = [_P] * 9 + [_I64] * 3 + [_F, _INT, _P]
+    lib.logprob_top_bwd_ld.argtypes = [_P] * 4 + [_I64] + [_P] * 5 + [_I64] * 4 + [_F, _INT, _P]
+    for f in ("qk_norm_rope_fwd", "qk_norm_rope_bwd", "route_fwd", "route_bwd", "logprob_top_fwd",
+              "logprob_top_fwd_ld", "logprob_top_bwd", "logprob_top_bwd_ld"):
         getattr(lib, f).restype = _INT
     lib.nrm_status_string.argtypes = [_INT]
     lib.nrm_status_string.restype = ctypes.c_char_p
@@ -959,6 +966,144 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, positions, wq=None, wk=None, e
             positions.data_ptr(), _ptr(wq), _ptr(wk), *dqo, *dko, _ptr(dwq), _ptr(dwk), tokens, *sizes, eps,
             1 if interleaved else 0, _code(dtype), ws, wsb)
     return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------------------
+# Routing to experts.
+# ---------------------------------------------------------------------------
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    code = _SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be one of {', '.join(_SCORES)}, not {score!r}")
+    return code
+
+
+def route_fwd(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, group_top=1, renormalize=True,
+              scale=1.0, want_scores=False, weights=None, ids=None, scores=None, stream=None):
+    """The k experts of each token of logits [..., experts] with the largest
+    score + bias (bias binary32 [experts], ties: lowest index), score softmax or
+    sigmoid of the logits; with top_groups < groups from the top_groups groups of
+    neighbouring experts with the largest sums of their group_top best.  Their
+    weights are scale * score, renormalized to a sum of scale.  Experts with a
+    logit or bias of -inf are not available; places without one get id -1 and
+    weight 0.  Returns (weights, ids, scores or None): binary32 and int64
+    [..., k], all scores in binary32 with want_scores."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return route_fwd(logits, k, bias, score=score, groups=groups, top_groups=top_groups, group_top=group_top,
+                             renormalize=renormalize, scale=scale, want_scores=want_scores, weights=weights, ids=ids,
+                             scores=scores)
+    tokens, experts, ldl = _rows(logits, "logits")
+    shape, dev = logits.shape, logits.get_device()
+    code = _code(logits.dtype)
+    _weight(bias, experts, _F32, dev, "bias")
+    out = (*shape[:-1], k)
+    device = logits.device
+    weights = torch.empty(out, dtype=_F32, device=device) if weights is None else _flat(weights, out, _F32, dev, "weights")
+    ids = torch.empty(out, dtype=torch.int64, device=device) if ids is None else _flat(ids, out, torch.int64, dev, "ids")
+    if scores is not None:
+        _flat(scores, shape, _F32, dev, "scores")
+    elif want_scores:
+        scores = torch.empty(shape, dtype=_F32, device=device)
+    _launch("route_fwd", dev, logits.data_ptr(), ldl, _ptr(bias), weights.data_ptr(), ids.data_ptr(), _ptr(scores), tokens,
+            experts, k, _score(score), groups, groups if top_groups is None else top_groups, group_top,
+            1 if renormalize else 0, scale, code)
+    return weights, ids, scores
+
+
+def route_bwd(dweights, logits, ids, *, score="softmax", renormalize=True, scale=1.0, dscores=None, out=None,
+              stream=None):
+    """Gradient of the logits from dweights, the gradient of route_fwd's weights
+    (binary32), its ids, and optionally dscores, the gradient of its scores
+    (binary32, like logits).  out may be logits.  Returns dlogits."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return route_bwd(dweights, logits, ids, score=score, renormalize=renormalize, scale=scale, dscores=dscores,
+                             out=out)
+    tokens, experts, ldl = _rows(logits, "logits")
+    shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
+    code = _code(dtype)
+    k = ids.shape[-1]
+    per_token = (*shape[:-1], k)
+    _flat(ids, per_token, torch.int64, dev, "ids")
+    _flat(dweights, per_token, _F32, dev, "dweights")
+    if dscores is not None:
+        _flat(dscores, shape, _F32, dev, "dscores")
+    out, lddl = _like(out, logits, shape, dtype, dev, "out")
+    _launch("route_bwd", dev, dweights.data_ptr(), logits.data_ptr(), ldl, ids.data_ptr(), _ptr(dscores), out.data_ptr(),
+            lddl, tokens, experts, k, _score(score), 1 if renormalize else 0, scale, code)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Rows of logits with entropy and alternatives.
+# ---------------------------------------------------------------------------
+def logprob_top_fwd(logits, targets, k, inv_temp=1.0, *, logp=None, entropy=None, top_ids=None, top_logp=None,
+                    stats=None, stream=None):
+    """Log-softmax of inv_temp * logits at one target (int64) per row of the last
+    dimension, the row's entropy and its k <= 32 largest logits (ties: lowest
+    index first) with their log-probabilities, from one pass.  Returns (logp,
+    entropy, top_ids, top_logp, stats): binary32 but for the ids, int64; stats
+    [..., 2] is for logprob_top_bwd (and logprob_bwd).  Rows with a target
+    outside [0, V) are not read: ids -1, all else 0.  Logits of -inf are no
+    alternatives: places without one get id -1 and -inf."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return logprob_top_fwd(logits, targets, k, inv_temp, logp=logp, entropy=entropy, top_ids=top_ids,
+                                   top_logp=top_logp, stats=stats)
+    rows, v, ldl = _rows(logits, "logits")
+    shape, dev, device = logits.shape[:-1], logits.get_device(), logits.device
+    code = _code(logits.dtype)
+    _flat(targets, shape, torch.int64, dev, "targets")
+    logp = torch.empty_like(targets, dtype=_F32) if logp is None else _flat(logp, shape, _F32, dev, "logp")
+    entropy = torch.empty_like(targets, dtype=_F32) if entropy is None else _flat(entropy, shape, _F32, dev, "entropy")
+    many, two = (*shape, k), (*shape, 2)
+    top_ids = torch.empty(many, dtype=torch.int64, device=device) if top_ids is None else _flat(
+        top_ids, many, torch.int64, dev, "top_ids")
+    top_logp = torch.empty(many, dtype=_F32, device=device) if top_logp is None else _flat(top_logp, many, _F32, dev, "top_logp")
+    stats = torch.empty(two, dtype=_F32, device=device) if stats is None else _flat(stats, two, _F32, dev, "stats")
+    _launch("logprob_top_fwd_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(), entropy.data_ptr(),
+            top_ids.data_ptr(), top_logp.data_ptr(), stats.data_ptr(), rows, v, k, inv_temp, code)
+    return logp, entropy, top_ids, top_logp, stats
+
+
+def logprob_top_bwd(dlogp, dentropy, dtop_logp, logits, targets, stats, entropy=None, top_ids=None, inv_temp=1.0, *,
+                    out=None, stream=None):
+    """Gradient of the logits from dlogp, dentropy and dtop_logp, the gradients of
+    logprob_top_fwd's outputs (binary32; each may be None, not all), and its stats,
+    entropy (with dentropy) and top_ids (with dtop_logp; any ids of a row, those
+    outside [0, V) have no part).  out may be logits.  Returns dlogits."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return logprob_top_bwd(dlogp, dentropy, dtop_logp, logits, targets, stats, entropy, top_ids, inv_temp, out=out)
+    rows, v, ldl = _rows(logits, "logits")
+    shape, dtype, dev = logits.shape, logits.dtype, logits.get_device()
+    code = _code(dtype)
+    per_row = shape[:-1]
+    _flat(targets, per_row, torch.int64, dev, "targets")
+    _flat(stats, (*per_row, 2), _F32, dev, "stats")
+    if dlogp is not None:
+        _flat(dlogp, per_row, _F32, dev, "dlogp")
+    if dentropy is not None:
+        if entropy is None:
+            raise ValueError("dentropy needs entropy")
+        _flat(dentropy, per_row, _F32, dev, "dentropy")
+        _flat(entropy, per_row, _F32, dev, "entropy")
+    k = 0
+    if dtop_logp is not None:
+        if top_ids is None:
+            raise ValueError("dtop_logp needs top_ids")
+        k = top_ids.shape[-1]
+        _flat(top_ids, (*per_row, k), torch.int64, dev, "top_ids")
+        _flat(dtop_logp, (*per_row, k), _F32, dev, "dtop_logp")
+    out, lddl = _like(out, logits, shape, dtype, dev, "out")
+    _launch("logprob_top_bwd_ld", dev, _ptr(dlogp), _ptr(dentropy), _ptr(dtop_logp), logits.data_ptr(), ldl,
+            targets.data_ptr(), stats.data_ptr(), _ptr(entropy), _ptr(top_ids), out.data_ptr(), lddl, rows, v, k, inv_temp,
+            code)
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -1652,6 +1652,233 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
     return launched(launch_qk_fold(a.part, dwq, dwk, parts, (int)D, stream));
 }
 
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Routing to experts (route.cuh).
+// ---------------------------------------------------------------------------
+int route_values(int64_t tokens, int64_t experts, int64_t k, int score, float scale, int dtype) {
+    if (!dtype_ok(dtype)) return NRM_ERR_DTYPE;
+    if (tokens < 0 || experts < 1 || k < 1 || k > experts) return NRM_ERR_SHAPE;
+    if (tokens > INT64_MAX / 64 / kRouteMaxExperts) return NRM_ERR_SHAPE;
+    if ((score != NRM_SCORE_SOFTMAX && score != NRM_SCORE_SIGMOID) || !std::isfinite(scale)) return NRM_ERR_VALUE;
+    return experts > kRouteMaxExperts || k > kRouteMaxK ? NRM_ERR_UNSUPPORTED : NRM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int route_fwd(const void *logits, int64_t ldl, const float *bias, float *weights, int64_t *ids, float *scores,
+              int64_t tokens, int64_t experts, int64_t k, int score, int64_t groups, int64_t top_groups,
+              int64_t group_top, int renormalize, float scale, int dtype, cudaStream_t stream) {
+    int st = route_values(tokens, experts, k, score, scale, dtype);
+    if (st != NRM_OK) return st;
+    if (groups < 1 || groups > experts || experts % groups || top_groups < 1 || top_groups > groups || group_top < 1 ||
+        k > experts / groups * top_groups)
+        return NRM_ERR_SHAPE;
+    RouteArgs a{};
+    a.groups = 1;
+    a.top_groups = 1;
+    a.group_top = (int)group_top;
+    a.log_lanes = 5;
+    if (top_groups < groups) {
+        if (groups > kRouteMaxGroups || group_top > 2) return NRM_ERR_UNSUPPORTED;
+        a.groups = (int)groups;
+        a.top_groups = (int)top_groups;
+        while (groups << a.log_lanes > 32) --a.log_lanes;
+    }
+    a.group_size = (int)experts / a.groups;
+    a.per_lane = (a.group_size + (1 << a.log_lanes) - 1) >> a.log_lanes;
+    if (a.per_lane > 32) return NRM_ERR_UNSUPPORTED;
+    if (tokens == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!logits || !weights || !ids) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(tokens, experts, es, {ldl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({bias, weights, scores}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({ids}, 8)) != NRM_OK) return st;
+    const RSpan sl = rspan(logits, ldl, tokens, experts, es), sb = rspan(bias, experts, 1, experts, 4),
+                sw = rspan(weights, tokens * k, 1, tokens * k, 4), si = rspan(ids, tokens * k, 1, tokens * k, 8),
+                ss = rspan(scores, tokens * experts, 1, tokens * experts, 4);
+    if ((st = check_alias({sw, si, ss}, {sl, sb})) != NRM_OK) return st;
+    if ((st = check_pointers({logits, bias, weights, ids, scores})) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    a.x = logits;
+    a.ldx = ldl;
+    a.bias = bias;
+    a.tokens = tokens;
+    a.experts = (int)experts;
+    a.k = (int)k;
+    a.softmax = score == NRM_SCORE_SOFTMAX;
+    a.renorm = renormalize != 0;
+    a.scale = scale;
+    a.by_score = bias || (a.groups > 1 && group_top > 1);
+    a.need_sum = a.by_score || !a.renorm || scores;
+    a.weights = weights;
+    a.ids = ids;
+    a.scores = scores;
+    // the kernel for up to 2, 4, 8, 16 or 32 experts a lane
+    const int pl = round_up_pow2(a.per_lane < 2 ? 2 : a.per_lane);
+    const size_t pack = pl * es < 16 ? pl * es : 16;
+    a.wide = a.per_lane == pl && a.group_size == pl << a.log_lanes && aligned(logits, pack) && (size_t)ldl * es % pack == 0;
+    Plan plan{};
+    return record_plan(launch_route(dtype, a, false, dev.sms, stream, &plan), plan);
+}
+
+int route_bwd(const float *dweights, const void *logits, int64_t ldl, const int64_t *ids, const float *dscores,
+              void *dlogits, int64_t lddl, int64_t tokens, int64_t experts, int64_t k, int score, int renormalize,
+              float scale, int dtype, cudaStream_t stream) {
+    int st = route_values(tokens, experts, k, score, scale, dtype);
+    if (st != NRM_OK) return st;
+    if (tokens == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!dweights || !logits || !ids || !dlogits) return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(tokens, experts, es, {ldl, lddl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits, dlogits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({dweights, dscores}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({ids}, 8)) != NRM_OK) return st;
+    const bool inplace = logits == dlogits && ldl == lddl;
+    const RSpan sl = rspan(inplace ? nullptr : logits, ldl, tokens, experts, es),
+                sw = rspan(dweights, tokens * k, 1, tokens * k, 4), si = rspan(ids, tokens * k, 1, tokens * k, 8),
+                ss = rspan(dscores, tokens * experts, 1, tokens * experts, 4), sd = rspan(dlogits, lddl, tokens, experts, es);
+    if ((st = check_alias({sd}, {sl, sw, si, ss})) != NRM_OK) return st;
+    if ((st = check_pointers({dweights, logits, ids, dscores, dlogits})) != NRM_OK) return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    RouteArgs a{};
+    a.x = logits;
+    a.ldx = ldl;
+    a.tokens = tokens;
+    a.experts = (int)experts;
+    a.k = (int)k;
+    a.softmax = score == NRM_SCORE_SOFTMAX;
+    a.renorm = renormalize != 0;
+    a.scale = scale;
+    a.dweights = dweights;
+    a.dscores = dscores;
+    a.ids_in = ids;
+    a.dx = dlogits;
+    a.lddx = lddl;
+    Plan plan{};
+    return record_plan(launch_route(dtype, a, true, dev.sms, stream, &plan), plan);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of logits with entropy and alternatives (logits_top.cuh).
+// ---------------------------------------------------------------------------
+int logprob_top_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, float *logp, float *entropy,
+                       int64_t *top_ids, float *top_logp, float *stats, int64_t rows, int64_t V, int64_t k,
+                       float inv_temp, int dtype, cudaStream_t stream) {
+    int st = validate_logits(rows, V, inv_temp, dtype);
+    if (st != NRM_OK) return st;
+    if (k < 0) return NRM_ERR_SHAPE;
+    if (k > kTopMaxK) return NRM_ERR_UNSUPPORTED;
+    if (rows == 0) return NRM_OK;  // empty input: no pointer is used
+    if (!logits || !targets || (k > 0 && (!top_ids || !top_logp)) || (k == 0 && !logp && !entropy && !stats))
+        return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, V, es, {ldl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logp, entropy, k ? top_logp : nullptr, stats}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({targets, k ? top_ids : nullptr}, 8)) != NRM_OK) return st;
+    const RSpan sl = rspan(logits, ldl, rows, V, es), stg = rspan(targets, rows, 1, rows, 8),
+                sp = rspan(logp, rows, 1, rows, 4), sh = rspan(entropy, rows, 1, rows, 4),
+                si = rspan(k ? top_ids : nullptr, rows * k, 1, rows * k, 8),
+                sa = rspan(k ? top_logp : nullptr, rows * k, 1, rows * k, 4),
+                ss = rspan(stats, 2 * rows, 1, 2 * rows, 4);
+    if ((st = check_alias({sp, sh, si, sa, ss}, {sl, stg})) != NRM_OK) return st;
+    if ((st = check_pointers({logits, targets, logp, entropy, k ? top_ids : nullptr, k ? top_logp : nullptr, stats})) !=
+        NRM_OK)
+        return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    TopArgs t{};
+    t.a.z = logits;
+    t.a.ldz = ldl;
+    t.a.target = targets;
+    t.a.rows = rows;
+    t.a.V = V;
+    t.a.scale = inv_temp;
+    t.a.logp = logp;
+    t.a.stats = stats;
+    t.k = (int)k;
+    t.entropy = entropy;
+    t.ids = top_ids;
+    t.top = top_logp;
+    Plan plan{};
+    return record_plan(launch_logit_top(dtype, t, dev.sms, stream, &plan), plan);
+}
+
+int logprob_top_fwd(const void *logits, const int64_t *targets, float *logp, float *entropy, int64_t *top_ids,
+                    float *top_logp, float *stats, int64_t rows, int64_t V, int64_t k, float inv_temp, int dtype,
+                    cudaStream_t stream) {
+    return logprob_top_fwd_ld(logits, V, targets, logp, entropy, top_ids, top_logp, stats, rows, V, k, inv_temp, dtype,
+                              stream);
+}
+
+int logprob_top_bwd_ld(const float *dlogp, const float *dentropy, const float *dtop_logp, const void *logits,
+                       int64_t ldl, const int64_t *targets, const float *stats, const float *entropy,
+                       const int64_t *top_ids, void *dlogits, int64_t lddl, int64_t rows, int64_t V, int64_t k,
+                       float inv_temp, int dtype, cudaStream_t stream) {
+    int st = validate_logits(rows, V, inv_temp, dtype);
+    if (st != NRM_OK) return st;
+    if (k < 0) return NRM_ERR_SHAPE;
+    if (k > kTopMaxK) return NRM_ERR_UNSUPPORTED;
+    if (rows == 0) return NRM_OK;  // empty input: no pointer is used
+    if (k == 0) dtop_logp = nullptr;
+    if (!dtop_logp) top_ids = nullptr;
+    if (!logits || !targets || !stats || !dlogits || (!dlogp && !dentropy && !dtop_logp) || (dentropy && !entropy) ||
+        (dtop_logp && !top_ids))
+        return NRM_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    if ((st = validate_ld(rows, V, es, {ldl, lddl})) != NRM_OK) return st;
+    if ((st = check_elem_alignment({logits, dlogits}, es)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({dlogp, dentropy, dtop_logp, stats, entropy}, 4)) != NRM_OK) return st;
+    if ((st = check_elem_alignment({targets, top_ids}, 8)) != NRM_OK) return st;
+    const bool inplace = logits == dlogits && ldl == lddl;
+    const RSpan sl = rspan(inplace ? nullptr : logits, ldl, rows, V, es), stg = rspan(targets, rows, 1, rows, 8),
+                sp = rspan(dlogp, rows, 1, rows, 4), sh = rspan(dentropy, rows, 1, rows, 4),
+                sa = rspan(dtop_logp, rows * k, 1, rows * k, 4), ss = rspan(stats, 2 * rows, 1, 2 * rows, 4),
+                se = rspan(entropy, rows, 1, rows, 4), si = rspan(top_ids, rows * k, 1, rows * k, 8),
+                sd = rspan(dlogits, lddl, rows, V, es);
+    if ((st = check_alias({sd}, {sl, stg, sp, sh, sa, ss, se, si})) != NRM_OK) return st;
+    if ((st = check_pointers({dlogp, dentropy, dtop_logp, logits, targets, stats, entropy, top_ids, dlogits})) != NRM_OK)
+        return st;
+    DevInfo dev;
+    if ((st = device_info(&dev)) != NRM_OK) return st;
+    TopArgs t{};
+    t.a.z = logits;
+    t.a.ldz = ldl;
+    t.a.target = targets;
+    t.a.rows = rows;
+    t.a.V = V;
+    t.a.scale = inv_temp;
+    t.a.dlogp = dlogp;
+    t.a.stats_in = stats;
+    t.a.dz = dlogits;
+    t.a.lddz = lddl;
+    t.k = dtop_logp ? (int)k : 0;
+    t.dentropy = dentropy;
+    t.dtop = dtop_logp;
+    t.entropy_in = entropy;
+    t.ids_in = top_ids;
+    Plan plan{};
+    plan.kind = PLAN_CTA;
+    plan.threads = 256;
+    return record_plan(launch_logit_top_grad(dtype, t, stream), plan);
+}
+
+int logprob_top_bwd(const float *dlogp, const float *dentropy, const float *dtop_logp, const void *logits,
+                    const int64_t *targets, const float *stats, const float *entropy, const int64_t *top_ids,
+                    void *dlogits, int64_t rows, int64_t V, int64_t k, float inv_temp, int dtype, cudaStream_t stream) {
+    return logprob_top_bwd_ld(dlogp, dentropy, dtop_logp, logits, V, targets, stats, entropy, top_ids, dlogits, V, rows, V,
+                              k, inv_temp, dtype, stream);
+}
+
 const char *nrm_status_string(int status) {
     switch (status) {
     case NRM_OK: return "ok";

@@ -1,0 +1,672 @@
+// logits_top.cuh -- the log-probability of one target per row of logits with the
+// row's entropy and its k largest alternatives, and the gradient of all three.
+// With s the inverse temperature, c = s log2(e), m the row's maximum and
+// x_j = (z_j - m) c,
+//
+//   d = sum_j 2^x_j,  A = sum_j 2^x_j x_j
+//   lp_j = s (z_j - m) - log d          logp = lp_target
+//   H = -sum_j p_j lp_j = log d - log(2) A / d
+//
+// all in the one pass that the log-probability alone takes (logits.cuh): A is
+// rescaled like d, and moves by d times the shift when the maximum does.  The k
+// largest logits (ties: the lowest index first) come out of the same pass.  A
+// thread keeps the maximum of each group of packs it has seen.  At the row's
+// end the k-th largest of the threads' own maxima, T, is a lower bound of the
+// k-th largest logit, for the k threads' maxima are k logits; so only groups
+// whose maximum reaches T can hold one of the k largest, and there are hardly
+// more than k of those.  They are read again (from L2), and their logits from T
+// on go, as 64-bit keys (value, then lower index first), into a sorted list of 32
+// that each warp keeps one entry a lane.  The warps' lists are joined by each
+// entry's rank.  Where many logits equal T (masked by one finite value, say) the
+// groups are in index order, and later ones of no larger maximum are left out.
+//
+// The gradient for g of logp, h of H and a_i of the alternatives' lp:
+//   dz_j = s (g [j = target] + sum_i a_i [j = id_i] - p_j (g + sum_i a_i + h (lp_j + H)))
+#pragma once
+
+#include "logits.cuh"
+
+namespace nrm {
+
+__device__ __forceinline__ uint32_t top_ordered(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 counts as 0
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float top_value(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+constexpr uint32_t kTopNone = 0x007fffffu;  // of -inf: nothing up to it is a candidate
+
+// A key: larger values first, then lower indices.  0: none.
+__device__ __forceinline__ uint64_t top_key(float v, uint32_t index) {
+    return (uint64_t)top_ordered(v) << 32 | (uint32_t)~index;
+}
+__device__ __forceinline__ bool top_finite(float v) { return v > -INFINITY; }  // not NaN either
+
+// One warp's sorted list: lane i holds the (i+1)-th largest key it was given.
+struct TopList {
+    uint64_t key = 0;
+    // the keys of the lanes that offer one
+    __device__ __forceinline__ void offer(bool on, uint64_t mine, int k, int lane) {
+        uint64_t least = __shfl_sync(0xffffffffu, key, k - 1);
+        uint32_t who = __ballot_sync(0xffffffffu, on && mine > least);
+        while (who) {
+            const int src = __ffs(who) - 1;
+            const uint64_t v = __shfl_sync(0xffffffffu, mine, src);
+            const uint32_t above = __ballot_sync(0xffffffffu, key > v);  // a prefix of the lanes
+            const uint64_t up = __shfl_up_sync(0xffffffffu, key, 1);
+            const int at = __popc(above);
+            key = lane < at ? key : lane == at ? v : up;
+            least = __shfl_sync(0xffffffffu, key, k - 1);
+            who &= who - 1;
+            who &= __ballot_sync(0xffffffffu, mine > least);
+        }
+    }
+};
+
+// (maximum, sum, A) of a set of logits.
+struct RowEnt {
+    float m, d, a;
+};
+// The same around another maximum M >= m.
+__device__ __forceinline__ void ent_to(RowEnt &r, float M, float c) {
+    if (M > r.m) {
+        if (r.m > -INFINITY) {
+            const float x = fmaxf((r.m - M) * c, -300.f), f = exp2_fast(x);
+            r.a = f * fmaf(r.d, x, r.a);
+            r.d *= f;
+        }
+        r.m = M;
+    }
+}
+// A term 2^x x is 0 from 2^-126 on; -inf times 0 is not.
+__device__ __forceinline__ float ent_x(float x) { return fmaxf(x, -200.f); }
+
+// Add a set of packs to (d, A) around m (packs_sum with the second sum).
+template <typename T, int PK>
+__device__ __forceinline__ void packs_ent(const uint4 (&raw)[PK], RowEnt &r, float c) {
+    constexpr int H = IO2<T>::H;
+    const Shift s(r.m, c);
+    float2 d = f2(0.f), a = f2(0.f);
+    if (!s.direct) {
+#pragma unroll
+        for (int k = 0; k < PK; ++k) {
+            float2 v[H];
+            IO2<T>::unpack(raw[k], v);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float2 x = __ffma2_rn(v[h], f2(c), f2(-s.b));
+                const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                d = __fadd2_rn(d, e);
+                a = __ffma2_rn(e, make_float2(ent_x(x.x), ent_x(x.y)), a);
+            }
+        }
+        const float sum = d.x + d.y;
+        // what the rounding of b leaves of every x
+        const float rest = r.m == -INFINITY ? 0.f : -fmaf(r.m, c, -s.b);
+        r.a += s.left * fmaf(sum, rest, a.x + a.y);
+        r.d += s.left * sum;
+        return;
+    }
+#pragma unroll 1
+    for (int k = 0; k < PK; ++k) {
+        uint4 q = raw[0];
+#pragma unroll
+        for (int j = 1; j < PK; ++j)
+            if (j == k) q = raw[j];
+        float2 v[H];
+        IO2<T>::unpack(q, v);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const float2 x = make_float2((v[h].x - r.m) * c, (v[h].y - r.m) * c);
+            const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            d = __fadd2_rn(d, e);
+            a = __ffma2_rn(e, make_float2(ent_x(x.x), ent_x(x.y)), a);
+        }
+    }
+    r.a += a.x + a.y;
+    r.d += d.x + d.y;
+}
+__device__ __forceinline__ void one_ent(float z, RowEnt &r, float c) {
+    if (z > r.m) ent_to(r, z, c);
+    const float x = (z - (r.m == -INFINITY ? 0.f : r.m)) * c, e = exp2_fast(x);
+    r.d += e;
+    r.a = fmaf(e, ent_x(x), r.a);
+}
+// Over a warp's lanes: every lane gets the same bits.
+__device__ __forceinline__ RowEnt lanes_ent(RowEnt r, float c) {
+    float M = r.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    ent_to(r, M, c);
+    return RowEnt{M, warp_sum_all(r.d), warp_sum_all(r.a)};
+}
+
+// The outputs of a row that has a distribution, or has not (`empty`).
+__device__ __forceinline__ void top_row(const TopArgs &t, int64_t row, const RowEnt &r, float za) {
+    const bool empty = r.m == -INFINITY && r.d == 0.f;
+    const float logd = empty ? -INFINITY : -log_prob(r.m, r.m, r.d, t.a.scale).hi;
+    if (t.a.logp) t.a.logp[row] = empty ? -INFINITY : log_prob(za, r.m, r.d, t.a.scale).hi;
+    if (t.entropy) t.entropy[row] = empty ? 0.f : fmaf(-0.693147181f, r.a / r.d, logd);
+    if (t.a.stats) {
+        t.a.stats[2 * row] = r.m;
+        t.a.stats[2 * row + 1] = logd;
+    }
+}
+// By one thread or by lanes of a warp: a row that takes no part.
+__device__ __forceinline__ void top_no_row(const TopArgs &t, int64_t row) {
+    if (t.a.logp) t.a.logp[row] = 0.f;
+    if (t.entropy) t.entropy[row] = 0.f;
+    if (t.a.stats) t.a.stats[2 * row] = t.a.stats[2 * row + 1] = 0.f;
+    for (int i = 0; i < t.k; ++i) {
+        t.ids[row * t.k + i] = -1;
+        t.top[row * t.k + i] = 0.f;
+    }
+}
+__device__ __forceinline__ void top_place(const TopArgs &t, int64_t row, int place, uint64_t key, const RowEnt &r) {
+    t.ids[row * t.k + place] = key ? (int64_t)(uint32_t)~(uint32_t)key : -1;
+    t.top[row * t.k + place] = key ? log_prob(top_value((uint32_t)(key >> 32)), r.m, r.d, t.a.scale).hi : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// Rows of up to 32 PK packs: one warp a row, the row in its registers.
+// ---------------------------------------------------------------------------
+template <typename T, int PK, int MINB>
+__global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs ta) {
+    constexpr int V = IO<T>::V;
+    const LogitArgs &a = ta.a;
+    const int lane = threadIdx.x & 31, k = ta.k;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float c = a.scale * kLog2e;
+    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < a.rows; row += (int64_t)gridDim.x * 4) {
+        const int64_t tgt = a.target[row];
+        if (tgt < 0 || tgt >= a.V) {
+            if (lane == 0) top_no_row(ta, row);
+            continue;
+        }
+        const RowView<T> w(a, row, 0, 0, lane);
+        const float za = IO<T>::to_f(w.z[tgt]);
+        const bool has = lane < w.ns;
+        const float zs = has ? IO<T>::to_f(w.z[w.sc]) : -INFINITY;
+        uint4 raw[PK];
+#pragma unroll
+        for (int p = 0; p < PK; ++p) {
+            raw[p] = no_pack<T>();
+            if (p * 32 < w.mine) raw[p] = ld_once(w.body + p * 32 * V);
+        }
+        RowEnt r{packs_max<PK>(raw, T()), 0.f, 0.f};
+        packs_ent<T, PK>(raw, r, c);
+        float tm = r.m;
+        if (has) {
+            one_ent(zs, r, c);
+            tm = fmaxf(tm, zs);
+        }
+        r = lanes_ent(r, c);
+        if (lane == 0) top_row(ta, row, r, za);
+        if (k == 0) continue;
+        // T: the k-th largest of the lanes' maxima, to 16 bits downwards
+        const uint32_t om = top_ordered(tm) >> 16;
+        uint32_t T16 = 0;
+#pragma unroll
+        for (int b = 15; b >= 0; --b) {
+            const uint32_t t = T16 | 1u << b;
+            if (__popc(__ballot_sync(0xffffffffu, om >= t)) >= k) T16 = t;
+        }
+        const uint32_t T32 = T16 << 16 > kTopNone ? T16 << 16 : kTopNone + 1u;
+        TopList list;
+#pragma unroll
+        for (int p = 0; p < PK; ++p) {
+            float f[V];
+            IO<T>::unpack(raw[p], f);
+            float pm = f[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) pm = fmaxf(pm, f[i]);
+            if (!__any_sync(0xffffffffu, top_ordered(pm) >= T32)) continue;
+            const uint32_t at = (uint32_t)(w.head + (lane + p * 32) * V);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                list.offer(top_finite(f[i]) && top_ordered(f[i]) >= T32, top_key(f[i], at + i), k, lane);
+        }
+        list.offer(has && top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
+        if (lane < k) top_place(ta, row, lane, list.key, r);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Any row: a CTA, or the CTAs of a cluster with a slice of the packs each, goes
+// over it in segments of TH x PK packs, the next segment on its way into shared
+// memory meanwhile.
+// ---------------------------------------------------------------------------
+constexpr int kTopGroups = 16;  // a thread's groups: their maxima wait in shared memory
+
+template <typename T> struct TopSlice {
+    const T *z, *body;
+    int head, tail, p0, mine, packs, ns;
+    int64_t sc;
+    __device__ __forceinline__ TopSlice(const LogitArgs &a, int64_t row, int rank, int cs, int t) {
+        z = static_cast<const T *>(a.z) + row * a.ldz;
+        const RowCut<T> cut = cut_row(z, a.V);
+        head = cut.head;
+        tail = cut.tail;
+        p0 = (int)((int64_t)cut.packs * rank / cs);
+        packs = (int)((int64_t)cut.packs * (rank + 1) / cs) - p0;
+        body = z + head + (int64_t)p0 * IO<T>::V;
+        mine = packs - t;
+        ns = rank == 0 ? head + tail : 0;
+        sc = t < head ? t : a.V - tail + (t - head);
+    }
+};
+
+template <typename T, int TH, int PK, int MINB>
+__global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, const int cs, const int batch) {
+    constexpr int NW = TH / 32, V = IO<T>::V, CSMAX = 8;
+    constexpr uint32_t ALL = 0xffffffffu;
+    extern __shared__ __align__(16) uint4 next_row[];                                     // [PK][TH]
+    float *const group_max = reinterpret_cast<float *>(next_row + PK * TH);               // [kTopGroups][TH]
+    unsigned short *const found = reinterpret_cast<unsigned short *>(group_max + kTopGroups * TH);  // [kTopGroups * TH]
+    __shared__ RowEnt slot[NW];
+    __shared__ uint64_t keys[(NW > CSMAX ? NW : CSMAX) * 32];
+    __shared__ uint64_t pub_keys[2][32];
+    __shared__ RowEnt pub[2];
+    __shared__ int count[2], per_group[kTopGroups];
+    const LogitArgs &a = ta.a;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k = ta.k;
+    const int rank = cs > 1 ? (int)cluster_rank() : 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float c = a.scale * kLog2e;
+    int parity = 1;
+    const int64_t first = (int64_t)(blockIdx.x / cs) * batch, step = (int64_t)(gridDim.x / cs) * batch;
+    for (int64_t r0 = first; r0 < a.rows; r0 += step) {
+        const bool have = lane < batch && r0 + lane < a.rows;
+        const int64_t my_target = have ? a.target[r0 + lane] : -1;
+        const bool takes_part = my_target >= 0 && my_target < a.V;
+        uint32_t live = __ballot_sync(ALL, takes_part);
+        if (rank == 0 && t < 32 && have && !takes_part) top_no_row(ta, r0 + lane);
+        float zn = 0.f;  // the next row's scalar element
+        auto fetch = [&](int64_t row, int seg) {
+            const TopSlice<T> w(a, row, rank, cs, t);
+            if (seg == 0 && t < w.ns) zn = IO<T>::to_f(w.z[w.sc]);
+#pragma unroll
+            for (int p = 0; p < PK; ++p) {
+                const int at = (seg * PK + p) * TH;
+                cp_async16_if(at < w.mine, &next_row[p * TH + t], w.body + (int64_t)(at + t) * V);
+            }
+        };
+        if (live) fetch(r0 + __ffs(live) - 1, 0);
+        while (live) {
+            const int at = __ffs(live) - 1;
+            const int64_t row = r0 + at, tgt = __shfl_sync(ALL, my_target, at);
+            live &= live - 1;
+            parity ^= 1;
+            const TopSlice<T> w(a, row, rank, cs, t);
+            const bool has = t < w.ns;
+            const float zs = has ? zn : -INFINITY;
+            const float za = t == 0 ? IO<T>::to_f(w.z[tgt]) : 0.f;
+            const int segs = w.packs > 0 ? (w.packs - 1) / (TH * PK) + 1 : 1;
+            const int per = (segs - 1) / kTopGroups + 1;  // segments of a group
+            RowEnt r{-INFINITY, 0.f, 0.f};
+            float tm = -INFINITY, gm = -INFINITY;
+            int in_group = 0, group = 0;
+            for (int seg = 0; seg < segs; ++seg) {
+                cp_async_wait();
+                uint4 raw[PK];
+#pragma unroll
+                for (int p = 0; p < PK; ++p) {
+                    raw[p] = no_pack<T>();
+                    if ((seg * PK + p) * TH < w.mine) raw[p] = next_row[p * TH + t];
+                }
+                float m = packs_max<PK>(raw, T());
+                // the maximum is there, so the packs have left shared memory
+                asm volatile("" : "+f"(m)::"memory");
+                if (seg + 1 < segs)
+                    fetch(row, seg + 1);
+                else if (live)
+                    fetch(r0 + __ffs(live) - 1, 0);
+                gm = fmaxf(gm, m);
+                if (++in_group == per || seg + 1 == segs) {
+                    group_max[group * TH + t] = gm;
+                    tm = fmaxf(tm, gm);
+                    gm = -INFINITY;
+                    in_group = 0;
+                    ++group;
+                }
+                ent_to(r, m, c);
+                packs_ent<T, PK>(raw, r, c);
+            }
+            if (has) {
+                one_ent(zs, r, c);
+                tm = fmaxf(tm, zs);
+            }
+            r = lanes_ent(r, c);
+            if (lane == 0) slot[warp] = r;
+            if (t == 0) count[0] = count[1] = 0;
+            if (t < kTopGroups) per_group[t] = 0;
+            __syncthreads();
+            r = lane < NW ? slot[lane] : RowEnt{-INFINITY, 0.f, 0.f};
+            r = lanes_ent(r, c);
+            uint64_t best = 0;  // thread i < k: the i-th largest key of this CTA's slice
+            if (k > 0) {
+                const uint32_t om = top_ordered(tm) >> 16;
+                uint32_t T16 = 0;
+#pragma unroll 1
+                for (int b = 15; b >= 0; --b) {
+                    const uint32_t v = T16 | 1u << b;
+                    if (__syncthreads_count(om >= v) >= k) T16 = v;
+                }
+                const uint32_t T32 = T16 << 16 > kTopNone ? T16 << 16 : kTopNone + 1u;
+                TopList list;
+                // one element a lane and pass: a group's packs are TH apart
+                auto scan = [&](int n) {
+                    constexpr int PASS = PK * V / 32 > 0 ? PK * V / 32 : 1, LANES = PK * V < 32 ? PK * V : 32;
+                    for (int i = warp; i < n; i += NW) {
+                        const int code = found[i], g = code / TH, th = code % TH;
+                        for (int sub = 0; sub < per; ++sub) {
+                            float f[PASS];
+                            int idx[PASS];
+#pragma unroll
+                            for (int q = 0; q < PASS; ++q) {
+                                const int e = q * 32 + lane, p = e / V;
+                                const int64_t pack = ((int64_t)(g * per + sub) * PK + p) * TH + th;
+                                idx[q] = -1;
+                                f[q] = -INFINITY;
+                                if (lane < LANES && pack < w.packs) {
+                                    idx[q] = (int)(w.head + (w.p0 + pack) * V + e % V);
+                                    f[q] = IO<T>::to_f(w.z[idx[q]]);
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < PASS; ++q)
+                                list.offer(top_finite(f[q]) && top_ordered(f[q]) >= T32, top_key(f[q], (uint32_t)idx[q]), k, lane);
+                        }
+                    }
+                };
+                for (int g = 0; g < group; ++g) {
+                    const uint32_t who = __ballot_sync(ALL, top_ordered(group_max[g * TH + t]) >= T32);
+                    if (who && lane == 0) atomicAdd(&per_group[g], __popc(who));
+                }
+                __syncthreads();
+                // groups up to `cut` hold k candidates; where there are many more
+                // (ties), later ones count only with a larger maximum
+                int sum = 0, cut = group;
+                for (int g = 0; g < group; ++g) {
+                    sum += per_group[g];
+                    if (sum >= k && cut == group) cut = g + 1;
+                }
+                if (sum <= 8 * 32) cut = group;
+                for (int g = 0; g < cut; ++g)
+                    if (top_ordered(group_max[g * TH + t]) >= T32) found[atomicAdd(&count[0], 1)] = (unsigned short)(g * TH + t);
+                __syncthreads();
+                scan(count[0]);
+                if (warp == 0) list.offer(has && top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
+                // the entries' ranks among all warps' sorted lists
+                auto rank_of = [&](uint64_t v, int lists) {
+                    int place = 0;
+                    for (int q = 0; q < lists; ++q) {
+                        int lo = 0;  // how many of list q are larger
+#pragma unroll
+                        for (int h = 16; h > 0; h >>= 1)
+                            if (keys[q * 32 + lo + h - 1] > v) lo += h;
+                        if (lo == 31 && keys[q * 32 + 31] > v) lo = 32;
+                        place += lo;
+                    }
+                    return place;
+                };
+                keys[t] = list.key;  // [warp][lane]
+                if (t < 32) pub_keys[parity][t] = 0;
+                __syncthreads();
+                if (list.key) {
+                    const int place = rank_of(list.key, NW);
+                    if (place < k) pub_keys[parity][place] = list.key;
+                }
+                __syncthreads();
+                if (cut < group) {
+                    // the same for the rest, from the k-th key on
+                    const uint32_t kth = (uint32_t)(pub_keys[parity][k - 1] >> 32);
+                    for (int g = cut; g < group; ++g)
+                        if (top_ordered(group_max[g * TH + t]) > kth)
+                            found[atomicAdd(&count[1], 1)] = (unsigned short)(g * TH + t);
+                    __syncthreads();
+                    if (count[1]) {
+                        scan(count[1]);
+                        keys[t] = list.key;
+                        if (t < 32) pub_keys[parity][t] = 0;
+                        __syncthreads();
+                        if (list.key) {
+                            const int place = rank_of(list.key, NW);
+                            if (place < k) pub_keys[parity][place] = list.key;
+                        }
+                        __syncthreads();
+                    }
+                }
+                if (t < k) best = pub_keys[parity][t];
+                if (cs > 1) {
+                    if (t == 0) pub[parity] = r;
+                    cluster_arrive();
+                    cluster_wait();
+                    if (rank == 0) {
+                        // every rank's list and sums
+                        uint64_t v = 0;
+                        if (t < cs * 32) {
+                            const float2 raw2 = ld_dsmem(reinterpret_cast<const float2 *>(&pub_keys[parity][lane]), (uint32_t)warp);
+                            v = lane < k ? (uint64_t)__float_as_uint(raw2.y) << 32 | __float_as_uint(raw2.x) : 0;
+                        }
+                        if (t < CSMAX * 32) keys[t] = v;
+                        if (t < 32) pub_keys[parity][t] = 0;
+                        __syncthreads();
+                        if (v) {
+                            const int place = rank_of(v, cs);
+                            if (place < k) pub_keys[parity][place] = v;
+                        }
+                        __syncthreads();
+                        if (t < k) best = pub_keys[parity][t];
+                    }
+                }
+            } else if (cs > 1) {
+                if (t == 0) pub[parity] = r;
+                cluster_arrive();
+                cluster_wait();
+            }
+            if (rank == 0) {
+                if (cs > 1) {
+                    r = RowEnt{-INFINITY, 0.f, 0.f};
+                    if (lane < cs) {
+                        r.m = ld_dsmem(&pub[parity].m, (uint32_t)lane);
+                        r.d = ld_dsmem(&pub[parity].d, (uint32_t)lane);
+                        r.a = ld_dsmem(&pub[parity].a, (uint32_t)lane);
+                    }
+                    r = lanes_ent(r, c);
+                }
+                if (t == 0) top_row(ta, row, r, za);
+                if (t < k) top_place(ta, row, t, best, r);
+            }
+            // the next row's slots and lists
+            __syncthreads();
+        }
+    }
+    if (cs > 1) {
+        // stay resident until the first rank has read this CTA's list
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The gradient: element-wise from the forward's statistics, tiles of 4 x TH
+// packs of a row.  The entries of the target and the alternatives are written
+// once more, whole, by a thread each: their logits are read before the tile is
+// written (dlogits may replace the logits), an entry named more than once is
+// written by the first of its names.
+// ---------------------------------------------------------------------------
+template <typename T> struct TopSlope {
+    float s, top, logd, gsum, h, gh;  // gh: gsum + h H
+    // -s p (gsum + h (lp + H)); p = 0 from lp = -88 on
+    __device__ __forceinline__ float one(float z) const {
+        const float lp = fmaf(z - top, s, -logd);
+        return -s * exp2_fast(lp * kLog2e) * fmaf(h, fmaxf(lp, -100.f), gh);
+    }
+    __device__ __forceinline__ uint4 pack(const uint4 &raw) const {
+        constexpr int H = IO2<T>::H;
+        float2 v[H];
+        IO2<T>::unpack(raw, v);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 lp = __ffma2_rn(__fadd2_rn(v[i], f2(-top)), f2(s), f2(-logd));
+            float2 p = __fmul2_rn(lp, f2(kLog2e));
+            p.x = exp2_fast(p.x);
+            p.y = exp2_fast(p.y);
+            const float2 q = __ffma2_rn(f2(h), make_float2(fmaxf(lp.x, -100.f), fmaxf(lp.y, -100.f)), f2(gh));
+            v[i] = __fmul2_rn(__fmul2_rn(p, f2(-s)), q);
+        }
+        return IO2<T>::pack(v);
+    }
+};
+
+template <typename T, int TH>
+__global__ void __launch_bounds__(256) logit_top_grad_kernel(const TopArgs ta, const int tiles) {
+    constexpr int G = 256 / TH, V = IO<T>::V, U = 4, NS = kTopMaxK + 1;
+    __shared__ int64_t name[G][NS];
+    __shared__ float part[G][NS];
+    const LogitArgs &a = ta.a;
+    const int t = threadIdx.x % TH, lane = threadIdx.x & 31, in = threadIdx.x / TH, k = ta.k;
+    auto sync = [] {
+        if (TH == 32) __syncwarp();
+        else __syncthreads();
+    };
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t total = a.rows * tiles;
+    for (int64_t id = (int64_t)blockIdx.x * G + in; id < total; id += (int64_t)gridDim.x * G) {
+        const int64_t row = total <= 0xffffffffll ? (int64_t)((uint32_t)id / (uint32_t)tiles) : id / tiles;
+        const int tile = (int)(id - row * tiles);
+        const T *Z = static_cast<const T *>(a.z) + row * a.ldz;
+        T *D = static_cast<T *>(a.dz) + row * a.lddz;
+        const int64_t tgt = a.target[row];
+        TopSlope<T> f;
+        f.s = a.scale;
+        f.top = a.stats_in[2 * row];
+        f.logd = a.stats_in[2 * row + 1];
+        const bool live = tgt >= 0 && tgt < a.V && f.logd != -INFINITY;
+        const float g = live && a.dlogp ? a.dlogp[row] : 0.f;
+        // every warp has the k alternatives, one a lane
+        int64_t mine = live && lane < k && ta.dtop ? ta.ids_in[row * k + lane] : -1;
+        if (mine < 0 || mine >= a.V) mine = -1;
+        const float al = mine >= 0 ? ta.dtop[row * k + lane] : 0.f;
+        f.h = live && ta.dentropy ? ta.dentropy[row] : 0.f;
+        f.gsum = g + warp_sum_all(al);
+        f.gh = f.h != 0.f ? fmaf(f.h, ta.entropy_in[row], f.gsum) : f.gsum;
+        const bool any = __any_sync(0xffffffffu, al != 0.f) || g != 0.f || f.h != 0.f;
+        const RowCut<T> cut = cut_row(Z, a.V);
+        const T *body = Z + cut.head;
+        T *out = D + cut.head;
+        const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+        const int base = tile * (TH * U), p0 = base + t;
+        const int ns = tile == 0 ? cut.head + cut.tail : 0;
+        const int64_t sc = t < cut.head ? t : a.V - cut.tail + (t - cut.head);
+        if (!any) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (p0 + u * TH < cut.packs) st_pack(out + (int64_t)(p0 + u * TH) * V, make_uint4(0, 0, 0, 0), wide);
+            if (t < ns) D[sc] = IO<T>::from_f(0.f);
+            continue;
+        }
+        // the names and their parts; who of them lies in this tile
+        if (t < 32) {
+            if (t < k) {
+                name[in][t] = mine;
+                part[in][t] = al;
+            }
+            if (t == 0) {
+                name[in][k] = tgt;
+                part[in][k] = g;
+            }
+        }
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (p0 + u * TH < cut.packs) raw[u] = ld_once(body + (int64_t)(p0 + u * TH) * V);
+        const float zs = t < ns ? IO<T>::to_f(Z[sc]) : 0.f;
+        sync();
+        constexpr int PER = (NS + TH - 1) / TH;  // names a thread
+        int64_t put[PER];
+        float val[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int i = t + q * TH;
+            put[q] = -1;
+            if (i > k) continue;
+            const int64_t j = name[in][i];
+            const bool scalar = j < cut.head || j >= a.V - cut.tail;
+            const int ip = (int)(j - cut.head) / V;
+            if (j < 0 || !(scalar ? tile == 0 : ip >= base && ip < base + TH * U)) continue;
+            bool again = false;
+            float sum = 0.f;
+            for (int o = 0; o <= k; ++o)
+                if (name[in][o] == j) {
+                    again = again || o < i;
+                    sum += part[in][o];
+                }
+            if (again) continue;
+            put[q] = j;
+            val[q] = fmaf(f.s, sum, f.one(IO<T>::to_f(Z[j])));
+        }
+        sync();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (p0 + u * TH < cut.packs) st_pack(out + (int64_t)(p0 + u * TH) * V, f.pack(raw[u]), wide);
+        if (t < ns) D[sc] = IO<T>::from_f(f.one(zs));
+        sync();
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (put[q] >= 0) D[put[q]] = IO<T>::from_f(val[q]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers, one instance of each per storage type (logits_<type>.cu).
+// ---------------------------------------------------------------------------
+template <typename T, int PK, int MINB> cudaError_t launch_top_warp(const TopArgs &a, cudaStream_t s, Plan *p) {
+    p->kind = PLAN_WARP;
+    p->threads = 128;
+    p->packs = PK;
+    const int64_t n = (a.a.rows + 3) / 4;
+    return launch_row(logit_top_warp_kernel<T, PK, MINB>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), 128u, 0, s, a);
+}
+template <typename T, int TH, int PK, int MINB>
+cudaError_t launch_top_cta(const TopArgs &a, int cs, int sms, cudaStream_t s, Plan *p) {
+    constexpr size_t smem = (size_t)PK * TH * 16 + (size_t)kTopGroups * TH * 6;
+    auto kernel = logit_top_kernel<T, TH, PK, MINB>;
+    int per_sm = 0;
+    const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), TH, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    p->kind = cs > 1 ? PLAN_CLUSTER : PLAN_CTA;
+    p->threads = TH;
+    p->packs = PK;
+    p->groups = cs > 1 ? cs : 0;
+    const int64_t batch = rows_per_batch(a.a.rows, (int64_t)sms * per_sm / cs, 1);
+    return launch_clusters(kernel, (a.a.rows + batch - 1) / batch, cs, TH, smem, s, a, cs, (int)batch);
+}
+
+template <typename T> cudaError_t launch_logit_top_t(const TopArgs &a, int sms, cudaStream_t s, Plan *p) {
+    const int64_t packs = a.a.V / IO<T>::V;
+    if (packs <= 32 * 4) return launch_top_warp<T, 4, 8>(a, s, p);
+    if (packs <= 32 * 16 && a.a.rows >= 2 * (int64_t)sms)
+        return packs <= 32 * 8 ? launch_top_warp<T, 8, 6>(a, s, p) : launch_top_warp<T, 16, 4>(a, s, p);
+    int cs = 1;
+    while (cs < 8 && a.a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * 256) cs *= 2;
+    return launch_top_cta<T, 256, 8, 3>(a, cs, sms, s, p);
+}
+
+template <typename T, int TH> cudaError_t launch_top_grad_g(const TopArgs &a, cudaStream_t s) {
+    constexpr int G = 256 / TH;
+    const int64_t packs = a.a.V / IO<T>::V + 1;
+    const int64_t tiles = (packs + 4 * TH - 1) / (4 * TH);
+    const int64_t n = (a.a.rows * tiles + G - 1) / G;
+    return launch_row(logit_top_grad_kernel<T, TH>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff), 256u, 0, s, a, (int)tiles);
+}
+template <typename T> cudaError_t launch_logit_top_grad_t(const TopArgs &a, cudaStream_t s) {
+    return a.a.V / IO<T>::V <= 512 ? launch_top_grad_g<T, 32>(a, s) : launch_top_grad_g<T, 256>(a, s);
+}
+
+}  // namespace nrm

@@ -382,6 +382,48 @@ NRM_BY_TYPE(launch_qk, (const QkArgs &a, int ve, bool back, int sms, cudaStream_
             (a, ve, back, sms, s, p, parts))
 // dwq[c] (c < D) and dwk[c - D]: the parts' sums; either may be NULL.
 cudaError_t launch_qk_fold(const float *part, float *dwq, float *dwk, int64_t parts, int D, cudaStream_t s);
+
+// Routing of tokens to experts (route.cuh).
+constexpr int kRouteMaxExperts = 1024, kRouteMaxK = 32, kRouteMaxGroups = 32;
+struct RouteArgs {
+    const void *x;
+    int64_t ldx;
+    const float *bias;      // [experts], or NULL
+    int64_t tokens;
+    int experts, k;
+    int softmax, renorm;
+    float scale;
+    // forward
+    int groups, top_groups, group_top;  // groups 1 where they do not limit the choice
+    int group_size, log_lanes, per_lane;  // lanes of a group: 2^log_lanes, experts each
+    int wide;               // a lane's experts are whole packs
+    int by_score;           // the order is that of the scores, not of the logits alone
+    int need_sum;           // the softmax' sum over all experts
+    float *weights;         // [tokens][k]
+    int64_t *ids;
+    float *scores;          // [tokens][experts], or NULL
+    // backward
+    const float *dweights, *dscores;  // dscores may be NULL
+    const int64_t *ids_in;
+    void *dx;
+    int64_t lddx;
+};
+NRM_BY_TYPE(launch_route, (const RouteArgs &a, bool back, int sms, cudaStream_t s, Plan *p), (a, back, sms, s, p))
+
+// Rows of logits with entropy and the k largest (logits_top.cuh); of a.* the
+// outputs logp and stats, backward dlogp and stats_in.
+constexpr int kTopMaxK = 32;
+struct TopArgs {
+    LogitArgs a;
+    int k;
+    float *entropy;         // [rows], or NULL
+    int64_t *ids;           // [rows][k]
+    float *top;             // [rows][k]: their log-probabilities
+    const float *dentropy, *dtop, *entropy_in;  // dentropy, dtop may be NULL
+    const int64_t *ids_in;
+};
+NRM_BY_TYPE(launch_logit_top, (const TopArgs &a, int sms, cudaStream_t s, Plan *p), (a, sms, s, p))
+NRM_BY_TYPE(launch_logit_top_grad, (const TopArgs &a, cudaStream_t s), (a, s))
 #undef NRM_UNPAREN
 #undef NRM_BY_TYPE
 cudaError_t launch_dw_fold(const float *part, float *dw, int64_t parts, int64_t N, cudaStream_t s);

@@ -293,10 +293,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                              ? (__float_as_uint(q) << kIdxBits) + (uint32_t)(kIdxMask - (r.first + i))
                              : 0u;
             }
-            // a score is good to 3e-7 (the exponent's argument, ex2, rcp), its
-            // sum with the bias to half a step; the difference and the fixed
-            // point add one step each
-            near_ = a.by_score ? 2.f * S * (3e-7f + 1.2e-7f * (fabsf(top) + 1.f)) + 2.f : 2.f;
+            // A sigmoid is good to 3e-7 (the exponent's argument, ex2, rcp), a
+            // softmax to 6e-7 of the largest and half a step for each addition
+            // of its sum; adding the bias and taking the difference to the
+            // largest cost half a step of their results each, the fixed point one
+            // step of its own.
+            const float score = a.softmax ? (6e-7f + 6e-8f * (PL + 6)) / d : 3e-7f;
+            near_ = a.by_score ? 2.f * S * (score + 1.2e-7f * (fabsf(top) + 1.f)) + 2.f : 2.f;
         }
         sort_desc<PL>(key);
         if (limited) {
@@ -333,29 +336,27 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
 #pragma unroll
         for (int i = 0; i < LIST; ++i) list[i] = key[i];
         list[LIST] = 0u;
-        int left = r.n < LIST ? r.n + 1 : LIST;  // heads that are the lane's largest for certain
-        uint32_t last = 0u;                      // the k-th place
+        // a lane whose list ran out may hold more
+        int left = PL > LIST && key[PL > LIST ? LIST : 0] ? LIST : PL + 1;
+        uint32_t last = 0u;  // the k-th place
         int places = 0;
-        bool out_of_list = false;
-        if (!again) {
-            for (; places < 32; ++places) {
-                const uint32_t w = __reduce_max_sync(ALL, list[0]);
-                if (w == 0u) break;
-                if (places >= a.k && (whole || (float)((last >> kIdxBits) - (w >> kIdxBits)) > near_)) break;
-                if (places == a.k - 1) last = w;
-                if (lane == places) mine = w;
-                if (list[0] == w) {
-#pragma unroll
-                    for (int i = 0; i < LIST; ++i) list[i] = list[i + 1];
-                    --left;
-                }
-                if (PL > LIST) {
-                    out_of_list = __any_sync(ALL, left == 0);
-                    if (out_of_list) break;
-                }
+        while (!again) {
+            const uint32_t w = __reduce_max_sync(ALL, list[0]);
+            if (w == 0u) break;
+            if (places >= a.k && (whole || (float)((last >> kIdxBits) - (w >> kIdxBits)) > near_)) break;
+            if (places == 32) {  // more in question than lanes
+                again = true;
+                break;
             }
-            // a lane whose list ran out may hold more; 32 places without an end
-            again = places == 32 || (out_of_list && places < a.k) || (out_of_list && !whole);
+            if (places == a.k - 1) last = w;
+            if (lane == places) mine = w;
+            ++places;
+            if (list[0] == w) {
+#pragma unroll
+                for (int i = 0; i < LIST; ++i) list[i] = list[i + 1];
+                --left;
+            }
+            if (PL > LIST && !(whole && places == a.k)) again = __any_sync(ALL, left == 0);
         }
         int id = mine ? kIdxMask - (int)(mine & kIdxMask) : -1;
         float xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
@@ -391,12 +392,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
             xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
         }
         const bool have = lane < a.k && id >= 0;
-        // the chosen scores; renormalised softmax scores need no sum over all
+        // The chosen scores.  Renormalised softmax scores need no sum over all, and
+        // are taken from the largest of the chosen: none of it underflows.
         float w;
         if (a.softmax) {
-            if (!a.need_sum) m = from_ordered32(__reduce_max_sync(ALL, ordered32(have ? xs : -INFINITY)));
-            w = have ? expf(xs - m) : 0.f;
-            if (a.need_sum) w /= d;
+            if (a.renorm) m = from_ordered32(__reduce_max_sync(ALL, ordered32(have ? xs : -INFINITY)));
+            w = !have ? 0.f : a.renorm ? expf(xs - m) : expf(xs - m) / d;
         } else {
             w = have ? 1.f / (1.f + expf(-xs)) : 0.f;
         }
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
             for (int i = 0; i < PL; ++i) dot = fmaf(g[i], x[i], dot);
             dot = warp_sum_all(fmaf(dw, s, dot));
         }
+        __syncwarp();  // dx may replace the logits: every lane has read its own
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
             const int e = i * 32 + lane;

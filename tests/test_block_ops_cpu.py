@@ -104,6 +104,115 @@ def test_binding_refuses_mismatches():
     import row_wise_normalization_reduce_gb300 as nrm
     x, pos, table = torch.zeros(4, 2, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(10, 8)
     for call in (lambda: nrm.qk_norm_rope_fwd(x, x, table, pos), lambda: nrm.qk_norm_rope_bwd(x, x, x, x, table, pos),
-                 lambda: nrm.qk_norm_rope_fwd(x, None, table, pos, stream=0)):
+                 lambda: nrm.qk_norm_rope_fwd(x, None, table, pos, stream=0), lambda: nrm.route_fwd(x, 2),
+                 lambda: nrm.route_bwd(x[..., :2], x, pos[:, None]), lambda: nrm.route_fwd(x, 2, score="none"),
+                 lambda: nrm.logprob_top_fwd(x, torch.zeros(4, 2, dtype=torch.int64), 2),
+                 lambda: nrm.logprob_top_bwd(None, None, None, x, torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2, 2))):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_gradient_against_differences(score, renorm):
+    g = torch.Generator().manual_seed(1)
+    x, dw, ds = (torch.randn(3, n, generator=g, dtype=torch.float64) for n in (7, 2, 7))
+    ids = R.route(x, 2, score=score)[1]
+    ids[2, 1] = -1
+
+    def f(x):
+        s = R.scores64(x, score)
+        w = torch.where(ids >= 0, s.gather(1, ids.clamp(0)), 0.0)
+        return 1.5 * ((w / w.sum(-1, keepdim=True) if renorm else w) * dw).sum() + (s * ds).sum()
+
+    dx, _ = R.route_grad(dw, x, ids, score=score, renormalize=renorm, scale=1.5, dscores=ds)
+    differences(f, x, dx, 1e-8)
+
+
+def test_route_definition_by_hand():
+    x = torch.tensor([[0.0, 2.0, 1.0, 1.0, -float("inf"), 5.0]])
+    w, ids = R.route(x, 3, renormalize=True)
+    e = torch.tensor([5.0, 2.0, 1.0], dtype=torch.float64).exp()
+    assert ids.tolist() == [[5, 1, 2]] and torch.allclose(w, (e / e.sum())[None], rtol=1e-14)
+    # groups (0, 1), (2, 3), (4, 5): sums of two 2, 2, 5 and of one 2, 1, 5
+    assert R.route(x, 2, groups=3, top_groups=1)[1].tolist() == [[5, -1]]
+    assert R.route(x, 3, groups=3, top_groups=2)[1].tolist() == [[5, 1, 0]]
+    b = torch.tensor([0.0, -1.0, 0.5, 0.0, 9.0, 0.0])
+    assert R.route(x, 2, b, score="sigmoid")[1].tolist() == [[2, 5]]
+
+
+def test_route_refusals(lib):
+    good = dict(x=A, ldx=64, bias=2 * A, w=3 * A, ids=4 * A, sc=5 * A, t=4, e=64, k=6, score=0, groups=8, top=3, gt=2, renorm=1,
+                scale=1.0, dtype=2, stream=None)
+    _bad(lib, "route_fwd", good, [
+        (dict(), (OK, DEVICE)), (dict(bias=None, sc=None), (OK, DEVICE)), (dict(t=0, x=None, w=None), OK), (dict(score=1), (OK, DEVICE)),
+        (dict(x=None), NULL), (dict(w=None), NULL), (dict(ids=None), NULL), (dict(t=-1), SHAPE), (dict(e=0, k=0), SHAPE),
+        (dict(k=0), SHAPE), (dict(k=65, top=8), SHAPE), (dict(k=25), SHAPE), (dict(ldx=63), SHAPE), (dict(groups=7), SHAPE),
+        (dict(groups=0), SHAPE), (dict(top=0), SHAPE), (dict(top=9), SHAPE), (dict(gt=0), SHAPE), (dict(t=2 ** 60), SHAPE),
+        (dict(gt=3), UNSUP), (dict(gt=3, top=8), (OK, DEVICE)), (dict(e=1025, ldx=1025, groups=1, top=1), UNSUP),
+        (dict(e=64, k=33, groups=1, top=1), UNSUP), (dict(groups=64, k=1, top=2), UNSUP), (dict(e=1020, ldx=1020, groups=17), UNSUP),
+        (dict(score=2), VALUE), (dict(scale=float("inf")), VALUE), (dict(x=A + 1), VALUE), (dict(bias=2 * A + 2), VALUE),
+        (dict(ids=4 * A + 4), VALUE), (dict(sc=5 * A + 1), VALUE), (dict(dtype=3), DTYPE), (dict(w=A), ALIAS), (dict(ids=2 * A), ALIAS),
+        (dict(sc=3 * A), ALIAS), (dict(sc=A), ALIAS),
+    ])
+    good = dict(dw=A, x=2 * A, ldx=64, ids=3 * A, ds=4 * A, dx=5 * A, lddx=64, t=4, e=64, k=6, score=0, renorm=1, scale=1.0, dtype=0,
+                stream=None)
+    _bad(lib, "route_bwd", good, [
+        (dict(), (OK, DEVICE)), (dict(ds=None), (OK, DEVICE)), (dict(dx=2 * A), (OK, DEVICE)), (dict(t=0, dw=None), OK),
+        (dict(dw=None), NULL), (dict(x=None), NULL), (dict(ids=None), NULL), (dict(dx=None), NULL), (dict(lddx=63), SHAPE),
+        (dict(k=65), SHAPE), (dict(k=33), UNSUP), (dict(score=-1), VALUE), (dict(dw=A + 2), VALUE), (dict(dx=2 * A, lddx=65), ALIAS),
+        (dict(dx=4 * A), ALIAS), (dict(dx=A), ALIAS), (dict(dx=3 * A), ALIAS), (dict(dtype=-1), DTYPE),
+    ])
+
+
+def test_logprob_top_gradient_against_differences():
+    g = torch.Generator().manual_seed(2)
+    rows, v, k, s = 3, 6, 2, 0.7
+    z, dh, da = (torch.randn(*n, generator=g, dtype=torch.float64) for n in ((rows, v), (rows,), (rows, k)))
+    dl, t = torch.randn(rows, generator=g, dtype=torch.float64), torch.tensor([0, 5, -100])
+    f, _ = R.logprob_top(z, t, k, s)
+    ids = f["ids"].clone()
+    ids[1] = torch.tensor([5, -1])
+
+    def loss(z):
+        lp = torch.log_softmax(s * z, -1)
+        h = -(lp.exp() * lp).sum(-1)
+        top = torch.where(ids >= 0, lp.gather(1, ids.clamp(0)), 0.0)
+        return ((lp.gather(1, t.clamp(0)[:, None])[:, 0] * dl + h * dh + (top * da).sum(1)) * (t >= 0)).sum()
+
+    dz, _ = R.logprob_top_grad(z, t, f["stats"], f["entropy"], ids, dl, dh, da, s)
+    differences(loss, z, dz, 1e-8)
+    assert not dz[2].any()
+
+
+def test_logprob_top_definition_by_hand():
+    z = torch.tensor([[1.0, 3.0, -float("inf"), 3.0, 0.0], [0.0] * 5, [-float("inf")] * 5])
+    f, _ = R.logprob_top(z, torch.tensor([3, 9, 0]), 5)
+    assert f["ids"].tolist() == [[1, 3, 0, 4, -1], [-1] * 5, [-1] * 5]
+    d = 2 + torch.tensor(-2.0, dtype=torch.float64).exp() + torch.tensor(-3.0, dtype=torch.float64).exp()
+    assert abs(float(f["logp"][0] + d.log())) < 1e-14 and f["logp"][1] == 0 and f["logp"][2] == -float("inf")
+    assert f["top"][0, 4] == -float("inf") and not f["top"][1].any()
+
+
+def test_logprob_top_refusals(lib):
+    good = dict(z=A, ldz=64, t=2 * A, logp=3 * A, ent=4 * A, ids=5 * A, top=6 * A, st=7 * A, rows=4, V=64, k=5, s=1.0, dtype=2,
+                stream=None)
+    _bad(lib, "logprob_top_fwd_ld", good, [
+        (dict(), (OK, DEVICE)), (dict(logp=None, ent=None, st=None), (OK, DEVICE)), (dict(k=0, ids=None, top=None), (OK, DEVICE)),
+        (dict(k=32), (OK, DEVICE)), (dict(V=3, ldz=3), (OK, DEVICE)), (dict(rows=0, z=None), OK), (dict(z=None), NULL),
+        (dict(t=None), NULL), (dict(ids=None), NULL), (dict(top=None), NULL), (dict(k=0, logp=None, ent=None, st=None), NULL),
+        (dict(k=33), UNSUP), (dict(k=-1), SHAPE), (dict(V=0), SHAPE), (dict(V=2 ** 31, ldz=2 ** 31), SHAPE), (dict(ldz=63), SHAPE),
+        (dict(s=0.0), VALUE), (dict(s=float("nan")), VALUE), (dict(s=3e38), VALUE), (dict(ids=5 * A + 4), VALUE),
+        (dict(st=7 * A + 2), VALUE), (dict(z=A + 1), VALUE), (dict(dtype=4), DTYPE), (dict(ids=A), ALIAS), (dict(top=5 * A), ALIAS),
+        (dict(ent=2 * A), ALIAS), (dict(st=3 * A), ALIAS),
+    ])
+    good = dict(g=A, h=2 * A, a=3 * A, z=4 * A, ldz=64, t=5 * A, st=6 * A, ent=7 * A, ids=8 * A, dz=9 * A, lddz=64, rows=4, V=64,
+                k=5, s=1.0, dtype=0, stream=None)
+    _bad(lib, "logprob_top_bwd_ld", good, [
+        (dict(), (OK, DEVICE)), (dict(dz=4 * A), (OK, DEVICE)), (dict(g=None, h=None, ent=None), (OK, DEVICE)),
+        (dict(a=None, ids=None), (OK, DEVICE)), (dict(k=0, a=None, ids=None), (OK, DEVICE)), (dict(rows=0, dz=None), OK),
+        (dict(g=None, h=None, a=None), NULL), (dict(ent=None), NULL), (dict(ids=None), NULL), (dict(st=None), NULL),
+        (dict(z=None), NULL), (dict(t=None), NULL), (dict(dz=None), NULL), (dict(k=0, g=None, h=None), NULL), (dict(k=33), UNSUP),
+        (dict(k=-1), SHAPE), (dict(lddz=63), SHAPE), (dict(dz=4 * A, lddz=65), ALIAS), (dict(dz=8 * A), ALIAS), (dict(dz=7 * A), ALIAS),
+        (dict(dz=3 * A), ALIAS), (dict(st=6 * A + 2), VALUE), (dict(ids=8 * A + 4), VALUE), (dict(s=-1.0), VALUE), (dict(dtype=3), DTYPE),
+    ])
