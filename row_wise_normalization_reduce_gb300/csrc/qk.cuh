@@ -30,19 +30,38 @@
 
 namespace nrm {
 
-// VE consecutive values in one access of 2 to 16 bytes, aligned to its size.
+// VE consecutive values in one access of 2 to 16 bytes, aligned to its size; in
+// registers as H pairs for the packed binary32 arithmetic (VE = 1: the second of
+// the pair is 0).
 template <int BYTES> struct RawOf;
 template <> struct RawOf<16> { using type = uint4; };
 template <> struct RawOf<8> { using type = uint2; };
 template <> struct RawOf<4> { using type = uint32_t; };
 template <> struct RawOf<2> { using type = unsigned short; };
+template <typename T> struct Two16;
+template <> struct Two16<__half> {
+    __device__ __forceinline__ static float2 wide(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
+    __device__ __forceinline__ static uint32_t narrow(float2 v) {
+        const __half2 h = __float22half2_rn(v);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+template <> struct Two16<__nv_bfloat16> {
+    __device__ __forceinline__ static float2 wide(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ static uint32_t narrow(float2 v) {
+        const __nv_bfloat162 h = __float22bfloat162_rn(v);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
 
 template <typename T, int VE> struct Pk {
-    static constexpr int BYTES = VE * (int)sizeof(T);
+    static constexpr int BYTES = VE * (int)sizeof(T), H = VE > 1 ? VE / 2 : 1;
     using Raw = typename RawOf<BYTES>::type;
     union Words {
         Raw r;
-        T t[VE];
+        uint32_t w[BYTES >= 4 ? BYTES / 4 : 1];
         __device__ __forceinline__ Words() {}
     };
     // coherent: an output may replace its input in place
@@ -50,24 +69,50 @@ template <typename T, int VE> struct Pk {
         if constexpr (BYTES == 16) return ld_once(p);
         return *reinterpret_cast<const Raw *>(p);
     }
-    __device__ __forceinline__ static void store(T *p, const float *f) {
-        Words w;
+    __device__ __forceinline__ static void store(T *p, const float2 *f) {
+        if constexpr (VE == 1) {
+            *p = IO<T>::from_f(f[0].x);
+        } else {
+            Words w;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) w.t[i] = IO<T>::from_f(f[i]);
-        if constexpr (BYTES == 16) st_stream(p, w.r);
-        else *reinterpret_cast<Raw *>(p) = w.r;
+            for (int i = 0; i < H; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w.w[2 * i] = __float_as_uint(f[i].x);
+                    w.w[2 * i + 1] = __float_as_uint(f[i].y);
+                } else {
+                    w.w[i] = Two16<T>::narrow(f[i]);
+                }
+            }
+            if constexpr (BYTES == 16) st_stream(p, w.r);
+            else *reinterpret_cast<Raw *>(p) = w.r;
+        }
     }
-    __device__ __forceinline__ static void unpack(const Raw &r, float *f) {
-        Words w;
-        w.r = r;
+    __device__ __forceinline__ static void unpack(const Raw &r, float2 *f) {
+        if constexpr (VE == 1) {
+            f[0] = make_float2(IO<T>::to_f(*reinterpret_cast<const T *>(&r)), 0.f);
+        } else {
+            Words w;
+            w.r = r;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) f[i] = IO<T>::to_f(w.t[i]);
+            for (int i = 0; i < H; ++i) {
+                if constexpr (sizeof(T) == 4) f[i] = make_float2(__uint_as_float(w.w[2 * i]), __uint_as_float(w.w[2 * i + 1]));
+                else f[i] = Two16<T>::wide(w.w[i]);
+            }
+        }
     }
     __device__ __forceinline__ static Raw all(float v) {
-        Words w;
+        if constexpr (VE == 1) {
+            const T t = IO<T>::from_f(v);
+            return *reinterpret_cast<const Raw *>(&t);
+        } else {
+            Words w;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) w.t[i] = IO<T>::from_f(v);
-        return w.r;
+            for (int i = 0; i < BYTES / 4; ++i) {
+                if constexpr (sizeof(T) == 4) w.w[i] = __float_as_uint(v);
+                else w.w[i] = Two16<T>::narrow(f2(v));
+            }
+            return w.r;
+        }
     }
 };
 
@@ -96,15 +141,15 @@ template <int N> __device__ __forceinline__ void ld_angles(const float *p, float
 //           with packs of one entry); the entries that do not turn fill the
 //           slots behind
 //   else    the pairs are neighbours inside a pack
-// Offsets of packs the row does not have are -1; angle -1 does not turn.
-template <int VE, int PP, bool CROSS> struct Slots {
+// Offsets of packs the row does not have are -1; with FULL it has them all.
+template <int VE, int PP, bool CROSS, bool FULL> struct Slots {
     int a[PP], b[PP];
     __device__ __forceinline__ Slots(int l, int lanes, const QkArgs &q) {
         const int D = q.D, half = q.half;
 #pragma unroll
         for (int p = 0; p < PP; ++p) {
             const int j = l + p * lanes;
-            if (CROSS && q.near) {  // VE = 1
+            if (CROSS && VE == 1 && q.near) {
                 a[p] = 2 * j < D ? 2 * j : -1;
                 b[p] = 2 * j + 1 < D ? 2 * j + 1 : -1;
             } else {
@@ -115,20 +160,32 @@ template <int VE, int PP, bool CROSS> struct Slots {
             }
         }
     }
-    // cosines and sines of one token; packs that do not turn get 1 and 0
-    __device__ __forceinline__ void angles(const QkArgs &q, int64_t pos, float (&c)[PP][VE], float (&s)[PP][VE]) const {
+    __device__ __forceinline__ bool has_a(int p) const { return FULL || a[p] >= 0; }
+    __device__ __forceinline__ bool has_b(int p) const { return FULL || b[p] >= 0; }
+    // Cosines and sines of one token; packs that do not turn get 1 and 0.  CROSS: one
+    // pair of numbers for two entries of a and of b; else the angles of a's pairs,
+    // then those of b's.
+    static constexpr int H = VE > 1 ? VE / 2 : 1;
+    __device__ __forceinline__ void angles(const QkArgs &q, int64_t pos, float2 (&c)[PP][H], float2 (&s)[PP][H]) const {
         const float *row = q.table + pos * (2 * q.half);
 #pragma unroll
         for (int p = 0; p < PP; ++p) {
+            float cc[2 * H], ss[2 * H];
+            cc[2 * H - 1] = ss[2 * H - 1] = 0.f;
             if constexpr (CROSS) {
                 // the pair's first entry is a: its angle is a's place among the
                 // first halves, or half its place among neighbours
-                const int at = q.near ? a[p] >> 1 : a[p];
-                const bool on = a[p] >= 0 && b[p] >= 0 && at < q.half;
-                get<VE>(row, at, on, q.half, c[p], s[p]);
+                const int at = VE == 1 && q.near ? a[p] >> 1 : a[p];
+                const bool on = has_a(p) && has_b(p) && at < q.half;
+                get<VE>(row, at, on, q.half, cc, ss);
             } else {
-                get<VE / 2>(row, a[p] / 2, a[p] >= 0 && a[p] < 2 * q.half, q.half, c[p], s[p]);
-                get<VE / 2>(row, b[p] / 2, b[p] >= 0 && b[p] < 2 * q.half, q.half, c[p] + VE / 2, s[p] + VE / 2);
+                get<VE / 2>(row, a[p] / 2, has_a(p) && a[p] < 2 * q.half, q.half, cc, ss);
+                get<VE / 2>(row, b[p] / 2, has_b(p) && b[p] < 2 * q.half, q.half, cc + VE / 2, ss + VE / 2);
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                c[p][i] = make_float2(cc[2 * i], cc[2 * i + 1]);
+                s[p][i] = make_float2(ss[2 * i], ss[2 * i + 1]);
             }
         }
     }
@@ -147,256 +204,317 @@ template <int VE, int PP, bool CROSS> struct Slots {
     }
 };
 
-// Turn a slot by its angles (sign = 1) or back (sign = -1).
-template <int VE, bool CROSS>
-__device__ __forceinline__ void turn(float *a, float *b, const float *c, const float *s, float sign) {
+// Turn a slot by its angles, or (BACK) by the negative ones.
+template <int VE, bool CROSS, bool BACK>
+__device__ __forceinline__ void turn(float2 *a, float2 *b, const float2 *c, const float2 *s) {
+    constexpr int H = VE > 1 ? VE / 2 : 1;
     if constexpr (CROSS) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            const float t = sign * s[i], x = a[i], y = b[i];
-            a[i] = fmaf(x, c[i], -(y * t));
-            b[i] = fmaf(y, c[i], x * t);
+        for (int i = 0; i < H; ++i) {
+            const float2 x = a[i], y = b[i], n = make_float2(-s[i].x, -s[i].y);
+            a[i] = __ffma2_rn(x, c[i], __fmul2_rn(y, BACK ? s[i] : n));
+            b[i] = __ffma2_rn(y, c[i], __fmul2_rn(x, BACK ? n : s[i]));
         }
     } else {
+        auto one = [](float2 &v, float c, float s) {
+            const float x = v.x, y = v.y, t = BACK ? -s : s;
+            v.x = fmaf(x, c, -(y * t));
+            v.y = fmaf(y, c, x * t);
+        };
+        // angle i of a slot is half a pair of numbers: a's come first
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) {
-            const float t = sign * s[i], x = a[2 * i], y = a[2 * i + 1];
-            a[2 * i] = fmaf(x, c[i], -(y * t));
-            a[2 * i + 1] = fmaf(y, c[i], x * t);
-            const float u = sign * s[VE / 2 + i], z = b[2 * i], w = b[2 * i + 1];
-            b[2 * i] = fmaf(z, c[VE / 2 + i], -(w * u));
-            b[2 * i + 1] = fmaf(w, c[VE / 2 + i], z * u);
+        for (int i = 0; i < H; ++i) {
+            const int k = i, m = H + i;
+            one(a[i], k % 2 ? c[k / 2].y : c[k / 2].x, k % 2 ? s[k / 2].y : s[k / 2].x);
+            one(b[i], m % 2 ? c[m / 2].y : c[m / 2].x, m % 2 ? s[m / 2].y : s[m / 2].x);
         }
     }
 }
 
 constexpr int kQkThreads = 256;
 
-// Forward.  One warp an item: `heads` heads of the queries or of the keys of one
-// token, 32 / lanes rows at a time, U such steps' loads in flight together.
-template <typename T, int VE, int PP, bool CROSS, int U>
-__global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const QkArgs q, const int log_lanes, const int heads,
-                                                            const int q_items, const int items) {
+// The heads [h0, h1) of one token and one side.
+struct QkItem {
+    int64_t token;
+    int h0, h1;
+};
+__device__ __forceinline__ QkItem qk_item(int64_t id, int64_t total, int items, int heads, int of) {
+    QkItem it;
+    it.token = total <= 0xffffffffll ? (int64_t)((uint32_t)id / (uint32_t)items) : id / items;
+    it.h0 = (int)(id - it.token * items) * heads;
+    it.h1 = min(it.h0 + heads, of);
+    return it;
+}
+
+// One row's packs of a lane, as they are in memory.
+template <typename T, int VE, int PP> struct QkRow {
+    typename Pk<T, VE>::Raw a[PP], b[PP];
+    template <typename S> __device__ __forceinline__ void load(const T *row, const S &at) {
+#pragma unroll
+        for (int p = 0; p < PP; ++p) {
+            if (at.has_a(p)) a[p] = Pk<T, VE>::load(row + at.a[p]);
+            else a[p] = Pk<T, VE>::all(0.f);
+            if (at.has_b(p)) b[p] = Pk<T, VE>::load(row + at.b[p]);
+            else b[p] = Pk<T, VE>::all(0.f);
+        }
+    }
+};
+template <typename T, int VE, int PP, typename S>
+__device__ __forceinline__ void qk_store(T *row, const S &at, const float2 (&a)[PP][Pk<T, VE>::H],
+                                         const float2 (&b)[PP][Pk<T, VE>::H]) {
+#pragma unroll
+    for (int p = 0; p < PP; ++p) {
+        if (at.has_a(p)) Pk<T, VE>::store(row + at.a[p], a[p]);
+        if (at.has_b(p)) Pk<T, VE>::store(row + at.b[p], b[p]);
+    }
+}
+// Zeros for the rows h, h + R, .. below h1.
+template <typename T, int VE, int PP, typename S>
+__device__ __forceinline__ void qk_zeros(T *out, int64_t stride, int h, int h1, int R, const S &at) {
+    float2 zero[PP][Pk<T, VE>::H];
+#pragma unroll
+    for (int p = 0; p < PP; ++p)
+#pragma unroll
+        for (int i = 0; i < Pk<T, VE>::H; ++i) zero[p][i] = f2(0.f);
+    for (; h < h1; h += R) qk_store<T, VE, PP>(out + h * stride, at, zero, zero);
+}
+// The weights of a lane's entries (none: ones).
+template <typename T, int VE, int PP, typename S>
+__device__ __forceinline__ void qk_weights(const void *w, const S &at, QkRow<T, VE, PP> &r) {
+#pragma unroll
+    for (int p = 0; p < PP; ++p) r.a[p] = r.b[p] = Pk<T, VE>::all(1.f);
+    if (w) r.load(static_cast<const T *>(w), at);
+}
+// Sum over the lanes of a row: 2^LL of them, or (LL < 0) `lanes`.
+template <int LL> __device__ __forceinline__ float qk_sum(float v, int lanes) {
+    if constexpr (LL >= 0) {
+        return group_sum_all<1 << (LL > 0 ? LL : 0)>(v);
+    } else {
+        for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+}
+
+// Rows a lane has on its way at once, forward.  With 80 registers and three CTAs
+// an SM two rows are ahead of four with 108 and two (16384 x 40 x 128 bf16 58.8 us
+// and 59.8, f32 8192 x 20 x 128 27.0 and 29.7); pairs inside a pack need more
+// registers, there four rows are (8192 x 32 x 128 24.2 us and 26.5).
+template <int VE, int PP, bool CROSS, int ES>
+constexpr int kQkFwdRows = CROSS || PP > 1 || VE * ES > 16 || ES == 4 ? 2 : 4;
+
+// Forward.  One warp an item of U times 32 / lanes rows, all of whose loads are in
+// flight together.  LL >= 0: every lane of 2^LL has its two packs.
+template <typename T, int VE, int PP, bool CROSS, int LL, int U>
+__global__ void __launch_bounds__(kQkThreads, PP > 1 ? 1 : CROSS || sizeof(T) == 4 ? 3 : 2) qk_fwd_kernel(const QkArgs q, const int log_lanes,
+                                                                             const int q_items, const int items) {
     using P = Pk<T, VE>;
-    const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, l = lane & (lanes - 1), sub = lane >> log_lanes,
-              R = 32 >> log_lanes;
-    const Slots<VE, PP, CROSS> at(l, lanes, q);
+    constexpr int H = P::H;
+    const int lane = threadIdx.x & 31, lanes = LL >= 0 ? 1 << (LL > 0 ? LL : 0) : 1 << log_lanes, l = lane & (lanes - 1),
+              sub = lane / lanes, R = 32 / lanes;
+    const Slots<VE, PP, CROSS, (LL >= 0)> at(l, lanes, q);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t total = q.tokens * items, step = (int64_t)gridDim.x * (kQkThreads / 32);
     for (int64_t id = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5); id < total; id += step) {
-        const int64_t token = total <= 0xffffffffll ? (int64_t)((uint32_t)id / (uint32_t)items) : id / items;
-        const int item = (int)(id - token * items);
-        const bool keys = item >= q_items;
+        QkItem it = qk_item(id, total, items, R * U, 0);
+        const bool keys = it.h0 >= q_items * (R * U);
         const QkSide &sd = q.side[keys];
-        const int h0 = (keys ? item - q_items : item) * heads, h1 = min(h0 + heads, sd.heads);
-        const int64_t pos = q.pos[token];
-        const bool live = pos >= 0 && pos < q.max_pos;
-        const T *x = static_cast<const T *>(sd.x) + token * sd.xt;
-        T *out = static_cast<T *>(sd.out) + token * sd.ot;
-        const T *w = static_cast<const T *>(sd.w);
-        typename P::Raw wa[PP], wb[PP];
-        float c[PP][VE], s[PP][VE];
-        if (live) {
-            at.angles(q, pos, c, s);
+        if (keys) it.h0 -= q_items * (R * U);
+        it.h1 = min(it.h0 + R * U, sd.heads);
+        const int64_t pos = q.pos[it.token];
+        const T *x = static_cast<const T *>(sd.x) + it.token * sd.xt + (it.h0 + sub) * sd.xh;
+        T *out = static_cast<T *>(sd.out) + it.token * sd.ot + (it.h0 + sub) * sd.oh;
+        if (pos < 0 || pos >= q.max_pos) {
+            qk_zeros<T, VE, PP>(out - (it.h0 + sub) * sd.oh, sd.oh, it.h0 + sub, it.h1, R, at);
+            continue;
+        }
+        const int n = it.h1 - it.h0;  // rows
+        QkRow<T, VE, PP> rows[U], w;
 #pragma unroll
-            for (int p = 0; p < PP; ++p) {
-                wa[p] = w && at.a[p] >= 0 ? P::load(w + at.a[p]) : P::all(1.f);
-                wb[p] = w && at.b[p] >= 0 ? P::load(w + at.b[p]) : P::all(1.f);
+        for (int u = 0; u < U; ++u)
+            // a row past the last is not loaded, and counts nowhere
+            if (u * R + sub < n) rows[u].load(x + u * R * sd.xh, at);
+        float2 c[PP][H], s[PP][H];
+        at.angles(q, pos, c, s);
+        qk_weights<T, VE, PP>(sd.w, at, w);
+        // Weights and angles in one: with ca = w_a c, sb = w_b s, cb = w_b c, sa =
+        // w_a s a row turns as r (a ca - b sb), r (b cb + a sa).  Pairs inside a pack
+        // take them one after the other.
+        float2 wa[PP][H], wb[PP][H], sa[PP][H], sb[PP][H];
+#pragma unroll
+        for (int p = 0; p < PP; ++p) {
+            P::unpack(w.a[p], wa[p]);
+            P::unpack(w.b[p], wb[p]);
+            if constexpr (CROSS) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    sa[p][i] = __fmul2_rn(wa[p][i], s[p][i]);
+                    sb[p][i] = __fmul2_rn(wb[p][i], make_float2(-s[p][i].x, -s[p][i].y));
+                    wa[p][i] = __fmul2_rn(wa[p][i], c[p][i]);
+                    wb[p][i] = __fmul2_rn(wb[p][i], c[p][i]);
+                }
             }
         }
-        for (int hb = h0; hb < h1; hb += R * U) {
-            typename P::Raw ra[U][PP], rb[U][PP];
-            if (live) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = hb + u * R + sub;
-                    const T *row = x + h * sd.xh;
+        for (int u = 0; u < U; ++u) {
+            if (u * R >= n) break;
+            float2 a[PP][H], b[PP][H], ss = f2(0.f);
 #pragma unroll
-                    for (int p = 0; p < PP; ++p) {
-                        ra[u][p] = rb[u][p] = P::all(0.f);
-                        if (h < h1 && at.a[p] >= 0) ra[u][p] = P::load(row + at.a[p]);
-                        if (h < h1 && at.b[p] >= 0) rb[u][p] = P::load(row + at.b[p]);
-                    }
-                }
+            for (int p = 0; p < PP; ++p) {
+                P::unpack(rows[u].a[p], a[p]);
+                P::unpack(rows[u].b[p], b[p]);
+#pragma unroll
+                for (int i = 0; i < H; ++i) ss = __ffma2_rn(a[p][i], a[p][i], __ffma2_rn(b[p][i], b[p][i], ss));
             }
+            const float2 r = f2(rsqrtf(fmaf(qk_sum<LL>(ss.x + ss.y, lanes), q.invD, q.eps)));
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = hb + u * R + sub;
-                T *row = out + h * sd.oh;
-                float a[PP][VE], b[PP][VE], ss = 0.f;
-                if (live) {
+            for (int p = 0; p < PP; ++p) {
 #pragma unroll
-                    for (int p = 0; p < PP; ++p) {
-                        P::unpack(ra[u][p], a[p]);
-                        P::unpack(rb[u][p], b[p]);
-#pragma unroll
-                        for (int i = 0; i < VE; ++i) ss = fmaf(a[p][i], a[p][i], fmaf(b[p][i], b[p][i], ss));
+                for (int i = 0; i < H; ++i) {
+                    const float2 x = __fmul2_rn(a[p][i], r), y = __fmul2_rn(b[p][i], r);
+                    if constexpr (CROSS) {
+                        a[p][i] = __ffma2_rn(x, wa[p][i], __fmul2_rn(y, sb[p][i]));
+                        b[p][i] = __ffma2_rn(y, wb[p][i], __fmul2_rn(x, sa[p][i]));
+                    } else {
+                        a[p][i] = __fmul2_rn(x, wa[p][i]);
+                        b[p][i] = __fmul2_rn(y, wb[p][i]);
                     }
-                    for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float r = rsqrtf(fmaf(ss, q.invD, q.eps));
-#pragma unroll
-                    for (int p = 0; p < PP; ++p) {
-                        float wf[VE];
-                        P::unpack(wa[p], wf);
-#pragma unroll
-                        for (int i = 0; i < VE; ++i) a[p][i] = a[p][i] * r * wf[i];
-                        P::unpack(wb[p], wf);
-#pragma unroll
-                        for (int i = 0; i < VE; ++i) b[p][i] = b[p][i] * r * wf[i];
-                        turn<VE, CROSS>(a[p], b[p], c[p], s[p], 1.f);
-                    }
-                } else {
-#pragma unroll
-                    for (int p = 0; p < PP; ++p)
-#pragma unroll
-                        for (int i = 0; i < VE; ++i) a[p][i] = b[p][i] = 0.f;
                 }
-#pragma unroll
-                for (int p = 0; p < PP; ++p) {
-                    if (h < h1 && at.a[p] >= 0) P::store(row + at.a[p], a[p]);
-                    if (h < h1 && at.b[p] >= 0) P::store(row + at.b[p], b[p]);
-                }
+                if constexpr (!CROSS) turn<VE, CROSS, false>(a[p], b[p], c[p], s[p]);
             }
+            if (u * R + sub < n) qk_store<T, VE, PP>(out + u * R * sd.oh, at, a, b);
         }
     }
 }
 
 // Backward.  The grid is resident at once; every warp goes over a share of the
-// queries' items, then of the keys', with the weight's gradient of its entries
-// in registers, which the CTA joins (rows of a warp by shuffles, warps in
-// shared memory, both in a fixed order) and leaves as one partial row for each
-// of the two, [CTA][2][D]; qk_fold_kernel adds those up.
-template <typename T, int VE, int PP, bool CROSS, int U>
-__global__ void __launch_bounds__(kQkThreads) qk_bwd_kernel(const QkArgs q, const int log_lanes, const int heads) {
+// queries' items, then of the keys', a row a lane group at a time, the next one's
+// packs on their way, with the weight's gradient of its entries in registers.
+// The CTA joins those (rows of a warp by shuffles, warps in shared memory, both
+// in a fixed order) and leaves one partial row for each of the two, [CTA][2][D];
+// qk_fold_kernel adds those up.
+template <typename T, int VE, int PP, bool CROSS, int LL>
+__global__ void __launch_bounds__(kQkThreads, PP > 1 ? 1 : 2) qk_bwd_kernel(const QkArgs q, const int log_lanes,
+                                                                             const int heads_q, const int heads_k) {
     using P = Pk<T, VE>;
-    constexpr int NW = kQkThreads / 32;
+    constexpr int NW = kQkThreads / 32, H = P::H;
     extern __shared__ float join[];  // [NW][D]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = 1 << log_lanes, l = lane & (lanes - 1),
-              sub = lane >> log_lanes, R = 32 >> log_lanes;
-    const Slots<VE, PP, CROSS> at(l, lanes, q);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5,
+              lanes = LL >= 0 ? 1 << (LL > 0 ? LL : 0) : 1 << log_lanes, l = lane & (lanes - 1), sub = lane / lanes,
+              R = 32 / lanes;
+    const Slots<VE, PP, CROSS, (LL >= 0)> at(l, lanes, q);
     pdl_wait();
     pdl_launch_dependents();
+    const int64_t step = (int64_t)gridDim.x * NW;
+    int64_t id = (int64_t)blockIdx.x * NW + warp;
     for (int keys = 0; keys < 2; ++keys) {
         const QkSide &sd = q.side[keys];
-        if (sd.heads == 0) continue;
-        const int items = (sd.heads + heads - 1) / heads;
-        const T *w = static_cast<const T *>(sd.w);
-        typename P::Raw wa[PP], wb[PP];
-        float dwa[PP][VE], dwb[PP][VE];
+        if (sd.heads == 0) break;
+        const int heads = keys ? heads_k : heads_q, items = (sd.heads + heads - 1) / heads;
+        const int64_t total = q.tokens * items;
+        QkRow<T, VE, PP> w;
+        qk_weights<T, VE, PP>(sd.w, at, w);
+        float2 dwa[PP][H], dwb[PP][H];
 #pragma unroll
-        for (int p = 0; p < PP; ++p) {
-            wa[p] = w && at.a[p] >= 0 ? P::load(w + at.a[p]) : P::all(1.f);
-            wb[p] = w && at.b[p] >= 0 ? P::load(w + at.b[p]) : P::all(1.f);
+        for (int p = 0; p < PP; ++p)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) dwa[p][i] = dwb[p][i] = 0.f;
-        }
-        const int64_t total = q.tokens * items, step = (int64_t)gridDim.x * NW;
-        for (int64_t id = (int64_t)warp * gridDim.x + blockIdx.x; id < total; id += step) {
-            const int64_t token = total <= 0xffffffffll ? (int64_t)((uint32_t)id / (uint32_t)items) : id / items;
-            const int h0 = (int)(id - token * items) * heads, h1 = min(h0 + heads, sd.heads);
-            const int64_t pos = q.pos[token];
-            const bool live = pos >= 0 && pos < q.max_pos;
-            const T *x = static_cast<const T *>(sd.x) + token * sd.xt, *dy = static_cast<const T *>(sd.dy) + token * sd.dt;
-            T *out = static_cast<T *>(sd.out) + token * sd.ot;
-            float c[PP][VE], s[PP][VE];
-            if (live) at.angles(q, pos, c, s);
-            for (int hb = h0; hb < h1; hb += R * U) {
-                typename P::Raw xa[U][PP], xb[U][PP], ga[U][PP], gb[U][PP];
-                if (live) {
+            for (int i = 0; i < H; ++i) dwa[p][i] = dwb[p][i] = f2(0.f);
+        // the next item whose token takes part (the others get their zeros); the
+        // position of the one after is on its way
+        auto token_at = [&](int64_t i) { return q.pos[qk_item(i, total, items, heads, 0).token]; };
+        int64_t coming = id < total ? token_at(id) : -1;
+        auto next_live = [&](QkItem &it, int64_t &pos) {
+            while (id < total) {
+                it = qk_item(id, total, items, heads, sd.heads);
+                pos = coming;
+                id += step;
+                if (id < total) coming = token_at(id);
+                if (pos >= 0 && pos < q.max_pos) return true;
+                qk_zeros<T, VE, PP>(static_cast<T *>(sd.out) + it.token * sd.ot, sd.oh, it.h0 + sub, it.h1, R, at);
+            }
+            return false;
+        };
+        QkItem it, next;
+        int64_t pos, pos_n;
+        QkRow<T, VE, PP> xr, gr;
+        float2 c[PP][H], s[PP][H];
+        auto load = [&](const QkItem &i, int h) {
+            if (h < i.h1) {
+                xr.load(static_cast<const T *>(sd.x) + i.token * sd.xt + h * sd.xh, at);
+                gr.load(static_cast<const T *>(sd.dy) + i.token * sd.dt + h * sd.dh, at);
+            }
+        };
+        if (next_live(it, pos)) {
+            load(it, it.h0 + sub);
+            at.angles(q, pos, c, s);
+            bool more = next_live(next, pos_n);
+            for (int hb = it.h0;;) {
+                const bool last = hb + R >= it.h1, on = hb + sub < it.h1;
+                float2 a[PP][H], b[PP][H], ua[PP][H], ub[PP][H], va[H], vb[H], ss = f2(0.f), ux = f2(0.f);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int h = hb + u * R + sub;
-                        const T *xr = x + h * sd.xh, *gr = dy + h * sd.dh;
+                for (int p = 0; p < PP; ++p) {
+                    P::unpack(xr.a[p], a[p]);
+                    P::unpack(xr.b[p], b[p]);
+                    P::unpack(gr.a[p], ua[p]);
+                    P::unpack(gr.b[p], ub[p]);
+                }
+                if (!last) load(it, hb + R + sub);
+                else if (more) load(next, next.h0 + sub);
 #pragma unroll
-                        for (int p = 0; p < PP; ++p) {
-                            xa[u][p] = xb[u][p] = ga[u][p] = gb[u][p] = P::all(0.f);
-                            if (h < h1 && at.a[p] >= 0) {
-                                xa[u][p] = P::load(xr + at.a[p]);
-                                ga[u][p] = P::load(gr + at.a[p]);
-                            }
-                            if (h < h1 && at.b[p] >= 0) {
-                                xb[u][p] = P::load(xr + at.b[p]);
-                                gb[u][p] = P::load(gr + at.b[p]);
-                            }
-                        }
+                for (int p = 0; p < PP; ++p) {
+                    turn<VE, CROSS, true>(ua[p], ub[p], c[p], s[p]);
+                    P::unpack(w.a[p], va);
+                    P::unpack(w.b[p], vb);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        ss = __ffma2_rn(a[p][i], a[p][i], __ffma2_rn(b[p][i], b[p][i], ss));
+                        ux = __ffma2_rn(__fmul2_rn(ua[p][i], va[i]), a[p][i],
+                                        __ffma2_rn(__fmul2_rn(ub[p][i], vb[i]), b[p][i], ux));
                     }
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = hb + u * R + sub;
-                    const bool on = h < h1;
-                    T *row = out + h * sd.oh;
-                    float a[PP][VE], b[PP][VE], ua[PP][VE], ub[PP][VE];
-                    if (live) {
-                        float ss = 0.f, ux = 0.f;
-#pragma unroll
-                        for (int p = 0; p < PP; ++p) {
-                            P::unpack(xa[u][p], a[p]);
-                            P::unpack(xb[u][p], b[p]);
-                            P::unpack(ga[u][p], ua[p]);
-                            P::unpack(gb[u][p], ub[p]);
-                            turn<VE, CROSS>(ua[p], ub[p], c[p], s[p], -1.f);
-                            float va[VE], vb[VE];
-                            P::unpack(wa[p], va);
-                            P::unpack(wb[p], vb);
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                ss = fmaf(a[p][i], a[p][i], fmaf(b[p][i], b[p][i], ss));
-                                ux = fmaf(ua[p][i] * va[i], a[p][i], fmaf(ub[p][i] * vb[i], b[p][i], ux));
-                            }
-                        }
-                        for (int o = lanes >> 1; o > 0; o >>= 1) {
-                            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                            ux += __shfl_xor_sync(0xffffffffu, ux, o);
-                        }
-                        const float r = rsqrtf(fmaf(ss, q.invD, q.eps));
-                        const float m = on ? r * (r * (ux * q.invD)) : 0.f;
-#pragma unroll
-                        for (int p = 0; p < PP; ++p) {
-                            float va[VE], vb[VE];
-                            P::unpack(wa[p], va);
-                            P::unpack(wb[p], vb);
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                // rows past the last are zeros with r = 1/sqrt(eps): no share
-                                if (on) {
-                                    dwa[p][i] = fmaf(ua[p][i], a[p][i] * r, dwa[p][i]);
-                                    dwb[p][i] = fmaf(ub[p][i], b[p][i] * r, dwb[p][i]);
-                                }
-                                a[p][i] = r * fmaf(ua[p][i], va[i], -(a[p][i] * m));
-                                b[p][i] = r * fmaf(ub[p][i], vb[i], -(b[p][i] * m));
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < PP; ++p)
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) a[p][i] = b[p][i] = 0.f;
-                    }
+                if (last && more) at.angles(q, pos_n, c, s);
+                const float sum = qk_sum<LL>(ss.x + ss.y, lanes), dot = qk_sum<LL>(ux.x + ux.y, lanes);
+                const float r = rsqrtf(fmaf(sum, q.invD, q.eps));
+                const float2 rr = f2(r), m = f2(-(r * (dot * q.invD)));
+                if (on) {
 #pragma unroll
                     for (int p = 0; p < PP; ++p) {
-                        if (on && at.a[p] >= 0) P::store(row + at.a[p], a[p]);
-                        if (on && at.b[p] >= 0) P::store(row + at.b[p], b[p]);
+                        P::unpack(w.a[p], va);
+                        P::unpack(w.b[p], vb);
+#pragma unroll
+                        for (int i = 0; i < H; ++i) {
+                            // x r, whose product with r mean(u x) is x r^2 mean(u x)
+                            const float2 ha = __fmul2_rn(a[p][i], rr), hb2 = __fmul2_rn(b[p][i], rr);
+                            dwa[p][i] = __ffma2_rn(ua[p][i], ha, dwa[p][i]);
+                            dwb[p][i] = __ffma2_rn(ub[p][i], hb2, dwb[p][i]);
+                            a[p][i] = __fmul2_rn(__ffma2_rn(ha, m, __fmul2_rn(ua[p][i], va[i])), rr);
+                            b[p][i] = __fmul2_rn(__ffma2_rn(hb2, m, __fmul2_rn(ub[p][i], vb[i])), rr);
+                        }
                     }
+                    qk_store<T, VE, PP>(static_cast<T *>(sd.out) + it.token * sd.ot + (hb + sub) * sd.oh, at, a, b);
+                }
+                hb += R;
+                if (last) {
+                    if (!more) break;
+                    it = next;
+                    hb = it.h0;
+                    more = next_live(next, pos_n);
                 }
             }
         }
+        id -= total;
         if (q.part) {
+            auto join_one = [&](float v, int i) {
+                for (int o = 16; o >= lanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (sub == 0 && i >= 0) join[warp * q.D + i] = v;
+            };
 #pragma unroll
-            for (int p = 0; p < PP; ++p) {
+            for (int p = 0; p < PP; ++p)
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    for (int o = 16; o >= lanes; o >>= 1) {
-                        dwa[p][i] += __shfl_xor_sync(0xffffffffu, dwa[p][i], o);
-                        dwb[p][i] += __shfl_xor_sync(0xffffffffu, dwb[p][i], o);
-                    }
-                    if (sub == 0) {
-                        if (at.a[p] >= 0) join[warp * q.D + at.a[p] + i] = dwa[p][i];
-                        if (at.b[p] >= 0) join[warp * q.D + at.b[p] + i] = dwb[p][i];
-                    }
+                    join_one(i % 2 ? dwa[p][i / 2].y : dwa[p][i / 2].x, at.has_a(p) ? at.a[p] + i : -1);
+                    join_one(i % 2 ? dwb[p][i / 2].y : dwb[p][i / 2].x, at.has_b(p) ? at.b[p] + i : -1);
                 }
-            }
             __syncthreads();
             for (int i = threadIdx.x; i < q.D; i += kQkThreads) {
                 float v = 0.f;
@@ -425,37 +543,55 @@ inline int qk_log_lanes(const QkArgs &q, int ve, int pp, bool cross) {
     return log;  // at most 5 by the choice of pp
 }
 
-template <typename T, int VE, int PP, bool CROSS>
-cudaError_t launch_qk_one(const QkArgs &q, bool back, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
-    const int log = qk_log_lanes(q, VE, PP, CROSS), R = 32 >> log;
-    constexpr int REG = VE * PP * (int)sizeof(T) / 16 > 0 ? VE * PP * (int)sizeof(T) / 16 : 1;  // 32-byte slots a row
+template <typename T, int VE, int PP, bool CROSS, int LL>
+cudaError_t launch_qk_one(const QkArgs &q, int log, bool back, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
+    const int R = 32 >> log;
     p->kind = PLAN_WARP;
     p->threads = kQkThreads;
     p->packs = VE;
     p->groups = 1 << log;
     if (!back) {
-        constexpr int U = REG > 1 ? 2 : 4;
+        constexpr int U = kQkFwdRows<VE, PP, CROSS, (int)sizeof(T)>;
         const int heads = R * U;
         const int q_items = (q.side[0].heads + heads - 1) / heads, items = q_items + (q.side[1].heads + heads - 1) / heads;
         const int64_t n = (q.tokens * items + kQkThreads / 32 - 1) / (kQkThreads / 32);
-        return launch_row(qk_fwd_kernel<T, VE, PP, CROSS, U>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff),
-                          (unsigned)kQkThreads, 0, s, q, log, heads, q_items, items);
+        return launch_row(qk_fwd_kernel<T, VE, PP, CROSS, LL, U>, (unsigned)(n < 0x7fffffff ? n : 0x7fffffff),
+                          (unsigned)kQkThreads, 0, s, q, log, q_items, items);
     }
-    constexpr int U = REG > 1 ? 1 : 2;
-    const int heads = R * U;
-    auto kernel = qk_bwd_kernel<T, VE, PP, CROSS, U>;
-    const size_t smem = (size_t)(kQkThreads / 32) * q.D * 4;
+    constexpr int NW = kQkThreads / 32;
+    auto kernel = qk_bwd_kernel<T, VE, PP, CROSS, LL>;
+    const size_t smem = (size_t)NW * q.D * 4;
     int per_sm = 0;
     const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), kQkThreads, smem, &per_sm);
     if (e != cudaSuccess) return e;
-    int64_t n = (int64_t)sms * per_sm;
-    const int most = q.side[0].heads > q.side[1].heads ? q.side[0].heads : q.side[1].heads;
-    const int64_t need = (q.tokens * ((most + heads - 1) / heads) + kQkThreads / 32 - 1) / (kQkThreads / 32);
-    if (n > need) n = need;
-    if (n > kDropMaxParts) n = kDropMaxParts;
-    if (n < 1) n = 1;
+    int64_t most = (int64_t)sms * per_sm;
+    if (most > kDropMaxParts) most = kDropMaxParts;
+    // heads an item: as many steps as leave every warp some items
+    auto heads = [&](int n) {
+        const int steps = (n + R - 1) / R;
+        int at_once = steps < 4 ? steps : 4;
+        while (at_once > 1 && q.tokens * ((steps + at_once - 1) / at_once) < most * NW * 4) at_once = (at_once + 1) / 2;
+        return at_once * R;
+    };
+    const int heads_q = heads(q.side[0].heads), heads_k = q.side[1].heads ? heads(q.side[1].heads) : 1;
+    const int64_t work = q.tokens * ((q.side[0].heads + heads_q - 1) / heads_q + (q.side[1].heads + heads_k - 1) / heads_k);
+    const int64_t need = (work + NW - 1) / NW, n = need < most ? need : most;
     *parts = n;
-    return launch_row(kernel, (unsigned)n, (unsigned)kQkThreads, smem, s, q, log, heads);
+    return launch_row(kernel, (unsigned)n, (unsigned)kQkThreads, smem, s, q, log, heads_q, heads_k);
+}
+
+// Rows whose packs fill a power of two of lanes have kernels of their own.
+template <typename T, int VE, int PP, bool CROSS>
+cudaError_t launch_qk_lanes(const QkArgs &q, bool back, int sms, cudaStream_t s, Plan *p, int64_t *parts) {
+    const int log = qk_log_lanes(q, VE, PP, CROSS);
+    const bool full = 2 * VE * PP << log == q.D && (!CROSS || !q.near) && (!CROSS || (q.D / VE - 2 * (q.half / VE)) % 2 == 0);
+    if constexpr (VE == IO<T>::V && PP == 1) {
+        constexpr int L = VE == 8 ? 2 : 3;  // D = 64, 128, 256
+        if (full && log == L) return launch_qk_one<T, VE, PP, CROSS, L>(q, log, back, sms, s, p, parts);
+        if (full && log == L + 1) return launch_qk_one<T, VE, PP, CROSS, L + 1>(q, log, back, sms, s, p, parts);
+        if (full && log == L + 2) return launch_qk_one<T, VE, PP, CROSS, L + 2>(q, log, back, sms, s, p, parts);
+    }
+    return launch_qk_one<T, VE, PP, CROSS, -1>(q, log, back, sms, s, p, parts);
 }
 
 // ve: the widest access that every row, weight and table row allows.  Rows of
@@ -465,25 +601,25 @@ cudaError_t launch_qk_t(const QkArgs &q, int ve, bool back, int sms, cudaStream_
     const bool wide = q.D > 64 * ve;  // more than 32 lanes of one slot
     if constexpr (IO<T>::V == 8) {
         if (ve == 8)
-            return q.near ? launch_qk_one<T, 8, 1, false>(q, back, sms, s, p, parts)
-                          : launch_qk_one<T, 8, 1, true>(q, back, sms, s, p, parts);
+            return q.near ? launch_qk_lanes<T, 8, 1, false>(q, back, sms, s, p, parts)
+                          : launch_qk_lanes<T, 8, 1, true>(q, back, sms, s, p, parts);
     }
     if (ve == 4) {
         if (q.near)
-            return wide ? launch_qk_one<T, 4, 2, false>(q, back, sms, s, p, parts)
-                        : launch_qk_one<T, 4, 1, false>(q, back, sms, s, p, parts);
-        return wide ? launch_qk_one<T, 4, 2, true>(q, back, sms, s, p, parts)
-                    : launch_qk_one<T, 4, 1, true>(q, back, sms, s, p, parts);
+            return wide ? launch_qk_lanes<T, 4, 2, false>(q, back, sms, s, p, parts)
+                        : launch_qk_lanes<T, 4, 1, false>(q, back, sms, s, p, parts);
+        return wide ? launch_qk_lanes<T, 4, 2, true>(q, back, sms, s, p, parts)
+                    : launch_qk_lanes<T, 4, 1, true>(q, back, sms, s, p, parts);
     }
     if (ve == 2) {
         if (q.near)
-            return wide ? launch_qk_one<T, 2, 4, false>(q, back, sms, s, p, parts)
-                        : launch_qk_one<T, 2, 1, false>(q, back, sms, s, p, parts);
-        return wide ? launch_qk_one<T, 2, 4, true>(q, back, sms, s, p, parts)
-                    : launch_qk_one<T, 2, 1, true>(q, back, sms, s, p, parts);
+            return wide ? launch_qk_lanes<T, 2, 4, false>(q, back, sms, s, p, parts)
+                        : launch_qk_lanes<T, 2, 1, false>(q, back, sms, s, p, parts);
+        return wide ? launch_qk_lanes<T, 2, 4, true>(q, back, sms, s, p, parts)
+                    : launch_qk_lanes<T, 2, 1, true>(q, back, sms, s, p, parts);
     }
-    return wide ? launch_qk_one<T, 1, 8, true>(q, back, sms, s, p, parts)
-                : launch_qk_one<T, 1, 1, true>(q, back, sms, s, p, parts);
+    return wide ? launch_qk_lanes<T, 1, 8, true>(q, back, sms, s, p, parts)
+                : launch_qk_lanes<T, 1, 1, true>(q, back, sms, s, p, parts);
 }
 
 }  // namespace nrm
