@@ -844,9 +844,11 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
 def _heads(t, shape, dtype, dev, name):
     """(token stride, head stride) of a tensor [..., heads, D] whose leading
     dimensions have one stride between tokens."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype} on device {dev}")
     st = t.stride()
+    if len(st) == 3 and st[2] == 1:
+        return st[0], st[1]
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"the entries of a head of {name} must be contiguous")
     step, n = None, 1
@@ -862,41 +864,35 @@ def _heads(t, shape, dtype, dev, name):
     return step or 0, st[-2]
 
 
-def _heads_out(t, shape, dtype, dev, device, name):
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-    return t, t.data_ptr(), *_heads(t, shape, dtype, dev, name)
-
-
-def _qk_inputs(q, k, table, positions, wq, wk):
-    """Checks of what both directions take.  Returns (shape of k or None, dtype,
-    device index, tokens, (q_heads, k_heads, D, rot, max_pos), [k and its strides])."""
+def _qk_sizes(q, k, table, positions, wq, wk):
+    """Checks of what both directions take.  Returns (shape of q, shape of k or None,
+    dtype code, dtype, device index, tokens, q_heads, k_heads, D, rot, max_pos)."""
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     if dev < 0:
         raise ValueError("q must be a CUDA tensor")
-    _code(dtype)
+    code = _code(dtype)
     if len(shape) < 2:
         raise ValueError("q must be [..., heads, D]")
-    lead, hq, d = shape[:-2], shape[-2], shape[-1]
-    tokens = lead.numel()
-    if positions.shape != lead:
-        raise ValueError(f"positions must be {tuple(lead)}")
-    _flat(positions, lead, torch.int64, dev, "positions")
-    if table.dim() != 2:
-        raise ValueError("table must be [positions, rotated entries]")
-    _flat(table, table.shape, _F32, dev, "table")
+    hq, d = shape[-2:]
+    lead = positions.shape
+    if lead != shape[:-2]:
+        raise ValueError(f"positions must be {tuple(shape[:-2])}")
+    if positions.dtype is not torch.int64 or positions.get_device() != dev or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous int64 tensor on device {dev}")
+    most = table.shape
+    if len(most) != 2 or table.dtype is not _F32 or table.get_device() != dev or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous [positions, rotated entries] float32 tensor on device {dev}")
     _weight(wq, d, dtype, dev, "wq")
-    if k is None:
-        if wk is not None:
-            raise ValueError("wk without k")
-        hk, kshape, kk = 0, None, (None, 0, 0)
-    else:
-        if k.dim() != len(shape) or k.shape[:-2] != lead or k.shape[-1] != d:
+    kshape, hk = None, 0
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != len(shape) or kshape[-1] != d or kshape[:-2] != lead:
             raise ValueError("k must be like q but for its heads")
-        hk, kshape = k.shape[-2], k.shape
-        kk = (k.data_ptr(), *_heads(k, kshape, dtype, dev, "k"))
+        hk = kshape[-2]
         _weight(wk, d, dtype, dev, "wk")
-    return kshape, dtype, dev, tokens, (hq, hk, d, table.shape[1], table.shape[0]), kk
+    elif wk is not None:
+        raise ValueError("wk without k")
+    return shape, kshape, code, dtype, dev, positions.numel(), hq, hk, d, most[1], most[0]
 
 
 def qk_norm_rope_fwd(q, k, table, positions, wq=None, wk=None, eps=1e-6, *, interleaved=False, q_out=None,
@@ -912,15 +908,27 @@ def qk_norm_rope_fwd(q, k, table, positions, wq=None, wk=None, eps=1e-6, *, inte
         with _on_stream(stream, q):
             return qk_norm_rope_fwd(q, k, table, positions, wq, wk, eps, interleaved=interleaved, q_out=q_out,
                                     k_out=k_out)
-    kshape, dtype, dev, tokens, sizes, kk = _qk_inputs(q, k, table, positions, wq, wk)
-    qs = _heads(q, q.shape, dtype, dev, "q")
-    q_out, *qo = _heads_out(q_out, q.shape, dtype, dev, q.device, "q_out")
-    if kshape is not None:
-        k_out, *ko = _heads_out(k_out, kshape, dtype, dev, q.device, "k_out")
+    shape, kshape, code, dtype, dev, tokens, hq, hk, d, rot, most = _qk_sizes(q, k, table, positions, wq, wk)
+    qt, qh = _heads(q, shape, dtype, dev, "q")
+    if q_out is None:
+        q_out, qot, qoh = torch.empty(shape, dtype=dtype, device=q.device), hq * d, d
     else:
-        k_out, ko = None, (None, 0, 0)
-    _launch("qk_norm_rope_fwd", dev, q.data_ptr(), *qs, *kk, table.data_ptr(), positions.data_ptr(), _ptr(wq), _ptr(wk),
-            *qo, *ko, tokens, *sizes, eps, 1 if interleaved else 0, _code(dtype))
+        qot, qoh = _heads(q_out, shape, dtype, dev, "q_out")
+    kp = kop = None
+    kt = kh = kot = koh = 0
+    if kshape is not None:
+        kp = k.data_ptr()
+        kt, kh = _heads(k, kshape, dtype, dev, "k")
+        if k_out is None:
+            k_out, kot, koh = torch.empty(kshape, dtype=dtype, device=q.device), hk * d, d
+        else:
+            kot, koh = _heads(k_out, kshape, dtype, dev, "k_out")
+        kop = k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _launch("qk_norm_rope_fwd", dev, q.data_ptr(), qt, qh, kp, kt, kh, table.data_ptr(), positions.data_ptr(),
+            None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), q_out.data_ptr(), qot, qoh, kop,
+            kot, koh, tokens, hq, hk, d, rot, most, eps, 1 if interleaved else 0, code)
     return q_out, k_out
 
 
@@ -939,32 +947,43 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, positions, wq=None, wk=None, e
         with _on_stream(stream, q):
             return qk_norm_rope_bwd(dq_out, dk_out, q, k, table, positions, wq, wk, eps, interleaved=interleaved, dq=dq,
                                     dk=dk, dwq=dwq, dwk=dwk, want_dw=want_dw, workspace=workspace)
-    kshape, dtype, dev, tokens, sizes, kk = _qk_inputs(q, k, table, positions, wq, wk)
-    d = sizes[2]
-    qs = _heads(q, q.shape, dtype, dev, "q")
-    dqs = _heads(dq_out, q.shape, dtype, dev, "dq_out")
-    dq, *dqo = _heads_out(dq, q.shape, dtype, dev, q.device, "dq")
-    if kshape is not None:
-        dks = (dk_out.data_ptr(), *_heads(dk_out, kshape, dtype, dev, "dk_out"))
-        dk, *dko = _heads_out(dk, kshape, dtype, dev, q.device, "dk")
+    shape, kshape, code, dtype, dev, tokens, hq, hk, d, rot, most = _qk_sizes(q, k, table, positions, wq, wk)
+    device = q.device
+    qt, qh = _heads(q, shape, dtype, dev, "q")
+    gqt, gqh = _heads(dq_out, shape, dtype, dev, "dq_out")
+    if dq is None:
+        dq, dqt, dqh = torch.empty(shape, dtype=dtype, device=device), hq * d, d
     else:
-        if dk_out is not None or dk is not None or dwk is not None:
-            raise ValueError("gradients of k without k")
-        dks, dko = (None, 0, 0), (None, 0, 0)
-    new_q = dwq is None and (want_dw if want_dw is not None else wq is not None)
-    new_k = kshape is not None and dwk is None and (want_dw if want_dw is not None else wk is not None)
-    _weight(dwq, d, _F32, dev, "dwq")
-    _weight(dwk, d, _F32, dev, "dwk")
-    if new_q or new_k:
-        both = torch.empty(2, d, dtype=_F32, device=q.device)
-        dwq = both[0] if new_q else dwq
-        dwk = both[1] if new_k else dwk
+        dqt, dqh = _heads(dq, shape, dtype, dev, "dq")
+    kp = gkp = dkp = None
+    kt = kh = gkt = gkh = dkt = dkh = 0
+    if kshape is not None:
+        kp, gkp = k.data_ptr(), dk_out.data_ptr()
+        kt, kh = _heads(k, kshape, dtype, dev, "k")
+        gkt, gkh = _heads(dk_out, kshape, dtype, dev, "dk_out")
+        if dk is None:
+            dk, dkt, dkh = torch.empty(kshape, dtype=dtype, device=device), hk * d, d
+        else:
+            dkt, dkh = _heads(dk, kshape, dtype, dev, "dk")
+        dkp = dk.data_ptr()
+    elif dk_out is not None or dk is not None or dwk is not None:
+        raise ValueError("gradients of k without k")
+    if dwq is not None:
+        _weight(dwq, d, _F32, dev, "dwq")
+    elif want_dw if want_dw is not None else wq is not None:
+        dwq = torch.empty(d, dtype=_F32, device=device)
+    if dwk is not None:
+        _weight(dwk, d, _F32, dev, "dwk")
+    elif kshape is not None and (want_dw if want_dw is not None else wk is not None):
+        dwk = torch.empty(d, dtype=_F32, device=device)
     ws, wsb = None, 0
     if dwq is not None or dwk is not None:
-        ws, wsb, workspace = _scratch_bytes(workspace, lib().qk_norm_rope_bwd_workspace_size(tokens, *sizes[:3]), q)
-    _launch("qk_norm_rope_bwd", dev, dq_out.data_ptr(), *dqs, *dks, q.data_ptr(), *qs, *kk, table.data_ptr(),
-            positions.data_ptr(), _ptr(wq), _ptr(wk), *dqo, *dko, _ptr(dwq), _ptr(dwk), tokens, *sizes, eps,
-            1 if interleaved else 0, _code(dtype), ws, wsb)
+        ws, wsb, workspace = _scratch_bytes(workspace, qk_norm_rope_bwd_workspace_size(tokens, hq, hk, d), q)
+    _launch("qk_norm_rope_bwd", dev, dq_out.data_ptr(), gqt, gqh, gkp, gkt, gkh, q.data_ptr(), qt, qh, kp, kt, kh,
+            table.data_ptr(), positions.data_ptr(), None if wq is None else wq.data_ptr(),
+            None if wk is None else wk.data_ptr(), dq.data_ptr(), dqt, dqh, dkp, dkt, dkh,
+            None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), tokens, hq, hk, d, rot, most,
+            eps, 1 if interleaved else 0, code, ws, wsb)
     return dq, dk, dwq, dwk
 
 
@@ -1058,13 +1077,13 @@ def logprob_top_fwd(logits, targets, k, inv_temp=1.0, *, logp=None, entropy=None
     shape, dev, device = logits.shape[:-1], logits.get_device(), logits.device
     code = _code(logits.dtype)
     _flat(targets, shape, torch.int64, dev, "targets")
-    logp = torch.empty_like(targets, dtype=_F32) if logp is None else _flat(logp, shape, _F32, dev, "logp")
-    entropy = torch.empty_like(targets, dtype=_F32) if entropy is None else _flat(entropy, shape, _F32, dev, "entropy")
     many, two = (*shape, k), (*shape, 2)
-    top_ids = torch.empty(many, dtype=torch.int64, device=device) if top_ids is None else _flat(
-        top_ids, many, torch.int64, dev, "top_ids")
-    top_logp = torch.empty(many, dtype=_F32, device=device) if top_logp is None else _flat(top_logp, many, _F32, dev, "top_logp")
-    stats = torch.empty(two, dtype=_F32, device=device) if stats is None else _flat(stats, two, _F32, dev, "stats")
+    empty = torch.empty
+    logp = empty(shape, dtype=_F32, device=device) if logp is None else _flat(logp, shape, _F32, dev, "logp")
+    entropy = empty(shape, dtype=_F32, device=device) if entropy is None else _flat(entropy, shape, _F32, dev, "entropy")
+    top_ids = empty(many, dtype=torch.int64, device=device) if top_ids is None else _flat(top_ids, many, torch.int64, dev, "top_ids")
+    top_logp = empty(many, dtype=_F32, device=device) if top_logp is None else _flat(top_logp, many, _F32, dev, "top_logp")
+    stats = empty(two, dtype=_F32, device=device) if stats is None else _flat(stats, two, _F32, dev, "stats")
     _launch("logprob_top_fwd_ld", dev, logits.data_ptr(), ldl, targets.data_ptr(), logp.data_ptr(), entropy.data_ptr(),
             top_ids.data_ptr(), top_logp.data_ptr(), stats.data_ptr(), rows, v, k, inv_temp, code)
     return logp, entropy, top_ids, top_logp, stats

@@ -15,9 +15,9 @@
 // redux.max over the lanes' heads.  The fixed point and binary32's own error can
 // put two experts in the wrong order only where their keys are a few steps
 // apart.  Such tokens are found afterwards by the gaps between neighbouring
-// places: the few experts in question are then compared in 64 bits, one a lane,
+// places: the few experts in question are then compared to 42 bits, one a lane,
 // and where a border between groups is that near the whole token is done again
-// in 64 bits.  Equal logits with equal biases are equal, not near.
+// so.  Equal logits with equal biases are equal, not near.
 //
 // Without a bias and without sums over two experts the order of c is that of x;
 // 16-bit logits then fit the key as they are and nothing is in question.
@@ -45,11 +45,6 @@ __device__ __forceinline__ uint32_t ordered32(float v) {
 __device__ __forceinline__ float from_ordered32(uint32_t u) {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
-__device__ __forceinline__ uint64_t ordered64(double v) {
-    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
-    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
-}
-
 // Descending order of N keys: K. E. Batcher's odd-even merge network.
 template <int N> __device__ __forceinline__ void sort_desc(uint32_t (&k)[N]) {
 #pragma unroll
@@ -112,70 +107,169 @@ __device__ __forceinline__ float route_rcp(float x) {
     return r;
 }
 
-__device__ __forceinline__ double warp_max64(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+// 1 / x, to a step, for x in [2^-100, 2^100].
+__device__ __forceinline__ float route_inv(float x) {
+    const float r = route_rcp(x);
+    return fmaf(r, fmaf(-x, r, 1.f), r);
 }
-__device__ __forceinline__ double warp_sum64(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// 1 / (1 + exp(-x)), to a few steps of 2^-24.
+__device__ __forceinline__ float route_sigmoid(float x) {
+    const float e = expf(-fabsf(x)), q = route_inv(1.f + e);
+    return x < 0.f ? e * q : q;
 }
 
-// A token's largest logit and the sum of exp(x - it), in 64 bits.
-template <typename T> __device__ __forceinline__ void route_softmax64(const RouteArgs &a, const T *row, int lane, double *m,
-                                                                      double *d) {
-    double top = -INFINITY, sum = 0.0;
-    for (int e = lane; e < a.experts; e += 32) top = fmax(top, (double)IO<T>::to_f(row[e]));
-    top = warp_max64(top);
-    for (int e = lane; e < a.experts; e += 32) sum += exp((double)IO<T>::to_f(row[e]) - top);
+// ---------------------------------------------------------------------------
+// What an expert is chosen by to some 42 bits, for choices that binary32 cannot
+// tell apart: as the unevaluated sum of two binary32 numbers.  (In binary64, of
+// which an SM adds two a cycle, one token of 256 experts held its warp for 30000
+// cycles, a fifth of the kernel.)  The products and sums are T. J. Dekker's and
+// D. E. Knuth's.
+// ---------------------------------------------------------------------------
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair pair_norm(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return Pair{s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair pair_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+    const Pair s = pair_sum(a.hi, b.hi), t = pair_sum(a.lo, b.lo);
+    const Pair u = pair_norm(s.hi, __fadd_rn(s.lo, t.hi));
+    return pair_norm(u.hi, __fadd_rn(u.lo, t.lo));
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    const float e = fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, __fmul_rn(a.lo, b.hi));
+    return pair_norm(p, e);
+}
+// 1 / a: a first quotient and one step of the remainder.
+__device__ __forceinline__ Pair pair_inv(Pair a) {
+    const float q = 1.f / a.hi, p = __fmul_rn(a.hi, q);
+    const float rest = __fsub_rn(__fsub_rn(__fsub_rn(1.f, p), fmaf(a.hi, q, -p)), __fmul_rn(a.lo, q));
+    return pair_norm(q, __fmul_rn(rest, q));
+}
+// exp(x) for x <= 0.  The reduction is W. J. Cody and W. Waite's ("Software Manual
+// for the Elementary Functions", 1980, EXP): x - n log 2 with log 2 = 355/512 + C,
+// the first product exact, C = -2.12194440054690583e-4 in two numbers.  Then the
+// Taylor series at an eighth of the rest, at most 0.044 (what comes after x^7 is
+// below 2^-47), in pairs up to x^4 and binary32 beyond (x^5 / 120 < 2^-29 and its
+// rounding 2^-53), and three squarings.
+__device__ __forceinline__ Pair pair_exp(Pair x) {
+    if (!(x.hi > -104.f)) return Pair{x.hi != x.hi ? x.hi : 0.f, 0.f};
+    const float n = rintf(x.hi * kRouteLog2e);
+    const float c = -2.12194440e-4f, c_rest = (float)(-2.12194440054690583e-4 - (double)-2.12194440e-4f);
+    const Pair nc{__fmul_rn(n, -c), fmaf(n, -c, -__fmul_rn(n, -c)) - n * c_rest};
+    Pair r = pair_add(pair_sum(fmaf(n, -355.f / 512.f, x.hi), x.lo), nc);
+    r.hi *= 0.125f;
+    r.lo *= 0.125f;
+    const float q = fmaf(r.hi, fmaf(r.hi, 1.f / 5040, 1.f / 720), 1.f / 120);
+    auto over = [](double v) { return Pair{(float)v, (float)(v - (double)(float)v)}; };
+    Pair s = pair_add(pair_mul(r, Pair{q, 0.f}), over(1.0 / 24));
+    s = pair_add(pair_mul(r, s), over(1.0 / 6));
+    s = pair_add(pair_mul(r, s), Pair{0.5f, 0.f});
+    s = pair_add(pair_mul(r, s), Pair{1.f, 0.f});
+    s = pair_add(pair_mul(r, s), Pair{1.f, 0.f});
+    s = pair_mul(s, s);
+    s = pair_mul(s, s);
+    s = pair_mul(s, s);
+    const float f = __int_as_float(((int)n / 2 + 127) << 23), h = __int_as_float(((int)n - (int)n / 2 + 127) << 23);
+    return Pair{s.hi * f * h, s.lo * f * h};  // 2^n, n >= -151, in two steps
+}
+// Order of pairs as that of integers: values first, then what they leave.
+__device__ __forceinline__ uint64_t ordered_pair(Pair v) {
+    if (!(fabsf(v.hi) < INFINITY)) v.lo = 0.f;
+    return (uint64_t)ordered32(v.hi) << 32 | ordered32(v.lo);
+}
+// A token's largest logit and 1 / the sum of exp(x - it).
+template <typename T>
+__device__ __forceinline__ void route_softmax_pair(const RouteArgs &a, const T *row, int lane, float *m, Pair *inv) {
+    float top = -INFINITY;
+    for (int e = lane; e < a.experts; e += 32) top = fmaxf(top, IO<T>::to_f(row[e]));
+    top = from_ordered32(__reduce_max_sync(0xffffffffu, ordered32(top)));
+    Pair sum{0.f, 0.f};
+    for (int e = lane; e < a.experts; e += 32) {
+        const float x = IO<T>::to_f(row[e]);
+        if (x > -INFINITY || x != x) sum = pair_add(sum, pair_exp(pair_sum(x, -top)));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum = pair_add(sum, Pair{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
     *m = top;
-    *d = warp_sum64(sum);
+    *inv = pair_inv(sum);
 }
-// What one expert is chosen by.
-__device__ __forceinline__ double route_choice64(const RouteArgs &a, float x, int e, double m, double d) {
-    const double s = a.softmax ? exp((double)x - m) / d : 1.0 / (1.0 + exp(-(double)x));
-    return x == -INFINITY ? -INFINITY : a.bias ? s + (double)a.bias[e] : s;
+// What one expert is chosen by; -inf where it is not available.
+__device__ __forceinline__ Pair route_choice(const RouteArgs &a, float x, int e, float m, Pair inv) {
+    const float b = a.bias ? a.bias[e] : 0.f;
+    if (x == -INFINITY || !(fabsf(b) < INFINITY)) return Pair{x == -INFINITY || b != b ? -INFINITY : b, 0.f};
+    Pair s;
+    if (a.softmax) {
+        s = pair_mul(pair_exp(pair_sum(x, -m)), inv);
+    } else {
+        const Pair z = pair_exp(Pair{-fabsf(x), 0.f});
+        s = pair_inv(pair_add(Pair{1.f, 0.f}, z));
+        if (x < 0.f) s = pair_mul(z, s);
+    }
+    s = pair_add(s, Pair{b, 0.f});
+    return s.hi != s.hi ? Pair{-INFINITY, 0.f} : s;
 }
 
-// The whole selection in 64 bits.  Lane r returns the expert at place r, or -1.
+// The whole selection by those.  Lane r returns the expert at place r, or -1.
 template <typename T, int PL>
 __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int lane) {
+    constexpr uint32_t ALL = 0xffffffffu;
     const RouteLane r(a, lane);
-    const uint64_t none = ordered64(-INFINITY);
-    double m = 0.0, d = 1.0;
-    if (a.softmax && a.by_score) route_softmax64(a, row, lane, &m, &d);
-    uint64_t key[PL];
-    double b1 = -INFINITY, b2 = -INFINITY;
+    const Pair no{-INFINITY, 0.f};
+    const uint64_t none = ordered_pair(no);
+    float m = 0.f;
+    Pair inv{1.f, 0.f};
+    if (a.softmax && a.by_score) route_softmax_pair(a, row, lane, &m, &inv);
+    uint64_t key[PL], k1 = none, k2 = none;
+    Pair b1 = no, b2 = no;  // the lane's two largest
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        double c = -INFINITY;
+        Pair c = no;
         if (i < r.n) {
             const float x = IO<T>::to_f(row[r.first + i]);
-            c = a.by_score ? route_choice64(a, x, r.first + i, m, d) : (double)x;
-            if (c != c) c = -INFINITY;
+            if (a.by_score) c = route_choice(a, x, r.first + i, m, inv);
+            else if (x > -INFINITY) c = Pair{x, 0.f};
         }
-        key[i] = ordered64(c);
-        if (c > b1) {
+        key[i] = ordered_pair(c);
+        if (key[i] > k1) {
             b2 = b1;
+            k2 = k1;
             b1 = c;
-        } else if (c > b2) {
+            k1 = key[i];
+        } else if (key[i] > k2) {
             b2 = c;
+            k2 = key[i];
         }
     }
     if (a.top_groups < a.groups) {
         const int lanes = 1 << a.log_lanes;
+        auto other = [&](Pair v, int o) { return Pair{__shfl_xor_sync(ALL, v.hi, o), __shfl_xor_sync(ALL, v.lo, o)}; };
         for (int o = 1; o < lanes; o <<= 1) {
-            const double c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
-            b2 = c1 > b1 ? fmax(b1, c2) : fmax(b2, c1);
-            b1 = fmax(b1, c1);
+            const Pair c1 = other(b1, o), c2 = other(b2, o);
+            const uint64_t j1 = __shfl_xor_sync(ALL, k1, o), j2 = __shfl_xor_sync(ALL, k2, o);
+            if (j1 > k1) {
+                b2 = j2 > k1 ? c2 : b1;
+                k2 = j2 > k1 ? j2 : k1;
+                b1 = c1;
+                k1 = j1;
+            } else if (j1 > k2) {
+                b2 = c1;
+                k2 = j1;
+            }
         }
-        const double worth = a.group_top > 1 && b2 > -INFINITY ? b1 + b2 : b1;
+        const bool two = a.group_top > 1 && k2 > none && fabsf(b1.hi) < INFINITY && fabsf(b2.hi) < INFINITY;
+        const uint64_t worth = ordered_pair(two ? pair_add(b1, b2) : b1);
         int rank = 0;
         const int g = lane >> a.log_lanes;
         for (int h = 0; h < a.groups; ++h) {
-            const double w = __shfl_sync(0xffffffffu, worth, h << a.log_lanes);
+            const uint64_t w = __shfl_sync(ALL, worth, h << a.log_lanes);
             if (w > worth || (w == worth && h < g)) ++rank;
         }
         if (rank >= a.top_groups) {
@@ -193,15 +287,11 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
                 best = key[i];
                 at = i;
             }
-        uint64_t top = best;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const uint64_t v = __shfl_xor_sync(0xffffffffu, top, o);
-            top = v > top ? v : top;
-        }
-        const uint32_t who = __ballot_sync(0xffffffffu, best == top && at >= 0);
+        const uint32_t hi = __reduce_max_sync(ALL, (uint32_t)(best >> 32));
+        const uint32_t lo = __reduce_max_sync(ALL, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        const uint32_t who = __ballot_sync(ALL, at >= 0 && best == ((uint64_t)hi << 32 | lo));
         if (!who) break;
-        const int src = __ffs(who) - 1, id = __shfl_sync(0xffffffffu, r.first + at, src);
+        const int src = __ffs(who) - 1, id = __shfl_sync(ALL, r.first + at, src);
         if (lane == p) mine = id;
         if (lane == src) {
 #pragma unroll
@@ -212,20 +302,94 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
     return mine;
 }
 
-template <typename T, int PL>
+// What the forward's keys are made of.
+//   WHOLE   16-bit logits as they are: nothing is in question
+//   LOGIT   binary32 logits in fixed point, up to 16 below the row's largest
+//   SCORE   score + bias in fixed point over the range that they can have, [least
+//           bias, 1 + largest bias]: one multiply-add from the score
+enum RouteKey { KEY_WHOLE, KEY_LOGIT, KEY_SCORE };
+
+// Places that may be in the wrong order: the experts around and on the border of
+// the k-th place, one a lane, compared as pairs.  `mine` is the key at this
+// lane's place, `list` the lane's remaining keys; returns false where there are
+// more of them than lanes.  Called by few tokens, so kept out of line.
+template <typename T, int PL, int LIST>
+__device__ __noinline__ bool route_resolve(const RouteArgs &a, const T *row, int lane, uint32_t mine, uint32_t last,
+                                           uint32_t (&list)[LIST + 1], int left, float near_, int *id, float *xs) {
+    constexpr uint32_t ALL = 0xffffffffu;
+    int places = a.k;
+    while (true) {
+        const uint32_t w = __reduce_max_sync(ALL, list[0]);
+        if (w == 0u || (float)((last >> kIdxBits) - (w >> kIdxBits)) > near_) break;
+        if (places == 32) return false;
+        if (lane == places) mine = w;
+        ++places;
+        if (list[0] == w) {
+#pragma unroll
+            for (int i = 0; i < LIST; ++i) list[i] = list[i + 1];
+            --left;
+        }
+        if (PL > LIST && __any_sync(ALL, left == 0)) return false;
+    }
+    const int e = mine ? kIdxMask - (int)(mine & kIdxMask) : -1;
+    const float x = e >= 0 ? IO<T>::to_f(row[e]) : -INFINITY;
+    float m = 0.f;
+    Pair inv{1.f, 0.f};
+    if (a.softmax && a.by_score) route_softmax_pair(a, row, lane, &m, &inv);
+    uint64_t key = 0;
+    if (e >= 0) key = ordered_pair(a.by_score ? route_choice(a, x, e, m, inv) : Pair{x, 0.f});
+    int rank = 0;
+    for (int p = 0; p < places; ++p) {
+        const uint64_t o = __shfl_sync(ALL, key, p);
+        const int oe = __shfl_sync(ALL, e, p);
+        rank += o > key || (o == key && oe < e);
+    }
+    // who has the rank of this lane?
+    int src = lane;
+    for (int p = 0; p < places; ++p)
+        if (__shfl_sync(ALL, rank, p) == lane) src = p;
+    *id = __shfl_sync(ALL, e, src);
+    *xs = __shfl_sync(ALL, x, src);
+    return true;
+}
+
+template <typename T, int PL, int MODE>
 __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArgs a) {
     constexpr int LIST = PL < 8 ? PL : 8;
     constexpr uint32_t ALL = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     const RouteLane r(a, lane);
     const bool limited = a.top_groups < a.groups;
-    // 16-bit logits that order by themselves go into the key whole
-    const bool whole = sizeof(T) == 2 && !a.by_score;
-    float bias[PL];
+    const int g = lane >> a.log_lanes;
+    // (expert's part of the key of slot i: first - i)
+    const uint32_t index = (uint32_t)(kIdxMask - r.first);
     pdl_wait();
     pdl_launch_dependents();
+    // SCORE: the fixed point's step is 1 / S, and bias i's part base[i]
+    float base[MODE == KEY_SCORE ? PL : 1], S = 262143.f, near_bias = 0.f;
+    bool odd_bias = false;  // infinite or NaN ones
+    if constexpr (MODE == KEY_SCORE) {
+        float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) bias[i] = a.bias && i < r.n ? a.bias[r.first + i] : 0.f;
+        for (int i = 0; i < PL; ++i) {
+            base[i] = i < r.n ? (a.bias ? a.bias[r.first + i] : 0.f) : -INFINITY;
+            if (fabsf(base[i]) < INFINITY) {
+                lo = fminf(lo, base[i]);
+                hi = fmaxf(hi, base[i]);
+            } else if (i < r.n) {
+                odd_bias = true;
+            }
+        }
+        odd_bias = __any_sync(ALL, odd_bias);
+        lo = from_ordered32(__reduce_min_sync(ALL, ordered32(lo)));
+        hi = from_ordered32(__reduce_max_sync(ALL, ordered32(hi)));
+        if (!(hi >= lo)) lo = hi = 0.f;  // no expert has a finite bias
+        S = 4194300.f / (1.f + (hi - lo));
+        // the rounding of base: half a step of its size, relative to 2^23
+        near_bias = 1.2e-7f * (fabsf(lo) + fabsf(hi)) * S + 1.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) base[i] = fmaf(base[i] - lo, S, 8388610.f);
+    }
     const int64_t step = (int64_t)gridDim.x * (kRouteThreads / 32);
     for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5); t < a.tokens; t += step) {
         const T *row = static_cast<const T *>(a.x) + t * a.ldx;
@@ -238,12 +402,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
 #pragma unroll
             for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
             m = from_ordered32(__reduce_max_sync(ALL, ordered32(m)));
-            const float mr = m == -INFINITY ? 0.f : m;
+            m = m == -INFINITY ? 0.f : m;
             d = 0.f;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) d += route_exp2((x[i] - mr) * kRouteLog2e);
+            for (int i = 0; i < PL; ++i) d += route_exp2((x[i] - m) * kRouteLog2e);
             d = warp_sum_all(d);
-            m = mr;
         }
         if (a.scores) {
 #pragma unroll
@@ -252,142 +415,147 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                     a.scores[t * a.experts + r.first + i] =
                         x[i] == -INFINITY ? 0.f : a.softmax ? expf(x[i] - m) / d : 1.f / (1.f + expf(-x[i]));
         }
-        // keys, largest first
+        // keys, largest first; 0: not available
         uint32_t key[PL];
-        float near_ = 0.f;  // keys no further apart than this are in question
-        bool again = false; // the whole token is
-        if (whole) {
+        float near_ = 0.f;   // keys no further apart than this are in question
+        bool again = false;  // the whole token is
+        if constexpr (MODE == KEY_WHOLE) {
 #pragma unroll
-            for (int i = 0; i < PL; ++i)
-                key[i] = x[i] > -INFINITY ? (ordered32(x[i]) >> 16 << kIdxBits) + (uint32_t)(kIdxMask - (r.first + i)) : 0u;
-            if (std::is_same<T, __half>::value) {  // binary16 keeps more bits than a binary32's upper half
-#pragma unroll
-                for (int i = 0; i < PL; ++i) {
-                    const uint32_t b = __half_as_ushort(__float2half_rn(x[i] + 0.f));
-                    key[i] = x[i] > -INFINITY ? ((b & 0x8000u ? ~b & 0xffffu : b | 0x8000u) << kIdxBits) +
-                                                    (uint32_t)(kIdxMask - (r.first + i))
-                                              : 0u;
+            for (int i = 0; i < PL; ++i) {
+                uint32_t b = ordered32(x[i]) >> 16;
+                if (std::is_same<T, __half>::value) {  // binary16 keeps more bits than a binary32's upper half
+                    b = __half_as_ushort(__float2half_rn(x[i] + 0.f));
+                    b = b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
                 }
+                key[i] = x[i] > -INFINITY ? (b << kIdxBits) + (index - i) : 0u;
             }
-        } else {
+        } else if constexpr (MODE == KEY_LOGIT) {
             float top = -INFINITY;
-            if (a.by_score) {
-                const float inv = 1.f / d;
-#pragma unroll
-                for (int i = 0; i < PL; ++i) {
-                    const float s = a.softmax ? route_exp2((x[i] - m) * kRouteLog2e) * inv
-                                              : route_rcp(1.f + route_exp2(x[i] * -kRouteLog2e));
-                    x[i] = x[i] == -INFINITY ? -INFINITY : s + bias[i];
-                }
-            }
 #pragma unroll
             for (int i = 0; i < PL; ++i) top = fmaxf(top, x[i]);
             top = from_ordered32(__reduce_max_sync(ALL, ordered32(top)));
-            // scores lie within 1 of each other; logits are taken 16 below the largest
-            const float S = a.by_score ? 4194300.f : 262143.f;
             again = top == INFINITY;
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
                 const float q = fmaxf(fmaf(x[i] - top, S, 8388608.f + 4194303.f), 8388609.f);
-                key[i] = x[i] > -INFINITY
-                             ? (__float_as_uint(q) << kIdxBits) + (uint32_t)(kIdxMask - (r.first + i))
-                             : 0u;
+                key[i] = x[i] > -INFINITY ? (__float_as_uint(q) << kIdxBits) + (index - i) : 0u;
             }
+            near_ = 2.f;  // the difference and the fixed point: half a step each, of either
+        } else {
             // A sigmoid is good to 3e-7 (the exponent's argument, ex2, rcp), a
             // softmax to 6e-7 of the largest and half a step for each addition
-            // of its sum; adding the bias and taking the difference to the
-            // largest cost half a step of their results each, the fixed point one
-            // step of its own.
-            const float score = a.softmax ? (6e-7f + 6e-8f * (PL + 6)) / d : 3e-7f;
-            near_ = a.by_score ? 2.f * S * (score + 1.2e-7f * (fabsf(top) + 1.f)) + 2.f : 2.f;
+            // of its sum; the multiply-add rounds to half a step.
+            const float inv = a.softmax ? 1.f / d : 1.f;
+            near_ = 2.f * (S * (a.softmax ? (6e-7f + 6e-8f * (PL + 6)) * inv : 3e-7f) + near_bias);
+            float odd = 0.f;  // NaN or inf where a logit is
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                odd += x[i];
+                const float s = a.softmax ? route_exp2((x[i] - m) * kRouteLog2e) * inv
+                                          : route_rcp(1.f + route_exp2(x[i] * -kRouteLog2e));
+                key[i] = (__float_as_uint(fmaf(s, S, base[i])) << kIdxBits) + (index - i);
+            }
+            // experts that a lane has not, and those that are not available
+            if (__any_sync(ALL, !(fabsf(odd) < INFINITY)) || odd_bias) {
+                bool far = false;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    if (!(x[i] > -INFINITY) || !(base[i] > 0.f) || !(d < INFINITY)) key[i] = 0u;
+                    far = far || x[i] == INFINITY || base[i] == INFINITY;
+                }
+                again = __any_sync(ALL, far);
+            }
         }
         sort_desc<PL>(key);
         if (limited) {
-            uint32_t b1 = key[0] >> kIdxBits, b2 = PL > 1 ? key[PL > 1 ? 1 : 0] >> kIdxBits : 0u;
+            uint32_t b1 = key[0] >> kIdxBits, b2 = key[PL > 1 ? 1 : 0] >> kIdxBits;
             for (int o = 1; o < 1 << a.log_lanes; o <<= 1) {
                 const uint32_t c1 = __shfl_xor_sync(ALL, b1, o), c2 = __shfl_xor_sync(ALL, b2, o);
                 b2 = max(min(b1, c1), max(b2, c2));
                 b1 = max(b1, c1);
             }
-            const bool two = a.group_top > 1;
-            const uint32_t worth = two ? b1 + b2 : b1;
-            int rank = 0;
-            const int g = lane >> a.log_lanes;
-            for (int h = 0; h < a.groups; ++h) {
-                const uint32_t w = __shfl_sync(ALL, worth, h << a.log_lanes);
-                rank += w > worth || (w == worth && h < g);
+            // sum and then the lower group first; + 1: groups without an expert are
+            // still groups
+            const bool two = a.group_top > 1, real = g < a.groups;
+            const uint32_t worth = real ? ((two ? b1 + b2 : b1) + 1u) * 32u + (uint32_t)(31 - g) : 0u;
+            uint32_t rest = worth, least = 0u;
+            for (int i = 0; i < a.top_groups; ++i) {
+                least = __reduce_max_sync(ALL, rest);
+                rest = rest == least ? 0u : rest;
             }
-            const bool keep = g < a.groups && rank < a.top_groups;
-            if (!whole) {
-                const uint32_t least = __reduce_min_sync(ALL, keep ? worth : ALL);
-                const uint32_t most = __reduce_max_sync(ALL, keep || g >= a.groups ? 0u : worth);
-                // too near; or a kept group owes its place to a value below the fixed point's range
-                const bool low = keep && (b1 == 1u || (two && b2 == 1u));
-                again = again || (most > 0u && (float)(least - most) <= (two ? 2.f : 1.f) * near_) ||
-                        __any_sync(ALL, low);
+            const bool keep = real && rest == 0u;
+            if constexpr (MODE != KEY_WHOLE) {
+                const uint32_t most = __reduce_max_sync(ALL, rest);
+                // too near; or a kept group owes its place to a logit below the range
+                const bool low = MODE == KEY_LOGIT && keep && (b1 == 1u || (two && b2 == 1u));
+                again = again || (float)(least / 32u - most / 32u) <= (two ? 2.f : 1.f) * near_ || __any_sync(ALL, low);
             }
-            if (!keep) {
-#pragma unroll
-                for (int i = 0; i < PL; ++i) key[i] = 0u;
-            }
+            if (!keep) key[0] = 0u;  // never the largest, so nothing behind it is
         }
-        // places: the k largest, and those that may belong among them
-        uint32_t list[LIST + 1], mine = 0u;
+        // places: the k largest
+        uint32_t list[LIST + 1], mine = 0u, last = 0u;
 #pragma unroll
         for (int i = 0; i < LIST; ++i) list[i] = key[i];
         list[LIST] = 0u;
-        // a lane whose list ran out may hold more
+        // a lane whose list runs out may hold more
         int left = PL > LIST && key[PL > LIST ? LIST : 0] ? LIST : PL + 1;
-        uint32_t last = 0u;  // the k-th place
-        int places = 0;
-        while (!again) {
-            const uint32_t w = __reduce_max_sync(ALL, list[0]);
-            if (w == 0u) break;
-            if (places >= a.k && (whole || (float)((last >> kIdxBits) - (w >> kIdxBits)) > near_)) break;
-            if (places == 32) {  // more in question than lanes
-                again = true;
-                break;
-            }
-            if (places == a.k - 1) last = w;
-            if (lane == places) mine = w;
-            ++places;
-            if (list[0] == w) {
+        for (int p = 0; p < a.k; ++p) {
+            last = __reduce_max_sync(ALL, list[0]);
+            if (lane == p) mine = last;
+            if (list[0] == last) {
 #pragma unroll
                 for (int i = 0; i < LIST; ++i) list[i] = list[i + 1];
-                --left;
+                if (PL > LIST) --left;
             }
-            if (PL > LIST && !(whole && places == a.k)) again = __any_sync(ALL, left == 0);
+            if (PL > LIST && __any_sync(ALL, left == 0)) {
+                again = again || MODE != KEY_WHOLE || p + 1 < a.k;
+                left = PL + 1;
+            }
         }
         int id = mine ? kIdxMask - (int)(mine & kIdxMask) : -1;
         float xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
-        if (!whole && !again) {
-            const float bs = a.bias && id >= 0 ? a.bias[id] : 0.f;
+        if constexpr (MODE != KEY_WHOLE) {
+            // gaps between neighbouring places, and to the first one left out
+            const uint32_t after = __reduce_max_sync(ALL, list[0]);
             const uint32_t up = __shfl_up_sync(ALL, mine, 1);
-            const float xu = __shfl_up_sync(ALL, xs, 1), bu = __shfl_up_sync(ALL, bs, 1);
-            const bool close = lane > 0 && id >= 0 && (float)((up >> kIdxBits) - (mine >> kIdxBits)) <= near_ &&
-                               !(xs == xu && bs == bu);
+            const float xu = __shfl_up_sync(ALL, xs, 1);
+            bool close = false;
+            if (lane == 0) close = after && (float)((last >> kIdxBits) - (after >> kIdxBits)) <= near_;
+            else if (mine) close = (float)((up >> kIdxBits) - (mine >> kIdxBits)) <= near_;
             if (__any_sync(ALL, close)) {
-                // one expert a lane in 64 bits, and its rank among them
-                double ms = 0.0, ds = 1.0;
-                if (a.softmax && a.by_score) route_softmax64(a, row, lane, &ms, &ds);
-                double c = -INFINITY;
-                if (id >= 0) c = a.by_score ? route_choice64(a, xs, id, ms, ds) : (double)xs;
-                const uint64_t ck = id >= 0 ? ordered64(c) : 0ull;
-                int rank = 0;
-                for (int p = 0; p < places; ++p) {
-                    const uint64_t o = __shfl_sync(ALL, ck, p);
-                    const int oid = __shfl_sync(ALL, id, p);
-                    rank += o > ck || (o == ck && oid < id);
+                // equal logits with equal biases are equal, not near
+                const float bs = MODE == KEY_SCORE && a.bias && id >= 0 ? a.bias[id] : 0.f;
+                const float bu = __shfl_up_sync(ALL, bs, 1);
+                if (lane > 0) close = close && !(xs == xu && bs == bu);
+                // those equal to the last place come after it
+                uint32_t w = after, rest[LIST + 1];
+#pragma unroll
+                for (int i = 0; i <= LIST; ++i) rest[i] = list[i];
+                const float xl = __shfl_sync(ALL, xs, a.k - 1), bl = __shfl_sync(ALL, bs, a.k - 1);
+                bool border = false;
+                while (w && (float)((last >> kIdxBits) - (w >> kIdxBits)) <= near_) {
+                    const int e = kIdxMask - (int)(w & kIdxMask);
+                    border = !(IO<T>::to_f(row[e]) == xl && (MODE == KEY_SCORE && a.bias ? a.bias[e] : 0.f) == bl);
+                    if (border) break;
+                    if (rest[0] == w) {
+#pragma unroll
+                        for (int i = 0; i < LIST; ++i) rest[i] = rest[i + 1];
+                        --left;
+                    }
+                    if (PL > LIST && __any_sync(ALL, left == 0)) {
+                        again = true;
+                        break;
+                    }
+                    w = __reduce_max_sync(ALL, rest[0]);
                 }
-                // lane `rank` takes the expert: who has the rank of this lane?
-                int src = lane;
-                for (int p = 0; p < places; ++p)
-                    if (__shfl_sync(ALL, rank, p) == lane) src = p;
-                id = __shfl_sync(ALL, id, src);
-                xs = __shfl_sync(ALL, xs, src);
+                if (!again && (border || __any_sync(ALL, close && lane > 0)))
+                    again = !route_resolve<T, PL, LIST>(a, row, lane, mine, last, rest, left, near_, &id, &xs);
             }
-        }
-        if (again) {
+            if (again) {
+                id = route_exact<T, PL>(a, row, lane);
+                xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
+            }
+        } else if (again) {
             id = route_exact<T, PL>(a, row, lane);
             xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
         }
@@ -399,11 +567,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
             if (a.renorm) m = from_ordered32(__reduce_max_sync(ALL, ordered32(have ? xs : -INFINITY)));
             w = !have ? 0.f : a.renorm ? expf(xs - m) : expf(xs - m) / d;
         } else {
-            w = have ? 1.f / (1.f + expf(-xs)) : 0.f;
+            w = have ? route_sigmoid(xs) : 0.f;
         }
         if (a.renorm) {
             const float sum = warp_sum_all(w);
-            w = sum == 0.f ? 0.f : w / sum;
+            w = sum > 1e-30f ? w * route_inv(sum) : sum == 0.f ? 0.f : w / sum;
         }
         if (lane < a.k) {
             a.weights[t * a.k + lane] = w * a.scale;
@@ -513,7 +681,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
 // Launchers, one instance of each per storage type (route_<type>.cu).
 // ---------------------------------------------------------------------------
 template <typename T, int PL> cudaError_t launch_route_n(const RouteArgs &a, bool back, int sms, cudaStream_t s, Plan *p) {
-    auto kernel = back ? route_bwd_kernel<T, PL> : route_fwd_kernel<T, PL>;
+    auto kernel = back         ? route_bwd_kernel<T, PL>
+                  : a.by_score ? route_fwd_kernel<T, PL, KEY_SCORE>
+                               : route_fwd_kernel<T, PL, (sizeof(T) == 2 ? KEY_WHOLE : KEY_LOGIT)>;
     int per_sm = 0;
     const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), kRouteThreads, 0, &per_sm);
     if (e != cudaSuccess) return e;
