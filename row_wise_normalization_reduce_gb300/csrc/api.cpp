@@ -1725,6 +1725,17 @@ int route_fwd(const void *logits, int64_t ldl, const float *bias, float *weights
     const int pl = round_up_pow2(a.per_lane < 2 ? 2 : a.per_lane);
     const size_t pack = pl * es < 16 ? pl * es : 16;
     a.wide = a.per_lane == pl && a.group_size == pl << a.log_lanes && aligned(logits, pack) && (size_t)ldl * es % pack == 0;
+    // eight lanes a token, with 8, 16 or 32 experts each
+    if (k <= 8 && a.groups <= 8 && !forced_generic()) {
+        a.oct_log_lanes = 3;
+        while (a.groups << a.oct_log_lanes > 8) --a.oct_log_lanes;
+        const int n = (a.group_size + (1 << a.oct_log_lanes) - 1) >> a.oct_log_lanes;
+        const int most = n <= 8 ? 8 : n <= 16 ? 16 : 32;
+        if (n <= 32 && a.per_lane <= 8) {
+            a.oct_per_lane = n;
+            a.oct_wide = n == most && a.group_size == n << a.oct_log_lanes && aligned(logits, 16) && (size_t)ldl * es % 16 == 0;
+        }
+    }
     Plan plan{};
     return record_plan(launch_route(dtype, a, false, dev.sms, stream, &plan), plan);
 }

@@ -397,6 +397,8 @@ struct RouteArgs {
     int groups, top_groups, group_top;  // groups 1 where they do not limit the choice
     int group_size, log_lanes, per_lane;  // lanes of a group: 2^log_lanes, experts each
     int wide;               // a lane's experts are whole packs
+    // the same for eight lanes a token; oct_per_lane 0: more than they take
+    int oct_log_lanes, oct_per_lane, oct_wide;
     int by_score;           // the order is that of the scores, not of the logits alone
     int need_sum;           // the softmax' sum over all experts
     float *weights;         // [tokens][k]

@@ -227,9 +227,11 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
     float m = 0.f;
     Pair inv{1.f, 0.f};
     if (a.softmax && a.by_score) route_softmax_pair(a, row, lane, &m, &inv);
+    // (loops, not unrolled: this code is cold when it runs, and fetching eight
+    // copies of a choice took longer than computing them, 30000 cycles in all)
     uint64_t key[PL], k1 = none, k2 = none;
     Pair b1 = no, b2 = no;  // the lane's two largest
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < PL; ++i) {
         Pair c = no;
         if (i < r.n) {
@@ -237,15 +239,16 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
             if (a.by_score) c = route_choice(a, x, r.first + i, m, inv);
             else if (x > -INFINITY) c = Pair{x, 0.f};
         }
-        key[i] = ordered_pair(c);
-        if (key[i] > k1) {
+        const uint64_t k = ordered_pair(c);
+        key[i] = k;
+        if (k > k1) {
             b2 = b1;
             k2 = k1;
             b1 = c;
-            k1 = key[i];
-        } else if (key[i] > k2) {
+            k1 = k;
+        } else if (k > k2) {
             b2 = c;
-            k2 = key[i];
+            k2 = k;
         }
     }
     if (a.top_groups < a.groups) {
@@ -273,7 +276,7 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
             if (w > worth || (w == worth && h < g)) ++rank;
         }
         if (rank >= a.top_groups) {
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < PL; ++i) key[i] = none;
         }
     }
@@ -281,7 +284,7 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
     for (int p = 0; p < a.k; ++p) {
         uint64_t best = none;
         int at = -1;
-#pragma unroll
+#pragma unroll 1
         for (int i = PL - 1; i >= 0; --i)
             if (key[i] > none && key[i] >= best) {
                 best = key[i];
@@ -293,11 +296,7 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
         if (!who) break;
         const int src = __ffs(who) - 1, id = __shfl_sync(ALL, r.first + at, src);
         if (lane == p) mine = id;
-        if (lane == src) {
-#pragma unroll
-            for (int i = 0; i < PL; ++i)
-                if (i == at) key[i] = none;
-        }
+        if (lane == src) key[at] = none;
     }
     return mine;
 }
@@ -581,6 +580,356 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
 }
 
 // ---------------------------------------------------------------------------
+// Up to 8 places of up to 256 experts (and 8 groups): eight lanes a token, four
+// tokens a warp, so that what passes between lanes is done for four at once.  A
+// lane takes its experts in chunks of eight, sorts each chunk's keys and keeps the
+// eight largest (the larger of entry i of one list and entry 7 - i of the other
+// are the eight largest of both, and three stages of exchanges sort them); three
+// merges of the same kind join the lanes.  65536 x 256 bf16 in 8 groups: XX us, a
+// warp a token 64.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {
+    const uint32_t hi = max(a, b), lo = min(a, b);
+    a = hi;
+    b = lo;
+}
+// list: the 8 largest of two descending lists of 8, descending.
+__device__ __forceinline__ void merge8(uint32_t (&list)[8], const uint32_t (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) list[i] = max(list[i], o[7 - i]);
+#pragma unroll
+    for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) exchange(list[i], list[i + d]);
+}
+// Over the eight lanes of a token.
+__device__ __forceinline__ uint32_t oct_max(uint32_t v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ uint32_t oct_min(uint32_t v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float oct_max(float v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+#ifndef RT_M
+#define RT_M 3
+#endif
+template <typename T, int NC, int MODE>
+__global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const RouteArgs a) {
+    constexpr uint32_t ALL = 0xffffffffu;
+    constexpr int PL = 8 * NC;
+    // SCORE: the biases in fixed point, a lane's 8 NC together and 4 apart from the
+    // next lane's (the lanes' 16-byte loads fall on different banks)
+    __shared__ __align__(16) float base_of[MODE == KEY_SCORE ? 8 * (PL + 4) : 1];
+    __shared__ float range[2];
+    const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
+    const int g = l >> a.oct_log_lanes, first = g * a.group_size + (l & ((1 << a.oct_log_lanes) - 1)) * a.oct_per_lane;
+    const int n = g < a.groups ? max(0, min(a.oct_per_lane, (g + 1) * a.group_size - first)) : 0;
+    const bool limited = a.top_groups < a.groups;
+    const uint32_t index = (uint32_t)(kIdxMask - first);
+    float S = 262143.f, near_bias = 0.f;
+    bool odd_bias = false;  // infinite or NaN ones
+    pdl_wait();
+    pdl_launch_dependents();
+    if constexpr (MODE == KEY_SCORE) {
+        if (threadIdx.x < 32) {
+            float lo = INFINITY, hi = -INFINITY;
+            for (int e = lane; e < a.experts; e += 32) {
+                const float b = a.bias ? a.bias[e] : 0.f;
+                if (fabsf(b) < INFINITY) {
+                    lo = fminf(lo, b);
+                    hi = fmaxf(hi, b);
+                } else {
+                    odd_bias = true;
+                }
+            }
+            lo = from_ordered32(__reduce_min_sync(ALL, ordered32(lo)));
+            hi = from_ordered32(__reduce_max_sync(ALL, ordered32(hi)));
+            if (!(hi >= lo)) lo = hi = 0.f;  // no expert has a finite bias
+            if (lane == 0) {
+                range[0] = lo;
+                range[1] = hi;
+            }
+        }
+        odd_bias = __syncthreads_or(odd_bias);
+        const float lo = range[0], hi = range[1];
+        S = 4194300.f / (1.f + (hi - lo));
+        // the rounding of base: half a step of its size, relative to 2^23
+        near_bias = 1.2e-7f * (fabsf(lo) + fabsf(hi)) * S + 1.f;
+        if (threadIdx.x < 8) {
+            for (int i = 0; i < PL; ++i)
+                base_of[l * (PL + 4) + i] =
+                    i < n ? fmaf((a.bias ? a.bias[first + i] : 0.f) - lo, S, 8388610.f) : -INFINITY;
+        }
+        __syncthreads();
+    }
+    const int64_t step = (int64_t)gridDim.x * (kRouteThreads / 8);
+    for (int64_t t0 = (int64_t)blockIdx.x * (kRouteThreads / 8) + (threadIdx.x >> 5) * 4; t0 < a.tokens; t0 += step) {
+        const bool real = t0 + sub < a.tokens;
+        const int64_t t = real ? t0 + sub : a.tokens - 1;
+        const T *row = static_cast<const T *>(a.x) + t * a.ldx;
+        // a lane's logits: whole packs, or one by one
+        constexpr int W = 8 / IO<T>::V;  // packs a chunk
+        uint4 raw[NC][W];
+        if (a.oct_wide) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    raw[c][w] = n > 0 ? ld_once(row + first + c * 8 + w * IO<T>::V) : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = c * 8 + i < n ? IO<T>::to_f(row[first + c * 8 + i]) : -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) raw[c][w] = IO<T>::pack(v + w * IO<T>::V);
+            }
+        }
+        auto chunk = [&](int c, float (&x)[8]) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) IO<T>::unpack(raw[c][w], x + w * IO<T>::V);
+            if (a.oct_wide && n == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
+            }
+        };
+        // the softmax' maximum and sum, where they are needed; binary32 logits' largest
+        float m = 0.f, d = 1.f, inv = 1.f;
+        if (MODE == KEY_LOGIT || (a.softmax && a.need_sum)) {
+            m = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float x[8];
+                chunk(c, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, x[i]);
+            }
+            m = oct_max(m);
+        }
+        const float top = m;
+        if (a.softmax && a.need_sum) {
+            m = m == -INFINITY ? 0.f : m;
+            d = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float x[8];
+                chunk(c, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d += route_exp2((x[i] - m) * kRouteLog2e);
+            }
+            d = group_sum_all<8>(d);
+            inv = 1.f / d;
+        }
+        if (a.scores && real) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float x[8];
+                chunk(c, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c * 8 + i < n)
+                        a.scores[t * a.experts + first + c * 8 + i] =
+                            x[i] == -INFINITY ? 0.f : a.softmax ? expf(x[i] - m) / d : 1.f / (1.f + expf(-x[i]));
+            }
+        }
+        // keys, largest first; 0: not available
+        uint32_t list[8];
+        float near_ = MODE == KEY_LOGIT ? 2.f : 0.f;  // keys no further apart than this are in question
+        bool again = false;                           // the whole token is
+        if constexpr (MODE == KEY_SCORE)
+            // as in route_fwd_kernel; the sum is at most 8 NC + 3 additions deep
+            near_ = 2.f * (S * (a.softmax ? (6e-7f + 6e-8f * (PL + 3)) * inv : 3e-7f) + near_bias);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float x[8];
+            uint32_t key[8];
+            chunk(c, x);
+            if constexpr (MODE == KEY_WHOLE) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t b = ordered32(x[i]) >> 16;
+                    if (std::is_same<T, __half>::value) {  // binary16 keeps more bits than a binary32's upper half
+                        b = __half_as_ushort(__float2half_rn(x[i] + 0.f));
+                        b = b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
+                    }
+                    key[i] = x[i] > -INFINITY ? (b << kIdxBits) + (index - (c * 8 + i)) : 0u;
+                }
+            } else if constexpr (MODE == KEY_LOGIT) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float q = fmaxf(fmaf(x[i] - top, S, 8388608.f + 4194303.f), 8388609.f);
+                    key[i] = x[i] > -INFINITY ? (__float_as_uint(q) << kIdxBits) + (index - (c * 8 + i)) : 0u;
+                }
+                again = top == INFINITY;
+            } else {
+                float odd = 0.f, base[8];  // odd: NaN or inf where a logit is
+                const float4 b0 = *reinterpret_cast<const float4 *>(&base_of[l * (PL + 4) + c * 8]),
+                             b1 = *reinterpret_cast<const float4 *>(&base_of[l * (PL + 4) + c * 8 + 4]);
+                base[0] = b0.x, base[1] = b0.y, base[2] = b0.z, base[3] = b0.w;
+                base[4] = b1.x, base[5] = b1.y, base[6] = b1.z, base[7] = b1.w;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    odd += x[i];
+                    const float s = a.softmax ? route_exp2((x[i] - m) * kRouteLog2e) * inv
+                                              : route_rcp(1.f + route_exp2(x[i] * -kRouteLog2e));
+                    key[i] = (__float_as_uint(fmaf(s, S, base[i])) << kIdxBits) + (index - (c * 8 + i));
+                }
+                // experts that a lane has not, and those that are not available
+                if (__any_sync(ALL, !(fabsf(odd) < INFINITY)) || odd_bias) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!(x[i] > -INFINITY) || !(base[i] > 0.f) || !(d < INFINITY)) key[i] = 0u;
+                        again = again || x[i] == INFINITY || base[i] == INFINITY;
+                    }
+                }
+            }
+            sort_desc<8>(key);
+            if (c == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) list[i] = key[i];
+            } else {
+                merge8(list, key);
+            }
+        }
+        if (limited) {
+            uint32_t b1 = list[0] >> kIdxBits, b2 = list[1] >> kIdxBits;
+            for (int o = 1; o < 1 << a.oct_log_lanes; o <<= 1) {
+                const uint32_t c1 = __shfl_xor_sync(ALL, b1, o), c2 = __shfl_xor_sync(ALL, b2, o);
+                b2 = max(min(b1, c1), max(b2, c2));
+                b1 = max(b1, c1);
+            }
+            // sum and then the lower group first; + 1: groups without an expert are
+            // still groups
+            const bool two = a.group_top > 1, is = g < a.groups;
+            const uint32_t worth = is ? ((two ? b1 + b2 : b1) + 1u) * 32u + (uint32_t)(31 - g) : 0u;
+            int rank = 0;
+            for (int h = 0; h < a.groups; ++h)
+                rank += __shfl_sync(ALL, worth, (lane & 24) | h << a.oct_log_lanes) > worth;
+            const bool keep = is && rank < a.top_groups;
+            if constexpr (MODE != KEY_WHOLE) {
+                const uint32_t least = oct_min(keep ? worth : ALL), most = oct_max(keep ? 0u : worth);
+                // too near; or a kept group owes its place to a logit below the range
+                const bool low = MODE == KEY_LOGIT && keep && (b1 == 1u || (two && b2 == 1u));
+                again = again || (float)(least / 32u - most / 32u) <= (two ? 2.f : 1.f) * near_ || low;
+            }
+            if (!keep) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) list[i] = 0u;
+            }
+        }
+        uint32_t own[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own[i] = list[i];
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) {
+            uint32_t other[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(ALL, list[i], o);
+            merge8(list, other);
+        }
+        // place l
+        uint32_t mine;
+        {
+            const uint32_t p = l & 4 ? list[4] : list[0], q = l & 4 ? list[5] : list[1], u = l & 4 ? list[6] : list[2],
+                           v = l & 4 ? list[7] : list[3];
+            const uint32_t w = l & 2 ? u : p, z = l & 2 ? v : q;
+            mine = l & 1 ? z : w;
+        }
+        const uint32_t last = __shfl_sync(ALL, mine, (lane & 24) | (a.k - 1));
+        if (l >= a.k) mine = 0u;
+        int id = mine ? kIdxMask - (int)(mine & kIdxMask) : -1;
+        float xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
+        if constexpr (MODE != KEY_WHOLE) {
+            // the first one left out: the largest below the last place
+            uint32_t after = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) after = max(after, own[i] < last ? own[i] : 0u);
+            after = oct_max(after);
+            // a lane that has all its eight among the places may hold the next
+            again = again || (PL > 8 && last && own[7] >= last);
+            const uint32_t up = __shfl_up_sync(ALL, mine, 1);
+            bool close = l > 0 && mine && (float)((up >> kIdxBits) - (mine >> kIdxBits)) <= near_;
+            bool border = after && (float)((last >> kIdxBits) - (after >> kIdxBits)) <= near_;
+            if (__any_sync(ALL, close || border)) {
+                // equal logits with equal biases are equal, not near
+                const float bs = MODE == KEY_SCORE && a.bias && id >= 0 ? a.bias[id] : 0.f;
+                const float xu = __shfl_up_sync(ALL, xs, 1), bu = __shfl_up_sync(ALL, bs, 1);
+                close = close && !(xs == xu && bs == bu);
+                const float xl = __shfl_sync(ALL, xs, (lane & 24) | (a.k - 1)), bl = __shfl_sync(ALL, bs, (lane & 24) | (a.k - 1));
+                // those equal to the last place come after it
+                while (__any_sync(ALL, border)) {
+                    if (border) {
+                        const int e = kIdxMask - (int)(after & kIdxMask);
+                        again = again || !(IO<T>::to_f(row[e]) == xl && (MODE == KEY_SCORE && a.bias ? a.bias[e] : 0.f) == bl);
+                    }
+                    const uint32_t below = after;
+                    after = 0u;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) after = max(after, own[i] < below ? own[i] : 0u);
+                    after = oct_max(after);
+                    again = again || (PL > 8 && border && own[7] && own[7] >= below);
+                    border = border && after && (float)((last >> kIdxBits) - (after >> kIdxBits)) <= near_;
+                }
+                if (a.softmax && a.by_score) {
+                    again = again || close;
+                } else if (__any_sync(ALL, close)) {
+                    // the places in their order, one expert a lane
+                    uint64_t key = 0;
+                    if (id >= 0) key = ordered_pair(a.by_score ? route_choice(a, xs, id, 0.f, Pair{1.f, 0.f}) : Pair{xs, 0.f});
+                    int rank = 0, src = lane;
+                    for (int p = 0; p < 8; ++p) {
+                        const uint64_t o = __shfl_sync(ALL, key, (lane & 24) | p);
+                        const int oe = __shfl_sync(ALL, id, (lane & 24) | p);
+                        rank += o > key || (o == key && oe < id);
+                    }
+                    if (id < 0) rank = l;
+                    for (int p = 0; p < 8; ++p)
+                        if (__shfl_sync(ALL, rank, (lane & 24) | p) == l) src = (lane & 24) | p;
+                    id = __shfl_sync(ALL, id, src);
+                    xs = __shfl_sync(ALL, xs, src);
+                }
+            }
+            for (uint32_t who = __ballot_sync(ALL, again && real); who;) {
+                const int of = __ffs(who) - 1 >> 3;
+                who &= ~(0xffu << of * 8);
+                const T *r = static_cast<const T *>(a.x) + (t0 + of) * a.ldx;
+                const int e = __shfl_sync(ALL, route_exact<T, 8>(a, r, lane), l);
+                if (sub == of) {
+                    id = l < a.k ? e : -1;
+                    xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
+                }
+            }
+        }
+        float w;
+        if (a.softmax) {
+            if (a.renorm) m = oct_max(id >= 0 ? xs : -INFINITY);
+            w = id < 0 ? 0.f : a.renorm ? expf(xs - m) : expf(xs - m) / d;
+        } else {
+            w = id >= 0 ? route_sigmoid(xs) : 0.f;
+        }
+        if (a.renorm) {
+            const float sum = group_sum_all<8>(w);
+            w = sum > 1e-30f ? w * route_inv(sum) : sum == 0.f ? 0.f : w / sum;
+        }
+        if (real && l < a.k) {
+            a.weights[t * a.k + l] = w * a.scale;
+            a.ids[t * a.k + l] = id;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The gradient of the logits.  With d_i the gradient of chosen weight i times
 // scale, s_i its score and S the chosen scores' sum, the scores' gradients are
 //   ds_i = d_i,  or renormalised  (d_i - sum_j d_j s_j / S) / S,
@@ -680,21 +1029,36 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
 // ---------------------------------------------------------------------------
 // Launchers, one instance of each per storage type (route_<type>.cu).
 // ---------------------------------------------------------------------------
-template <typename T, int PL> cudaError_t launch_route_n(const RouteArgs &a, bool back, int sms, cudaStream_t s, Plan *p) {
-    auto kernel = back         ? route_bwd_kernel<T, PL>
-                  : a.by_score ? route_fwd_kernel<T, PL, KEY_SCORE>
-                               : route_fwd_kernel<T, PL, (sizeof(T) == 2 ? KEY_WHOLE : KEY_LOGIT)>;
+template <typename K>
+cudaError_t launch_route_k(K kernel, const RouteArgs &a, int per_cta, int pl, int sms, cudaStream_t s, Plan *p) {
     int per_sm = 0;
     const cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), kRouteThreads, 0, &per_sm);
     if (e != cudaSuccess) return e;
-    const int64_t need = (a.tokens + kRouteThreads / 32 - 1) / (kRouteThreads / 32), most = (int64_t)sms * per_sm;
+    const int64_t need = (a.tokens + per_cta - 1) / per_cta, most = (int64_t)sms * per_sm;
     p->kind = PLAN_WARP;
     p->threads = kRouteThreads;
-    p->packs = PL;
+    p->packs = pl;
+    p->groups = per_cta;
     return launch_row(kernel, (unsigned)(need < most ? need : most), (unsigned)kRouteThreads, 0, s, a);
 }
 
+template <typename T, int PL> cudaError_t launch_route_n(const RouteArgs &a, bool back, int sms, cudaStream_t s, Plan *p) {
+    constexpr int LOGIT = sizeof(T) == 2 ? KEY_WHOLE : KEY_LOGIT;
+    auto kernel = back ? route_bwd_kernel<T, PL> : a.by_score ? route_fwd_kernel<T, PL, KEY_SCORE> : route_fwd_kernel<T, PL, LOGIT>;
+    return launch_route_k(kernel, a, kRouteThreads / 32, PL, sms, s, p);
+}
+template <typename T, int NC> cudaError_t launch_route_oct(const RouteArgs &a, int sms, cudaStream_t s, Plan *p) {
+    constexpr int LOGIT = sizeof(T) == 2 ? KEY_WHOLE : KEY_LOGIT;
+    auto kernel = a.by_score ? route_oct_kernel<T, NC, KEY_SCORE> : route_oct_kernel<T, NC, LOGIT>;
+    return launch_route_k(kernel, a, kRouteThreads / 8, 8 * NC, sms, s, p);
+}
+
 template <typename T> cudaError_t launch_route_t(const RouteArgs &a, bool back, int sms, cudaStream_t s, Plan *p) {
+    if (!back && a.oct_per_lane) {
+        if (a.oct_per_lane <= 8) return launch_route_oct<T, 1>(a, sms, s, p);
+        if (a.oct_per_lane <= 16) return launch_route_oct<T, 2>(a, sms, s, p);
+        return launch_route_oct<T, 4>(a, sms, s, p);
+    }
     const int n = back ? (a.experts + 31) / 32 : a.per_lane;
     if (n <= 2) return launch_route_n<T, 2>(a, back, sms, s, p);
     if (n <= 4) return launch_route_n<T, 4>(a, back, sms, s, p);
