@@ -11,8 +11,9 @@
 // rescaled like d, and moves by d times the shift when the maximum does.  The k
 // largest logits (ties: the lowest index first) come out of the same pass.  A
 // thread keeps the maximum of each group of packs it has seen.  At the row's
-// end the k-th largest of the threads' own maxima, T, is a lower bound of the
-// k-th largest logit, for the k threads' maxima are k logits; so only groups
+// end the k-th largest of some threads' own maxima, T (of a warp's rows: of its
+// lanes', of a CTA's: of each warp's four largest), is a lower bound of the k-th
+// largest logit, for k threads' maxima are k logits; so only groups
 // whose maximum reaches T can hold one of the k largest, and there are hardly
 // more than k of those.  They are read again (from L2), and their logits from T
 // on go, as 64-bit keys (value, then lower index first), into a sorted list of 32
@@ -82,9 +83,10 @@ __device__ __forceinline__ void ent_to(RowEnt &r, float M, float c) {
 // A term 2^x x is 0 from 2^-126 on; -inf times 0 is not.
 __device__ __forceinline__ float ent_x(float x) { return fmaxf(x, -200.f); }
 
-// Add a set of packs to (d, A) around m (packs_sum with the second sum).
-template <typename T, int PK>
-__device__ __forceinline__ void packs_ent(const uint4 (&raw)[PK], RowEnt &r, float c) {
+// Add a set of packs to (d, A) around m (packs_sum with the second sum).  CLAMP:
+// logits of -inf may be among them.
+template <typename T, int PK, bool CLAMP>
+__device__ __forceinline__ void packs_ent_any(const uint4 (&raw)[PK], RowEnt &r, float c) {
     constexpr int H = IO2<T>::H;
     const Shift s(r.m, c);
     float2 d = f2(0.f), a = f2(0.f);
@@ -95,10 +97,11 @@ __device__ __forceinline__ void packs_ent(const uint4 (&raw)[PK], RowEnt &r, flo
             IO2<T>::unpack(raw[k], v);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const float2 x = __ffma2_rn(v[h], f2(c), f2(-s.b));
+                float2 x = __ffma2_rn(v[h], f2(c), f2(-s.b));
                 const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                 d = __fadd2_rn(d, e);
-                a = __ffma2_rn(e, make_float2(ent_x(x.x), ent_x(x.y)), a);
+                if (CLAMP) x = make_float2(ent_x(x.x), ent_x(x.y));
+                a = __ffma2_rn(e, x, a);
             }
         }
         const float sum = d.x + d.y;
@@ -126,6 +129,20 @@ __device__ __forceinline__ void packs_ent(const uint4 (&raw)[PK], RowEnt &r, flo
     }
     r.a += a.x + a.y;
     r.d += d.x + d.y;
+}
+// The clamp is one instruction a logit of seven: left out until a thread finds its
+// A without a value, which -inf leaves (0 times -inf); then the packs at hand are
+// taken again.
+template <typename T, int PK>
+__device__ __forceinline__ void packs_ent(const uint4 (&raw)[PK], RowEnt &r, float c, bool &clamp) {
+    const RowEnt before = r;
+    if (!clamp) {
+        packs_ent_any<T, PK, false>(raw, r, c);
+        clamp = __any_sync(0xffffffffu, r.a != r.a);
+        if (!clamp) return;
+        r = before;
+    }
+    packs_ent_any<T, PK, true>(raw, r, c);
 }
 __device__ __forceinline__ void one_ent(float z, RowEnt &r, float c) {
     if (z > r.m) ent_to(r, z, c);
@@ -196,7 +213,8 @@ __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs
             if (p * 32 < w.mine) raw[p] = ld_once(w.body + p * 32 * V);
         }
         RowEnt r{packs_max<PK>(raw, T()), 0.f, 0.f};
-        packs_ent<T, PK>(raw, r, c);
+        bool clamp = false;
+        packs_ent<T, PK>(raw, r, c, clamp);
         float tm = r.m;
         if (has) {
             one_ent(zs, r, c);
@@ -238,7 +256,7 @@ __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs
 // over it in segments of TH x PK packs, the next segment on its way into shared
 // memory meanwhile.
 // ---------------------------------------------------------------------------
-constexpr int kTopGroups = 16;  // a thread's groups: their maxima wait in shared memory
+constexpr int kTopGroups = 8;  // a thread's groups: their maxima wait in shared memory
 
 template <typename T> struct TopSlice {
     const T *z, *body;
@@ -265,11 +283,13 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
     extern __shared__ __align__(16) uint4 next_row[];                                     // [PK][TH]
     float *const group_max = reinterpret_cast<float *>(next_row + PK * TH);               // [kTopGroups][TH]
     unsigned short *const found = reinterpret_cast<unsigned short *>(group_max + kTopGroups * TH);  // [kTopGroups * TH]
-    __shared__ RowEnt slot[NW];
+    __shared__ RowEnt slot[2][NW];
+    __shared__ __align__(16) uint32_t tops[2][NW * 4];  // each warp's four largest
     __shared__ uint64_t keys[(NW > CSMAX ? NW : CSMAX) * 32];
     __shared__ uint64_t pub_keys[2][32];
     __shared__ RowEnt pub[2];
-    __shared__ int count[2], per_group[kTopGroups];
+    __shared__ int count, held[NW], per_group[kTopGroups];
+    static_assert(NW == 8, "a lane's key for each of the warps' four largest");
     const LogitArgs &a = ta.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k = ta.k;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
@@ -277,6 +297,8 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
     pdl_launch_dependents();
     const float c = a.scale * kLog2e;
     int parity = 1;
+    bool clamp = false;
+    if (t == 0) count = 0;  // the first row's barrier is ahead of its first use
     const int64_t first = (int64_t)(blockIdx.x / cs) * batch, step = (int64_t)(gridDim.x / cs) * batch;
     for (int64_t r0 = first; r0 < a.rows; r0 += step) {
         const bool have = lane < batch && r0 + lane < a.rows;
@@ -333,74 +355,105 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
                     ++group;
                 }
                 ent_to(r, m, c);
-                packs_ent<T, PK>(raw, r, c);
+                packs_ent<T, PK>(raw, r, c, clamp);
             }
             if (has) {
                 one_ent(zs, r, c);
                 tm = fmaxf(tm, zs);
             }
             r = lanes_ent(r, c);
-            if (lane == 0) slot[warp] = r;
-            if (t == 0) count[0] = count[1] = 0;
-            if (t < kTopGroups) per_group[t] = 0;
-            __syncthreads();
-            r = lane < NW ? slot[lane] : RowEnt{-INFINITY, 0.f, 0.f};
-            r = lanes_ent(r, c);
-            uint64_t best = 0;  // thread i < k: the i-th largest key of this CTA's slice
+            if (lane == 0) slot[parity][warp] = r;
             if (k > 0) {
-                const uint32_t om = top_ordered(tm) >> 16;
-                uint32_t T16 = 0;
-#pragma unroll 1
-                for (int b = 15; b >= 0; --b) {
-                    const uint32_t v = T16 | 1u << b;
-                    if (__syncthreads_count(om >= v) >= k) T16 = v;
-                }
-                const uint32_t T32 = T16 << 16 > kTopNone ? T16 << 16 : kTopNone + 1u;
-                TopList list;
-                // one element a lane and pass: a group's packs are TH apart
-                auto scan = [&](int n) {
-                    constexpr int PASS = PK * V / 32 > 0 ? PK * V / 32 : 1, LANES = PK * V < 32 ? PK * V : 32;
-                    for (int i = warp; i < n; i += NW) {
-                        const int code = found[i], g = code / TH, th = code % TH;
-                        for (int sub = 0; sub < per; ++sub) {
-                            float f[PASS];
-                            int idx[PASS];
+                uint32_t v = top_ordered(tm);
 #pragma unroll
-                            for (int q = 0; q < PASS; ++q) {
-                                const int e = q * 32 + lane, p = e / V;
-                                const int64_t pack = ((int64_t)(g * per + sub) * PK + p) * TH + th;
-                                idx[q] = -1;
-                                f[q] = -INFINITY;
-                                if (lane < LANES && pack < w.packs) {
-                                    idx[q] = (int)(w.head + (w.p0 + pack) * V + e % V);
-                                    f[q] = IO<T>::to_f(w.z[idx[q]]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t m = __reduce_max_sync(ALL, v);
+                    if (lane == i) tops[parity][warp * 4 + i] = m;
+                    if (lane == __ffs(__ballot_sync(ALL, v == m)) - 1) v = 0u;
+                }
+            }
+            __syncthreads();
+            r = lane < NW ? slot[parity][lane] : RowEnt{-INFINITY, 0.f, 0.f};
+            r = lanes_ent(r, c);
+            uint64_t best = 0;  // cs > 1: thread i < k, the i-th largest key
+            if (k > 0) {
+                // T: the k-th of those 32, maxima of as many threads
+                uint32_t T32;
+                {
+                    const uint32_t v = tops[parity][lane];
+                    int place = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 o = reinterpret_cast<const uint4 *>(tops[parity])[i];
+                        place += (o.x > v || (o.x == v && 4 * i < lane)) + (o.y > v || (o.y == v && 4 * i + 1 < lane)) +
+                                 (o.z > v || (o.z == v && 4 * i + 2 < lane)) + (o.w > v || (o.w == v && 4 * i + 3 < lane));
+                    }
+                    T32 = __shfl_sync(ALL, v, __ffs(__ballot_sync(ALL, place == k - 1)) - 1);
+                    if (T32 <= kTopNone) T32 = kTopNone + 1u;
+                }
+                TopList list;
+                // the found groups, four at a time in flight: a lane's elements, an
+                // element a pass, are TH packs apart
+                auto scan = [&](int n) {
+                    constexpr int PASS = PK * V / 32;
+                    static_assert(PASS >= 1, "a group has an element for each lane");
+                    for (int i0 = warp; i0 < n; i0 += 4 * NW) {
+                        for (int sub = 0; sub < per; ++sub) {
+                            float f[4][PASS];
+                            int idx[4][PASS];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int i = i0 + j * NW;
+                                const int code = i < n ? found[i] : 0, g = code / TH, th = code % TH;
+#pragma unroll
+                                for (int q = 0; q < PASS; ++q) {
+                                    const int e = q * 32 + lane, pack = ((g * per + sub) * PK + e / V) * TH + th;
+                                    f[j][q] = -INFINITY;
+                                    idx[j][q] = w.head + (w.p0 + pack) * V + e % V;
+                                    if (i < n && pack < w.packs) f[j][q] = IO<T>::to_f(w.z[idx[j][q]]);
                                 }
                             }
 #pragma unroll
-                            for (int q = 0; q < PASS; ++q)
-                                list.offer(top_finite(f[q]) && top_ordered(f[q]) >= T32, top_key(f[q], (uint32_t)idx[q]), k, lane);
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int q = 0; q < PASS; ++q)
+                                    if (i0 + j * NW < n)
+                                        list.offer(top_finite(f[j][q]) && top_ordered(f[j][q]) >= T32,
+                                                   top_key(f[j][q], (uint32_t)idx[j][q]), k, lane);
                         }
                     }
                 };
-                for (int g = 0; g < group; ++g) {
-                    const uint32_t who = __ballot_sync(ALL, top_ordered(group_max[g * TH + t]) >= T32);
-                    if (who && lane == 0) atomicAdd(&per_group[g], __popc(who));
-                }
+                // (the places in the list are in no order: the result has one, and
+                // that of its keys)
+                for (int g = 0; g < group; ++g)
+                    if (top_ordered(group_max[g * TH + t]) >= T32) found[atomicAdd(&count, 1)] = (unsigned short)(g * TH + t);
                 __syncthreads();
-                // groups up to `cut` hold k candidates; where there are many more
-                // (ties), later ones count only with a larger maximum
-                int sum = 0, cut = group;
-                for (int g = 0; g < group; ++g) {
-                    sum += per_group[g];
-                    if (sum >= k && cut == group) cut = g + 1;
+                int n = count, cut = group;
+                if (n > 8 * 32) {
+                    // Many more than k (ties): groups up to `cut` hold k candidates, and
+                    // later ones count only with a larger maximum.
+                    __syncthreads();
+                    if (t < kTopGroups) per_group[t] = 0;
+                    if (t == 0) count = 0;
+                    __syncthreads();
+                    for (int g = 0; g < group; ++g) {
+                        const uint32_t who = __ballot_sync(ALL, top_ordered(group_max[g * TH + t]) >= T32);
+                        if (who && lane == 0) atomicAdd(&per_group[g], __popc(who));
+                    }
+                    __syncthreads();
+                    int sum = 0;
+                    for (int g = 0; g < group && sum < k; ++g) {
+                        sum += per_group[g];
+                        cut = g + 1;
+                    }
+                    for (int g = 0; g < cut; ++g)
+                        if (top_ordered(group_max[g * TH + t]) >= T32) found[atomicAdd(&count, 1)] = (unsigned short)(g * TH + t);
+                    __syncthreads();
+                    n = count;
                 }
-                if (sum <= 8 * 32) cut = group;
-                for (int g = 0; g < cut; ++g)
-                    if (top_ordered(group_max[g * TH + t]) >= T32) found[atomicAdd(&count[0], 1)] = (unsigned short)(g * TH + t);
-                __syncthreads();
-                scan(count[0]);
+                scan(n);
                 if (warp == 0) list.offer(has && top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
-                // the entries' ranks among all warps' sorted lists
+                // an entry's rank among all warps' sorted lists
                 auto rank_of = [&](uint64_t v, int lists) {
                     int place = 0;
                     for (int q = 0; q < lists; ++q) {
@@ -413,34 +466,39 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
                     }
                     return place;
                 };
-                keys[t] = list.key;  // [warp][lane]
-                if (t < 32) pub_keys[parity][t] = 0;
-                __syncthreads();
-                if (list.key) {
-                    const int place = rank_of(list.key, NW);
-                    if (place < k) pub_keys[parity][place] = list.key;
-                }
-                __syncthreads();
+                auto share = [&] {
+                    keys[t] = list.key;  // [warp][lane]
+                    const int n = __popc(__ballot_sync(ALL, list.key != 0));
+                    if (lane == 0) held[warp] = n;
+                    __syncthreads();
+                };
+                share();
+                if (t == 0) count = 0;  // nobody reads it before the next barrier
                 if (cut < group) {
-                    // the same for the rest, from the k-th key on
+                    // the rest, from the k-th key on
+                    if (list.key && rank_of(list.key, NW) == k - 1) pub_keys[parity][k - 1] = list.key;
+                    __syncthreads();
                     const uint32_t kth = (uint32_t)(pub_keys[parity][k - 1] >> 32);
                     for (int g = cut; g < group; ++g)
-                        if (top_ordered(group_max[g * TH + t]) > kth)
-                            found[atomicAdd(&count[1], 1)] = (unsigned short)(g * TH + t);
+                        if (top_ordered(group_max[g * TH + t]) > kth) found[atomicAdd(&count, 1)] = (unsigned short)(g * TH + t);
                     __syncthreads();
-                    if (count[1]) {
-                        scan(count[1]);
-                        keys[t] = list.key;
-                        if (t < 32) pub_keys[parity][t] = 0;
-                        __syncthreads();
-                        if (list.key) {
-                            const int place = rank_of(list.key, NW);
-                            if (place < k) pub_keys[parity][place] = list.key;
-                        }
-                        __syncthreads();
-                    }
+                    scan(count);
+                    __syncthreads();
+                    if (t == 0) count = 0;
+                    share();
                 }
-                if (t < k) best = pub_keys[parity][t];
+                int total = 0;
+#pragma unroll
+                for (int q = 0; q < NW; ++q) total += held[q];
+                const int place = list.key ? rank_of(list.key, NW) : k;
+                if (cs == 1) {
+                    if (place < k) top_place(ta, row, place, list.key, r);
+                    if (t >= total && t < k) top_place(ta, row, t, 0, r);
+                } else {
+                    if (place < k) pub_keys[parity][place] = list.key;
+                    if (t >= total && t < k) pub_keys[parity][t] = 0;
+                    __syncthreads();
+                }
                 if (cs > 1) {
                     if (t == 0) pub[parity] = r;
                     cluster_arrive();
@@ -479,10 +537,10 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
                     r = lanes_ent(r, c);
                 }
                 if (t == 0) top_row(ta, row, r, za);
-                if (t < k) top_place(ta, row, t, best, r);
+                if (cs > 1 && t < k) top_place(ta, row, t, best, r);
             }
-            // the next row's slots and lists
-            __syncthreads();
+            // The next row's slots and tops are the other ones, and whatever else is
+            // shared is written behind its first barrier.
         }
     }
     if (cs > 1) {
@@ -655,7 +713,7 @@ template <typename T> cudaError_t launch_logit_top_t(const TopArgs &a, int sms, 
         return packs <= 32 * 8 ? launch_top_warp<T, 8, 6>(a, s, p) : launch_top_warp<T, 16, 4>(a, s, p);
     int cs = 1;
     while (cs < 8 && a.a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * 256) cs *= 2;
-    return launch_top_cta<T, 256, 8, 3>(a, cs, sms, s, p);
+    return launch_top_cta<T, 256, 8, 4>(a, cs, sms, s, p);
 }
 
 template <typename T, int TH> cudaError_t launch_top_grad_g(const TopArgs &a, cudaStream_t s) {

@@ -620,11 +620,13 @@ __device__ __forceinline__ float oct_max(float v) {
     return v;
 }
 
-#ifndef RT_M
-#define RT_M 3
-#endif
+template <typename T> __device__ __forceinline__ uint4 no_expert() {  // a pack of -inf
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+
 template <typename T, int NC, int MODE>
-__global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const RouteArgs a) {
     constexpr uint32_t ALL = 0xffffffffu;
     constexpr int PL = 8 * NC;
     // SCORE: the biases in fixed point, a lane's 8 NC together and 4 apart from the
@@ -679,36 +681,33 @@ __global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const Ro
         const T *row = static_cast<const T *>(a.x) + t * a.ldx;
         // a lane's logits: whole packs, or one by one
         constexpr int W = 8 / IO<T>::V;  // packs a chunk
-        uint4 raw[NC][W];
-        if (a.oct_wide) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
+        auto fetch = [&](int c, uint4 (&raw)[W]) {
+            if (a.oct_wide) {
 #pragma unroll
                 for (int w = 0; w < W; ++w)
-                    raw[c][w] = n > 0 ? ld_once(row + first + c * 8 + w * IO<T>::V) : make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
+                    raw[w] = n > 0 ? *reinterpret_cast<const uint4 *>(row + first + c * 8 + w * IO<T>::V) : no_expert<T>();
+            } else {
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = c * 8 + i < n ? IO<T>::to_f(row[first + c * 8 + i]) : -INFINITY;
 #pragma unroll
-                for (int w = 0; w < W; ++w) raw[c][w] = IO<T>::pack(v + w * IO<T>::V);
+                for (int w = 0; w < W; ++w) raw[w] = IO<T>::pack(v + w * IO<T>::V);
             }
-        }
+        };
+        auto unpack = [&](const uint4 (&raw)[W], float (&x)[8]) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) IO<T>::unpack(raw[w], x + w * IO<T>::V);
+        };
         auto chunk = [&](int c, float (&x)[8]) {
-#pragma unroll
-            for (int w = 0; w < W; ++w) IO<T>::unpack(raw[c][w], x + w * IO<T>::V);
-            if (a.oct_wide && n == 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
-            }
+            uint4 raw[W];
+            fetch(c, raw);
+            unpack(raw, x);
         };
         // the softmax' maximum and sum, where they are needed; binary32 logits' largest
         float m = 0.f, d = 1.f, inv = 1.f;
         if (MODE == KEY_LOGIT || (a.softmax && a.need_sum)) {
             m = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < NC; ++c) {
                 float x[8];
                 chunk(c, x);
@@ -721,7 +720,7 @@ __global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const Ro
         if (a.softmax && a.need_sum) {
             m = m == -INFINITY ? 0.f : m;
             d = 0.f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < NC; ++c) {
                 float x[8];
                 chunk(c, x);
@@ -732,7 +731,7 @@ __global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const Ro
             inv = 1.f / d;
         }
         if (a.scores && real) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < NC; ++c) {
                 float x[8];
                 chunk(c, x);
@@ -751,10 +750,16 @@ __global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const Ro
             // as in route_fwd_kernel; the sum is at most 8 NC + 3 additions deep
             near_ = 2.f * (S * (a.softmax ? (6e-7f + 6e-8f * (PL + 3)) * inv : 3e-7f) + near_bias);
 #pragma unroll
+        for (int i = 0; i < 8; ++i) list[i] = 0u;
+        uint4 coming[W];
+        fetch(0, coming);
+        // (one copy of the loop's code: four did not fit the instruction cache)
+#pragma unroll 1
         for (int c = 0; c < NC; ++c) {
             float x[8];
             uint32_t key[8];
-            chunk(c, x);
+            unpack(coming, x);
+            if (c + 1 < NC) fetch(c + 1, coming);
             if constexpr (MODE == KEY_WHOLE) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -795,12 +800,7 @@ __global__ void __launch_bounds__(kRouteThreads, RT_M) route_oct_kernel(const Ro
                 }
             }
             sort_desc<8>(key);
-            if (c == 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) list[i] = key[i];
-            } else {
-                merge8(list, key);
-            }
+            merge8(list, key);
         }
         if (limited) {
             uint32_t b1 = list[0] >> kIdxBits, b2 = list[1] >> kIdxBits;
