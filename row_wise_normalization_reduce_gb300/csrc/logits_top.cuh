@@ -65,6 +65,39 @@ struct TopList {
     }
 };
 
+// Candidates in shared memory, in no order: one key is one logit, so the places
+// that their ranks give them do not depend on it.
+#ifndef TOP_M
+#define TOP_M 4
+#endif
+constexpr int kTopCand = 256;
+__device__ __forceinline__ void top_add(bool on, uint64_t key, uint64_t *cand, int *n) {
+    if (on) {
+        const int at = atomicAdd(n, 1);
+        if (at < kTopCand) cand[at] = key;
+    }
+}
+__device__ __forceinline__ int top_rank(const uint64_t *cand, int n, uint64_t v) {
+    int place = 0, i = 0;
+    for (; i + 4 <= n; i += 4) {
+        const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(cand + i), q = *reinterpret_cast<const ulonglong2 *>(cand + i + 2);
+        place += (p.x > v) + (p.y > v) + (q.x > v) + (q.y > v);
+    }
+    for (; i < n; ++i) place += cand[i] > v;
+    return place;
+}
+// By `threads` threads, of which this is t: `put` takes the first k places, 0 where
+// there is none.
+template <typename F>
+__device__ __forceinline__ void top_ranks(const uint64_t *cand, int n, int k, int t, int threads, F put) {
+    for (int i = t; i < n; i += threads) {
+        const uint64_t v = cand[i];
+        const int place = top_rank(cand, n, v);
+        if (place < k) put(place, v);
+    }
+    if (t >= n && t < k) put(t, 0);
+}
+
 // (maximum, sum, A) of a set of logits.
 struct RowEnt {
     float m, d, a;
@@ -191,12 +224,14 @@ __device__ __forceinline__ void top_place(const TopArgs &t, int64_t row, int pla
 template <typename T, int PK, int MINB>
 __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs ta) {
     constexpr int V = IO<T>::V;
+    __shared__ __align__(16) uint64_t cand[4][kTopCand];
+    __shared__ int count[4];
     const LogitArgs &a = ta.a;
-    const int lane = threadIdx.x & 31, k = ta.k;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = ta.k;
     pdl_wait();
     pdl_launch_dependents();
     const float c = a.scale * kLog2e;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < a.rows; row += (int64_t)gridDim.x * 4) {
+    for (int64_t row = (int64_t)blockIdx.x * 4 + warp; row < a.rows; row += (int64_t)gridDim.x * 4) {
         const int64_t tgt = a.target[row];
         if (tgt < 0 || tgt >= a.V) {
             if (lane == 0) top_no_row(ta, row);
@@ -232,7 +267,11 @@ __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs
             if (__popc(__ballot_sync(0xffffffffu, om >= t)) >= k) T16 = t;
         }
         const uint32_t T32 = T16 << 16 > kTopNone ? T16 << 16 : kTopNone + 1u;
-        TopList list;
+        // (a prefix below that of the lowest finite value stands for it: compared as
+        // values, NaN and -inf fail)
+        const float low = fmaxf(top_value(T32), -3.4028235e38f);
+        if (lane == 0) count[warp] = 0;
+        __syncwarp();
 #pragma unroll
         for (int p = 0; p < PK; ++p) {
             float f[V];
@@ -240,13 +279,34 @@ __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs
             float pm = f[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) pm = fmaxf(pm, f[i]);
-            if (!__any_sync(0xffffffffu, top_ordered(pm) >= T32)) continue;
+            if (!(pm >= low)) continue;
             const uint32_t at = (uint32_t)(w.head + (lane + p * 32) * V);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                list.offer(top_finite(f[i]) && top_ordered(f[i]) >= T32, top_key(f[i], at + i), k, lane);
+            for (int i = 0; i < V; ++i) top_add(f[i] >= low, top_key(f[i], at + i), cand[warp], &count[warp]);
         }
-        list.offer(has && top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
+        top_add(has && zs >= low, top_key(zs, (uint32_t)w.sc), cand[warp], &count[warp]);
+        __syncwarp();
+        const int n = count[warp];
+        if (n <= kTopCand) {
+            top_ranks(cand[warp], n, k, lane, 32, [&](int place, uint64_t key) { top_place(ta, row, place, key, r); });
+            __syncwarp();
+            continue;
+        }
+        // many more than k (ties): a sorted list of the largest so far
+        TopList list;
+#pragma unroll 1
+        for (int p = 0; p < PK; ++p) {
+            uint4 q = raw[0];
+#pragma unroll
+            for (int j = 1; j < PK; ++j)
+                if (j == p) q = raw[j];
+            float f[V];
+            IO<T>::unpack(q, f);
+            const uint32_t at = (uint32_t)(w.head + (lane + p * 32) * V);
+#pragma unroll
+            for (int i = 0; i < V; ++i) list.offer(f[i] >= low, top_key(f[i], at + i), k, lane);
+        }
+        list.offer(has && zs >= low, top_key(zs, (uint32_t)w.sc), k, lane);
         if (lane < k) top_place(ta, row, lane, list.key, r);
     }
 }
@@ -276,20 +336,60 @@ template <typename T> struct TopSlice {
     }
 };
 
+// What the CTA's warps share.  The arrays of two alternate between rows.
+constexpr int kTopWarps = 8, kTopClusterMax = 8;
+struct TopShared {
+    RowEnt slot[2][kTopWarps];
+    __align__(16) uint32_t tops[2][kTopWarps * 4];  // each warp's four largest
+    __align__(16) uint64_t cand[kTopCand];  // room for every warp's list
+    float target[2], ends[2][16];           // the target's logit; the row's scalar elements
+    uint64_t pub_keys[2][32];
+    RowEnt pub[2];
+    int groups_found[2], cands[2], per_group[kTopGroups];
+};
+static_assert(kTopWarps == kTopClusterMax && kTopCand == kTopWarps * 32, "a warp reads one CTA's list");
+
+// A found group's elements, PASS a lane (a group's packs are TH apart), four groups
+// in flight: `use` gets each value and its column.
+template <typename T, int TH, int PK, typename F>
+__device__ __forceinline__ void top_scan(const TopSlice<T> &w, const unsigned short *found, int n, int per, F use) {
+    constexpr int NW = TH / 32, V = IO<T>::V, PASS = PK * V / 32;
+    static_assert(PASS >= 1, "a group has an element for each lane");
+    const int lane = threadIdx.x & 31;
+    for (int i0 = threadIdx.x >> 5; i0 < n; i0 += 4 * NW) {
+        for (int sub = 0; sub < per; ++sub) {
+            float f[4][PASS];
+            int idx[4][PASS];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * NW;
+                const int code = i < n ? found[i] : 0, g = code / TH, th = code % TH;
+#pragma unroll
+                for (int q = 0; q < PASS; ++q) {
+                    const int e = q * 32 + lane, pack = ((g * per + sub) * PK + e / V) * TH + th;
+                    f[j][q] = -INFINITY;
+                    idx[j][q] = w.head + (w.p0 + pack) * V + e % V;
+                    if (i < n && pack < w.packs) f[j][q] = IO<T>::to_f(w.z[idx[j][q]]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < PASS; ++q)
+                    if (i0 + j * NW < n) use(f[j][q], (uint32_t)idx[j][q]);
+        }
+    }
+}
+
 template <typename T, int TH, int PK, int MINB>
 __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, const int cs, const int batch) {
-    constexpr int NW = TH / 32, V = IO<T>::V, CSMAX = 8;
+    constexpr int V = IO<T>::V;
+    static_assert(TH == 32 * kTopWarps, "as TopShared has it");
     constexpr uint32_t ALL = 0xffffffffu;
     extern __shared__ __align__(16) uint4 next_row[];                                     // [PK][TH]
     float *const group_max = reinterpret_cast<float *>(next_row + PK * TH);               // [kTopGroups][TH]
     unsigned short *const found = reinterpret_cast<unsigned short *>(group_max + kTopGroups * TH);  // [kTopGroups * TH]
-    __shared__ RowEnt slot[2][NW];
-    __shared__ __align__(16) uint32_t tops[2][NW * 4];  // each warp's four largest
-    __shared__ uint64_t keys[(NW > CSMAX ? NW : CSMAX) * 32];
-    __shared__ uint64_t pub_keys[2][32];
-    __shared__ RowEnt pub[2];
-    __shared__ int count, held[NW], per_group[kTopGroups];
-    static_assert(NW == 8, "a lane's key for each of the warps' four largest");
+    __shared__ TopShared sh;
     const LogitArgs &a = ta.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k = ta.k;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
@@ -298,7 +398,7 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
     const float c = a.scale * kLog2e;
     int parity = 1;
     bool clamp = false;
-    if (t == 0) count = 0;  // the first row's barrier is ahead of its first use
+    if (t == 0) sh.groups_found[0] = sh.cands[0] = 0;  // the first row's barrier is ahead of their first use
     const int64_t first = (int64_t)(blockIdx.x / cs) * batch, step = (int64_t)(gridDim.x / cs) * batch;
     for (int64_t r0 = first; r0 < a.rows; r0 += step) {
         const bool have = lane < batch && r0 + lane < a.rows;
@@ -323,14 +423,12 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
             live &= live - 1;
             parity ^= 1;
             const TopSlice<T> w(a, row, rank, cs, t);
-            const bool has = t < w.ns;
-            const float zs = has ? zn : -INFINITY;
-            const float za = t == 0 ? IO<T>::to_f(w.z[tgt]) : 0.f;
+            if (t < w.ns) sh.ends[parity][t] = zn;
+            if (t == 0) sh.target[parity] = IO<T>::to_f(w.z[tgt]);
             const int segs = w.packs > 0 ? (w.packs - 1) / (TH * PK) + 1 : 1;
-            const int per = (segs - 1) / kTopGroups + 1;  // segments of a group
+            int log_per = 0;  // segments of a group: 2^log_per
+            while ((segs - 1) >> log_per >= kTopGroups) ++log_per;
             RowEnt r{-INFINITY, 0.f, 0.f};
-            float tm = -INFINITY, gm = -INFINITY;
-            int in_group = 0, group = 0;
             for (int seg = 0; seg < segs; ++seg) {
                 cp_async_wait();
                 uint4 raw[PK];
@@ -346,201 +444,152 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
                     fetch(row, seg + 1);
                 else if (live)
                     fetch(r0 + __ffs(live) - 1, 0);
-                gm = fmaxf(gm, m);
-                if (++in_group == per || seg + 1 == segs) {
-                    group_max[group * TH + t] = gm;
-                    tm = fmaxf(tm, gm);
-                    gm = -INFINITY;
-                    in_group = 0;
-                    ++group;
-                }
+                float &gm = group_max[(seg >> log_per) * TH + t];
+                gm = seg & ((1 << log_per) - 1) ? fmaxf(gm, m) : m;
                 ent_to(r, m, c);
                 packs_ent<T, PK>(raw, r, c, clamp);
             }
-            if (has) {
+            const int group = ((segs - 1) >> log_per) + 1, per = 1 << log_per;
+            float tm = -INFINITY;
+            if (k > 0)
+                for (int g = 0; g < group; ++g) tm = fmaxf(tm, group_max[g * TH + t]);
+            if (t < w.ns) {
+                const float zs = sh.ends[parity][t];
                 one_ent(zs, r, c);
                 tm = fmaxf(tm, zs);
             }
             r = lanes_ent(r, c);
-            if (lane == 0) slot[parity][warp] = r;
+            if (lane == 0) sh.slot[parity][warp] = r;
             if (k > 0) {
                 uint32_t v = top_ordered(tm);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t m = __reduce_max_sync(ALL, v);
-                    if (lane == i) tops[parity][warp * 4 + i] = m;
+                    if (lane == i) sh.tops[parity][warp * 4 + i] = m;
                     if (lane == __ffs(__ballot_sync(ALL, v == m)) - 1) v = 0u;
                 }
             }
             __syncthreads();
-            r = lane < NW ? slot[parity][lane] : RowEnt{-INFINITY, 0.f, 0.f};
-            r = lanes_ent(r, c);
-            uint64_t best = 0;  // cs > 1: thread i < k, the i-th largest key
             if (k > 0) {
-                // T: the k-th of those 32, maxima of as many threads
+                // T: the k-th of those 32, maxima of as many threads.  (The k-th of their
+                // different values is one redux.max each, but 16-bit logits have many
+                // equal ones: 4096 x 131072 bf16 with 20 alternatives 169 us.)
                 uint32_t T32;
                 {
-                    const uint32_t v = tops[parity][lane];
+                    const uint32_t v = sh.tops[parity][lane];
                     int place = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 o = reinterpret_cast<const uint4 *>(tops[parity])[i];
+                        const uint4 o = reinterpret_cast<const uint4 *>(sh.tops[parity])[i];
                         place += (o.x > v || (o.x == v && 4 * i < lane)) + (o.y > v || (o.y == v && 4 * i + 1 < lane)) +
                                  (o.z > v || (o.z == v && 4 * i + 2 < lane)) + (o.w > v || (o.w == v && 4 * i + 3 < lane));
                     }
                     T32 = __shfl_sync(ALL, v, __ffs(__ballot_sync(ALL, place == k - 1)) - 1);
                     if (T32 <= kTopNone) T32 = kTopNone + 1u;
                 }
-                TopList list;
-                // the found groups, four at a time in flight: a lane's elements, an
-                // element a pass, are TH packs apart
-                auto scan = [&](int n) {
-                    constexpr int PASS = PK * V / 32;
-                    static_assert(PASS >= 1, "a group has an element for each lane");
-                    for (int i0 = warp; i0 < n; i0 += 4 * NW) {
-                        for (int sub = 0; sub < per; ++sub) {
-                            float f[4][PASS];
-                            int idx[4][PASS];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int i = i0 + j * NW;
-                                const int code = i < n ? found[i] : 0, g = code / TH, th = code % TH;
-#pragma unroll
-                                for (int q = 0; q < PASS; ++q) {
-                                    const int e = q * 32 + lane, pack = ((g * per + sub) * PK + e / V) * TH + th;
-                                    f[j][q] = -INFINITY;
-                                    idx[j][q] = w.head + (w.p0 + pack) * V + e % V;
-                                    if (i < n && pack < w.packs) f[j][q] = IO<T>::to_f(w.z[idx[j][q]]);
-                                }
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                                for (int q = 0; q < PASS; ++q)
-                                    if (i0 + j * NW < n)
-                                        list.offer(top_finite(f[j][q]) && top_ordered(f[j][q]) >= T32,
-                                                   top_key(f[j][q], (uint32_t)idx[j][q]), k, lane);
-                        }
-                    }
-                };
-                // (the places in the list are in no order: the result has one, and
-                // that of its keys)
                 for (int g = 0; g < group; ++g)
-                    if (top_ordered(group_max[g * TH + t]) >= T32) found[atomicAdd(&count, 1)] = (unsigned short)(g * TH + t);
+                    if (top_ordered(group_max[g * TH + t]) >= T32)
+                        found[atomicAdd(&sh.groups_found[parity], 1)] = (unsigned short)(g * TH + t);
                 __syncthreads();
-                int n = count, cut = group;
-                if (n > 8 * 32) {
-                    // Many more than k (ties): groups up to `cut` hold k candidates, and
-                    // later ones count only with a larger maximum.
+                int n = sh.groups_found[parity], cut = group;
+                if (n > kTopCand) {
+                    // Many more than k (ties): groups up to `cut` hold k candidates, and later
+                    // ones count only with a larger maximum.
                     __syncthreads();
-                    if (t < kTopGroups) per_group[t] = 0;
-                    if (t == 0) count = 0;
+                    if (t < kTopGroups) sh.per_group[t] = 0;
+                    if (t == 0) sh.groups_found[parity] = 0;
                     __syncthreads();
                     for (int g = 0; g < group; ++g) {
                         const uint32_t who = __ballot_sync(ALL, top_ordered(group_max[g * TH + t]) >= T32);
-                        if (who && lane == 0) atomicAdd(&per_group[g], __popc(who));
+                        if (who && lane == 0) atomicAdd(&sh.per_group[g], __popc(who));
                     }
                     __syncthreads();
                     int sum = 0;
                     for (int g = 0; g < group && sum < k; ++g) {
-                        sum += per_group[g];
+                        sum += sh.per_group[g];
                         cut = g + 1;
                     }
                     for (int g = 0; g < cut; ++g)
-                        if (top_ordered(group_max[g * TH + t]) >= T32) found[atomicAdd(&count, 1)] = (unsigned short)(g * TH + t);
+                        if (top_ordered(group_max[g * TH + t]) >= T32)
+                            found[atomicAdd(&sh.groups_found[parity], 1)] = (unsigned short)(g * TH + t);
                     __syncthreads();
-                    n = count;
+                    n = sh.groups_found[parity];
                 }
-                scan(n);
-                if (warp == 0) list.offer(has && top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
-                // an entry's rank among all warps' sorted lists
-                auto rank_of = [&](uint64_t v, int lists) {
-                    int place = 0;
-                    for (int q = 0; q < lists; ++q) {
-                        int lo = 0;  // how many of list q are larger
-#pragma unroll
-                        for (int h = 16; h > 0; h >>= 1)
-                            if (keys[q * 32 + lo + h - 1] > v) lo += h;
-                        if (lo == 31 && keys[q * 32 + 31] > v) lo = 32;
-                        place += lo;
+                TopList list;
+                bool again = false;
+                while (true) {
+                    top_scan<T, TH, PK>(w, found, n, per, [&](float f, uint32_t at) {
+                        list.offer(top_finite(f) && top_ordered(f) >= T32, top_key(f, at), k, lane);
+                    });
+                    if (warp == 0 && !again) {
+                        const float zs = t < w.ns ? sh.ends[parity][t] : -INFINITY;
+                        list.offer(top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
                     }
-                    return place;
-                };
-                auto share = [&] {
-                    keys[t] = list.key;  // [warp][lane]
-                    const int n = __popc(__ballot_sync(ALL, list.key != 0));
-                    if (lane == 0) held[warp] = n;
+                    // the warps' lists, one behind the other
+                    const uint32_t held = __ballot_sync(ALL, list.key != 0);
+                    int base = 0;
+                    if (lane == 0 && held) base = atomicAdd(&sh.cands[parity], __popc(held));
+                    base = __shfl_sync(ALL, base, 0);
+                    if (list.key) sh.cand[base + lane] = list.key;
+                    if (t == 0) sh.groups_found[parity ^ 1] = sh.cands[parity ^ 1] = 0;  // the next row's
                     __syncthreads();
-                };
-                share();
-                if (t == 0) count = 0;  // nobody reads it before the next barrier
-                if (cut < group) {
+                    if (cut == group) break;
                     // the rest, from the k-th key on
-                    if (list.key && rank_of(list.key, NW) == k - 1) pub_keys[parity][k - 1] = list.key;
+                    const int nc = sh.cands[parity];
+                    if (t < nc && top_rank(sh.cand, nc, sh.cand[t]) == k - 1) sh.pub_keys[parity][k - 1] = sh.cand[t];
                     __syncthreads();
-                    const uint32_t kth = (uint32_t)(pub_keys[parity][k - 1] >> 32);
-                    for (int g = cut; g < group; ++g)
-                        if (top_ordered(group_max[g * TH + t]) > kth) found[atomicAdd(&count, 1)] = (unsigned short)(g * TH + t);
+                    const uint32_t kth = (uint32_t)(sh.pub_keys[parity][k - 1] >> 32);
+                    if (t == 0) sh.groups_found[parity] = sh.cands[parity] = 0;
                     __syncthreads();
-                    scan(count);
+                    for (; cut < group; ++cut)
+                        if (top_ordered(group_max[cut * TH + t]) > kth)
+                            found[atomicAdd(&sh.groups_found[parity], 1)] = (unsigned short)(cut * TH + t);
                     __syncthreads();
-                    if (t == 0) count = 0;
-                    share();
+                    n = sh.groups_found[parity];
+                    again = true;
                 }
-                int total = 0;
-#pragma unroll
-                for (int q = 0; q < NW; ++q) total += held[q];
-                const int place = list.key ? rank_of(list.key, NW) : k;
+            }
+            // The row's outputs, by the threads that find a candidate.  (For one warp
+            // alone, while the others go on, the compiler spilled 53 registers a row.)
+            // A warp without one goes on to the next row, whose first barrier is ahead
+            // of what it would overwrite.
+            {
+                r = lanes_ent(lane < kTopWarps ? sh.slot[parity][lane] : RowEnt{-INFINITY, 0.f, 0.f}, c);
+                const int nc = k > 0 ? sh.cands[parity] : 0;
                 if (cs == 1) {
-                    if (place < k) top_place(ta, row, place, list.key, r);
-                    if (t >= total && t < k) top_place(ta, row, t, 0, r);
+                    if (t == 0) top_row(ta, row, r, sh.target[parity]);
+                    top_ranks(sh.cand, nc, k, t, TH, [&](int place, uint64_t key) { top_place(ta, row, place, key, r); });
                 } else {
-                    if (place < k) pub_keys[parity][place] = list.key;
-                    if (t >= total && t < k) pub_keys[parity][t] = 0;
-                    __syncthreads();
+                    if (t == 0) sh.pub[parity] = r;
+                    top_ranks(sh.cand, nc, k, t, TH, [&](int place, uint64_t key) { sh.pub_keys[parity][place] = key; });
                 }
-                if (cs > 1) {
-                    if (t == 0) pub[parity] = r;
-                    cluster_arrive();
-                    cluster_wait();
-                    if (rank == 0) {
-                        // every rank's list and sums
-                        uint64_t v = 0;
-                        if (t < cs * 32) {
-                            const float2 raw2 = ld_dsmem(reinterpret_cast<const float2 *>(&pub_keys[parity][lane]), (uint32_t)warp);
-                            v = lane < k ? (uint64_t)__float_as_uint(raw2.y) << 32 | __float_as_uint(raw2.x) : 0;
-                        }
-                        if (t < CSMAX * 32) keys[t] = v;
-                        if (t < 32) pub_keys[parity][t] = 0;
-                        __syncthreads();
-                        if (v) {
-                            const int place = rank_of(v, cs);
-                            if (place < k) pub_keys[parity][place] = v;
-                        }
-                        __syncthreads();
-                        if (t < k) best = pub_keys[parity][t];
-                    }
-                }
-            } else if (cs > 1) {
-                if (t == 0) pub[parity] = r;
+            }
+            if (cs > 1) {
+                __syncwarp();
                 cluster_arrive();
                 cluster_wait();
-            }
-            if (rank == 0) {
-                if (cs > 1) {
+                if (rank == 0) {
+                    // every CTA's sums and list
+                    if (t == 0) sh.cands[parity] = 0;
+                    __syncthreads();
+                    uint64_t v = 0;
+                    if (warp < cs && lane < k) {
+                        const float2 u = ld_dsmem(reinterpret_cast<const float2 *>(&sh.pub_keys[parity][lane]), (uint32_t)warp);
+                        v = (uint64_t)__float_as_uint(u.y) << 32 | __float_as_uint(u.x);
+                    }
+                    if (v) sh.cand[atomicAdd(&sh.cands[parity], 1)] = v;
                     r = RowEnt{-INFINITY, 0.f, 0.f};
                     if (lane < cs) {
-                        r.m = ld_dsmem(&pub[parity].m, (uint32_t)lane);
-                        r.d = ld_dsmem(&pub[parity].d, (uint32_t)lane);
-                        r.a = ld_dsmem(&pub[parity].a, (uint32_t)lane);
+                        r.m = ld_dsmem(&sh.pub[parity].m, (uint32_t)lane);
+                        r.d = ld_dsmem(&sh.pub[parity].d, (uint32_t)lane);
+                        r.a = ld_dsmem(&sh.pub[parity].a, (uint32_t)lane);
                     }
                     r = lanes_ent(r, c);
+                    if (t == 0) top_row(ta, row, r, sh.target[parity]);
+                    __syncthreads();
+                    top_ranks(sh.cand, sh.cands[parity], k, t, TH, [&](int place, uint64_t key) { top_place(ta, row, place, key, r); });
                 }
-                if (t == 0) top_row(ta, row, r, za);
-                if (cs > 1 && t < k) top_place(ta, row, t, best, r);
             }
-            // The next row's slots and tops are the other ones, and whatever else is
-            // shared is written behind its first barrier.
         }
     }
     if (cs > 1) {
@@ -713,7 +762,7 @@ template <typename T> cudaError_t launch_logit_top_t(const TopArgs &a, int sms, 
         return packs <= 32 * 8 ? launch_top_warp<T, 8, 6>(a, s, p) : launch_top_warp<T, 16, 4>(a, s, p);
     int cs = 1;
     while (cs < 8 && a.a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * 256) cs *= 2;
-    return launch_top_cta<T, 256, 8, 4>(a, cs, sms, s, p);
+    return launch_top_cta<T, 256, 8, TOP_M>(a, cs, sms, s, p);
 }
 
 template <typename T, int TH> cudaError_t launch_top_grad_g(const TopArgs &a, cudaStream_t s) {
