@@ -604,8 +604,8 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
  * neighbouring experts stay that have the largest sums of their group_top (1 or 2)
  * largest c.  Of those that stay the k largest c are taken, largest first; their
  * weights are scale s, or with `renormalize` scale s / (the sum of the chosen s).
- * The order is that of the exact c (differences below binary32's are found, in
- * binary64), among equal ones that of the index, lowest first.
+ * The order is that of the exact c: what binary32 cannot tell apart is compared to
+ * some 42 bits.  Among equal c the lowest index comes first.
  *   logits      [tokens, experts] dtype (row stride ldl)
  *   bias        [experts] binary32 or NULL (= 0); it has no part in the weights
  *   weights     [tokens, k] binary32

@@ -12,7 +12,7 @@
 // largest logits (ties: the lowest index first) come out of the same pass.  A
 // thread keeps the maximum of each group of packs it has seen.  At the row's
 // end the k-th largest of some threads' own maxima, T (of a warp's rows: of its
-// lanes', of a CTA's: of each warp's four largest), is a lower bound of the k-th
+// lanes', of a CTA's: of each warp's four or eight largest), is a lower bound of the k-th
 // largest logit, for k threads' maxima are k logits; so only groups
 // whose maximum reaches T can hold one of the k largest, and there are hardly
 // more than k of those.  They are read again (from L2), and their logits from T
@@ -67,9 +67,6 @@ struct TopList {
 
 // Candidates in shared memory, in no order: one key is one logit, so the places
 // that their ranks give them do not depend on it.
-#ifndef TOP_M
-#define TOP_M 4
-#endif
 constexpr int kTopCand = 256;
 __device__ __forceinline__ void top_add(bool on, uint64_t key, uint64_t *cand, int *n) {
     if (on) {
@@ -314,7 +311,10 @@ __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs
 // ---------------------------------------------------------------------------
 // Any row: a CTA, or the CTAs of a cluster with a slice of the packs each, goes
 // over it in segments of TH x PK packs, the next segment on its way into shared
-// memory meanwhile.
+// memory meanwhile.  4096 x 131072 bf16, a quarter of the rows out: without
+// alternatives 125 us, 95 % of the measured copy rate; with 20 148 us.  A row's
+// selection (three barriers, the found groups' way from L2) is a CTA's own time,
+// which the other three CTAs of its SM stream through.
 // ---------------------------------------------------------------------------
 constexpr int kTopGroups = 8;  // a thread's groups: their maxima wait in shared memory
 
@@ -337,17 +337,15 @@ template <typename T> struct TopSlice {
 };
 
 // What the CTA's warps share.  The arrays of two alternate between rows.
-constexpr int kTopWarps = 8, kTopClusterMax = 8;
-struct TopShared {
-    RowEnt slot[2][kTopWarps];
-    __align__(16) uint32_t tops[2][kTopWarps * 4];  // each warp's four largest
+template <int NW> struct TopShared {
+    RowEnt slot[2][NW];
+    __align__(16) uint32_t tops[2][32];     // each warp's 32 / NW largest
     __align__(16) uint64_t cand[kTopCand];  // room for every warp's list
     float target[2], ends[2][16];           // the target's logit; the row's scalar elements
     uint64_t pub_keys[2][32];
     RowEnt pub[2];
     int groups_found[2], cands[2], per_group[kTopGroups];
 };
-static_assert(kTopWarps == kTopClusterMax && kTopCand == kTopWarps * 32, "a warp reads one CTA's list");
 
 // A found group's elements, PASS a lane (a group's packs are TH apart), four groups
 // in flight: `use` gets each value and its column.
@@ -384,12 +382,13 @@ __device__ __forceinline__ void top_scan(const TopSlice<T> &w, const unsigned sh
 template <typename T, int TH, int PK, int MINB>
 __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, const int cs, const int batch) {
     constexpr int V = IO<T>::V;
-    static_assert(TH == 32 * kTopWarps, "as TopShared has it");
+    constexpr int NW = TH / 32, TOPS = 32 / NW;
+    static_assert(kTopCand >= 32 * NW, "room for every warp's list");
     constexpr uint32_t ALL = 0xffffffffu;
     extern __shared__ __align__(16) uint4 next_row[];                                     // [PK][TH]
     float *const group_max = reinterpret_cast<float *>(next_row + PK * TH);               // [kTopGroups][TH]
     unsigned short *const found = reinterpret_cast<unsigned short *>(group_max + kTopGroups * TH);  // [kTopGroups * TH]
-    __shared__ TopShared sh;
+    __shared__ TopShared<NW> sh;
     const LogitArgs &a = ta.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k = ta.k;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
@@ -463,9 +462,9 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
             if (k > 0) {
                 uint32_t v = top_ordered(tm);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < TOPS; ++i) {
                     const uint32_t m = __reduce_max_sync(ALL, v);
-                    if (lane == i) sh.tops[parity][warp * 4 + i] = m;
+                    if (lane == i) sh.tops[parity][warp * TOPS + i] = m;
                     if (lane == __ffs(__ballot_sync(ALL, v == m)) - 1) v = 0u;
                 }
             }
@@ -554,7 +553,7 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
             // A warp without one goes on to the next row, whose first barrier is ahead
             // of what it would overwrite.
             {
-                r = lanes_ent(lane < kTopWarps ? sh.slot[parity][lane] : RowEnt{-INFINITY, 0.f, 0.f}, c);
+                r = lanes_ent(lane < NW ? sh.slot[parity][lane] : RowEnt{-INFINITY, 0.f, 0.f}, c);
                 const int nc = k > 0 ? sh.cands[parity] : 0;
                 if (cs == 1) {
                     if (t == 0) top_row(ta, row, r, sh.target[parity]);
@@ -602,9 +601,11 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
 // ---------------------------------------------------------------------------
 // The gradient: element-wise from the forward's statistics, tiles of 4 x TH
 // packs of a row.  The entries of the target and the alternatives are written
-// once more, whole, by a thread each: their logits are read before the tile is
-// written (dlogits may replace the logits), an entry named more than once is
-// written by the first of its names.
+// once more, whole, each by the thread that wrote its pack just now, from the
+// logit that it still has in its registers (dlogits may replace the logits); every
+// warp has the names, one a lane, and looks at those in its tile.  2048 x 131072
+// bf16: 151 us, 92 % of the measured copy rate; with the names in shared memory and
+// barriers around the tile's stores 161.
 // ---------------------------------------------------------------------------
 template <typename T> struct TopSlope {
     float s, top, logd, gsum, h, gh;  // gh: gsum + h H
@@ -630,21 +631,33 @@ template <typename T> struct TopSlope {
     }
 };
 
+// Value e of a thread's packs, e = pack * V + its place.
+template <typename T, int U> __device__ __forceinline__ float pick(const uint4 (&raw)[U], int e) {
+    constexpr int V = IO<T>::V, PER = V / 4;
+    const int word = e / PER;
+    uint32_t w = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (word == 4 * u) w = raw[u].x;
+        if (word == 4 * u + 1) w = raw[u].y;
+        if (word == 4 * u + 2) w = raw[u].z;
+        if (word == 4 * u + 3) w = raw[u].w;
+    }
+    float f[V];
+    IO<T>::unpack(make_uint4(w, w, w, w), f);
+    return PER == 2 && e % 2 ? f[1] : f[0];
+}
+
 template <typename T, int TH>
 __global__ void __launch_bounds__(256) logit_top_grad_kernel(const TopArgs ta, const int tiles) {
-    constexpr int G = 256 / TH, V = IO<T>::V, U = 4, NS = kTopMaxK + 1;
-    __shared__ int64_t name[G][NS];
-    __shared__ float part[G][NS];
+    constexpr int G = 256 / TH, V = IO<T>::V, U = 4;
+    constexpr uint32_t ALL = 0xffffffffu;
     const LogitArgs &a = ta.a;
-    const int t = threadIdx.x % TH, lane = threadIdx.x & 31, in = threadIdx.x / TH, k = ta.k;
-    auto sync = [] {
-        if (TH == 32) __syncwarp();
-        else __syncthreads();
-    };
+    const int t = threadIdx.x % TH, lane = threadIdx.x & 31, k = ta.k;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t total = a.rows * tiles;
-    for (int64_t id = (int64_t)blockIdx.x * G + in; id < total; id += (int64_t)gridDim.x * G) {
+    for (int64_t id = (int64_t)blockIdx.x * G + threadIdx.x / TH; id < total; id += (int64_t)gridDim.x * G) {
         const int64_t row = total <= 0xffffffffll ? (int64_t)((uint32_t)id / (uint32_t)tiles) : id / tiles;
         const int tile = (int)(id - row * tiles);
         const T *Z = static_cast<const T *>(a.z) + row * a.ldz;
@@ -656,14 +669,14 @@ __global__ void __launch_bounds__(256) logit_top_grad_kernel(const TopArgs ta, c
         f.logd = a.stats_in[2 * row + 1];
         const bool live = tgt >= 0 && tgt < a.V && f.logd != -INFINITY;
         const float g = live && a.dlogp ? a.dlogp[row] : 0.f;
-        // every warp has the k alternatives, one a lane
-        int64_t mine = live && lane < k && ta.dtop ? ta.ids_in[row * k + lane] : -1;
-        if (mine < 0 || mine >= a.V) mine = -1;
-        const float al = mine >= 0 ? ta.dtop[row * k + lane] : 0.f;
+        // the alternatives, one a lane (a column fits 32 bits); -1: none
+        const int64_t named = live && lane < k && ta.dtop ? ta.ids_in[row * k + lane] : -1;
+        const int name = named >= 0 && named < a.V ? (int)named : -1;
+        const float al = name >= 0 ? ta.dtop[row * k + lane] : 0.f;
         f.h = live && ta.dentropy ? ta.dentropy[row] : 0.f;
         f.gsum = g + warp_sum_all(al);
         f.gh = f.h != 0.f ? fmaf(f.h, ta.entropy_in[row], f.gsum) : f.gsum;
-        const bool any = __any_sync(0xffffffffu, al != 0.f) || g != 0.f || f.h != 0.f;
+        const bool any = __any_sync(ALL, al != 0.f) || g != 0.f || f.h != 0.f;
         const RowCut<T> cut = cut_row(Z, a.V);
         const T *body = Z + cut.head;
         T *out = D + cut.head;
@@ -678,55 +691,35 @@ __global__ void __launch_bounds__(256) logit_top_grad_kernel(const TopArgs ta, c
             if (t < ns) D[sc] = IO<T>::from_f(0.f);
             continue;
         }
-        // the names and their parts; who of them lies in this tile
-        if (t < 32) {
-            if (t < k) {
-                name[in][t] = mine;
-                part[in][t] = al;
-            }
-            if (t == 0) {
-                name[in][k] = tgt;
-                part[in][k] = g;
-            }
-        }
         uint4 raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (p0 + u * TH < cut.packs) raw[u] = ld_once(body + (int64_t)(p0 + u * TH) * V);
         const float zs = t < ns ? IO<T>::to_f(Z[sc]) : 0.f;
-        sync();
-        constexpr int PER = (NS + TH - 1) / TH;  // names a thread
-        int64_t put[PER];
-        float val[PER];
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            const int i = t + q * TH;
-            put[q] = -1;
-            if (i > k) continue;
-            const int64_t j = name[in][i];
-            const bool scalar = j < cut.head || j >= a.V - cut.tail;
-            const int ip = (int)(j - cut.head) / V;
-            if (j < 0 || !(scalar ? tile == 0 : ip >= base && ip < base + TH * U)) continue;
-            bool again = false;
-            float sum = 0.f;
-            for (int o = 0; o <= k; ++o)
-                if (name[in][o] == j) {
-                    again = again || o < i;
-                    sum += part[in][o];
-                }
-            if (again) continue;
-            put[q] = j;
-            val[q] = fmaf(f.s, sum, f.one(IO<T>::to_f(Z[j])));
-        }
-        sync();
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (p0 + u * TH < cut.packs) st_pack(out + (int64_t)(p0 + u * TH) * V, f.pack(raw[u]), wide);
         if (t < ns) D[sc] = IO<T>::from_f(f.one(zs));
-        sync();
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-            if (put[q] >= 0) D[put[q]] = IO<T>::from_f(val[q]);
+        // the columns of this tile that have a name: the target, and those of the
+        // alternatives that are not the target
+        const int c0 = cut.head + base * V, c1 = (int)min((int64_t)cut.head + (int64_t)(base + TH * U) * V, a.V - cut.tail);
+        auto here = [&](int j) { return (j >= c0 && j < c1) || (tile == 0 && (j < cut.head || j >= a.V - cut.tail)); };
+        auto write = [&](int j, float part) {
+            if (j >= cut.head && j < a.V - cut.tail) {
+                const int e = j - c0, p = e / V;  // of the tile
+                if (p % TH == t) D[j] = IO<T>::from_f(fmaf(f.s, part, f.one(pick<T, U>(raw, p / TH * V + e % V))));
+            } else if (t < ns && sc == j) {
+                D[j] = IO<T>::from_f(fmaf(f.s, part, f.one(zs)));
+            }
+        };
+        const int it = (int)tgt;
+        if (here(it)) write(it, g + warp_sum_all(name == it ? al : 0.f));
+        uint32_t left = __ballot_sync(ALL, name >= 0 && name != it && here(name));
+        while (left) {
+            const int j = __shfl_sync(ALL, name, __ffs(left) - 1);
+            left &= ~__ballot_sync(ALL, name == j);
+            write(j, warp_sum_all(name == j ? al : 0.f));
+        }
     }
 }
 
@@ -755,6 +748,15 @@ cudaError_t launch_top_cta(const TopArgs &a, int cs, int sms, cudaStream_t s, Pl
     return launch_clusters(kernel, (a.a.rows + batch - 1) / batch, cs, TH, smem, s, a, cs, (int)batch);
 }
 
+// Device times of bf16 with 20 alternatives, inputs beyond L2.  Rows of up to 512
+// packs by a warp, where rows are many: 8192 x 4000 45 us (with 32 alternatives,
+// whose lower bound is the least of the lanes' maxima, 100; by CTAs of 128 113).
+// Then CTAs of 128 threads up to 4096 packs, for what a row costs beside its packs
+// is paid by each warp: 4096 x 8000 46 us, by CTAs of 256 72; 4096 x 32000 86 and 87.
+// Longer rows keep more in flight by 256: 4096 x 131072 148, by 128 171.  A row over
+// two or more CTAs while they do not cover the SMs twice: 200 x 32000 12.6 us by
+// two and 19.8 by four; beyond that the second list a row costs more than it
+// gives: f32 513 x 50001 27 us, by two CTAs 33.
 template <typename T> cudaError_t launch_logit_top_t(const TopArgs &a, int sms, cudaStream_t s, Plan *p) {
     const int64_t packs = a.a.V / IO<T>::V;
     if (packs <= 32 * 4) return launch_top_warp<T, 4, 8>(a, s, p);
@@ -762,7 +764,8 @@ template <typename T> cudaError_t launch_logit_top_t(const TopArgs &a, int sms, 
         return packs <= 32 * 8 ? launch_top_warp<T, 8, 6>(a, s, p) : launch_top_warp<T, 16, 4>(a, s, p);
     int cs = 1;
     while (cs < 8 && a.a.rows * cs < 2 * (int64_t)sms && packs >= 2 * cs * 256) cs *= 2;
-    return launch_top_cta<T, 256, 8, TOP_M>(a, cs, sms, s, p);
+    if (cs == 1 && packs <= 4096) return launch_top_cta<T, 128, 8, 8>(a, 1, sms, s, p);
+    return launch_top_cta<T, 256, 8, 4>(a, cs, sms, s, p);
 }
 
 template <typename T, int TH> cudaError_t launch_top_grad_g(const TopArgs &a, cudaStream_t s) {

@@ -15,7 +15,10 @@
 // few lanes: 2 VE PP entries each, arranged so that both entries of a pair are
 // in the same lane and a row needs no exchange but the sums.  The lanes' angles
 // depend on the token alone and stay in registers over its heads.  HBM bounds
-// it: each row once in, once out (backward: two in, one out).
+// it: each row once in, once out (backward: two in, one out).  16384 tokens x 40
+// heads x 128 bf16: 58.8 us forward, 85 % of the measured copy rate, and 8192 of
+// them 51 us backward, 73 %: there the registers of the weights' gradients leave 16
+// warps an SM, whose loads in flight are too few.
 //
 // A token whose position lies outside the table takes no part: its rows are not
 // read, its outputs and gradients are 0.
