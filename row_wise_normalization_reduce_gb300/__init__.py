@@ -4,8 +4,10 @@ LayerNorm, RMSNorm, fused residual-add + RMSNorm, BatchNorm2d training
 forward, inference forward, training backward and their synchronized
 (multi-process) form, row softmax, and the training operators around them
 (dropout from a counter-based generator, alone and fused with the residual
-add and RMSNorm, forward and backward; target log-probabilities of logits and
-the clipped policy loss, with their gradients), computed by the hand-written CUDA kernels of libnrm.so (C ABI in include/nrm.h).  This
+add and RMSNorm, forward and backward; target log-probabilities of logits, alone
+and with entropy and top alternatives, and the clipped policy loss, with their
+gradients) and inside a block (norms of queries and keys with the position
+rotation, routing to experts, with their gradients), computed by the hand-written CUDA kernels of libnrm.so (C ABI in include/nrm.h).  This
 package is the thin Python binding over that library.
 """
 from ._binding import (  # noqa: F401

@@ -301,14 +301,16 @@ template <int LL> __device__ __forceinline__ float qk_sum(float v, int lanes) {
 // Rows a lane has on its way at once, forward.  With 80 registers and three CTAs
 // an SM two rows are ahead of four with 108 and two (16384 x 40 x 128 bf16 58.8 us
 // and 59.8, f32 8192 x 20 x 128 27.0 and 29.7); pairs inside a pack need more
-// registers, there four rows are (8192 x 32 x 128 24.2 us and 26.5).
-template <int VE, int PP, bool CROSS, int ES>
-constexpr int kQkFwdRows = CROSS || PP > 1 || VE * ES > 16 || ES == 4 ? 2 : 4;
+// registers, there four rows are (8192 x 32 x 128 24.2 us and 26.5), and so without a
+// constant number of lanes, where an item costs more beside its rows (8192 x 32 x
+// 80, half of it turned, 28.1 us and 32.0).
+template <int VE, int PP, bool CROSS, int ES, int LL>
+constexpr int kQkFwdRows = PP > 1 || ES == 4 || (CROSS && LL >= 0) ? 2 : 4;
 
 // Forward.  One warp an item of U times 32 / lanes rows, all of whose loads are in
 // flight together.  LL >= 0: every lane of 2^LL has its two packs.
 template <typename T, int VE, int PP, bool CROSS, int LL, int U>
-__global__ void __launch_bounds__(kQkThreads, PP > 1 ? 1 : CROSS || sizeof(T) == 4 ? 3 : 2) qk_fwd_kernel(const QkArgs q, const int log_lanes,
+__global__ void __launch_bounds__(kQkThreads, PP > 1 ? 1 : U == 2 ? 3 : 2) qk_fwd_kernel(const QkArgs q, const int log_lanes,
                                                                              const int q_items, const int items) {
     using P = Pk<T, VE>;
     constexpr int H = P::H;
@@ -554,7 +556,7 @@ cudaError_t launch_qk_one(const QkArgs &q, int log, bool back, int sms, cudaStre
     p->packs = VE;
     p->groups = 1 << log;
     if (!back) {
-        constexpr int U = kQkFwdRows<VE, PP, CROSS, (int)sizeof(T)>;
+        constexpr int U = kQkFwdRows<VE, PP, CROSS, (int)sizeof(T), LL>;
         const int heads = R * U;
         const int q_items = (q.side[0].heads + heads - 1) / heads, items = q_items + (q.side[1].heads + heads - 1) / heads;
         const int64_t n = (q.tokens * items + kQkThreads / 32 - 1) / (kQkThreads / 32);

@@ -218,6 +218,7 @@ __device__ __forceinline__ Pair route_choice(const RouteArgs &a, float x, int e,
 }
 
 // The whole selection by those.  Lane r returns the expert at place r, or -1.
+// (Taking only the experts in question as pairs, in two steps, changed nothing.)
 template <typename T, int PL>
 __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int lane) {
     constexpr uint32_t ALL = 0xffffffffu;
@@ -585,9 +586,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
 // lane takes its experts in chunks of eight, sorts each chunk's keys and keeps the
 // eight largest (the larger of entry i of one list and entry 7 - i of the other
 // are the eight largest of both, and three stages of exchanges sort them); three
-// merges of the same kind join the lanes.  65536 x 256 bf16 in 8 groups: 37 us, a
-// warp a token 64; without groups and bias 22 and 32.  Bound by instructions: 290 a
-// token, the keys' exponentials and sorting networks most of them.
+// merges of the same kind join the lanes.  65536 x 256 bf16 in 8 groups: 38 us, a
+// warp a token 64; without groups and bias 23 and 32.  Bound by instructions, 320 a
+// token (the keys' exponentials and sorting networks most of them), and by the
+// last turn: 3.4 of four.  (Taking tokens from a counter instead: no change.)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {
     const uint32_t hi = max(a, b), lo = min(a, b);
