@@ -1786,7 +1786,7 @@ int logprob_top_fwd_ld(const void *logits, int64_t ldl, const int64_t *targets, 
                        float inv_temp, int dtype, cudaStream_t stream) {
     int st = validate_logits(rows, V, inv_temp, dtype);
     if (st != NRM_OK) return st;
-    if (k < 0) return NRM_ERR_SHAPE;
+    if (k < 0 || rows > INT64_MAX / 8 / kTopMaxK) return NRM_ERR_SHAPE;
     if (k > kTopMaxK) return NRM_ERR_UNSUPPORTED;
     if (rows == 0) return NRM_OK;  // empty input: no pointer is used
     if (!logits || !targets || (k > 0 && (!top_ids || !top_logp)) || (k == 0 && !logp && !entropy && !stats))
@@ -1837,7 +1837,7 @@ int logprob_top_bwd_ld(const float *dlogp, const float *dentropy, const float *d
                        float inv_temp, int dtype, cudaStream_t stream) {
     int st = validate_logits(rows, V, inv_temp, dtype);
     if (st != NRM_OK) return st;
-    if (k < 0) return NRM_ERR_SHAPE;
+    if (k < 0 || rows > INT64_MAX / 8 / kTopMaxK) return NRM_ERR_SHAPE;
     if (k > kTopMaxK) return NRM_ERR_UNSUPPORTED;
     if (rows == 0) return NRM_OK;  // empty input: no pointer is used
     if (k == 0) dtop_logp = nullptr;

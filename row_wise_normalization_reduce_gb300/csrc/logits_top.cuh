@@ -366,7 +366,7 @@ __device__ __forceinline__ void top_scan(const TopSlice<T> &w, const unsigned sh
                 for (int q = 0; q < PASS; ++q) {
                     const int e = q * 32 + lane, pack = ((g * per + sub) * PK + e / V) * TH + th;
                     f[j][q] = -INFINITY;
-                    idx[j][q] = w.head + (w.p0 + pack) * V + e % V;
+                    idx[j][q] = (int)((uint32_t)w.head + (uint32_t)(w.p0 + pack) * V + e % V);
                     if (i < n && pack < w.packs) f[j][q] = IO<T>::to_f(w.z[idx[j][q]]);
                 }
             }

@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
     // SCORE: the fixed point's step is 1 / S, and bias i's part base[i]
     float base[MODE == KEY_SCORE ? PL : 1], S = 262143.f, near_bias = 0.f;
     bool odd_bias = false;  // infinite or NaN ones
+    bool wild = false;      // their range is beyond binary32: every token is done again
     if constexpr (MODE == KEY_SCORE) {
         float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
         hi = from_ordered32(__reduce_max_sync(ALL, ordered32(hi)));
         if (!(hi >= lo)) lo = hi = 0.f;  // no expert has a finite bias
         S = 4194300.f / (1.f + (hi - lo));
+        wild = !(hi - lo < INFINITY);
         // the rounding of base: half a step of its size, relative to 2^23
         near_bias = 1.2e-7f * (fabsf(lo) + fabsf(hi)) * S + 1.f;
 #pragma unroll
@@ -465,6 +467,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                 }
                 again = __any_sync(ALL, far);
             }
+            again = again || wild;
         }
         sort_desc<PL>(key);
         if (limited) {
@@ -643,6 +646,7 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
     const uint32_t index = (uint32_t)(kIdxMask - first);
     float S = 262143.f, near_bias = 0.f;
     bool odd_bias = false;  // infinite or NaN ones
+    bool wild = false;      // their range is beyond binary32: every token is done again
     pdl_wait();
     pdl_launch_dependents();
     if constexpr (MODE == KEY_SCORE) {
@@ -668,6 +672,7 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
         odd_bias = __syncthreads_or(odd_bias);
         const float lo = range[0], hi = range[1];
         S = 4194300.f / (1.f + (hi - lo));
+        wild = !(hi - lo < INFINITY);
         // the rounding of base: half a step of its size, relative to 2^23
         near_bias = 1.2e-7f * (fabsf(lo) + fabsf(hi)) * S + 1.f;
         if (threadIdx.x < 8) {
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
         // keys, largest first; 0: not available
         uint32_t list[8];
         float near_ = MODE == KEY_LOGIT ? 2.f : 0.f;  // keys no further apart than this are in question
-        bool again = false;                           // the whole token is
+        bool again = wild;                            // the whole token is
         if constexpr (MODE == KEY_SCORE)
             // as in route_fwd_kernel; the sum is at most 8 NC + 3 additions deep
             near_ = 2.f * (S * (a.softmax ? (6e-7f + 6e-8f * (PL + 3)) * inv : 3e-7f) + near_bias);

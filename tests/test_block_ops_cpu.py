@@ -201,7 +201,7 @@ def test_logprob_top_refusals(lib):
         (dict(), (OK, DEVICE)), (dict(logp=None, ent=None, st=None), (OK, DEVICE)), (dict(k=0, ids=None, top=None), (OK, DEVICE)),
         (dict(k=32), (OK, DEVICE)), (dict(V=3, ldz=3), (OK, DEVICE)), (dict(rows=0, z=None), OK), (dict(z=None), NULL),
         (dict(t=None), NULL), (dict(ids=None), NULL), (dict(top=None), NULL), (dict(k=0, logp=None, ent=None, st=None), NULL),
-        (dict(k=33), UNSUP), (dict(k=-1), SHAPE), (dict(V=0), SHAPE), (dict(V=2 ** 31, ldz=2 ** 31), SHAPE), (dict(ldz=63), SHAPE),
+        (dict(k=33), UNSUP), (dict(k=-1), SHAPE), (dict(V=0), SHAPE), (dict(rows=2 ** 58, V=1, ldz=1), SHAPE), (dict(V=2 ** 31, ldz=2 ** 31), SHAPE), (dict(ldz=63), SHAPE),
         (dict(s=0.0), VALUE), (dict(s=float("nan")), VALUE), (dict(s=3e38), VALUE), (dict(ids=5 * A + 4), VALUE),
         (dict(st=7 * A + 2), VALUE), (dict(z=A + 1), VALUE), (dict(dtype=4), DTYPE), (dict(ids=A), ALIAS), (dict(top=5 * A), ALIAS),
         (dict(ent=2 * A), ALIAS), (dict(st=3 * A), ALIAS),

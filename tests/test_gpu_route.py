@@ -167,6 +167,28 @@ def test_far_logits_and_large_biases():
     assert not w.any() and (ids >= 0).all()
 
 
+@pytest.mark.parametrize("experts,k", [(64, 6), (64, 12), (700, 9)])
+def test_biases_whose_range_is_beyond_binary32(experts, k):
+    x = randn(21, experts, seed=8)
+    bias = randn(experts, seed=9, scale=0.1)
+    bias[3], bias[5], bias[6] = 3e38, -3e38, 2.9e38
+    for score in ("softmax", "sigmoid"):
+        check(x, k, bias, score=score)
+        check(x, k, bias, score=score, groups=4, top_groups=2, group_top=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_saturated_scores(score):
+    # sigmoids that binary32 rounds to 1, softmaxes of one expert alone
+    x = 20.0 + randn(30, 128, seed=12, scale=3.0)
+    x[1::2] += 200.0 * (torch.arange(128, device="cuda") == 77)
+    bias = randn(128, seed=13, scale=1e-6)
+    check(x, 8, None, score=score)
+    check(x, 8, bias, score=score)
+    check(x, 20, bias, score=score)
+    check(x, 8, bias, score=score, groups=8, top_groups=3, group_top=2)
+
+
 @pytest.mark.parametrize("dtype", R.DTYPES)
 def test_strides_and_outputs(dtype):
     full = randn(77, 300, seed=10).to(dtype)
