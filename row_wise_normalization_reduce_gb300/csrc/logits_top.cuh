@@ -11,15 +11,16 @@
 // rescaled like d, and moves by d times the shift when the maximum does.  The k
 // largest logits (ties: the lowest index first) come out of the same pass.  A
 // thread keeps the maximum of each group of packs it has seen.  At the row's
-// end the k-th largest of some threads' own maxima, T (of a warp's rows: of its
-// lanes', of a CTA's: of each warp's four or eight largest), is a lower bound of the k-th
-// largest logit, for k threads' maxima are k logits; so only groups
-// whose maximum reaches T can hold one of the k largest, and there are hardly
-// more than k of those.  They are read again (from L2), and their logits from T
-// on go, as 64-bit keys (value, then lower index first), into a sorted list of 32
-// that each warp keeps one entry a lane.  The warps' lists are joined by each
-// entry's rank.  Where many logits equal T (masked by one finite value, say) the
-// groups are in index order, and later ones of no larger maximum are left out.
+// end the k-th largest of some threads' own maxima, T (a row of one warp: of its
+// lanes'; of a CTA: of each warp's four or eight largest), is a lower bound of the
+// k-th largest logit, for k threads' maxima are k logits; so only groups whose
+// maximum reaches T can hold one of the k largest, and there are hardly more than
+// k of those.  A CTA reads them again, from L2; their logits from T on go, as
+// 64-bit keys (value, then lower index first), into a sorted list of 32 that each
+// warp keeps one entry a lane, and an entry's rank among all lists is its place.
+// (One warp ranks the logits from T on without lists, up to 256 of them.)  Where
+// many logits equal T (masked by one finite value, say) the groups are in index
+// order, and later ones of no larger maximum are left out.
 //
 // The gradient for g of logp, h of H and a_i of the alternatives' lp:
 //   dz_j = s (g [j = target] + sum_i a_i [j = id_i] - p_j (g + sum_i a_i + h (lp_j + H)))
