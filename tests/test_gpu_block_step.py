@@ -196,3 +196,35 @@ def test_the_forward_captured_with_an_eager_graph_alive():
     torch.cuda.synchronize()
     got = [t.clone() for t in got]
     assert all(torch.equal(a, b) for a, b in zip(got, run()))
+
+
+def test_two_streams_at_once():
+    # the same operators on two streams, each call with scratch and outputs of its own
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+        return r(900, 8, 128), r(900, 2, 128), r(900, 8, 128), r(900, 2, 128), r(900, 256), r(300, 30000)
+
+    w = torch.ones(128, device="cuda", dtype=torch.bfloat16)
+    table, pos = R.angle_table(900, 128, device="cuda"), torch.arange(900, device="cuda")
+    targets = torch.arange(300, device="cuda")
+
+    def run(i):
+        q, k, gq, gk, router, logits = i
+        f = nrm.logprob_top_fwd(logits, targets, 9)
+        w_, ids, _ = nrm.route_fwd(router, 8, score="sigmoid")
+        return (*nrm.qk_norm_rope_bwd(gq, gk, q, k, table, pos, w, w), *f, w_, ids, nrm.route_bwd(w_, router, ids, score="sigmoid"),
+                nrm.logprob_top_bwd(f[0], f[1], f[3], logits, targets, f[4], f[1], f[2]))
+
+    both = [inputs(1), inputs(2)]
+    want = [run(i) for i in both]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for i, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                got.append(run(i))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))

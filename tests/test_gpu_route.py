@@ -278,3 +278,24 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(a[1], ids.flip(0)) and torch.equal(b, dx.flip(0))
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("experts,k,groups,top_groups,group_top", [(64, 6, 1, 1, 1), (160, 6, 8, 3, 2), (256, 8, 8, 4, 2), (255, 8, 1, 1, 1),
+                                                                   (7, 3, 1, 1, 1), (128, 8, 4, 2, 1)])
+def test_the_plans_agree(experts, k, groups, top_groups, group_top, dtype):
+    # a warp a token, by force, where eight lanes a token are the rule
+    x, bias = randn(500, experts, seed=14).to(dtype), randn(experts, seed=15, scale=0.05)
+    for b in (bias, None):
+        for score in ("sigmoid", "softmax"):
+            how = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top)
+            w, ids, _ = nrm.route_fwd(x, k, b, **how)
+            assert nrm.last_plan()[4] == 32  # tokens a CTA
+            nrm.force_plan(nrm.PLAN_GENERIC)
+            try:
+                w2, ids2, _ = nrm.route_fwd(x, k, b, **how)
+                assert nrm.last_plan()[4] == 8
+                check(x, k, b, **how)
+            finally:
+                nrm.force_plan(nrm.PLAN_AUTO)
+            assert torch.equal(ids, ids2) and (w - w2).abs().max() <= 2 * R.SCORE
