@@ -493,7 +493,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                 const bool low = MODE == KEY_LOGIT && keep && (b1 == 1u || (two && b2 == 1u));
                 again = again || (float)(least / 32u - most / 32u) <= (two ? 2.f : 1.f) * near_ || __any_sync(ALL, low);
             }
-            if (!keep) key[0] = 0u;  // never the largest, so nothing behind it is
+            // all that the list below may take, for an emptied place would move up
+            // what lies behind it
+            if (!keep) {
+#pragma unroll
+                for (int i = 0; i < (PL > LIST ? LIST + 1 : PL); ++i) key[i] = 0u;
+            }
         }
         // places: the k largest
         uint32_t list[LIST + 1], mine = 0u, last = 0u;
@@ -504,6 +509,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
         int left = PL > LIST && key[PL > LIST ? LIST : 0] ? LIST : PL + 1;
         for (int p = 0; p < a.k; ++p) {
             last = __reduce_max_sync(ALL, list[0]);
+            if (last == 0u) break;  // nobody is left
             if (lane == p) mine = last;
             if (list[0] == last) {
 #pragma unroll

@@ -1,0 +1,77 @@
+"""Which experts routing takes where the choice is delicate, on the GPU against
+the 64-bit definition of block_ref.py, by both plans (eight lanes a token, and
+by force a warp a token)."""
+import pytest
+import torch
+
+import block_ref as R
+
+pytestmark = pytest.mark.gpu
+
+import row_wise_normalization_reduce_gb300 as nrm  # noqa: E402
+
+INF = float("inf")
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _built():
+    nrm.build()
+
+
+@pytest.fixture(params=["auto", "a warp a token"], autouse=True)
+def plan(request):
+    nrm.force_plan(nrm.PLAN_AUTO if request.param == "auto" else nrm.PLAN_GENERIC)
+    yield
+    nrm.force_plan(nrm.PLAN_AUTO)
+
+
+def randn(*shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return scale * torch.randn(*shape, generator=g, device="cuda")
+
+
+def rand(*shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.rand(*shape, generator=g, device="cuda")
+
+
+def check(x, k, bias=None, **how):
+    """ids equal; weights of scores within 2^-17 each (block_ref.py: SCORE), which
+    their sum is as well."""
+    want, ids = R.route(x, k, bias, **how)
+    w, got, _ = nrm.route_fwd(x, k, bias, **how)
+    wrong = (got.cpu() != ids).any(1).nonzero()[:, 0]
+    assert not len(wrong), (len(wrong), int(wrong[0]), got[wrong[0]].tolist(), ids[wrong[0]].tolist())
+    R.check(w.cpu(), want, 2 * R.SCORE * want.abs() + 2.0 ** -126, "weights")
+
+
+# experts, k, groups, top_groups
+GROUPED = [(64, 12, 4, 1), (64, 8, 4, 2), (160, 6, 8, 3), (256, 8, 8, 4), (256, 8, 8, 2), (512, 10, 4, 2), (1024, 32, 32, 7),
+           (96, 3, 12, 5), (32, 4, 32, 6), (756, 20, 12, 2), (768, 8, 3, 1), (255, 8, 3, 2), (24, 6, 8, 4)]
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("experts,k,groups,top_groups", GROUPED)
+@pytest.mark.parametrize("score,with_bias,group_top", [("softmax", False, 1), ("sigmoid", False, 1), ("softmax", False, 2),
+                                                       ("sigmoid", False, 2), ("softmax", True, 1), ("sigmoid", True, 1)])
+def test_kept_groups_with_fewer_experts_than_places(experts, k, groups, top_groups, score, with_bias, group_top, dtype):
+    # from no available expert a token to a third of them: what the kept groups
+    # have not is nobody's place
+    x = randn(300, experts, seed=experts + k, scale=1.5).to(dtype)
+    x[rand(300, experts, seed=1) > torch.arange(300, device="cuda")[:, None] / 900] = -INF
+    bias = None
+    if with_bias:
+        bias = randn(experts, seed=3, scale=0.05)
+        bias[rand(experts, seed=4) < 0.2] = -INF
+    check(x, k, bias, score=score, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+def test_kept_groups_with_fewer_experts_than_places_by_hand():
+    # four groups of 128, two kept, eight available in them, ten places
+    x = torch.full((1, 512), -INF, device="cuda")
+    for e, v in ((0, 8.0), (1, 8.5), (2, 9.0), (3, 9.5), (128, 8.25), (129, 8.75), (130, 9.25), (131, 9.75), (256, 1.0), (257, 1.5),
+                 (358, 2.0), (359, 1.75)):
+        x[0, e] = v
+    for dtype in R.DTYPES:
+        ids = nrm.route_fwd(x.to(dtype), 10, groups=4, top_groups=2)[1]
+        assert ids[0].tolist() == [131, 3, 130, 2, 129, 1, 128, 0, -1, -1]
