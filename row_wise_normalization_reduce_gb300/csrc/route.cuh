@@ -45,6 +45,15 @@ __device__ __forceinline__ uint32_t ordered32(float v) {
 __device__ __forceinline__ float from_ordered32(uint32_t u) {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
+// What a group's sum of two is in fixed point where it has one available expert
+// alone, whose key counts the least bias once, not twice: that key and the one of c =
+// 0, `zero`.  With a `zero` beyond kZeroMost (biases far from 0 for their range) sums
+// would not fit, and the token is done again.  Groups without an expert come last.
+constexpr float kZeroMost = 33554432.f;
+constexpr int kWorthNone = 1, kWorthBase = 33554432 + 2;  // so that any sum is above kWorthNone
+__device__ __forceinline__ uint32_t pair_worth(uint32_t b1, uint32_t b2, int zero) {
+    return (uint32_t)(b1 ? (int)b1 + (b2 ? (int)b2 : zero) + kWorthBase : kWorthNone);
+}
 // Descending order of N keys: K. E. Batcher's odd-even merge network.
 template <int N> __device__ __forceinline__ void sort_desc(uint32_t (&k)[N]) {
 #pragma unroll
@@ -367,6 +376,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
     pdl_launch_dependents();
     // SCORE: the fixed point's step is 1 / S, and bias i's part base[i]
     float base[MODE == KEY_SCORE ? PL : 1], S = 262143.f, near_bias = 0.f;
+    int zero = 0;           // what a missing second of a group counts
+    bool zero_far = false;  // beyond what sums hold
     bool odd_bias = false;  // infinite or NaN ones
     bool wild = false;      // their range is beyond binary32: every token is done again
     if constexpr (MODE == KEY_SCORE) {
@@ -389,6 +400,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
         wild = !(hi - lo < INFINITY);
         // the rounding of base: half a step of its size, relative to 2^23
         near_bias = 1.2e-7f * (fabsf(lo) + fabsf(hi)) * S + 1.f;
+        const float z = rintf(fmaf(-lo, S, 2.f));
+        zero_far = !(fabsf(z) < kZeroMost);
+        zero = zero_far ? 0 : (int)z;
 #pragma unroll
         for (int i = 0; i < PL; ++i) base[i] = fmaf(base[i] - lo, S, 8388610.f);
     }
@@ -479,8 +493,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
             }
             // sum and then the lower group first; + 1: groups without an expert are
             // still groups
-            const bool two = a.group_top > 1, real = g < a.groups;
-            const uint32_t worth = real ? ((two ? b1 + b2 : b1) + 1u) * 32u + (uint32_t)(31 - g) : 0u;
+            const bool two = MODE == KEY_SCORE && a.group_top > 1, real = g < a.groups;
+            if (two) again = again || (zero_far && __any_sync(ALL, b1 && !b2));
+            const uint32_t sum = two ? pair_worth(b1, b2, zero) : b1 + 1u;
+            const uint32_t worth = real ? sum * 32u + (uint32_t)(31 - g) : 0u;
             uint32_t rest = worth, least = 0u;
             for (int i = 0; i < a.top_groups; ++i) {
                 least = __reduce_max_sync(ALL, rest);
@@ -490,7 +506,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
             if constexpr (MODE != KEY_WHOLE) {
                 const uint32_t most = __reduce_max_sync(ALL, rest);
                 // too near; or a kept group owes its place to a logit below the range
-                const bool low = MODE == KEY_LOGIT && keep && (b1 == 1u || (two && b2 == 1u));
+                const bool low = MODE == KEY_LOGIT && keep && b1 == 1u;
                 again = again || (float)(least / 32u - most / 32u) <= (two ? 2.f : 1.f) * near_ || __any_sync(ALL, low);
             }
             // all that the list below may take, for an emptied place would move up
@@ -651,6 +667,8 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
     const bool limited = a.top_groups < a.groups;
     const uint32_t index = (uint32_t)(kIdxMask - first);
     float S = 262143.f, near_bias = 0.f;
+    int zero = 0;           // what a missing second of a group counts
+    bool zero_far = false;  // beyond what sums hold
     bool odd_bias = false;  // infinite or NaN ones
     bool wild = false;      // their range is beyond binary32: every token is done again
     pdl_wait();
@@ -681,6 +699,9 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
         wild = !(hi - lo < INFINITY);
         // the rounding of base: half a step of its size, relative to 2^23
         near_bias = 1.2e-7f * (fabsf(lo) + fabsf(hi)) * S + 1.f;
+        const float z = rintf(fmaf(-lo, S, 2.f));
+        zero_far = !(fabsf(z) < kZeroMost);
+        zero = zero_far ? 0 : (int)z;
         if (threadIdx.x < 8) {
             for (int i = 0; i < PL; ++i)
                 base_of[l * (PL + 4) + i] =
@@ -825,8 +846,10 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
             }
             // sum and then the lower group first; + 1: groups without an expert are
             // still groups
-            const bool two = a.group_top > 1, is = g < a.groups;
-            const uint32_t worth = is ? ((two ? b1 + b2 : b1) + 1u) * 32u + (uint32_t)(31 - g) : 0u;
+            const bool two = MODE == KEY_SCORE && a.group_top > 1, is = g < a.groups;
+            if (two) again = again || (zero_far && b1 && !b2);
+            const uint32_t sum = two ? pair_worth(b1, b2, zero) : b1 + 1u;
+            const uint32_t worth = is ? sum * 32u + (uint32_t)(31 - g) : 0u;
             int rank = 0;
             for (int h = 0; h < a.groups; ++h)
                 rank += __shfl_sync(ALL, worth, (lane & 24) | h << a.oct_log_lanes) > worth;
@@ -834,7 +857,7 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
             if constexpr (MODE != KEY_WHOLE) {
                 const uint32_t least = oct_min(keep ? worth : ALL), most = oct_max(keep ? 0u : worth);
                 // too near; or a kept group owes its place to a logit below the range
-                const bool low = MODE == KEY_LOGIT && keep && (b1 == 1u || (two && b2 == 1u));
+                const bool low = MODE == KEY_LOGIT && keep && b1 == 1u;
                 again = again || (float)(least / 32u - most / 32u) <= (two ? 2.f : 1.f) * near_ || low;
             }
             if (!keep) {

@@ -75,3 +75,30 @@ def test_kept_groups_with_fewer_experts_than_places_by_hand():
     for dtype in R.DTYPES:
         ids = nrm.route_fwd(x.to(dtype), 10, groups=4, top_groups=2)[1]
         assert ids[0].tolist() == [131, 3, 130, 2, 129, 1, 128, 0, -1, -1]
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("experts,k,groups,top_groups", GROUPED)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("least", [-0.5, -40.0, 0.75, 1000.0])
+def test_groups_of_one_available_expert(experts, k, groups, top_groups, score, least, dtype):
+    # the sum of a group's two best counts the one it has, whatever the biases' range
+    x = randn(300, experts, seed=experts + k, scale=1.5).to(dtype)
+    x[rand(300, experts, seed=1) > 0.2 + 1.5 * groups / experts] = -INF
+    bias = (least + rand(experts, seed=5) * (1.5 if abs(least) < 1 else 0.3)).double().float()
+    check(x, k, bias, score=score, groups=groups, top_groups=top_groups, group_top=2)
+    bias[rand(experts, seed=4) < 0.3] = -INF
+    check(x, k, bias, score=score, groups=groups, top_groups=top_groups, group_top=2)
+
+
+def test_groups_of_one_available_expert_by_hand():
+    # a sigmoid of 0 is 1/2: one expert of 1.25 against two of 0.5 each, biases from -0.5 on
+    x = torch.zeros(1, 64, device="cuda")
+    x[0, 1:4] = x[0, 6:] = -INF
+    bias = torch.full((64,), -0.5, device="cuda")
+    bias[0], bias[4], bias[5] = 0.75, 0.0, 0.0
+    assert nrm.route_fwd(x, 2, bias, score="sigmoid", groups=16, top_groups=1, group_top=2)[1].tolist() == [[0, -1]]
+    # biases of 1 and more: two of 1.75 each are more than one of 3
+    bias = torch.ones(64, device="cuda")
+    bias[0], bias[4], bias[5] = 2.5, 1.25, 1.25
+    assert nrm.route_fwd(x, 2, bias, score="sigmoid", groups=16, top_groups=1, group_top=2)[1].tolist() == [[4, 5]]
