@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                 const float bs = MODE == KEY_SCORE && a.bias && id >= 0 ? a.bias[id] : 0.f;
                 const float bu = __shfl_up_sync(ALL, bs, 1);
                 if (lane > 0) close = close && !(xs == xu && bs == bu);
-                // those equal to the last place come after it
+                // those equal to the last place come after it, but before a place in
+                // question that turns out to be smaller: `list` keeps them
                 uint32_t w = after, rest[LIST + 1];
+                int rest_left = left;
 #pragma unroll
                 for (int i = 0; i <= LIST; ++i) rest[i] = list[i];
                 const float xl = __shfl_sync(ALL, xs, a.k - 1), bl = __shfl_sync(ALL, bs, a.k - 1);
@@ -565,16 +567,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                     if (rest[0] == w) {
 #pragma unroll
                         for (int i = 0; i < LIST; ++i) rest[i] = rest[i + 1];
-                        --left;
+                        --rest_left;
                     }
-                    if (PL > LIST && __any_sync(ALL, left == 0)) {
+                    if (PL > LIST && __any_sync(ALL, rest_left == 0)) {
                         again = true;
                         break;
                     }
                     w = __reduce_max_sync(ALL, rest[0]);
                 }
                 if (!again && (border || __any_sync(ALL, close && lane > 0)))
-                    again = !route_resolve<T, PL, LIST>(a, row, lane, mine, last, rest, left, near_, &id, &xs);
+                    again = !route_resolve<T, PL, LIST>(a, row, lane, mine, last, list, left, near_, &id, &xs);
             }
             if (again) {
                 id = route_exact<T, PL>(a, row, lane);
@@ -904,7 +906,9 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
                 const float xu = __shfl_up_sync(ALL, xs, 1), bu = __shfl_up_sync(ALL, bs, 1);
                 close = close && !(xs == xu && bs == bu);
                 const float xl = __shfl_sync(ALL, xs, (lane & 24) | (a.k - 1)), bl = __shfl_sync(ALL, bs, (lane & 24) | (a.k - 1));
-                // those equal to the last place come after it
+                // those equal to the last place come after it, but before a place in
+                // question that turns out to be smaller
+                const bool equal = border;
                 while (__any_sync(ALL, border)) {
                     if (border) {
                         const int e = kIdxMask - (int)(after & kIdxMask);
@@ -918,9 +922,8 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
                     again = again || (PL > 8 && border && own[7] && own[7] >= below);
                     border = border && after && (float)((last >> kIdxBits) - (after >> kIdxBits)) <= near_;
                 }
-                if (a.softmax && a.by_score) {
-                    again = again || close;
-                } else if (__any_sync(ALL, close)) {
+                again = again || (close && (equal || (a.softmax && a.by_score)));
+                if (!(a.softmax && a.by_score) && __any_sync(ALL, close)) {
                     // the places in their order, one expert a lane
                     uint64_t key = 0;
                     if (id >= 0) key = ordered_pair(a.by_score ? route_choice(a, xs, id, 0.f, Pair{1.f, 0.f}) : Pair{xs, 0.f});

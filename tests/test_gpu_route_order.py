@@ -102,3 +102,37 @@ def test_groups_of_one_available_expert_by_hand():
     bias = torch.ones(64, device="cuda")
     bias[0], bias[4], bias[5] = 2.5, 1.25, 1.25
     assert nrm.route_fwd(x, 2, bias, score="sigmoid", groups=16, top_groups=1, group_top=2)[1].tolist() == [[4, 5]]
+
+
+def step_up(x, steps):
+    return (x.view(torch.int32) + steps).view(torch.float32)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("experts,k", [(64, 2), (64, 6), (256, 8), (512, 10), (128, 20)])
+def test_equal_ones_left_out_beside_a_smaller_one_taken(experts, k, with_bias, score):
+    # some logits a step apart, most of them equal to another, the rest far below:
+    # which of them come first is a matter of their last bits
+    tokens = 400
+    x = randn(tokens, experts, seed=1, scale=0.1) - 4.0
+    x = torch.where(rand(tokens, experts, seed=2) < 1.6 * k / experts,
+                    step_up(torch.ones(tokens, experts, device="cuda"), (rand(tokens, experts, seed=3) * 3).int()), x)
+    bias = torch.zeros(experts, device="cuda") if with_bias else None
+    check(x, k, bias, score=score)
+    check(x, k, bias, score=score, groups=4, top_groups=2, group_top=1)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+def test_equal_ones_left_out_by_hand(dtype):
+    x = torch.zeros(2, 64, device="cuda", dtype=dtype)
+    x[0, 0], x[0, 1], x[0, 2] = 16.0, 16.125, 16.125  # one step of the fixed point for all three
+    x[1, 7], x[1, 3], x[1, 60] = 16.125, 16.0, 16.125
+    bias = torch.zeros(64, device="cuda")
+    assert nrm.route_fwd(x, 2, bias, score="sigmoid")[1].tolist() == [[1, 2], [7, 60]]
+    if dtype is torch.float32:
+        x = torch.full((1, 64), -3.0, device="cuda")
+        x[0, 3], x[0, 7], x[0, 20] = 1.0, 1.0 + 2.0 ** -23, 1.0 + 2.0 ** -23
+        for score in ("softmax", "sigmoid"):
+            for b in (None, bias):
+                assert nrm.route_fwd(x, 2, b, score=score)[1].tolist() == [[7, 20]]
