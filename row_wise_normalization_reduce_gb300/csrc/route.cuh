@@ -278,7 +278,9 @@ __device__ __noinline__ int route_exact(const RouteArgs &a, const T *row, int la
             }
         }
         const bool two = a.group_top > 1 && k2 > none && fabsf(b1.hi) < INFINITY && fabsf(b2.hi) < INFINITY;
-        const uint64_t worth = ordered_pair(two ? pair_add(b1, b2) : b1);
+        // (halves: the sum of two large biases is beyond binary32)
+        auto half = [](Pair v) { return Pair{0.5f * v.hi, 0.5f * v.lo}; };
+        const uint64_t worth = ordered_pair(two ? pair_add(half(b1), half(b2)) : half(b1));
         int rank = 0;
         const int g = lane >> a.log_lanes;
         for (int h = 0; h < a.groups; ++h) {

@@ -136,3 +136,14 @@ def test_equal_ones_left_out_by_hand(dtype):
         for score in ("softmax", "sigmoid"):
             for b in (None, bias):
                 assert nrm.route_fwd(x, 2, b, score=score)[1].tolist() == [[7, 20]]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_sum_is_beyond_binary32(score):
+    x = randn(20, 64, seed=6)
+    bias = 1.8e38 + 1.2e38 * rand(64, seed=7)
+    check(x, 6, bias, score=score, groups=8, top_groups=3, group_top=2)
+    check(x, 6, -bias, score=score, groups=8, top_groups=3, group_top=2)
+    x[:, ::3] = -INF
+    bias[5] = -3e38
+    check(x, 6, bias, score=score, groups=8, top_groups=3, group_top=2)
