@@ -614,8 +614,9 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
  *   1 <= k <= experts / groups * top_groups, scale finite; at most 1024 experts,
  *   k 32, and where groups limit the choice 32 groups, group_top 2 and 32 times the
  *   largest power of two in 32 / groups experts a group (else NRM_ERR_UNSUPPORTED)
- * An expert whose logit or bias is -inf, or whose c is NaN, is not available.  A
- * group's sum counts those it has; one without any comes last.  Places that no
+ * An expert whose logit or bias is -inf, or whose c is NaN, is not available (with
+ * softmax a NaN or +inf among a token's logits leaves none).  A group's sum counts
+ * those it has; one without any comes last.  Places that no
  * available expert is left for get id -1 and weight 0, and where the sum of the
  * chosen s is 0 (sigmoids below binary32's range) all weights are 0.
  *

@@ -1007,9 +1007,9 @@ def route_fwd(logits, k, bias=None, *, score="softmax", groups=1, top_groups=Non
     sigmoid of the logits; with top_groups < groups from the top_groups groups of
     neighbouring experts with the largest sums of their group_top best.  Their
     weights are scale * score, renormalized to a sum of scale.  Experts with a
-    logit or bias of -inf are not available; places without one get id -1 and
-    weight 0.  Returns (weights, ids, scores or None): binary32 and int64
-    [..., k], all scores in binary32 with want_scores."""
+    logit or bias of -inf are not available (none is where a softmax is NaN);
+    places without one get id -1 and weight 0.  Returns (weights, ids, scores or
+    None): binary32 and int64 [..., k], all scores in binary32 with want_scores."""
     if stream is not None:
         with _on_stream(stream, logits):
             return route_fwd(logits, k, bias, score=score, groups=groups, top_groups=top_groups, group_top=group_top,

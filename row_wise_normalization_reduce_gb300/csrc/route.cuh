@@ -518,16 +518,32 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                 for (int i = 0; i < (PL > LIST ? LIST + 1 : PL); ++i) key[i] = 0u;
             }
         }
+        // a softmax of a NaN or of infinity is NaN for every expert (keys of scores
+        // show that themselves)
+        if (MODE != KEY_SCORE && a.softmax) {
+            float odd = 0.f;  // finite or -inf where none is, but for overflow
+#pragma unroll
+            for (int i = 0; i < PL; ++i) odd += x[i];
+            if (__any_sync(ALL, !(odd < INFINITY))) {
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) bad = bad || !(x[i] < INFINITY);
+                if (__any_sync(ALL, bad)) {
+                    again = false;
+#pragma unroll
+                    for (int i = 0; i < PL; ++i) key[i] = 0u;
+                }
+            }
+        }
         // places: the k largest
         uint32_t list[LIST + 1], mine = 0u, last = 0u;
 #pragma unroll
         for (int i = 0; i < LIST; ++i) list[i] = key[i];
         list[LIST] = 0u;
         // a lane whose list runs out may hold more
-        int left = PL > LIST && key[PL > LIST ? LIST : 0] ? LIST : PL + 1;
+        int left = PL > LIST && key[PL > LIST ? LIST : 0] ? LIST : kRouteMaxK + 1;
         for (int p = 0; p < a.k; ++p) {
             last = __reduce_max_sync(ALL, list[0]);
-            if (last == 0u) break;  // nobody is left
             if (lane == p) mine = last;
             if (list[0] == last) {
 #pragma unroll
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
             }
             if (PL > LIST && __any_sync(ALL, left == 0)) {
                 again = again || MODE != KEY_WHOLE || p + 1 < a.k;
-                left = PL + 1;
+                left = kRouteMaxK + 1;
             }
         }
         int id = mine ? kIdxMask - (int)(mine & kIdxMask) : -1;
@@ -577,8 +593,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                     }
                     w = __reduce_max_sync(ALL, rest[0]);
                 }
-                if (!again && (border || __any_sync(ALL, close && lane > 0)))
-                    again = !route_resolve<T, PL, LIST>(a, row, lane, mine, last, list, left, near_, &id, &xs);
+                if (!again && (border || __any_sync(ALL, close && lane > 0))) {
+                    // (a copy: by reference to `list` itself it would not stay in registers)
+#pragma unroll
+                    for (int i = 0; i <= LIST; ++i) rest[i] = list[i];
+                    again = !route_resolve<T, PL, LIST>(a, row, lane, mine, last, rest, left, near_, &id, &xs);
+                }
             }
             if (again) {
                 id = route_exact<T, PL>(a, row, lane);
@@ -785,6 +805,7 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
         uint32_t list[8];
         float near_ = MODE == KEY_LOGIT ? 2.f : 0.f;  // keys no further apart than this are in question
         bool again = wild;                            // the whole token is
+        float odd_sum = 0.f;                          // NaN or infinity where a logit is, but for overflow
         if constexpr (MODE == KEY_SCORE)
             // as in route_fwd_kernel; the sum is at most 8 NC + 3 additions deep
             near_ = 2.f * (S * (a.softmax ? (6e-7f + 6e-8f * (PL + 3)) * inv : 3e-7f) + near_bias);
@@ -799,6 +820,10 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
             uint32_t key[8];
             unpack(coming, x);
             if (c + 1 < NC) fetch(c + 1, coming);
+            if constexpr (MODE != KEY_SCORE) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) odd_sum += x[i];
+            }
             if constexpr (MODE == KEY_WHOLE) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -865,6 +890,23 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
                 again = again || (float)(least / 32u - most / 32u) <= (two ? 2.f : 1.f) * near_ || low;
             }
             if (!keep) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) list[i] = 0u;
+            }
+        }
+        // a softmax of a NaN or of infinity is NaN for every expert (keys of scores
+        // show that themselves)
+        if (MODE != KEY_SCORE && a.softmax && __any_sync(ALL, !(odd_sum < INFINITY))) {
+            bool bad = false;
+#pragma unroll 1
+            for (int c = 0; c < NC; ++c) {
+                float x[8];
+                chunk(c, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bad = bad || !(x[i] < INFINITY);
+            }
+            if (__ballot_sync(ALL, bad) & 0xffu << (lane & 24)) {
+                again = false;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) list[i] = 0u;
             }

@@ -147,3 +147,28 @@ def test_groups_whose_sum_is_beyond_binary32(score):
     x[:, ::3] = -INF
     bias[5] = -3e38
     check(x, 6, bias, score=score, groups=8, top_groups=3, group_top=2)
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("experts,k,groups,top_groups,group_top", [(64, 6, 1, 1, 1), (64, 6, 8, 2, 1), (64, 6, 8, 2, 2), (256, 8, 1, 1, 1),
+                                                                   (500, 20, 1, 1, 1), (7, 2, 1, 1, 1)])
+def test_softmax_without_a_value(experts, k, groups, top_groups, group_top, dtype):
+    # a NaN or an infinity among a token's logits leaves no softmax, so no expert is
+    # available; the tokens beside it have theirs
+    x = randn(40, experts, seed=8).to(dtype)
+    bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+    bad[1::3] = True
+    x[1::6, experts // 2] = float("nan")
+    x[4::12, experts - 1] = INF
+    x[10::12, 0] = -float("nan")
+    x[7, :] = float("nan")
+    how = dict(groups=groups, top_groups=top_groups, group_top=group_top)
+    want, ids = R.route(torch.where(bad[:, None], -INF, x), k, **how)
+    for bias in (None, torch.zeros(experts, device="cuda")):
+        for renorm in (True, False):
+            w, got, _ = nrm.route_fwd(x, k, bias, renormalize=renorm, **how)
+            assert torch.equal(got.cpu(), ids) and (got[bad] == -1).all() and not w[bad].any()
+            assert torch.isfinite(w).all()
+    # a sigmoid is each expert's own: a NaN is not available, an infinity is 1
+    got = nrm.route_fwd(x, k, score="sigmoid", **how)[1].cpu()
+    assert torch.equal(got, R.route(x, k, score="sigmoid", **how)[1])
