@@ -622,7 +622,8 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
  *
  * The backward takes the gradient of the weights, the forward's logits and ids and
  * optionally the gradient of the scores, and writes the gradient of the logits.
- * The choice itself has no gradient, nor has the bias.
+ * The choice itself has no gradient, nor has the bias, nor weights that are 0 for
+ * their sum's.
  *   ids         entries outside [0, experts) have no part; an expert listed more than
  *               once gets the sum of its gradients
  *   dscores     [tokens, experts] binary32 or NULL (= 0)

@@ -1015,10 +1015,15 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
 
 // ---------------------------------------------------------------------------
 // The gradient of the logits.  With d_i the gradient of chosen weight i times
-// scale, s_i its score and S the chosen scores' sum, the scores' gradients are
-//   ds_i = d_i,  or renormalised  (d_i - sum_j d_j s_j / S) / S,
-// plus dscores on every expert, and
-//   softmax  dx = s (ds - sum ds s),   sigmoid  dx = ds s (1 - s).
+// scale, s the scores and g the gradient of all of them (dscores, or 0),
+//   softmax  dx = s (ds - sum ds s),   sigmoid  dx = ds s (1 - s),
+// where ds is g plus, for each place i of an expert, d_i.  Renormalised weights w_i =
+// s_i / S, S the chosen scores' sum, have ds_i = (d_i - sum_j d_j w_j) / S, whose sum
+// with s over the chosen is 0, so that their part of dx is
+//   softmax  w_i (d_i - sum_j d_j w_j),   sigmoid  that times 1 - s_i,
+// without a division by S: w comes from the largest of the chosen, as exp(x - largest)
+// (sigmoid: with the factors 1 + exp(-|x|) of the two), and nothing of it underflows
+// that counts.  Sigmoids that are all 0 have weights of 0 and no such part.
 // One warp a token; the row is written without the chosen experts' part first,
 // then lane i writes the entry of chosen expert i whole.
 // ---------------------------------------------------------------------------
@@ -1046,7 +1051,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
         const float xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
         const float gs = id >= 0 && dsc ? dsc[id] : 0.f;
         float m = 0.f, inv = 1.f;
-        if (a.softmax) {
+        if (a.softmax && (dsc || !a.renorm)) {
             m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
@@ -1063,37 +1068,53 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
 #pragma unroll
             for (int i = 0; i < PL; ++i) x[i] *= inv;
         }
-        // the chosen score and its slope in the logit
-        float s, slope;
+        // the chosen score, its slope in the logit, and a sigmoid's 1 - s
+        float s = 0.f, slope = 0.f, rest = 1.f, e = 0.f;
         if (a.softmax) {
-            s = slope = id >= 0 ? expf(xs - m) * inv : 0.f;
-        } else {
-            const float e = expf(-fabsf(xs)), q = 1.f / (1.f + e);
-            s = id >= 0 ? (xs < 0.f ? e * q : q) : 0.f;
-            slope = id >= 0 ? e * q * q : 0.f;
+            if (id >= 0 && (dsc || !a.renorm)) s = slope = expf(xs - m) * inv;
+        } else if (id >= 0) {
+            e = expf(-fabsf(xs));
+            const float q = 1.f / (1.f + e);
+            s = xs < 0.f ? e * q : q;
+            rest = xs < 0.f ? q : e * q;
+            slope = e * q * q;
         }
-        if (a.renorm) {
-            const float sum = warp_sum_all(s), mean = warp_sum_all(dw * s) / sum;
-            dw = sum == 0.f ? 0.f : (dw - mean) / sum;
-        }
+        // dw: the weights' part of dx; the scores' part of a softmax has its sum in dot
         float dot = 0.f;
-        if (a.softmax) {
+        if (a.renorm) {
+            const float top = from_ordered32(__reduce_max_sync(ALL, ordered32(id >= 0 ? xs : -INFINITY)));
+            const bool some = a.softmax ? top != -INFINITY : __any_sync(ALL, s != 0.f);
+            float w = 0.f;
+            if (id >= 0 && some) {
+                // beyond 0 a sigmoid's exponential is the other factor's
+                w = a.softmax ? expf(xs - top)
+                              : expf(fminf(xs, 0.f) - fminf(top, 0.f)) * (1.f + expf(-fabsf(top))) / (1.f + e);
+            }
+            const float sum = warp_sum_all(w);
+            w = some ? w / sum : 0.f;
+            dw = w * (dw - warp_sum_all(dw * w)) * rest;
+        } else {
+            dot = a.softmax ? warp_sum_all(dw * s) : 0.f;
+            dw *= slope;
+        }
+        if (a.softmax && dsc) {
+            float all = 0.f;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) dot = fmaf(g[i], x[i], dot);
-            dot = warp_sum_all(fmaf(dw, s, dot));
+            for (int i = 0; i < PL; ++i) all = fmaf(g[i], x[i], all);
+            dot += warp_sum_all(all);
         }
         __syncwarp();  // dx may replace the logits: every lane has read its own
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-            const int e = i * 32 + lane;
-            float v;
+            const int j = i * 32 + lane;
+            float v = 0.f;
             if (a.softmax) {
-                v = x[i] * (g[i] - dot);
-            } else {
+                if (dsc || !a.renorm) v = x[i] * (g[i] - dot);
+            } else if (dsc) {
                 const float z = expf(-fabsf(x[i])), q = 1.f / (1.f + z);
                 v = g[i] * z * q * q;
             }
-            if (e < a.experts) out[e] = IO<T>::from_f(v);
+            if (j < a.experts) out[j] = IO<T>::from_f(v);
         }
         // an expert listed twice: its gradients add up, and its first lane writes
         const uint32_t same = __match_any_sync(ALL, (int)id);
@@ -1106,7 +1127,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
             dw = all;
         }
         __syncwarp();
-        if (id >= 0 && lane == __ffs(same) - 1) out[id] = IO<T>::from_f(slope * (gs + dw - dot));
+        if (id >= 0 && lane == __ffs(same) - 1) out[id] = IO<T>::from_f(fmaf(slope, gs - dot, dw));
     }
 }
 
