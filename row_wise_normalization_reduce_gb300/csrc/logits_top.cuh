@@ -516,12 +516,13 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
                     n = sh.groups_found[parity];
                 }
                 TopList list;
-                bool again = false;
                 while (true) {
                     top_scan<T, TH, PK>(w, found, n, per, [&](float f, uint32_t at) {
                         list.offer(top_finite(f) && top_ordered(f) >= T32, top_key(f, at), k, lane);
                     });
-                    if (warp == 0 && !again) {
+                    // the row's ends at last: the tail's columns are above all groups', so it
+                    // may not raise the bound for them
+                    if (warp == 0 && cut == group) {
                         const float zs = t < w.ns ? sh.ends[parity][t] : -INFINITY;
                         list.offer(top_finite(zs), top_key(zs, (uint32_t)w.sc), k, lane);
                     }
@@ -546,7 +547,6 @@ __global__ void __launch_bounds__(TH, MINB) logit_top_kernel(const TopArgs ta, c
                             found[atomicAdd(&sh.groups_found[parity], 1)] = (unsigned short)(cut * TH + t);
                     __syncthreads();
                     n = sh.groups_found[parity];
-                    again = true;
                 }
             }
             // The row's outputs, by the threads that find a candidate.  (For one warp

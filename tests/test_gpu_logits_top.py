@@ -280,3 +280,21 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert nrm.device_fault() == 0
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("rows,v,shift", [(310, 16385, 0), (310, 16389, 3), (310, 16387, 5), (700, 8193, 0), (3, 65537, 0), (620, 300007, 0)])
+@pytest.mark.parametrize("k", [1, 2, 5, 32])
+def test_ties_with_the_last_columns(rows, v, shift, k, dtype):
+    # most logits are equal, some larger ones as well, and the k-th largest among
+    # the columns behind the last whole pack: lower columns of its value come first
+    flat = torch.zeros(rows * v + shift, device="cuda", dtype=dtype)
+    z = flat[shift:].view(rows, v)
+    for r in range(min(rows, 9)):
+        z[r, v - 1 - r % 3] = 1.0
+        z[r, :k - 1] = 1.0  # k with the one at the end
+        z[r, v // 4 + 3::4096] = 1.0
+    z[min(rows, 9) - 1, :] = 1.0
+    if rows > 9:
+        z[9:, 0], z[9:, min(4096, v // 2)], z[9:, v - 1] = 1.0, 1.0, 1.0
+    check_fwd(z, torch.zeros(rows, dtype=torch.int64, device="cuda"), k)
