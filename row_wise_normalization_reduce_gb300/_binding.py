@@ -851,6 +851,8 @@ def _heads(t, shape, dtype, dev, name):
         return st[0], st[1]
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"the entries of a head of {name} must be contiguous")
+    if 0 in shape[:-2]:
+        return 0, st[-2]  # no tokens: no stride is used
     step, n = None, 1
     for d in range(t.dim() - 3, -1, -1):
         if shape[d] == 1:

@@ -210,3 +210,16 @@ def test_streams_graphs_and_shared_workspace():
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     again = nrm.qk_norm_rope_bwd(gk, gk, k, k, table, pos, wk, wk)
     assert all(torch.equal(a, b) for a, b in zip(outs[6:], again))
+
+
+def test_empty_batches_of_several_dimensions():
+    q, k, wq, wk, table, pos = make(6, 4, 2, 64, 64, torch.bfloat16, 6)
+    for lead in ((2, 0), (0, 2), (0, 0, 3), (3, 2, 0)):
+        def none(heads, inner=64):
+            return torch.empty(*lead, heads, inner, dtype=torch.bfloat16, device="cuda")
+        p = torch.empty(lead, dtype=torch.int64, device="cuda")
+        yq, yk = nrm.qk_norm_rope_fwd(none(4), none(2), table, p, wq, wk, q_out=none(4))
+        assert yq.shape == (*lead, 4, 64) and yk.shape == (*lead, 2, 64)
+        sliced = none(8)
+        dq, dk, dwq, dwk = nrm.qk_norm_rope_bwd(none(4), none(2), sliced[..., :4, :], sliced[..., 4:6, :], table, p, wq, wk)
+        assert dq.shape == (*lead, 4, 64) and dk.shape == (*lead, 2, 64) and not dwq.any() and not dwk.any()
