@@ -844,6 +844,8 @@ def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=No
 def _heads(t, shape, dtype, dev, name):
     """(token stride, head stride) of a tensor [..., heads, D] whose leading
     dimensions have one stride between tokens."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype} on device {dev}")
     st = t.stride()
@@ -960,9 +962,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, positions, wq=None, wk=None, e
     kp = gkp = dkp = None
     kt = kh = gkt = gkh = dkt = dkh = 0
     if kshape is not None:
-        kp, gkp = k.data_ptr(), dk_out.data_ptr()
         kt, kh = _heads(k, kshape, dtype, dev, "k")
         gkt, gkh = _heads(dk_out, kshape, dtype, dev, "dk_out")
+        kp, gkp = k.data_ptr(), dk_out.data_ptr()
         if dk is None:
             dk, dkt, dkh = torch.empty(kshape, dtype=dtype, device=device), hk * d, d
         else:

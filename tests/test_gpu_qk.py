@@ -223,3 +223,11 @@ def test_empty_batches_of_several_dimensions():
         sliced = none(8)
         dq, dk, dwq, dwk = nrm.qk_norm_rope_bwd(none(4), none(2), sliced[..., :4, :], sliced[..., 4:6, :], table, p, wq, wk)
         assert dq.shape == (*lead, 4, 64) and dk.shape == (*lead, 2, 64) and not dwq.any() and not dwk.any()
+
+
+def test_gradient_of_the_keys_is_asked_for():
+    q, k, wq, wk, table, pos = make(6, 4, 2, 64, 64, torch.float32, 6)
+    with pytest.raises(ValueError, match="dk_out"):
+        nrm.qk_norm_rope_bwd(q, None, q, k, table, pos, wq, wk)
+    with pytest.raises(ValueError, match="dq_out"):
+        nrm.qk_norm_rope_bwd(None, k, q, k, table, pos, wq, wk)
