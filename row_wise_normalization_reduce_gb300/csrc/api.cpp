@@ -1567,6 +1567,8 @@ int qk_norm_rope_fwd(const void *q, int64_t q_token, int64_t q_head, const void 
     int st = qk_values(tokens, q_heads, k_heads, D, rot, max_pos, eps, dtype);
     if (st != NRM_OK) return st;
     if (tokens == 0) return NRM_OK;  // empty input: no pointer is used
+    if (k_heads == 0) k = wk = nullptr, k_out = nullptr;  // what is not used is not looked at
+    if (rot == 0) table = nullptr;
     QkArgs a{};
     a.side[0] = QkSide{q, wq, nullptr, q_out, q_token, q_head, 0, 0, qo_token, qo_head, (int)q_heads};
     a.side[1] = QkSide{k, wk, nullptr, k_out, k_token, k_head, 0, 0, ko_token, ko_head, (int)k_heads};
@@ -1608,6 +1610,8 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
         if ((st = check_pointers({dwq, dwk})) != NRM_OK) return st;
         return launched(launch_qk_fold(nullptr, dwq, dwk, 0, (int)D, stream));
     }
+    if (k_heads == 0) k = wk = dk_out = nullptr, dk = nullptr;  // what is not used is not looked at
+    if (rot == 0) table = nullptr;
     QkArgs a{};
     a.side[0] = QkSide{q, wq, dq_out, dq, q_token, q_head, dqo_token, dqo_head, dq_token, dq_head, (int)q_heads};
     a.side[1] = QkSide{k, wk, dk_out, dk, k_token, k_head, dko_token, dko_head, dk_token, dk_head, (int)k_heads};
@@ -1842,6 +1846,7 @@ int logprob_top_bwd_ld(const float *dlogp, const float *dentropy, const float *d
     if (rows == 0) return NRM_OK;  // empty input: no pointer is used
     if (k == 0) dtop_logp = nullptr;
     if (!dtop_logp) top_ids = nullptr;
+    if (!dentropy) entropy = nullptr;
     if (!logits || !targets || !stats || !dlogits || (!dlogp && !dentropy && !dtop_logp) || (dentropy && !entropy) ||
         (dtop_logp && !top_ids))
         return NRM_ERR_NULL;

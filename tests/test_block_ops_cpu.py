@@ -216,3 +216,22 @@ def test_logprob_top_refusals(lib):
         (dict(k=-1), SHAPE), (dict(lddz=63), SHAPE), (dict(dz=4 * A, lddz=65), ALIAS), (dict(dz=8 * A), ALIAS), (dict(dz=7 * A), ALIAS),
         (dict(dz=3 * A), ALIAS), (dict(st=6 * A + 2), VALUE), (dict(ids=8 * A + 4), VALUE), (dict(s=-1.0), VALUE), (dict(dtype=3), DTYPE),
     ])
+
+
+def test_pointers_that_are_not_used_are_not_looked_at(lib):
+    # refused by nothing: off their alignment, or where an output lies
+    good = dict(q=A, qt=64, qh=64, k=None, kt=0, kh=0, tab=2 * A, pos=3 * A, wq=None, wk=None, qo=6 * A, qot=64, qoh=64,
+                         ko=None, kot=0, koh=0, t=4, hq=1, hk=0, d=64, rot=64, most=100, eps=1e-6, near=0, dtype=0, stream=None)
+    _bad(lib, "qk_norm_rope_fwd", good, [
+        (dict(), (OK, DEVICE)), (dict(k=A + 1, wk=A + 1, ko=A + 1), (OK, DEVICE)), (dict(wk=6 * A), (OK, DEVICE)),
+        (dict(rot=0, tab=2 * A + 1), (OK, DEVICE)), (dict(rot=0, tab=6 * A), (OK, DEVICE))])
+    back = dict(gq=A, gqt=64, gqh=64, gk=None, gkt=0, gkh=0, q=2 * A, qt=64, qh=64, k=None, kt=0, kh=0, tab=3 * A, pos=4 * A, wq=None,
+                wk=None, dq=5 * A, dqt=64, dqh=64, dk=None, dkt=0, dkh=0, dwq=6 * A, dwk=None, t=4, hq=1, hk=0, d=64, rot=64, most=100,
+                eps=1e-6, near=0, dtype=0, ws=7 * A, wsb=608 * 2 * 64 * 4, stream=None)
+    _bad(lib, "qk_norm_rope_bwd", back, [
+        (dict(), (OK, DEVICE)), (dict(gk=A + 1, k=A + 1, wk=A + 1, dk=A + 1), (OK, DEVICE)), (dict(wk=6 * A), (OK, DEVICE)),
+        (dict(rot=0, tab=3 * A + 1), (OK, DEVICE)), (dict(rot=0, tab=7 * A), (OK, DEVICE))])
+    top = dict(g=A, h=None, a=None, z=2 * A, ldz=64, t=3 * A, st=4 * A, ent=None, ids=None, dz=5 * A, lddz=64, rows=4, V=64, k=5, s=1.0,
+               dtype=0, stream=None)
+    _bad(lib, "logprob_top_bwd_ld", top, [
+        (dict(), (OK, DEVICE)), (dict(ent=6 * A + 1), (OK, DEVICE)), (dict(ent=5 * A), (OK, DEVICE)), (dict(ids=5 * A), (OK, DEVICE))])
