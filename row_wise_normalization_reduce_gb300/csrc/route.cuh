@@ -116,14 +116,9 @@ __device__ __forceinline__ float route_rcp(float x) {
     return r;
 }
 
-// 1 / x, to a step, for x in [2^-100, 2^100].
-__device__ __forceinline__ float route_inv(float x) {
-    const float r = route_rcp(x);
-    return fmaf(r, fmaf(-x, r, 1.f), r);
-}
 // 1 / (1 + exp(-x)), to a few steps of 2^-24.
 __device__ __forceinline__ float route_sigmoid(float x) {
-    const float e = expf(-fabsf(x)), q = route_inv(1.f + e);
+    const float e = expf(-fabsf(x)), q = __fdividef(1.f, 1.f + e);
     return x < 0.f ? e * q : q;
 }
 
@@ -620,7 +615,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
         }
         if (a.renorm) {
             const float sum = warp_sum_all(w);
-            w = sum > 1e-30f ? w * route_inv(sum) : sum == 0.f ? 0.f : w / sum;
+            w = sum > 1e-30f ? __fdividef(w, sum) : sum == 0.f ? 0.f : w / sum;
         }
         if (lane < a.k) {
             a.weights[t * a.k + lane] = w * a.scale;
@@ -1004,7 +999,7 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
         }
         if (a.renorm) {
             const float sum = group_sum_all<8>(w);
-            w = sum > 1e-30f ? w * route_inv(sum) : sum == 0.f ? 0.f : w / sum;
+            w = sum > 1e-30f ? __fdividef(w, sum) : sum == 0.f ? 0.f : w / sum;
         }
         if (real && l < a.k) {
             a.weights[t * a.k + l] = w * a.scale;

@@ -299,3 +299,25 @@ def test_the_plans_agree(experts, k, groups, top_groups, group_top, dtype):
             finally:
                 nrm.force_plan(nrm.PLAN_AUTO)
             assert torch.equal(ids, ids2) and (w - w2).abs().max() <= 2 * R.SCORE
+
+
+@pytest.mark.parametrize("k", [8, 20])
+def test_weights_to_the_last_bits(k):
+    # u = 2^-24.  expf is good to 2 steps (4 u), __fdividef as well, a sum or product to
+    # u: a sigmoid to 10 u, renormalised with 5 levels of additions to 10 + 10 + 5 + 4 =
+    # 29 u; a renormalised softmax of logits at most 16 below the chosen ones' largest,
+    # whose differences are exact here, to 4 + 4 + 5 + 4 = 17 u
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.rand(4000, 64, generator=g, device="cuda") * 160 - 80
+    w, ids, _ = nrm.route_fwd(x, k, score="sigmoid", renormalize=False)
+    s = torch.sigmoid(x.double()).gather(1, ids)
+    assert ((w.double() - s).abs() <= 10 * R.U * s).all()
+    x = x.abs().neg()  # scores of all sizes among the chosen
+    w, ids, _ = nrm.route_fwd(x, k, score="sigmoid")
+    s = torch.sigmoid(x.double()).gather(1, ids)
+    s /= s.sum(1, keepdim=True)
+    assert ((w.double() - s).abs() <= 29 * R.U * s).all()
+    x = torch.randint(0, 16 * 64, (4000, 64), generator=g, device="cuda") / 64.0
+    w, ids, _ = nrm.route_fwd(x, k)
+    s = torch.softmax(x.double().gather(1, ids), -1)
+    assert ((w.double() - s).abs() <= 17 * R.U * s).all()
