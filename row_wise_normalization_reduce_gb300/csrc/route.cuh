@@ -566,34 +566,32 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
                 const float bu = __shfl_up_sync(ALL, bs, 1);
                 if (lane > 0) close = close && !(xs == xu && bs == bu);
                 // those equal to the last place come after it, but before a place in
-                // question that turns out to be smaller: `list` keeps them
+                // question that turns out to be smaller: with any passed over, such a
+                // token is done again (kept beside the list, for route_resolve, they would
+                // cost 16 to 27 registers and with them a CTA an SM)
                 uint32_t w = after, rest[LIST + 1];
-                int rest_left = left;
 #pragma unroll
                 for (int i = 0; i <= LIST; ++i) rest[i] = list[i];
                 const float xl = __shfl_sync(ALL, xs, a.k - 1), bl = __shfl_sync(ALL, bs, a.k - 1);
-                bool border = false;
+                bool border = false, equal = false;
                 while (w && (float)((last >> kIdxBits) - (w >> kIdxBits)) <= near_) {
                     const int e = kIdxMask - (int)(w & kIdxMask);
                     border = !(IO<T>::to_f(row[e]) == xl && (MODE == KEY_SCORE && a.bias ? a.bias[e] : 0.f) == bl);
                     if (border) break;
+                    equal = true;
                     if (rest[0] == w) {
 #pragma unroll
                         for (int i = 0; i < LIST; ++i) rest[i] = rest[i + 1];
-                        --rest_left;
+                        --left;
                     }
-                    if (PL > LIST && __any_sync(ALL, rest_left == 0)) {
+                    if (PL > LIST && __any_sync(ALL, left == 0)) {
                         again = true;
                         break;
                     }
                     w = __reduce_max_sync(ALL, rest[0]);
                 }
-                if (!again && (border || __any_sync(ALL, close && lane > 0))) {
-                    // (a copy: by reference to `list` itself it would not stay in registers)
-#pragma unroll
-                    for (int i = 0; i <= LIST; ++i) rest[i] = list[i];
-                    again = !route_resolve<T, PL, LIST>(a, row, lane, mine, last, rest, left, near_, &id, &xs);
-                }
+                if (!again && (border || __any_sync(ALL, close && lane > 0)))
+                    again = equal || !route_resolve<T, PL, LIST>(a, row, lane, mine, last, rest, left, near_, &id, &xs);
             }
             if (again) {
                 id = route_exact<T, PL>(a, row, lane);
