@@ -1014,9 +1014,10 @@ __global__ void __launch_bounds__(kRouteThreads, 4) route_oct_kernel(const Route
 // s_i / S, S the chosen scores' sum, have ds_i = (d_i - sum_j d_j w_j) / S, whose sum
 // with s over the chosen is 0, so that their part of dx is
 //   softmax  w_i (d_i - sum_j d_j w_j),   sigmoid  that times 1 - s_i,
-// without a division by S: w comes from the largest of the chosen, as exp(x - largest)
-// (sigmoid: with the factors 1 + exp(-|x|) of the two), and nothing of it underflows
-// that counts.  Sigmoids that are all 0 have weights of 0 and no such part.
+// without a division by S, which may be 0 or subnormal where the weights are
+// ordinary numbers: w comes from the largest of the chosen, as exp(x - largest),
+// sigmoid that / (1 + exp(x)) below 0.  Sigmoids that are all 0 have weights of 0
+// and no such part.
 // One warp a token; the row is written without the chosen experts' part first,
 // then lane i writes the entry of chosen expert i whole.
 // ---------------------------------------------------------------------------
@@ -1044,7 +1045,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
         const float xs = id >= 0 ? IO<T>::to_f(row[id]) : -INFINITY;
         const float gs = id >= 0 && dsc ? dsc[id] : 0.f;
         float m = 0.f, inv = 1.f;
-        if (a.softmax && (dsc || !a.renorm)) {
+        if (a.softmax) {
             m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
@@ -1062,52 +1063,50 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
             for (int i = 0; i < PL; ++i) x[i] *= inv;
         }
         // the chosen score, its slope in the logit, and a sigmoid's 1 - s
-        float s = 0.f, slope = 0.f, rest = 1.f, e = 0.f;
+        float s, slope, rest = 1.f;
         if (a.softmax) {
-            if (id >= 0 && (dsc || !a.renorm)) s = slope = expf(xs - m) * inv;
-        } else if (id >= 0) {
-            e = expf(-fabsf(xs));
-            const float q = 1.f / (1.f + e);
-            s = xs < 0.f ? e * q : q;
+            s = slope = id >= 0 ? expf(xs - m) * inv : 0.f;
+        } else {
+            const float e = expf(-fabsf(xs)), q = 1.f / (1.f + e);
+            s = id >= 0 ? (xs < 0.f ? e * q : q) : 0.f;
             rest = xs < 0.f ? q : e * q;
-            slope = e * q * q;
+            slope = id >= 0 ? e * q * q : 0.f;
         }
-        // dw: the weights' part of dx; the scores' part of a softmax has its sum in dot
+        // dw: the weights' part of dx; dot: a softmax' sum of ds s without that
         float dot = 0.f;
         if (a.renorm) {
+            // w from s where the row's largest is among the chosen (of sigmoids: one of
+            // 1/2 and more), else from the differences to the chosen ones' largest
             const float top = from_ordered32(__reduce_max_sync(ALL, ordered32(id >= 0 ? xs : -INFINITY)));
-            const bool some = a.softmax ? top != -INFINITY : __any_sync(ALL, s != 0.f);
-            float w = 0.f;
-            if (id >= 0 && some) {
-                // beyond 0 a sigmoid's exponential is the other factor's
-                w = a.softmax ? expf(xs - top)
-                              : expf(fminf(xs, 0.f) - fminf(top, 0.f)) * (1.f + expf(-fabsf(top))) / (1.f + e);
+            float w = s;
+            if (!(top >= m)) {
+                const bool none = a.softmax ? top == -INFINITY : expf(top) == 0.f;
+                w = id >= 0 && !none ? expf(xs - top) * rest : 0.f;
             }
             const float sum = warp_sum_all(w);
-            w = some ? w / sum : 0.f;
+            w *= sum == 0.f ? 0.f : 1.f / sum;
             dw = w * (dw - warp_sum_all(dw * w)) * rest;
         } else {
-            dot = a.softmax ? warp_sum_all(dw * s) : 0.f;
+            if (a.softmax) dot = dw * s;
             dw *= slope;
         }
-        if (a.softmax && dsc) {
-            float all = 0.f;
+        if (a.softmax) {
 #pragma unroll
-            for (int i = 0; i < PL; ++i) all = fmaf(g[i], x[i], all);
-            dot += warp_sum_all(all);
+            for (int i = 0; i < PL; ++i) dot = fmaf(g[i], x[i], dot);
+            dot = warp_sum_all(dot);
         }
         __syncwarp();  // dx may replace the logits: every lane has read its own
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-            const int j = i * 32 + lane;
-            float v = 0.f;
+            const int e = i * 32 + lane;
+            float v;
             if (a.softmax) {
-                if (dsc || !a.renorm) v = x[i] * (g[i] - dot);
-            } else if (dsc) {
+                v = x[i] * (g[i] - dot);
+            } else {
                 const float z = expf(-fabsf(x[i])), q = 1.f / (1.f + z);
                 v = g[i] * z * q * q;
             }
-            if (j < a.experts) out[j] = IO<T>::from_f(v);
+            if (e < a.experts) out[e] = IO<T>::from_f(v);
         }
         // an expert listed twice: its gradients add up, and its first lane writes
         const uint32_t same = __match_any_sync(ALL, (int)id);
