@@ -568,7 +568,9 @@ int policy_loss_ld(const void *logits, int64_t ldl, const int64_t *targets, cons
  *               (the same pointer and strides)
  *   0 <= rot <= D, rot even; 1 <= D <= 512 (else NRM_ERR_UNSUPPORTED); eps >= 0
  * A token whose position lies outside the table takes no part: its rows are not
- * read, its outputs are 0.  All arithmetic is binary32, rounded once at the end.
+ * read, its outputs are 0.  All arithmetic is binary32, rounded once at the end.  A
+ * row or weight with an infinity or a NaN may give NaN in any entry of the rows that
+ * it has a part in.
  *
  * The backward takes the gradients of q_out and k_out and q, k as the forward got
  * them.  With g = the output's gradient turned back and u = g w:
@@ -605,7 +607,9 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
  * largest c.  Of those that stay the k largest c are taken, largest first; their
  * weights are scale s, or with `renormalize` scale s / (the sum of the chosen s).
  * The order is that of the exact c: what binary32 cannot tell apart is compared to
- * some 42 bits.  Among equal c the lowest index comes first.
+ * some 42 bits of the score and the bias (a score below 2^-100 to fewer, down to
+ * 2^-149).  Among equal c the lowest index comes first; groups whose sums differ by less
+ * than that may come in either order.
  *   logits      [tokens, experts] dtype (row stride ldl)
  *   bias        [experts] binary32 or NULL (= 0); it has no part in the weights
  *   weights     [tokens, k] binary32
@@ -616,14 +620,14 @@ int qk_norm_rope_bwd(const void *dq_out, int64_t dqo_token, int64_t dqo_head, co
  *   largest power of two in 32 / groups experts a group (else NRM_ERR_UNSUPPORTED)
  * An expert whose logit or bias is -inf, or whose c is NaN, is not available (with
  * softmax a NaN or +inf among a token's logits leaves none).  A group's sum counts
- * those it has; one without any comes last.  Places that no
- * available expert is left for get id -1 and weight 0, and where the sum of the
- * chosen s is 0 (sigmoids below binary32's range) all weights are 0.
+ * those it has; one without any comes last.  Places that no available expert is left
+ * for get id -1 and weight 0, and where the sum of the chosen s is 0 (sigmoids below
+ * binary32's range) all weights are 0.
  *
  * The backward takes the gradient of the weights, the forward's logits and ids and
  * optionally the gradient of the scores, and writes the gradient of the logits.
- * The choice itself has no gradient, nor has the bias, nor weights that are 0 for
- * their sum's.
+ * The choice itself has no gradient, nor has the bias, nor have weights that are 0
+ * because the chosen s are.
  *   ids         entries outside [0, experts) have no part; an expert listed more than
  *               once gets the sum of its gradients
  *   dscores     [tokens, experts] binary32 or NULL (= 0)

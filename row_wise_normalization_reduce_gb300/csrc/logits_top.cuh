@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(128, MINB) logit_top_warp_kernel(const TopArgs
 // Any row: a CTA, or the CTAs of a cluster with a slice of the packs each, goes
 // over it in segments of TH x PK packs, the next segment on its way into shared
 // memory meanwhile.  4096 x 131072 bf16, a quarter of the rows out: without
-// alternatives 125 us, 95 % of the measured copy rate; with 20 148 us.  A row's
+// alternatives 126 us, 94 % of the measured copy rate; with 20 150 us.  A row's
 // selection (three barriers, the found groups' way from L2) is a CTA's own time,
 // which the other three CTAs of its SM stream through.
 // ---------------------------------------------------------------------------
@@ -749,15 +749,18 @@ cudaError_t launch_top_cta(const TopArgs &a, int cs, int sms, cudaStream_t s, Pl
     return launch_clusters(kernel, (a.a.rows + batch - 1) / batch, cs, TH, smem, s, a, cs, (int)batch);
 }
 
-// Device times of bf16 with 20 alternatives, inputs beyond L2.  Rows of up to 512
-// packs by a warp, where rows are many: 8192 x 4000 45 us (with 32 alternatives,
-// whose lower bound is the least of the lanes' maxima, 100; by CTAs of 128 113).
-// Then CTAs of 128 threads up to 4096 packs, for what a row costs beside its packs
-// is paid by each warp: 4096 x 8000 46 us, by CTAs of 256 72; 4096 x 32000 86 and 87.
-// Longer rows keep more in flight by 256: 4096 x 131072 148, by 128 171.  A row over
-// two or more CTAs while they do not cover the SMs twice: 200 x 32000 12.6 us by
-// two and 19.8 by four; beyond that the second list a row costs more than it
-// gives: f32 513 x 50001 27 us, by two CTAs 33.
+// Device times of bf16 with 20 alternatives, inputs beyond L2, all of them of this
+// form of the kernels.  Rows of up to 512 packs by a warp, where rows are many: 8192 x
+// 4000 45 us, by CTAs of 128 threads 92, of 256 137 (with 32 alternatives, whose lower
+// bound is the least of the lanes' maxima, 103 and 122 by CTAs of 128); 8192 x 1000
+// 17.5 and 91.  Then CTAs of 128 up to 4096 packs, for what a row costs beside its packs
+// is paid by each warp: 4096 x 8000 47 us, by CTAs of 256 77; 4096 x 32000 88 and 93.
+// Longer rows keep more in flight by 256: 4096 x 131072 149, by 128 173; the two meet
+// above the border (4096 x 50257 136, by 128 124).  A row over two or more CTAs while
+// they do not cover the SMs twice, so that a few long rows are not one SM's each: 200 x
+// 32000 13.6 us by two and 22 by four, but 10.6 by one, so that this border, too, is
+// not where the two meet; beyond it the second list a row costs more than it gives
+// (f32 513 x 50001 26.5 us, by two CTAs 32).
 template <typename T> cudaError_t launch_logit_top_t(const TopArgs &a, int sms, cudaStream_t s, Plan *p) {
     const int64_t packs = a.a.V / IO<T>::V;
     if (packs <= 32 * 4) return launch_top_warp<T, 4, 8>(a, s, p);

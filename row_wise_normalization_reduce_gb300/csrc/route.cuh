@@ -16,8 +16,8 @@
 // put two experts in the wrong order only where their keys are a few steps
 // apart.  Such tokens are found afterwards by the gaps between neighbouring
 // places: the few experts in question are then compared to 42 bits, one a lane,
-// and where a border between groups is that near the whole token is done again
-// so.  Equal logits with equal biases are equal, not near.
+// and where a border between groups is that near, or experts equal to the last place
+// were passed over, the whole token is done again so.  Equal logits with equal biases are equal, not near.
 //
 // Without a bias and without sums over two experts the order of c is that of x;
 // 16-bit logits then fit the key as they are and nothing is in question.
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_fwd_kernel(const RouteArg
 // eight largest (the larger of entry i of one list and entry 7 - i of the other
 // are the eight largest of both, and three stages of exchanges sort them); three
 // merges of the same kind join the lanes.  65536 x 256 bf16 in 8 groups: 38 us, a
-// warp a token 64; without groups and bias 23 and 32.  Bound by instructions, 320 a
+// warp a token 65; without groups and bias 23 and 34.  Bound by instructions, 320 a
 // token (the keys' exponentials and sorting networks most of them), and by the
 // last turn: 3.4 of four.  (Taking tokens from a counter instead: no change.)
 // ---------------------------------------------------------------------------
