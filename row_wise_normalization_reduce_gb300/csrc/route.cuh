@@ -1084,7 +1084,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
                 w = id >= 0 && !none ? expf(xs - top) * rest : 0.f;
             }
             const float sum = warp_sum_all(w);
-            w *= sum == 0.f ? 0.f : 1.f / sum;
+            // (one expert alone has a weight of 1, exactly, and no gradient)
+            w = sum == 0.f ? 0.f : w == sum ? 1.f : w * (1.f / sum);
             dw = w * (dw - warp_sum_all(dw * w)) * rest;
         } else {
             if (a.softmax) dot = dw * s;

@@ -142,3 +142,14 @@ def test_far_below_against_differences(score):
         d = sum(s * (renormalised(dw, v, ids, score, 1.0)[2] * dw).sum(1) for s, v in ((1, hi), (-1, lo))) / (2 * step)
         # third derivatives of a softmax are below 1: step^2 / 6 of sum |dw|
         assert ((d - dx.gather(1, ids[:, j:j + 1])[:, 0]).abs() <= (step ** 2 / 6 + 2.0 ** -14) * dw.abs().sum(1)).all()
+
+
+@pytest.mark.parametrize("dtype", R.DTYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_expert_alone(score, dtype):
+    # its weight is the scale, whatever its logit
+    x = randn(500, 96, seed=1, scale=4.0).to(dtype)
+    ids = some_ids(500, 96, 3, 2)
+    assert not nrm.route_bwd(randn(500, 1, seed=3), x, ids[:, :1].contiguous(), score=score).any()
+    ids[:, 0] = ids[:, 2] = -1
+    assert not nrm.route_bwd(randn(500, 3, seed=3), x, ids, score=score).any()
